@@ -38,7 +38,7 @@ def _load() -> ctypes.CDLL:
         raise ImportError(
             f"{LIB_PATH} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
     L = ctypes.CDLL(LIB_PATH)
-    p, i, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    p, i, f, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
     sig = {
         "sk_init": ([ctypes.c_size_t], i),
         "sk_shutdown": ([], i),
@@ -59,6 +59,10 @@ def _load() -> ctypes.CDLL:
         "sk_version": ([], i),
         "sk_inject_wait_timeout": ([i], None),
         "nvfp4_gemm_noalloc": ([p, p, p, f, p, i, i, i, p], i),
+        "kv4_append": ([p, ll, p, ll, p, p, f, f, p, p, i, i, i, i, i, p], i),
+        "kv4_attention": ([p, ll, p, p, p, f, f, f, p, p, p, p, i, i, i, i, i, i, i, i, p], i),
+        "kv4_evict": ([p, p, p, p, p, p, p, p, i, i, i, i, i, i, i, i, i, p], i),
+        "token_logprobs": ([p, i, ll, p, f, i, p, p, p, p, p, i, i, p], i),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -72,7 +76,7 @@ lib = _load()
 # Names declared in include/skinny.h (the tests check that each is exported).
 EXPORTS = ("sk_init", "sk_shutdown", "sk_stream_workspace", "nvfp4_gemm", "nvfp4_gemm_f16out", "fp8_gemm",
            "fp8_gemm_f16out", "lm_head_argmax", "lm_head_verify", "lm_head_sample", "fp8_quantize",
-           "nvfp4_quantize",
+           "nvfp4_quantize", "kv4_append", "kv4_attention", "kv4_evict", "token_logprobs",
            "sk_status_string", "sk_last_device_error",
            "sk_set_pdl", "sk_set_variant", "sk_inject_wait_timeout", "nvfp4_gemm_noalloc", "sk_version")
 
@@ -278,3 +282,176 @@ def lm_head_sample(x, W_codes, W_scales, W_gscale: float, u, temperature: float,
                               logits.data_ptr(), u.data_ptr(), float(temperature), int(top_k), float(top_p),
                               token.data_ptr(), M, N, K, _stream_ptr(stream)), "lm_head_sample")
     return logits, token
+
+
+# ------------------------------------------- key/value cache in 4 bits ------
+
+def kv4_cache(pages: int, kv_heads: int, head_dim: int, page_size: int, device="cuda"):
+    """An empty cache: uint8 [pages][kv_heads][page_size / 16][18 * head_dim] (include/skinny.h has the record)."""
+    import torch
+
+    if page_size % 16 or head_dim not in (64, 128, 256):
+        raise ValueError("page_size must be a multiple of 16 and head_dim 64, 128 or 256")
+    return torch.zeros((pages, kv_heads, page_size // 16, 18 * head_dim), dtype=torch.uint8, device=device)
+
+
+def _cache_dims(cache):
+    """(pages, kv_heads, head_dim, page_size) of a cache."""
+    import torch
+
+    if cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_cuda or not cache.is_contiguous():
+        raise TypeError("cache must be a contiguous 4-D CUDA uint8 tensor [pages][kv_heads][page_size/16][18 head_dim]")
+    pages, heads, recs, rec = cache.shape
+    if rec % 18:
+        raise ValueError(f"cache records of {rec} bytes: expected 18 * head_dim")
+    return pages, heads, rec // 18, recs * 16
+
+
+def _need(t, dtype, shape, what):
+    """`t` as a contiguous CUDA tensor of this type and shape, or an error naming it."""
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _rows_f16(t, heads, dim, what):
+    """Strided rows [T][heads][dim] of FP16: (rows, elements from row to row)."""
+    import torch
+
+    if t.dtype != torch.float16 or t.dim() != 3 or not t.is_cuda or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{what} must be a CUDA float16 tensor [T][{heads}][{dim}]")
+    row, head, one = t.stride()
+    if (one != 1 and dim > 1) or (head != dim and heads > 1):
+        raise ValueError(f"{what}: heads and components must be contiguous (only the row stride is free)")
+    n = t.shape[0]
+    return n, row if n > 1 else max(row, heads * dim)
+
+
+def _raw_stream(stream):
+    import torch
+
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def kv4_append(k, v, slots, cache, k_scale: float, v_scale: float, k_held=None, v_held=None, stream=None) -> None:
+    """Write keys and values (FP16 [T][kv_heads][head_dim], row stride free) to the cache's slots
+    (int32 [T], page * page_size + offset; negative: skipped).
+
+    k_held and v_held (FP16 [T][kv_heads][head_dim], both or neither) get the values the cache then stands for."""
+    import torch
+
+    pages, heads, dim, page = _cache_dims(cache)
+    n, ks = _rows_f16(k, heads, dim, "k")
+    nv, vs = _rows_f16(v, heads, dim, "v")
+    if n != nv:
+        raise ValueError("k and v have different numbers of tokens")
+    sp = _need(slots, torch.int32, (n,), "slots")
+    hk = None if k_held is None else _need(k_held, torch.float16, (n, heads, dim), "k_held")
+    hv = None if v_held is None else _need(v_held, torch.float16, (n, heads, dim), "v_held")
+    _check(lib.kv4_append(k.data_ptr(), ks, v.data_ptr(), vs, sp, cache.data_ptr(), k_scale, v_scale, hk, hv,
+                          n, pages, heads, dim, page, _raw_stream(stream)), "kv4_append")
+
+
+def kv4_attention(q, cache, table, lens, k_scale: float, v_scale: float, scale: float, rows: int = 1, out=None,
+                  lse=None, acc=None, acc_out=None, stream=None):
+    """Attention of `rows` query rows per sequence (q FP16 [seqs * rows][q_heads][head_dim], row stride free)
+    over the cache's pages (table int32 [seqs][width]) up to lens (int32 [seqs]).
+
+    acc_out (float32 [seqs][kv_heads][width * page_size], may be acc) gets acc plus the weight each position
+    received; acc may be None (zeros).  Returns (out FP16, lse float32 [seqs * rows][q_heads])."""
+    import torch
+
+    pages, heads, dim, page = _cache_dims(cache)
+    if q.dim() != 3:
+        raise ValueError("q must be a CUDA float16 tensor [seqs * rows][q_heads][head_dim]")
+    hq = q.shape[1]
+    n, qs = _rows_f16(q, hq, dim, "q")
+    if table.dim() != 2:
+        raise ValueError("table must be a contiguous CUDA int32 tensor [seqs][width]")
+    seqs, width = table.shape
+    if seqs * rows != n:
+        raise ValueError(f"q has {n} rows, expected {seqs} sequences x {rows}")
+    tp = _need(table, torch.int32, (seqs, width), "table")
+    lp = _need(lens, torch.int32, (seqs,), "lens")
+    if out is None:
+        out = torch.empty((n, hq, dim), dtype=torch.float16, device=q.device)
+    if lse is None:
+        lse = torch.empty((n, hq), dtype=torch.float32, device=q.device)
+    ap = None if acc is None else _need(acc, torch.float32, (seqs, heads, width * page), "acc")
+    op = None if acc_out is None else _need(acc_out, torch.float32, (seqs, heads, width * page), "acc_out")
+    _check(lib.kv4_attention(q.data_ptr(), qs, cache.data_ptr(), tp, lp, k_scale, v_scale, scale,
+                             _need(out, torch.float16, (n, hq, dim), "out"), _need(lse, torch.float32, (n, hq), "lse"),
+                             ap, op, seqs, rows, hq, heads, dim, pages, page, width, _raw_stream(stream)),
+           "kv4_attention")
+    return out, lse
+
+
+def kv4_evict(cache, table, lens, acc, dst_table, budget: int, recent: int, kept=None, new_lens=None, acc_out=None,
+              stream=None):
+    """Keep at most `budget` positions per sequence and kv head (the last `recent` and the largest of
+    acc, float32 [seqs][kv_heads][width * page_size]) and copy them, in order, to the pages of dst_table.
+
+    Returns (new_lens int32 [seqs], kept int32 [seqs][kv_heads][budget], acc_out float32
+    [seqs][kv_heads][dst_width * page_size])."""
+    import torch
+
+    pages, heads, dim, page = _cache_dims(cache)
+    if table.dim() != 2 or dst_table.dim() != 2:
+        raise ValueError("table and dst_table must be contiguous CUDA int32 tensors [seqs][width]")
+    seqs, width = table.shape
+    dwidth = dst_table.shape[1]
+    if new_lens is None:
+        new_lens = torch.empty((seqs,), dtype=torch.int32, device=cache.device)
+    if kept is None:
+        kept = torch.empty((seqs, heads, budget), dtype=torch.int32, device=cache.device)
+    if acc_out is None:
+        acc_out = torch.empty((seqs, heads, dwidth * page), dtype=torch.float32, device=cache.device)
+    i32, f32 = torch.int32, torch.float32
+    _check(lib.kv4_evict(cache.data_ptr(), _need(table, i32, (seqs, width), "table"), _need(lens, i32, (seqs,), "lens"),
+                         _need(acc, f32, (seqs, heads, width * page), "acc"),
+                         _need(dst_table, i32, (seqs, dwidth), "dst_table"),
+                         _need(kept, i32, (seqs, heads, budget), "kept"), _need(new_lens, i32, (seqs,), "new_lens"),
+                         _need(acc_out, f32, (seqs, heads, dwidth * page), "acc_out"), seqs, budget, recent, heads, dim,
+                         pages, page, width, dwidth, _raw_stream(stream)), "kv4_evict")
+    return new_lens, kept, acc_out
+
+
+def token_logprobs(logits, tokens=None, top_n: int = 0, temperature: float = 1.0, logprob=None, rank=None,
+                   entropy=None, top_ids=None, top_logprobs=None, stream=None):
+    """Log probability and rank of `tokens` (int32 [M], or None) under softmax(logits / temperature), the rows'
+    entropy and their top_n alternatives; logits float32 or float16 [M][N], row stride free.
+
+    Returns (logprob float32 [M], rank int32 [M], entropy float32 [M], top_ids int32 [M][top_n],
+    top_logprobs float32 [M][top_n]); logprob and rank are None without tokens."""
+    import torch
+
+    f32, i32 = torch.float32, torch.int32
+    if logits.dim() != 2 or logits.dtype not in (f32, torch.float16) or not logits.is_cuda:
+        raise TypeError("logits must be a 2-D CUDA float32 or float16 tensor [M][N]")
+    M, N = logits.shape
+    stride, one = logits.stride()
+    if N > 1 and one != 1:
+        raise ValueError("logits: the entries of a row must be contiguous (only the row stride is free)")
+    dev = logits.device
+    tp = lp = rp = None
+    if tokens is not None:
+        tp = _need(tokens, i32, (M,), "tokens")
+        if logprob is None:
+            logprob = torch.empty((M,), dtype=f32, device=dev)
+        if rank is None:
+            rank = torch.empty((M,), dtype=i32, device=dev)
+        lp, rp = _need(logprob, f32, (M,), "logprob"), _need(rank, i32, (M,), "rank")
+    else:
+        logprob = rank = None
+    if entropy is None:
+        entropy = torch.empty((M,), dtype=f32, device=dev)
+    if top_ids is None:
+        top_ids = torch.empty((M, top_n), dtype=i32, device=dev)
+    if top_logprobs is None:
+        top_logprobs = torch.empty((M, top_n), dtype=f32, device=dev)
+    _check(lib.token_logprobs(logits.data_ptr(), 0 if logits.dtype == f32 else 1, stride if M > 1 else max(stride, N),
+                              tp, temperature, top_n, lp, rp, _need(entropy, f32, (M,), "entropy"),
+                              _need(top_ids, i32, (M, top_n), "top_ids"),
+                              _need(top_logprobs, f32, (M, top_n), "top_logprobs"), M, N, _raw_stream(stream)),
+           "token_logprobs")
+    return logprob, rank, entropy, top_ids, top_logprobs

@@ -64,6 +64,9 @@ sk_status resolve_encode() {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// The cache operators' scratch memory starts behind a workspace's `bytes`.
+size_t scratch_offset(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
 // The workspace a call on `s` uses on the current device: the stream's own if
 // it has one (then `own` is set), else the device's; false if neither exists.
 struct WsRef {
@@ -299,6 +302,15 @@ unsigned char *workspace_for(cudaStream_t stream) {
     return workspace_ref(stream, &r) ? r.ws : nullptr;
 }
 
+bool scratch_for(cudaStream_t stream, Scratch *s) {
+    WsRef r;
+    if (!workspace_ref(stream, &r)) return false;
+    s->base = r.ws + scratch_offset(r.bytes);
+    s->err = &reinterpret_cast<Ctrl *>(r.ws)->err;
+    s->num_sms = r.num_sms;
+    return true;
+}
+
 bool use_wide_x(const void *x, int M) {
     return M >= 4 && reinterpret_cast<uintptr_t>(x) % 32 == 0;
 }
@@ -334,7 +346,7 @@ sk_status sk_init(size_t workspace_bytes) {
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SK_ERR_CUDA;
     void *p = nullptr;
-    if (cudaMalloc(&p, bytes) != cudaSuccess) return SK_ERR_CUDA;
+    if (cudaMalloc(&p, scratch_offset(bytes) + sk::SCRATCH_BYTES) != cudaSuccess) return SK_ERR_CUDA;
     if (cudaMemset(p, 0, sk::WS_CTRL_BYTES) != cudaSuccess ||
         sk::empty_partials(static_cast<unsigned char *>(p), bytes - sk::WS_PARTIAL_OFFSET, 0) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
@@ -373,7 +385,7 @@ sk_status sk_stream_workspace(void *stream, size_t workspace_bytes) {
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SK_ERR_CUDA;
     const size_t bytes = workspace_bytes < sk::WS_PARTIAL_OFFSET ? sk::WS_PARTIAL_OFFSET : workspace_bytes;
     void *p = nullptr;
-    if (cudaMalloc(&p, bytes) != cudaSuccess) return SK_ERR_CUDA;
+    if (cudaMalloc(&p, scratch_offset(bytes) + sk::SCRATCH_BYTES) != cudaSuccess) return SK_ERR_CUDA;
     if (cudaMemset(p, 0, sk::WS_CTRL_BYTES) != cudaSuccess ||
         sk::empty_partials(static_cast<unsigned char *>(p), bytes - sk::WS_PARTIAL_OFFSET, 0) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
@@ -480,6 +492,6 @@ int sk_set_pdl(int enable) {
 
 void sk_inject_wait_timeout(int enable) { g_inject_stall.store(enable ? 1 : 0); }
 
-int sk_version(void) { return 100; }
+int sk_version(void) { return 200; }
 
 }  // extern "C"

@@ -59,6 +59,18 @@ bool take_weights_written(cudaStream_t stream);
 // own (sk_stream_workspace), else the device's (sk_init); null if neither.
 unsigned char *workspace_for(cudaStream_t stream);
 
+// Scratch memory of the cache operators: SCRATCH_BYTES behind the workspace
+// that calls on `stream` use (sk_stream_workspace, else sk_init), with the
+// workspace's error word.  Its contents mean nothing between calls.  False if
+// there is no workspace.
+constexpr size_t SCRATCH_BYTES = size_t(48) << 20;
+struct Scratch {
+    unsigned char *base = nullptr;
+    unsigned int *err = nullptr;
+    int num_sms = 0;
+};
+bool scratch_for(cudaStream_t stream, Scratch *s);
+
 // Whether the tensor-core variant loads the activations 32 bytes per lane
 // and instruction (kernel.cuh, load_x) instead of 16: for M >= 4 and x
 // 32-byte aligned.  Half the load instructions and line look-ups before the

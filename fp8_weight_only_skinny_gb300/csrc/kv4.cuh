@@ -1,0 +1,59 @@
+// kv4.cuh -- the paged key/value cache held in 4 bits: its record layout and
+// the device helpers its kernels share (kv4_append.cu, kv4_attention.cu,
+// kv4_evict.cu).
+//
+// The cache is u8 [pages][kv_heads][page_size / 16][18 D]: one record of 18 D
+// bytes holds the keys and values of 16 consecutive positions of one head of
+// size D, so that a reader fetches it with a single bulk copy and, a page's
+// records of a head being contiguous, streams whole DRAM pages.  In a record:
+//
+//   [0, 8 D)       key codes    [16 positions][D / 2]
+//   [8 D, 9 D)     key scales   [16 positions][D / 16]
+//   [9 D, 17 D)    value codes  [2][D / 16][8][8]   (half of the positions,
+//                               block of 16 components, position, byte)
+//   [17 D, 18 D)   value scales [D / 16][16 positions]
+//
+// Codes are E2M1, two per byte, the even component in the low nibble; scales
+// are E4M3, one per 16 consecutive components of a position.  Keys are the
+// k x n operand of q . k^T: a row is read along the components.  Values are
+// the operand of p . v, read along the positions: a lane that needs one block
+// of two neighbouring positions finds them in one aligned 16-byte word, and
+// its pairs of scales in one 16-bit word.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace sk {
+
+constexpr int KV4_REC = 16;   // positions per record
+
+// Byte offsets inside a record of a head of size D.
+__host__ __device__ constexpr int kv4_rec_bytes(int D) { return 18 * D; }
+__host__ __device__ constexpr int kv4_key_scales(int D) { return 8 * D; }
+__host__ __device__ constexpr int kv4_val_codes(int D) { return 9 * D; }
+__host__ __device__ constexpr int kv4_val_scales(int D) { return 17 * D; }
+
+// Where position i (< 16) of a record keeps block b (16 components): the
+// eight code bytes and the scale byte, for keys (VALUE = false) and values.
+template <bool VALUE>
+__device__ __forceinline__ int kv4_code_at(int D, int i, int b) {
+    return VALUE ? 9 * D + (i >> 3) * 4 * D + b * 64 + (i & 7) * 8 : i * (D / 2) + b * 8;
+}
+template <bool VALUE>
+__device__ __forceinline__ int kv4_scale_at(int D, int i, int b) {
+    return VALUE ? 17 * D + b * 16 + i : 8 * D + i * (D / 16) + b;
+}
+
+// The record holding position `pos` of a sequence whose pages are `table`.  A
+// page id outside the pool is brought into it: the read stays in the cache's
+// memory, its values are unspecified.
+__device__ __forceinline__ size_t kv4_record(const int32_t *table, int rec, int recs_per_page, int pages, int heads,
+                                             int head) {
+    const int pg = rec / recs_per_page;
+    const int id = min(max(table[pg], 0), pages - 1);
+    return (size_t(id) * heads + head) * recs_per_page + (rec - pg * recs_per_page);
+}
+
+}  // namespace sk

@@ -1,0 +1,447 @@
+// logprobs.cu -- log probability and rank of a given token per row of logits,
+// the row's entropy, and its most likely alternatives.
+//
+// With t_j = z_j / T, m = max t, S = sum exp(t_j - m):
+//     logprob = t_tok - m - ln S,   entropy = ln S - sum exp(t_j - m) (t_j - m) / S,
+//     rank    = 1 + #{j : z_j > z_tok, or z_j = z_tok and j < tok},
+//     top     = the top_n largest z_j, ties to the lower j.
+// One pass over the logits: every thread keeps a running maximum, sum and
+// weighted sum (FP32), the count for the rank, and appends what may still be
+// among the top_n to a list in shared memory.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/skinny.h"
+#include "internal.h"
+#include "launch_util.cuh"
+#include "ptx.cuh"
+
+namespace {
+
+constexpr int LT = 256;                  // threads per CTA
+constexpr int PER = 16;                  // logits per thread and round
+constexpr int ROUND = LT * PER;
+constexpr int MAX_TOP = 64;
+constexpr int SOFT = 512;                // candidates that trigger a cut after a round
+constexpr int LIST = SOFT + ROUND;       // a round can add all of its logits
+constexpr int MAX_CLUSTER = 16;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float LOWEST = -3.402823466e38f;
+
+struct LogprobParams {
+    const void *logits;
+    long long stride;                    // elements between rows
+    const int32_t *tokens;
+    float *logprob, *entropy, *top_logprobs;
+    int32_t *rank, *top_ids;
+    float inv_t, inv_t2;                 // 1 / temperature, and times log2 e
+    int N, top_n;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// max that hands on a NaN instead of dropping it
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+__device__ __forceinline__ unsigned int key_of(float v) {
+    const unsigned int u = __float_as_uint(v + 0.f);      // -0 = +0
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(unsigned int k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+__device__ __forceinline__ unsigned long long cand_of(float v, int i) {
+    return (static_cast<unsigned long long>(key_of(v)) << 32) | static_cast<unsigned int>(~i);
+}
+
+__device__ __forceinline__ unsigned int cluster_rank() {
+    unsigned int r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ unsigned int cluster_size() {
+    unsigned int r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer(const void *p, unsigned int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(sk::smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_peer_f32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned long long ld_peer_u64(uint32_t a) {
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// Running softmax statistics in units of log2: the maximum m of the raw logits
+// and, against it, s = sum 2^d and w = sum 2^d d with d = (z - m) log2 e / T.
+struct Stats {
+    float m, s, w;
+};
+__device__ __forceinline__ Stats join(const Stats &a, const Stats &b, float c) {
+    Stats r;
+    r.m = fmaxf(a.m, b.m);
+    const float da = max_nan((a.m - r.m) * c, -200.f), db = max_nan((b.m - r.m) * c, -200.f);
+    const float fa = ex2(da), fb = ex2(db);
+    r.s = a.s * fa + b.s * fb;
+    r.w = fa * (a.w + da * a.s) + fb * (b.w + db * b.s);
+    return r;
+}
+
+struct Shared {
+    unsigned long long list[LIST];
+    unsigned long long best[MAX_TOP];
+    unsigned long long maxima[LT];
+    Stats stats[LT / 32];
+    Stats mine;
+    unsigned int above[LT / 32];
+    float above_sum;                     // logits that rank before the token (exact below 2^24)
+    int count, kept;
+    unsigned long long floor;            // candidates must exceed this
+};
+
+// The `n` largest of src[0 .. count) in descending order into sh.best, by
+// counting for each how many are larger (the entries differ: each holds its
+// index).  With many candidates, those below the n-th largest of the threads'
+// maxima go first: at least n are at or above it.
+__device__ __forceinline__ void pick_best(Shared &sh, int count, int n) {
+    const int tid = threadIdx.x;
+    __syncthreads();
+    if (count > 2 * LT) {
+        unsigned long long mx = 0;
+        for (int i = tid; i < count; i += LT) mx = sh.list[i] > mx ? sh.list[i] : mx;
+        sh.maxima[tid] = mx;
+        if (tid == 0) sh.kept = 0;
+        __syncthreads();
+        int larger = 0;
+        for (int j = 0; j < LT; ++j) larger += sh.maxima[j] > mx;
+        if (larger == n - 1) sh.floor = mx;
+        __syncthreads();
+        const unsigned long long lim = sh.floor;
+        // in place, a stretch at a time: kept entries never overtake the reads
+        for (int i0 = 0; i0 < count; i0 += LT) {
+            const unsigned long long v = i0 + tid < count ? sh.list[i0 + tid] : 0ull;
+            __syncthreads();
+            if (i0 + tid < count && v >= lim) sh.list[atomicAdd(&sh.kept, 1)] = v;
+            __syncthreads();
+        }
+        count = sh.kept;
+    }
+    for (int i = tid; i < count; i += LT) {
+        const unsigned long long v = sh.list[i];
+        int larger = 0;
+        for (int j = 0; j < count; ++j) larger += sh.list[j] > v;
+        if (larger < n) sh.best[larger] = v;
+    }
+    for (int i = count + tid; i < n; i += LT) sh.best[i] = 0ull;
+    __syncthreads();
+}
+
+template <typename T>
+struct Load;
+template <>
+struct Load<float> {
+    static constexpr int VEC = 4;
+    static __device__ __forceinline__ void get(const float *p, float (&z)[4]) {
+        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
+        z[0] = v.x;
+        z[1] = v.y;
+        z[2] = v.z;
+        z[3] = v.w;
+    }
+    static __device__ __forceinline__ float one(const float *p) { return *p; }
+};
+template <>
+struct Load<__half> {
+    static constexpr int VEC = 8;
+    static __device__ __forceinline__ void get(const __half *p, float (&z)[8]) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = sk::f16x2_to_f32x2(w[i]);
+            z[2 * i] = f.x;
+            z[2 * i + 1] = f.y;
+        }
+    }
+    static __device__ __forceinline__ float one(const __half *p) { return __half2float(*p); }
+};
+
+// One cluster per row (a single CTA where the rows alone fill the GPU); CTA r
+// takes the r-th contiguous part of the row.
+template <typename T>
+__global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ LogprobParams p) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    Shared &sh = *reinterpret_cast<Shared *>(raw);
+    constexpr int VEC = Load<T>::VEC, NV = PER / VEC;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const unsigned int rank = cluster_rank(), C = cluster_size();
+    const int row = blockIdx.x / C;
+    sk::pdl_launch_dependents();
+    sk::pdl_wait_primary();
+    const T *z0 = static_cast<const T *>(p.logits) + (long long)row * p.stride;
+    const int tok = p.tokens ? p.tokens[row] : -1;
+    const bool given = tok >= 0 && tok < p.N;
+    const float ztok = given ? Load<T>::one(z0 + tok) : 0.f;
+    const float c = p.inv_t2;
+    const int n = min(p.top_n, p.N);
+
+    // this CTA's part; `base` = the 16-byte boundary at or below its first logit
+    const int part = (p.N + int(C) - 1) / int(C);
+    const int lo = min(p.N, int(rank) * part), hi = min(p.N, lo + part);
+    const int skew = int((reinterpret_cast<uintptr_t>(z0 + lo) & 15u) / sizeof(T));
+    const int first = lo - skew;
+    if (tid == 0) {
+        sh.count = 0;
+        sh.floor = 0ull;
+    }
+    __syncthreads();
+
+    Stats st = {LOWEST, 0.f, 0.f};
+    unsigned int above = 0;
+    unsigned long long floor = 0ull;         // a candidate's key must exceed this
+    float zfloor = __uint_as_float(0xFFC00000u);   // NaN: everything passes until a floor is known
+    bool have_floor = false;
+    for (int i0 = first; i0 < hi; i0 += ROUND) {
+        float z[PER];
+        int at[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            at[v] = i0 + (v * LT + tid) * VEC;
+            float (&zv)[VEC] = *reinterpret_cast<float (*)[VEC]>(&z[v * VEC]);
+            if (at[v] >= lo && at[v] + VEC <= hi) {
+                Load<T>::get(z0 + at[v], zv);
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j)
+                    zv[j] = at[v] + j >= lo && at[v] + j < hi ? Load<T>::one(z0 + at[v] + j)
+                                                              : -__builtin_huge_valf();
+            }
+        }
+        float mx = z[0];
+#pragma unroll
+        for (int j = 1; j < PER; ++j) mx = fmaxf(mx, z[j]);
+        if (mx > st.m) {
+            const float d = max_nan((st.m - mx) * c, -200.f), f = ex2(d);
+            st.w = f * (st.w + d * st.s);
+            st.s *= f;
+            st.m = mx;
+        }
+        // 2^-200 is zero in FP32, so a logit of minus infinity (or the type's
+        // lowest value) adds nothing, and nothing times -200 to the second sum
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const float d = max_nan((z[j] - st.m) * c, -200.f), e = ex2(d);
+            st.s += e;
+            st.w = fmaf(e, d, st.w);
+        }
+        if (given && !(mx < ztok)) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    const float x = z[v * VEC + j];
+                    const int i = at[v] + j;
+                    above += i >= lo && i < hi && (x > ztok || (x == ztok && i < tok));
+                }
+        }
+        if (n > 0) {
+            if (!have_floor) {
+                // the n-th largest of the threads' own maxima bounds the n-th largest logit from below
+                unsigned long long best = 0ull;
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j)
+                        if (at[v] + j >= lo && at[v] + j < hi) {
+                            const unsigned long long k = cand_of(z[v * VEC + j], at[v] + j);
+                            best = k > best ? k : best;
+                        }
+                sh.maxima[tid] = best;
+                __syncthreads();
+                int larger = 0;
+                for (int j = 0; j < LT; ++j) larger += sh.maxima[j] > best;
+                if (larger == n - 1 && best != 0ull) sh.floor = best - 1ull;
+                __syncthreads();
+                floor = sh.floor;
+                have_floor = true;
+                zfloor = floor ? value_of(static_cast<unsigned int>((floor + 1ull) >> 32)) : __uint_as_float(0xFFC00000u);
+            }
+            if (!(mx < zfloor)) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j)
+                        if (!(z[v * VEC + j] < zfloor) && at[v] + j >= lo && at[v] + j < hi) {
+                            const unsigned long long k = cand_of(z[v * VEC + j], at[v] + j);
+                            if (k > floor) sh.list[atomicAdd(&sh.count, 1)] = k;
+                        }
+            }
+            __syncthreads();
+            const int count = sh.count;
+            __syncthreads();
+            if (count > SOFT) {
+                pick_best(sh, count, n);
+                for (int i = tid; i < n; i += LT) sh.list[i] = sh.best[i];
+                if (tid == 0) sh.count = n;
+                floor = sh.best[n - 1];
+                zfloor = value_of(static_cast<unsigned int>(floor >> 32));
+                __syncthreads();
+            }
+        }
+    }
+
+    // ---- the CTA's statistics, in a fixed order
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        Stats x;
+        x.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+        x.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+        x.w = __shfl_xor_sync(0xffffffffu, st.w, o);
+        st = (lane & o) ? join(x, st, c) : join(st, x, c);
+        above += __shfl_xor_sync(0xffffffffu, above, o);
+    }
+    if (lane == 0) {
+        sh.stats[wid] = st;
+        sh.above[wid] = above;
+    }
+    if (n > 0) {
+        __syncthreads();
+        pick_best(sh, sh.count, n);
+    }
+    __syncthreads();
+    if (tid == 0) {
+        Stats a = sh.stats[0];
+        unsigned int r = sh.above[0];
+        for (int w = 1; w < LT / 32; ++w) {
+            a = join(a, sh.stats[w], c);
+            r += sh.above[w];
+        }
+        sh.mine = a;
+        sh.above_sum = __uint_as_float(r);
+    }
+    // ---- the cluster's, in its first CTA
+    if (C > 1) {
+        cluster_sync();
+        if (rank == 0) {
+            if (tid == 0) {
+                Stats a = sh.mine;
+                unsigned int r = __float_as_uint(sh.above_sum);
+                for (unsigned int k = 1; k < C; ++k) {
+                    const uint32_t q = peer(&sh.mine, k);
+                    const Stats x = {ld_peer_f32(q), ld_peer_f32(q + 4), ld_peer_f32(q + 8)};
+                    a = join(a, x, c);
+                    r += __float_as_uint(ld_peer_f32(peer(&sh.above_sum, k)));
+                }
+                sh.mine = a;
+                sh.above_sum = __uint_as_float(r);
+            }
+            if (n > 0) {
+                for (int i = tid; i < int(C) * n; i += LT) {
+                    const unsigned int k = unsigned(i / n);
+                    sh.list[i] = ld_peer_u64(peer(&sh.best[i - int(k) * n], k));
+                }
+                // empty entries (zero) only where the row itself is shorter
+                __syncthreads();
+                if (tid == 0) sh.kept = 0;
+                __syncthreads();
+                const int all = int(C) * n;
+                for (int i0 = 0; i0 < all; i0 += LT) {
+                    const unsigned long long v = i0 + tid < all ? sh.list[i0 + tid] : 0ull;
+                    __syncthreads();
+                    if (v != 0ull) sh.list[atomicAdd(&sh.kept, 1)] = v;
+                    __syncthreads();
+                }
+                pick_best(sh, sh.kept, n);
+            }
+            __syncthreads();
+        }
+        cluster_sync();
+        if (rank != 0) return;
+    } else {
+        __syncthreads();
+    }
+    const Stats a = sh.mine;
+    // A row of nothing but minus infinity has no distribution: minus infinity
+    // for every log probability, no entropy.
+    const bool none = a.s == 0.f;
+    const float lg = __log2f(a.s);
+    auto logprob = [&](float z) { return none ? -__builtin_huge_valf() : fmaf(z - a.m, p.inv_t, -lg * LN2); };
+    if (tid == 0) {
+        if (p.logprob) p.logprob[row] = given ? logprob(ztok) : 0.f;
+        if (p.rank) p.rank[row] = given ? int32_t(1u + __float_as_uint(sh.above_sum)) : 0;
+        if (p.entropy) p.entropy[row] = none ? 0.f : (lg - a.w / a.s) * LN2;
+    }
+    for (int i = tid; i < p.top_n; i += LT) {
+        const bool in = i < n;
+        const unsigned long long k = in ? sh.best[i] : 0ull;
+        p.top_ids[(long long)row * p.top_n + i] = in ? int32_t(~static_cast<unsigned int>(k)) : -1;
+        p.top_logprobs[(long long)row * p.top_n + i] =
+            in ? logprob(value_of(static_cast<unsigned int>(k >> 32))) : -__builtin_huge_valf();
+    }
+}
+
+template <typename T>
+sk_status launch(const LogprobParams &p, int rows, int cluster, cudaStream_t s) {
+    if (sk::prepare_kernel<logprobs_kernel<T>>(sizeof(Shared), true) != cudaSuccess) return SK_ERR_CUDA;
+    return sk::launch_pdl_cluster(logprobs_kernel<T>, cluster, dim3(unsigned(rows) * unsigned(cluster)), dim3(LT),
+                                  sizeof(Shared), s, p) == cudaSuccess
+               ? SK_OK
+               : SK_ERR_CUDA;
+}
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+}  // namespace
+
+extern "C" sk_status token_logprobs(const void *logits, int f16, long long row_stride, const int32_t *tokens,
+                                    float temperature, int top_n, float *logprob, int32_t *rank, float *entropy,
+                                    int32_t *top_ids, float *top_logprobs, int rows, int N, void *stream) {
+    if (rows < 0 || N < 1 || top_n < 0 || (f16 != 0 && f16 != 1) || row_stride < N) return SK_ERR_INVALID_ARG;
+    if (!(temperature >= 1e-6f && temperature <= 1e6f)) return SK_ERR_INVALID_ARG;
+    if (top_n > MAX_TOP || rows > (1 << 26)) return SK_ERR_UNSUPPORTED_SHAPE;
+    if (rows == 0) return SK_OK;
+    if (!logits || (top_n > 0 && (!top_ids || !top_logprobs))) return SK_ERR_INVALID_ARG;
+    if (!tokens && (logprob || rank)) return SK_ERR_INVALID_ARG;
+    if (!aligned(logits, f16 ? 2 : 4) || !aligned(tokens, 4) || !aligned(logprob, 4) || !aligned(rank, 4) ||
+        !aligned(entropy, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4))
+        return SK_ERR_MISALIGNED;
+    LogprobParams p = {};
+    p.logits = logits;
+    p.stride = row_stride;
+    p.tokens = tokens;
+    p.logprob = logprob;
+    p.rank = rank;
+    p.entropy = entropy;
+    p.top_ids = top_ids;
+    p.top_logprobs = top_logprobs;
+    p.inv_t = 1.f / temperature;
+    p.inv_t2 = LOG2E / temperature;
+    p.N = N;
+    p.top_n = top_n;
+    // CTAs per row: enough to fill the GPU, at most a cluster of 16, each with a round or more to read
+    int cluster = 1;
+    while (cluster < MAX_CLUSTER && rows * cluster < 2 * sk::device_sm_count() && cluster * ROUND < N) cluster *= 2;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return f16 ? launch<__half>(p, rows, cluster, s) : launch<float>(p, rows, cluster, s);
+}

@@ -102,7 +102,8 @@ typedef enum {
 /*
  * Allocate (cudaMalloc) and initialise the workspace of the CURRENT device
  * (a zeroed 4 KiB control block followed by split-K partial-sum slots, all
- * marked empty; every call leaves them empty again).
+ * marked empty; every call leaves them empty again), and behind it 48 MiB of
+ * scratch memory for kv4_attention.
  * workspace_bytes = 0 picks the default, 64 MiB, which covers the largest call
  * below (N = 151936, K = 5120, M = 8 needs about 25 MB).  Calling it again on
  * the same device frees and re-creates the workspace (wait for all work of the
@@ -263,6 +264,133 @@ SK_API sk_status nvfp4_quantize(const void *w, uint8_t *codes, uint8_t *scales, 
 SK_API sk_status lm_head_sample(const void *x, const uint8_t *W_codes, const uint8_t *W_scales,
                                 float W_gscale, float *logits, const float *u, float temperature, int top_k,
                                 float top_p, int32_t *token, int M, int N, int K, void *stream);
+
+/*
+ * Key/value cache in 4 bits: the attention beside the linear layers, for decode
+ * (M = 1) and speculative verify rounds (M = 2..8) over many sequences.  (The
+ * pages keep an FP16 cache -- page "NVFP4 在 Volta 上！", "KV 缓存 → FP16" --
+ * and have no counterpart; formats and rules here are this library's.)
+ *
+ * The cache is one u8 array, 16-byte aligned, [pages][kv_heads][page_size/16][18 D],
+ * D = head_dim in {64, 128, 256}, page_size a multiple of 16, pages * page_size
+ * < 2^31.  Each record of 18 D bytes holds 16 consecutive positions of a head:
+ *     [0, 8 D)     key codes    [16 positions][D/2]
+ *     [8 D, 9 D)   key scales   [16 positions][D/16]
+ *     [9 D, 17 D)  value codes  [2][D/16][8][8]: half of the positions, block of
+ *                  16 components, position, byte
+ *     [17 D, 18 D) value scales [D/16][16 positions]
+ * Codes are E2M1 (low nibble = even component), scales E4M3, one per 16
+ * consecutive components; a component is E2M1(code) * E4M3(scale) * k_scale
+ * (v_scale for values), the two FP32 scales being fixed by the caller for the
+ * cache's life, 1e-20 <= scale <= 1e20 (G of nvfp4_quantize: 1/2688 of the
+ * largest magnitude expected uses the whole range; larger inputs saturate).
+ *   table  const i32 [seqs][table_width]: the pages of each sequence, in order;
+ *   lens   const i32 [seqs]: positions it holds (taken as 0 when negative and as
+ *          table_width * page_size when larger).
+ * Only entries that lens reaches are read.  A page id outside [0, pages) is
+ * brought into that range: memory-safe, results unspecified.  Tables, lengths
+ * and slots stay on the device, so a captured graph serves changing lengths.
+ */
+
+/*
+ * kv4_append: write `tokens` new keys and values.  Block by block (16
+ * components w of one head):  b = max |w|;  sc = E4M3((b / 6) / G);  S = the
+ * value of sc;  code = E2M1(w / (S * G)) (S = 0: signed zeros), with G = k_scale
+ * or v_scale -- the steps and roundings of nvfp4_quantize, bit-for-bit
+ * reproducible.  Non-finite inputs give unspecified codes.
+ *   k, v     const f16 [tokens][kv_heads][D]; k_stride, v_stride: elements from
+ *            one token to the next (a multiple of 8, >= kv_heads * D, so the
+ *            fused qkv projection's output is read in place), 16-byte aligned
+ *   slots    const i32 [tokens]: page * page_size + offset; a negative or too
+ *            large one is skipped (padding).  No slot may occur twice in a call.
+ *   k_held, v_held  f16 [tokens][kv_heads][D], 16-byte aligned, or both NULL:
+ *            the values the cache then stands for, rounded to FP16 (so that a
+ *            prompt's own attention can use the keys later tokens will see)
+ *   tokens = 0: nothing is launched.  Needs no workspace.
+ */
+SK_API sk_status kv4_append(const void *k, long long k_stride, const void *v, long long v_stride,
+                            const int32_t *slots, uint8_t *cache, float k_scale, float v_scale, void *k_held,
+                            void *v_held, int tokens, int pages, int kv_heads, int head_dim, int page_size,
+                            void *stream);
+
+/*
+ * kv4_attention: M = `rows` query rows per sequence (the last M positions of
+ * the sequence, already appended) over its cache.  Query row m of sequence b
+ * sees the positions j < lens[b] - (M - 1 - m); query head x reads kv head
+ * x / (q_heads / kv_heads).
+ *     p = softmax_j(scale * q . k_j),  out = sum_j p_j v_j,  lse = ln sum_j exp(scale * q . k_j)
+ *   q       const f16 [seqs * M][q_heads][D], q_stride elements from row to row
+ *           (a multiple of 8, >= q_heads * D), 16-byte aligned
+ *   scale   > 0 (usually 1 / sqrt(D))
+ *   out     f16 [seqs * M][q_heads][D], 16-byte aligned
+ *   lse     f32 [seqs * M][q_heads], or NULL
+ *   acc_in  const f32 [seqs][kv_heads][table_width * page_size], or NULL (zeros)
+ *   acc_out the same shape, or NULL; may be acc_in.  Per position below lens[b]:
+ *           acc_in + the sum of p over the M rows and the kv head's query heads
+ *           (what kv4_evict chooses by); positions from lens[b] on are not
+ *           written.  Needs lse.
+ *   A row that sees nothing gives zeros and a lse of minus infinity.  Cache
+ *   memory at unseen positions may hold anything; a scale code that is NaN or
+ *   negative (kv4_append writes neither) counts as zero.
+ *   1 <= M <= 8; q_heads a multiple of kv_heads.  Scores, maxima, sums and the
+ *   output are accumulated in FP32 in a fixed order (repeated calls are bitwise
+ *   identical); the weights p enter the second product rounded to FP16.
+ *   seqs = 0: nothing is launched.  Uses the workspace of its stream (sk_init,
+ *   sk_stream_workspace), whose one-stream-at-a-time rule applies; a bounded
+ *   wait that ran out is reported by sk_last_device_error.
+ *   seqs * kv_heads * ceil(M * q_heads / kv_heads / 16) <= 131072.
+ */
+SK_API sk_status kv4_attention(const void *q, long long q_stride, const uint8_t *cache, const int32_t *table,
+                               const int32_t *lens, float k_scale, float v_scale, float scale, void *out, float *lse,
+                               const float *acc_in, float *acc_out, int seqs, int rows, int q_heads, int kv_heads,
+                               int head_dim, int pages, int page_size, int table_width, void *stream);
+
+/*
+ * kv4_evict: keep at most `budget` positions per sequence and kv head, in their
+ * order, copied into other pages.  With n = lens[b]: all n if n <= budget, else
+ * the last `recent` and, of the others, the budget - recent with the largest
+ * acc, ties to the lower position.  Kept position number j goes to slot j of
+ * the sequence's pages in dst_table.  The source pages are only read (they may
+ * be shared with other sequences) and can be freed afterwards.
+ *   acc       const f32 [seqs][kv_heads][table_width * page_size], not NaN
+ *   dst_table const i32 [seqs][dst_width]: pages of the same cache, none of them
+ *             a source page of the call, none twice; budget <= dst_width * page_size
+ *   kept      i32 [seqs][kv_heads][budget]: the kept positions, ascending, then -1
+ *   new_lens  i32 [seqs] = min(n, budget); must not be lens
+ *   acc_out   f32 [seqs][kv_heads][dst_width * page_size], or NULL: acc of the
+ *             kept positions, zeros after them; must not be acc
+ *   budget >= 1, 0 <= recent <= budget.  Slots of dst_table from new_lens on are
+ *   not written.  seqs = 0: nothing is launched.  Needs no workspace.
+ */
+SK_API sk_status kv4_evict(uint8_t *cache, const int32_t *table, const int32_t *lens, const float *acc,
+                           const int32_t *dst_table, int32_t *kept, int32_t *new_lens, float *acc_out, int seqs,
+                           int budget, int recent, int kv_heads, int head_dim, int pages, int page_size,
+                           int table_width, int dst_width, void *stream);
+
+/*
+ * token_logprobs: what is reported beside a token, from rows of logits z (those
+ * of nvfp4_gemm / lm_head_*, or any others), under softmax(z / temperature):
+ *   logprob  f32 [rows]: of tokens[r]; 0 where tokens[r] is outside [0, N)
+ *   rank     i32 [rows]: 1 + the number of logits above tokens[r]'s, an equal one
+ *            of a lower index counting as above; 0 where it is outside [0, N)
+ *   entropy  f32 [rows]: -sum_j p_j ln p_j
+ *   top_ids i32, top_logprobs f32 [rows][top_n]: the top_n largest logits,
+ *            descending, ties to the lower index; past N: -1, minus infinity
+ *   logits   const f32 (f16 = 0) or const f16 (f16 = 1), row_stride elements from
+ *            row to row (>= N), aligned to its type (16-byte aligned rows are no
+ *            faster)
+ *   tokens   const i32 [rows], or NULL (then logprob and rank are NULL too)
+ *   logprob, rank and entropy may each be NULL; 1e-6 <= temperature <= 1e6;
+ *   0 <= top_n <= 64 (larger: SK_ERR_UNSUPPORTED_SHAPE).
+ *   Masked logits may be minus infinity or the type's lowest value: their
+ *   probability is zero.  A row of only minus infinity gives log probabilities
+ *   of minus infinity and entropy 0.  A NaN or plus infinity in a row makes its
+ *   log probabilities and entropy NaN.  Sums are FP32 in a fixed order.
+ *   rows = 0: nothing is launched.  Needs no workspace.
+ */
+SK_API sk_status token_logprobs(const void *logits, int f16, long long row_stride, const int32_t *tokens,
+                                float temperature, int top_n, float *logprob, int32_t *rank, float *entropy,
+                                int32_t *top_ids, float *top_logprobs, int rows, int N, void *stream);
 
 /* Static, human-readable name of a status code. */
 SK_API const char *sk_status_string(sk_status status);

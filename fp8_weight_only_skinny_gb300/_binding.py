@@ -297,11 +297,10 @@ def kv4_cache(pages: int, kv_heads: int, head_dim: int, page_size: int, device="
 
 def _cache_dims(cache):
     """(pages, kv_heads, head_dim, page_size) of a cache."""
-    import torch
-
-    if cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_cuda or not cache.is_contiguous():
+    shape = cache.shape
+    if cache.dtype is not _torch().uint8 or len(shape) != 4 or not cache.is_cuda or not cache.is_contiguous():
         raise TypeError("cache must be a contiguous 4-D CUDA uint8 tensor [pages][kv_heads][page_size/16][18 head_dim]")
-    pages, heads, recs, rec = cache.shape
+    pages, heads, recs, rec = shape
     if rec % 18:
         raise ValueError(f"cache records of {rec} bytes: expected 18 * head_dim")
     return pages, heads, rec // 18, recs * 16
@@ -309,28 +308,43 @@ def _cache_dims(cache):
 
 def _need(t, dtype, shape, what):
     """`t` as a contiguous CUDA tensor of this type and shape, or an error naming it."""
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
     return t.data_ptr()
 
 
 def _rows_f16(t, heads, dim, what):
     """Strided rows [T][heads][dim] of FP16: (rows, elements from row to row)."""
-    import torch
-
-    if t.dtype != torch.float16 or t.dim() != 3 or not t.is_cuda or t.shape[1] != heads or t.shape[2] != dim:
+    shape = t.shape
+    if t.dtype is not _torch().float16 or len(shape) != 3 or shape[1] != heads or shape[2] != dim or not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA float16 tensor [T][{heads}][{dim}]")
     row, head, one = t.stride()
-    if (one != 1 and dim > 1) or (head != dim and heads > 1):
+    if one != 1 or (head != dim and heads > 1):
         raise ValueError(f"{what}: heads and components must be contiguous (only the row stride is free)")
-    n = t.shape[0]
+    n = shape[0]
     return n, row if n > 1 else max(row, heads * dim)
 
 
-def _raw_stream(stream):
-    import torch
+_TORCH = None
 
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+def _torch():
+    global _TORCH
+    if _TORCH is None:
+        import torch
+
+        _TORCH = torch
+    return _TORCH
+
+
+def _raw_stream(stream, device):
+    """The cudaStream_t of `stream`, or of the current stream of the tensors' device.  Asked for as a number:
+    building torch's stream object takes longer (2.9 us of a call's 11 us) than the launch itself."""
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    number = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(device).cuda_stream if number is None else number(device)
 
 
 def kv4_append(k, v, slots, cache, k_scale: float, v_scale: float, k_held=None, v_held=None, stream=None) -> None:
@@ -338,8 +352,7 @@ def kv4_append(k, v, slots, cache, k_scale: float, v_scale: float, k_held=None, 
     (int32 [T], page * page_size + offset; negative: skipped).
 
     k_held and v_held (FP16 [T][kv_heads][head_dim], both or neither) get the values the cache then stands for."""
-    import torch
-
+    torch = _torch()
     pages, heads, dim, page = _cache_dims(cache)
     n, ks = _rows_f16(k, heads, dim, "k")
     nv, vs = _rows_f16(v, heads, dim, "v")
@@ -349,7 +362,7 @@ def kv4_append(k, v, slots, cache, k_scale: float, v_scale: float, k_held=None, 
     hk = None if k_held is None else _need(k_held, torch.float16, (n, heads, dim), "k_held")
     hv = None if v_held is None else _need(v_held, torch.float16, (n, heads, dim), "v_held")
     _check(lib.kv4_append(k.data_ptr(), ks, v.data_ptr(), vs, sp, cache.data_ptr(), k_scale, v_scale, hk, hv,
-                          n, pages, heads, dim, page, _raw_stream(stream)), "kv4_append")
+                          n, pages, heads, dim, page, _raw_stream(stream, cache.get_device())), "kv4_append")
 
 
 def kv4_attention(q, cache, table, lens, k_scale: float, v_scale: float, scale: float, rows: int = 1, out=None,
@@ -359,8 +372,7 @@ def kv4_attention(q, cache, table, lens, k_scale: float, v_scale: float, scale: 
 
     acc_out (float32 [seqs][kv_heads][width * page_size], may be acc) gets acc plus the weight each position
     received; acc may be None (zeros).  Returns (out FP16, lse float32 [seqs * rows][q_heads])."""
-    import torch
-
+    torch = _torch()
     pages, heads, dim, page = _cache_dims(cache)
     if q.dim() != 3:
         raise ValueError("q must be a CUDA float16 tensor [seqs * rows][q_heads][head_dim]")
@@ -381,7 +393,8 @@ def kv4_attention(q, cache, table, lens, k_scale: float, v_scale: float, scale: 
     op = None if acc_out is None else _need(acc_out, torch.float32, (seqs, heads, width * page), "acc_out")
     _check(lib.kv4_attention(q.data_ptr(), qs, cache.data_ptr(), tp, lp, k_scale, v_scale, scale,
                              _need(out, torch.float16, (n, hq, dim), "out"), _need(lse, torch.float32, (n, hq), "lse"),
-                             ap, op, seqs, rows, hq, heads, dim, pages, page, width, _raw_stream(stream)),
+                             ap, op, seqs, rows, hq, heads, dim, pages, page, width,
+                             _raw_stream(stream, cache.get_device())),
            "kv4_attention")
     return out, lse
 
@@ -393,8 +406,7 @@ def kv4_evict(cache, table, lens, acc, dst_table, budget: int, recent: int, kept
 
     Returns (new_lens int32 [seqs], kept int32 [seqs][kv_heads][budget], acc_out float32
     [seqs][kv_heads][dst_width * page_size])."""
-    import torch
-
+    torch = _torch()
     pages, heads, dim, page = _cache_dims(cache)
     if table.dim() != 2 or dst_table.dim() != 2:
         raise ValueError("table and dst_table must be contiguous CUDA int32 tensors [seqs][width]")
@@ -412,7 +424,7 @@ def kv4_evict(cache, table, lens, acc, dst_table, budget: int, recent: int, kept
                          _need(dst_table, i32, (seqs, dwidth), "dst_table"),
                          _need(kept, i32, (seqs, heads, budget), "kept"), _need(new_lens, i32, (seqs,), "new_lens"),
                          _need(acc_out, f32, (seqs, heads, dwidth * page), "acc_out"), seqs, budget, recent, heads, dim,
-                         pages, page, width, dwidth, _raw_stream(stream)), "kv4_evict")
+                         pages, page, width, dwidth, _raw_stream(stream, cache.get_device())), "kv4_evict")
     return new_lens, kept, acc_out
 
 
@@ -423,8 +435,7 @@ def token_logprobs(logits, tokens=None, top_n: int = 0, temperature: float = 1.0
 
     Returns (logprob float32 [M], rank int32 [M], entropy float32 [M], top_ids int32 [M][top_n],
     top_logprobs float32 [M][top_n]); logprob and rank are None without tokens."""
-    import torch
-
+    torch = _torch()
     f32, i32 = torch.float32, torch.int32
     if logits.dim() != 2 or logits.dtype not in (f32, torch.float16) or not logits.is_cuda:
         raise TypeError("logits must be a 2-D CUDA float32 or float16 tensor [M][N]")
@@ -452,6 +463,7 @@ def token_logprobs(logits, tokens=None, top_n: int = 0, temperature: float = 1.0
     _check(lib.token_logprobs(logits.data_ptr(), 0 if logits.dtype == f32 else 1, stride if M > 1 else max(stride, N),
                               tp, temperature, top_n, lp, rp, _need(entropy, f32, (M,), "entropy"),
                               _need(top_ids, i32, (M, top_n), "top_ids"),
-                              _need(top_logprobs, f32, (M, top_n), "top_logprobs"), M, N, _raw_stream(stream)),
+                              _need(top_logprobs, f32, (M, top_n), "top_logprobs"), M, N,
+                              _raw_stream(stream, logits.get_device())),
            "token_logprobs")
     return logprob, rank, entropy, top_ids, top_logprobs

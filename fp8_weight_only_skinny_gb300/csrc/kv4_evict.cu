@@ -82,6 +82,48 @@ __device__ __forceinline__ unsigned int scan2(unsigned int v, unsigned int *tmp,
     return before + x - v;
 }
 
+// Copy m positions (from[x] -> to[x], each the address of a record plus the
+// position in it).  A lane always moves the same piece: eight code bytes of a
+// block, or its scale byte; a warp moves 32 / PIECES positions (D = 256: half
+// of one) at a time, eight in flight.
+template <int D>
+__device__ __forceinline__ void copy_rows(uint8_t *const *from, uint8_t *const *to, int m) {
+    constexpr int NB = D / 16, PIECES = 4 * NB;
+    const int piece = threadIdx.x % PIECES, blk = piece % NB, what = piece / NB;
+    constexpr int STRIDE = ET / PIECES, FLIGHT = 8;
+    auto at = [&](const uint8_t *r) {
+        const int i = int(reinterpret_cast<uintptr_t>(r) & 15u);
+        const int off = what == 0   ? sk::kv4_code_at<false>(D, i, blk)
+                        : what == 1 ? sk::kv4_code_at<true>(D, i, blk)
+                        : what == 2 ? sk::kv4_scale_at<false>(D, i, blk)
+                                    : sk::kv4_scale_at<true>(D, i, blk);
+        return off - i;
+    };
+    for (int x0 = threadIdx.x / PIECES; x0 < m; x0 += STRIDE * FLIGHT) {
+        uint2 v[FLIGHT];
+#pragma unroll
+        for (int f = 0; f < FLIGHT; ++f) {
+            const int x = x0 + f * STRIDE;
+            if (x < m) {
+                const uint8_t *s = from[x];
+                s += at(s);
+                if (what < 2) v[f] = *reinterpret_cast<const uint2 *>(s);
+                else v[f].x = *s;
+            }
+        }
+#pragma unroll
+        for (int f = 0; f < FLIGHT; ++f) {
+            const int x = x0 + f * STRIDE;
+            if (x < m) {
+                uint8_t *d = to[x];
+                d += at(d);
+                if (what < 2) *reinterpret_cast<uint2 *>(d) = v[f];
+                else *d = uint8_t(v[f].x);
+            }
+        }
+    }
+}
+
 // One cluster per (sequence, kv head); CTA r takes the r-th contiguous part of
 // the positions.  Selection is a radix select over the ordered weights, eight
 // bits a pass, on histograms summed over the cluster through distributed
@@ -95,6 +137,7 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
     __shared__ unsigned int tmp[ET / 32];
     __shared__ unsigned int s_prefix, s_need;
     __shared__ int src_pos[CHUNK];
+    __shared__ uint8_t *from_rec[CHUNK], *to_rec[CHUNK];
     sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
     const int tid = threadIdx.x, lane = tid & 31;
@@ -191,7 +234,6 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
     const int32_t *dtable = p.dst + size_t(b) * p.dst_width;
     int32_t *kept = p.kept + size_t(bh) * size_t(p.budget);
     float *acc_out = p.acc_out ? p.acc_out + size_t(bh) * size_t(p.dst_cap) : nullptr;
-    constexpr int NB = D / 16, ITEMS = 4 * NB;
     for (int c0 = lo; c0 < hi; c0 += CHUNK) {
         unsigned int k4[4], v = 0;
 #pragma unroll
@@ -215,26 +257,15 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
         const int m = int(gt_before + min(eq_before, need) - j0);
         __syncthreads();
         for (int x = tid; x < m; x += ET) {
-            kept[j0 + x] = src_pos[x];
-            if (acc_out) acc_out[j0 + x] = acc[src_pos[x]];
+            const int sp = src_pos[x], dp = int(j0) + x;
+            kept[dp] = sp;
+            if (acc_out) acc_out[dp] = acc[sp];
+            from_rec[x] = p.cache + sk::kv4_record(table, sp >> 4, p.recs, p.pages, p.heads, h) * sk::kv4_rec_bytes(D) + (sp & 15);
+            to_rec[x] = p.cache + sk::kv4_record(dtable, dp >> 4, p.recs, p.pages, p.heads, h) * sk::kv4_rec_bytes(D) + (dp & 15);
         }
-        // item: an eight-byte piece of key codes, of value codes, a key scale, a value scale
-#pragma unroll 4
-        for (int x = tid; x < m * ITEMS; x += ET) {
-            const int r = x / ITEMS, u = x - r * ITEMS, blk = u % NB, what = u / NB;
-            const int sp = src_pos[r], dp = int(j0) + r;
-            const uint8_t *from = p.cache + sk::kv4_record(table, sp >> 4, p.recs, p.pages, p.heads, h) * sk::kv4_rec_bytes(D);
-            uint8_t *to = p.cache + sk::kv4_record(dtable, dp >> 4, p.recs, p.pages, p.heads, h) * sk::kv4_rec_bytes(D);
-            if (what < 2) {
-                const int fa = what ? sk::kv4_code_at<true>(D, sp & 15, blk) : sk::kv4_code_at<false>(D, sp & 15, blk);
-                const int ta = what ? sk::kv4_code_at<true>(D, dp & 15, blk) : sk::kv4_code_at<false>(D, dp & 15, blk);
-                *reinterpret_cast<uint2 *>(to + ta) = *reinterpret_cast<const uint2 *>(from + fa);
-            } else {
-                const int fa = what == 3 ? sk::kv4_scale_at<true>(D, sp & 15, blk) : sk::kv4_scale_at<false>(D, sp & 15, blk);
-                const int ta = what == 3 ? sk::kv4_scale_at<true>(D, dp & 15, blk) : sk::kv4_scale_at<false>(D, dp & 15, blk);
-                to[ta] = from[fa];
-            }
-        }
+        __syncthreads();
+        // records start at multiples of 16: the low bits hold the position in one
+        copy_rows<D>(from_rec, to_rec, m);
         __syncthreads();
     }
     for (int j = out_n + int(rank) * ET + tid; j < p.budget; j += int(C) * ET) kept[j] = -1;

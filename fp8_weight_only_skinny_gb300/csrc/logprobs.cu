@@ -24,8 +24,8 @@ constexpr int LT = 256;                  // threads per CTA
 constexpr int PER = 16;                  // logits per thread and round
 constexpr int ROUND = LT * PER;
 constexpr int MAX_TOP = 64;
-constexpr int SOFT = 512;                // candidates that trigger a cut after a round
-constexpr int LIST = SOFT + ROUND;       // a round can add all of its logits
+constexpr int SOFT = 192;                // candidates that trigger a cut after a round
+constexpr int LIST = SOFT + ROUND + 2;   // a round can add all of its logits
 constexpr int MAX_CLUSTER = 16;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float LOWEST = -3.402823466e38f;
@@ -112,15 +112,18 @@ struct Shared {
     unsigned long long list[LIST];
     unsigned long long best[MAX_TOP];
     unsigned long long maxima[LT];
+    unsigned int top32[LT];
     Stats stats[LT / 32];
-    Stats mine;
+    Stats mine, all;
     unsigned int above[LT / 32];
-    float above_sum;                     // logits that rank before the token (exact below 2^24)
+    unsigned int above_mine, above_all;  // logits that rank before the token
+    unsigned int place[MAX_TOP];
     int count, kept;
-    unsigned long long floor;            // candidates must exceed this
+    float zfloor;
+    unsigned long long floor;
 };
 
-// The `n` largest of src[0 .. count) in descending order into sh.best, by
+// The `n` largest of sh.list[0 .. count) in descending order into sh.best, by
 // counting for each how many are larger (the entries differ: each holds its
 // index).  With many candidates, those below the n-th largest of the threads'
 // maxima go first: at least n are at or above it.
@@ -147,97 +150,121 @@ __device__ __forceinline__ void pick_best(Shared &sh, int count, int n) {
         }
         count = sh.kept;
     }
+    if (tid == 0 && (count & 1)) sh.list[count] = 0ull;     // read in pairs
+    __syncthreads();
     for (int i = tid; i < count; i += LT) {
         const unsigned long long v = sh.list[i];
         int larger = 0;
-        for (int j = 0; j < count; ++j) larger += sh.list[j] > v;
+#pragma unroll 4
+        for (int j = 0; j < count; j += 2) {
+            const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(&sh.list[j]);
+            larger += (w.x > v) + (w.y > v);
+        }
         if (larger < n) sh.best[larger] = v;
     }
     for (int i = count + tid; i < n; i += LT) sh.best[i] = 0ull;
     __syncthreads();
 }
 
+// Sixteen logits of a thread as loaded: NV words of 16 bytes, the v-th holding
+// logits i0 + (v LT + tid) VEC and on.
 template <typename T>
-struct Load;
-template <>
-struct Load<float> {
-    static constexpr int VEC = 4;
-    static __device__ __forceinline__ void get(const float *p, float (&z)[4]) {
-        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
-        z[0] = v.x;
-        z[1] = v.y;
-        z[2] = v.z;
-        z[3] = v.w;
-    }
-    static __device__ __forceinline__ float one(const float *p) { return *p; }
-};
-template <>
-struct Load<__half> {
-    static constexpr int VEC = 8;
-    static __device__ __forceinline__ void get(const __half *p, float (&z)[8]) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+struct Raw {
+    static constexpr int VEC = 16 / int(sizeof(T)), NV = PER / VEC;
+    uint4 w[NV];
+
+    // whole: all of the round's logits belong to [lo, hi); the others are read
+    // as minus infinity
+    __device__ __forceinline__ void load(const T *z, int i0, int lo, int hi) {
+        const int tid = threadIdx.x;
+        if (i0 >= lo && i0 + ROUND <= hi) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = sk::f16x2_to_f32x2(w[i]);
-            z[2 * i] = f.x;
-            z[2 * i + 1] = f.y;
+            for (int v = 0; v < NV; ++v) w[v] = __ldcs(reinterpret_cast<const uint4 *>(z + i0 + (v * LT + tid) * VEC));
+            return;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int at = i0 + (v * LT + tid) * VEC;
+            if (at >= lo && at + VEC <= hi) {
+                w[v] = __ldcs(reinterpret_cast<const uint4 *>(z + at));
+            } else {
+                uint32_t x[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if constexpr (sizeof(T) == 4) {
+                        x[q] = at + q >= lo && at + q < hi ? *reinterpret_cast<const uint32_t *>(z + at + q) : 0xFF800000u;
+                    } else {
+                        uint32_t h[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            h[e] = at + 2 * q + e >= lo && at + 2 * q + e < hi
+                                       ? *reinterpret_cast<const uint16_t *>(z + at + 2 * q + e)
+                                       : 0xFC00u;
+                        x[q] = h[0] | (h[1] << 16);
+                    }
+                }
+                w[v] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
         }
     }
-    static __device__ __forceinline__ float one(const __half *p) { return __half2float(*p); }
+    __device__ __forceinline__ void values(float (&z)[PER]) const {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const uint32_t x[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (sizeof(T) == 4) {
+                    z[v * 4 + q] = __uint_as_float(x[q]);
+                } else {
+                    const float2 f = sk::f16x2_to_f32x2(x[q]);
+                    z[v * 8 + 2 * q] = f.x;
+                    z[v * 8 + 2 * q + 1] = f.y;
+                }
+            }
+        }
+    }
 };
 
+__device__ __forceinline__ float one(const float *p) { return *p; }
+__device__ __forceinline__ float one(const __half *p) { return __half2float(*p); }
+
 // One cluster per row (a single CTA where the rows alone fill the GPU); CTA r
-// takes the r-th contiguous part of the row.
+// takes the r-th contiguous part of the row, a round of 4096 logits at a time,
+// the next round's loads in flight while one is summed.
 template <typename T>
 __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ LogprobParams p) {
-    extern __shared__ __align__(16) unsigned char raw[];
-    Shared &sh = *reinterpret_cast<Shared *>(raw);
-    constexpr int VEC = Load<T>::VEC, NV = PER / VEC;
+    extern __shared__ __align__(16) unsigned char raw_smem[];
+    Shared &sh = *reinterpret_cast<Shared *>(raw_smem);
+    constexpr int VEC = Raw<T>::VEC;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const unsigned int rank = cluster_rank(), C = cluster_size();
     const int row = blockIdx.x / C;
     sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
     const T *z0 = static_cast<const T *>(p.logits) + (long long)row * p.stride;
-    const int tok = p.tokens ? p.tokens[row] : -1;
-    const bool given = tok >= 0 && tok < p.N;
-    const float ztok = given ? Load<T>::one(z0 + tok) : 0.f;
-    const float c = p.inv_t2;
-    const int n = min(p.top_n, p.N);
-
-    // this CTA's part; `base` = the 16-byte boundary at or below its first logit
+    // this CTA's part, and the 16-byte boundary at or below its first logit
     const int part = (p.N + int(C) - 1) / int(C);
     const int lo = min(p.N, int(rank) * part), hi = min(p.N, lo + part);
-    const int skew = int((reinterpret_cast<uintptr_t>(z0 + lo) & 15u) / sizeof(T));
-    const int first = lo - skew;
-    if (tid == 0) {
-        sh.count = 0;
-        sh.floor = 0ull;
-    }
-    __syncthreads();
+    const int first = lo - int((reinterpret_cast<uintptr_t>(z0 + lo) & 15u) / sizeof(T));
+    Raw<T> next;
+    next.load(z0, first, lo, hi);
+    const int tok = p.tokens ? p.tokens[row] : -1;
+    const bool given = tok >= 0 && tok < p.N;
+    const float ztok = given ? one(z0 + tok) : 0.f;
+    const float c = p.inv_t2;
+    const int n = min(p.top_n, p.N);
+    if (tid == 0) sh.count = 0;
+    if (tid < MAX_TOP) sh.place[tid] = 0u;
 
     Stats st = {LOWEST, 0.f, 0.f};
     unsigned int above = 0;
-    unsigned long long floor = 0ull;         // a candidate's key must exceed this
-    float zfloor = __uint_as_float(0xFFC00000u);   // NaN: everything passes until a floor is known
-    bool have_floor = false;
+    // a candidate is at least zfloor, and its key exceeds `floor`
+    float zfloor = -__builtin_huge_valf();
+    unsigned long long floor = 0ull;
     for (int i0 = first; i0 < hi; i0 += ROUND) {
         float z[PER];
-        int at[NV];
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            at[v] = i0 + (v * LT + tid) * VEC;
-            float (&zv)[VEC] = *reinterpret_cast<float (*)[VEC]>(&z[v * VEC]);
-            if (at[v] >= lo && at[v] + VEC <= hi) {
-                Load<T>::get(z0 + at[v], zv);
-            } else {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    zv[j] = at[v] + j >= lo && at[v] + j < hi ? Load<T>::one(z0 + at[v] + j)
-                                                              : -__builtin_huge_valf();
-            }
-        }
+        next.values(z);
+        if (i0 + ROUND < hi) next.load(z0, i0 + ROUND, lo, hi);
         float mx = z[0];
 #pragma unroll
         for (int j = 1; j < PER; ++j) mx = fmaxf(mx, z[j]);
@@ -257,51 +284,45 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
         }
         if (given && !(mx < ztok)) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    const float x = z[v * VEC + j];
-                    const int i = at[v] + j;
-                    above += i >= lo && i < hi && (x > ztok || (x == ztok && i < tok));
-                }
+            for (int j = 0; j < PER; ++j) {
+                const int i = i0 + ((j / VEC) * LT + tid) * VEC + j % VEC;
+                above += i >= lo && i < hi && (z[j] > ztok || (z[j] == ztok && i < tok));
+            }
         }
         if (n > 0) {
-            if (!have_floor) {
-                // the n-th largest of the threads' own maxima bounds the n-th largest logit from below
-                unsigned long long best = 0ull;
-#pragma unroll
-                for (int v = 0; v < NV; ++v)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j)
-                        if (at[v] + j >= lo && at[v] + j < hi) {
-                            const unsigned long long k = cand_of(z[v * VEC + j], at[v] + j);
-                            best = k > best ? k : best;
-                        }
-                sh.maxima[tid] = best;
+            if (i0 == first) {
+                // the n-th largest of the threads' maxima bounds the n-th
+                // largest logit from below (the last byte holds the thread, so
+                // that they differ: at most a little lower)
+                const unsigned int mine = (key_of(mx) & ~255u) | unsigned(LT - 1 - tid);
+                sh.top32[tid] = mine;
                 __syncthreads();
                 int larger = 0;
-                for (int j = 0; j < LT; ++j) larger += sh.maxima[j] > best;
-                if (larger == n - 1 && best != 0ull) sh.floor = best - 1ull;
+#pragma unroll 8
+                for (int j = 0; j < LT; j += 4) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(&sh.top32[j]);
+                    larger += (w.x > mine) + (w.y > mine) + (w.z > mine) + (w.w > mine);
+                }
+                if (larger == n - 1) sh.zfloor = value_of(mine & ~255u);
                 __syncthreads();
-                floor = sh.floor;
-                have_floor = true;
-                zfloor = floor ? value_of(static_cast<unsigned int>((floor + 1ull) >> 32)) : __uint_as_float(0xFFC00000u);
+                zfloor = sh.zfloor;
             }
+            bool full = false;
             if (!(mx < zfloor)) {
 #pragma unroll
-                for (int v = 0; v < NV; ++v)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j)
-                        if (!(z[v * VEC + j] < zfloor) && at[v] + j >= lo && at[v] + j < hi) {
-                            const unsigned long long k = cand_of(z[v * VEC + j], at[v] + j);
-                            if (k > floor) sh.list[atomicAdd(&sh.count, 1)] = k;
+                for (int j = 0; j < PER; ++j)
+                    if (!(z[j] < zfloor)) {
+                        const int i = i0 + ((j / VEC) * LT + tid) * VEC + j % VEC;
+                        const unsigned long long k = cand_of(z[j], i);
+                        if (k > floor && i >= lo && i < hi) {
+                            const int at = atomicAdd(&sh.count, 1);
+                            sh.list[at] = k;
+                            full |= at >= SOFT;
                         }
+                    }
             }
-            __syncthreads();
-            const int count = sh.count;
-            __syncthreads();
-            if (count > SOFT) {
-                pick_best(sh, count, n);
+            if (__syncthreads_or(full)) {
+                pick_best(sh, sh.count, n);
                 for (int i = tid; i < n; i += LT) sh.list[i] = sh.best[i];
                 if (tid == 0) sh.count = n;
                 floor = sh.best[n - 1];
@@ -311,7 +332,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
         }
     }
 
-    // ---- the CTA's statistics, in a fixed order
+    // ---- the CTA's statistics and candidates, in a fixed order
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         Stats x;
@@ -325,11 +346,8 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
         sh.stats[wid] = st;
         sh.above[wid] = above;
     }
-    if (n > 0) {
-        __syncthreads();
-        pick_best(sh, sh.count, n);
-    }
     __syncthreads();
+    if (n > 0) pick_best(sh, sh.count, n);
     if (tid == 0) {
         Stats a = sh.stats[0];
         unsigned int r = sh.above[0];
@@ -338,67 +356,79 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
             r += sh.above[w];
         }
         sh.mine = a;
-        sh.above_sum = __uint_as_float(r);
+        sh.above_mine = r;
+        if (C == 1) {
+            sh.all = a;
+            sh.above_all = r;
+        }
     }
-    // ---- the cluster's, in its first CTA
+    // ---- the cluster's: every CTA joins all the statistics, and places its
+    // own candidates among everyone's
     if (C > 1) {
         cluster_sync();
-        if (rank == 0) {
-            if (tid == 0) {
-                Stats a = sh.mine;
-                unsigned int r = __float_as_uint(sh.above_sum);
-                for (unsigned int k = 1; k < C; ++k) {
-                    const uint32_t q = peer(&sh.mine, k);
-                    const Stats x = {ld_peer_f32(q), ld_peer_f32(q + 4), ld_peer_f32(q + 8)};
-                    a = join(a, x, c);
-                    r += __float_as_uint(ld_peer_f32(peer(&sh.above_sum, k)));
-                }
-                sh.mine = a;
-                sh.above_sum = __uint_as_float(r);
+        if (wid == 0) {
+            Stats a = {LOWEST, 0.f, 0.f};
+            unsigned int r = 0u;
+            if (unsigned(lane) < C) {
+                const uint32_t q = peer(&sh.mine, unsigned(lane));
+                a = Stats{ld_peer_f32(q), ld_peer_f32(q + 4), ld_peer_f32(q + 8)};
+                r = __float_as_uint(ld_peer_f32(peer(&sh.above_mine, unsigned(lane))));
             }
-            if (n > 0) {
-                for (int i = tid; i < int(C) * n; i += LT) {
-                    const unsigned int k = unsigned(i / n);
-                    sh.list[i] = ld_peer_u64(peer(&sh.best[i - int(k) * n], k));
-                }
-                // empty entries (zero) only where the row itself is shorter
-                __syncthreads();
-                if (tid == 0) sh.kept = 0;
-                __syncthreads();
-                const int all = int(C) * n;
-                for (int i0 = 0; i0 < all; i0 += LT) {
-                    const unsigned long long v = i0 + tid < all ? sh.list[i0 + tid] : 0ull;
-                    __syncthreads();
-                    if (v != 0ull) sh.list[atomicAdd(&sh.kept, 1)] = v;
-                    __syncthreads();
-                }
-                pick_best(sh, sh.kept, n);
+#pragma unroll
+            for (int o = 1; o < MAX_CLUSTER; o <<= 1) {
+                Stats x;
+                x.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+                x.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+                x.w = __shfl_xor_sync(0xffffffffu, a.w, o);
+                a = (lane & o) ? join(x, a, c) : join(a, x, c);
+                r += __shfl_xor_sync(0xffffffffu, r, o);
             }
-            __syncthreads();
+            if (lane == 0) {
+                sh.all = a;
+                sh.above_all = r;
+            }
         }
-        cluster_sync();
-        if (rank != 0) return;
-    } else {
-        __syncthreads();
+        // entry e of this CTA against the sorted entries of CTA k, both by thread
+        for (int x = tid; x < int(C) * n; x += LT) {
+            const int k = x / n, e = x - k * n;
+            if (unsigned(k) == rank) continue;
+            const unsigned long long v = sh.best[e];
+            const uint32_t theirs = peer(sh.best, unsigned(k));
+            int a = 0, b = n;                    // entries [0, a) are larger, [b, n) are not
+            while (a < b) {
+                const int h = (a + b) >> 1;
+                if (ld_peer_u64(theirs + 8 * h) > v) a = h + 1;
+                else b = h;
+            }
+            if (a) atomicAdd(&sh.place[e], unsigned(a));
+        }
+        cluster_sync();                          // and no CTA leaves while its entries are read
     }
-    const Stats a = sh.mine;
+    __syncthreads();
+    const Stats a = sh.all;
     // A row of nothing but minus infinity has no distribution: minus infinity
     // for every log probability, no entropy.
     const bool none = a.s == 0.f;
     const float lg = __log2f(a.s);
     auto logprob = [&](float z) { return none ? -__builtin_huge_valf() : fmaf(z - a.m, p.inv_t, -lg * LN2); };
-    if (tid == 0) {
+    if (rank == 0 && tid == 0) {
         if (p.logprob) p.logprob[row] = given ? logprob(ztok) : 0.f;
-        if (p.rank) p.rank[row] = given ? int32_t(1u + __float_as_uint(sh.above_sum)) : 0;
+        if (p.rank) p.rank[row] = given ? int32_t(1u + sh.above_all) : 0;
         if (p.entropy) p.entropy[row] = none ? 0.f : (lg - a.w / a.s) * LN2;
     }
-    for (int i = tid; i < p.top_n; i += LT) {
-        const bool in = i < n;
-        const unsigned long long k = in ? sh.best[i] : 0ull;
-        p.top_ids[(long long)row * p.top_n + i] = in ? int32_t(~static_cast<unsigned int>(k)) : -1;
-        p.top_logprobs[(long long)row * p.top_n + i] =
-            in ? logprob(value_of(static_cast<unsigned int>(k >> 32))) : -__builtin_huge_valf();
+    for (int e = tid; e < n; e += LT) {
+        const unsigned long long k = sh.best[e];
+        const int at = e + int(sh.place[e]);
+        if (k != 0ull && at < n) {
+            p.top_ids[(long long)row * p.top_n + at] = int32_t(~static_cast<unsigned int>(k));
+            p.top_logprobs[(long long)row * p.top_n + at] = logprob(value_of(static_cast<unsigned int>(k >> 32)));
+        }
     }
+    if (rank == 0)
+        for (int e = n + tid; e < p.top_n; e += LT) {
+            p.top_ids[(long long)row * p.top_n + e] = -1;
+            p.top_logprobs[(long long)row * p.top_n + e] = -__builtin_huge_valf();
+        }
 }
 
 template <typename T>

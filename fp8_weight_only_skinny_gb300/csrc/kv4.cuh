@@ -46,14 +46,30 @@ __device__ __forceinline__ int kv4_scale_at(int D, int i, int b) {
     return VALUE ? 17 * D + b * 16 + i : 8 * D + i * (D / 16) + b;
 }
 
-// The record holding position `pos` of a sequence whose pages are `table`.  A
-// page id outside the pool is brought into it: the read stays in the cache's
-// memory, its values are unspecified.
-__device__ __forceinline__ size_t kv4_record(const int32_t *table, int rec, int recs_per_page, int pages, int heads,
-                                             int head) {
-    const int pg = rec / recs_per_page;
+// Division by a number fixed at launch, for numerators below 2^31: with
+// 2^s < d <= 2^(s + 1) and mul = ceil(2^(32 + s) / d), the product's excess
+// mul d - 2^(32 + s) < d <= 2^(s + 1) keeps n mul / 2^(32 + s) below the next
+// integer.  mul = 0 stands for d = 1.
+struct Div {
+    uint32_t mul, shift;
+    Div(uint32_t d = 1) : mul(0), shift(0) {
+        if (d < 2) return;
+        while ((1u << (shift + 1)) < d) ++shift;
+        mul = uint32_t(((uint64_t(1) << (32 + shift)) + d - 1) / d);
+    }
+};
+__device__ __forceinline__ int quotient(int n, const Div &d) {
+    return d.mul ? int(__umulhi(uint32_t(n), d.mul) >> d.shift) : n;
+}
+
+// The record (index into the cache) holding records rec of a sequence whose
+// pages are `table`.  A page id outside the pool is brought into it: the read
+// stays in the cache's memory, its values are unspecified.
+__device__ __forceinline__ uint32_t kv4_record(const int32_t *table, int rec, int recs_per_page, const Div &by,
+                                               int pages, int heads, int head) {
+    const int pg = quotient(rec, by);
     const int id = min(max(table[pg], 0), pages - 1);
-    return (size_t(id) * heads + head) * recs_per_page + (rec - pg * recs_per_page);
+    return (uint32_t(id) * heads + head) * recs_per_page + (rec - pg * recs_per_page);
 }
 
 }  // namespace sk

@@ -20,29 +20,40 @@ constexpr int WARPS = 4;
 constexpr int CT = WARPS * 32;
 constexpr int STEP = 32;               // positions per warp step: two records
 constexpr int TILE = WARPS * STEP;     // positions per CTA step, the unit of the work split
-constexpr int ROWS = 16;               // query rows per tile (one m16 operand)
+constexpr int NROW = 8;                // query rows per n8 tile
 constexpr float NEG_INF = -__builtin_huge_valf();
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-// The weights p go to the second product in FP16, scaled by 2^P_SHIFT: at most
-// 2^15, and normal FP16 numbers down to 2^-29 of the row's largest.  Their
-// rounding (2^-12 relative at most, independent from position to position) is
-// of the size of the output's own rounding to FP16; the sum of the weights is
-// taken from the unrounded FP32 values.
-constexpr float P_SHIFT = 15.f;
+// Each row's weights are taken against a reference r, p = 2^(z - r + P_SHIFT):
+// any r gives the same quotient, so r is a maximum the row had earlier and is
+// moved only when a score passes it by more than SLACK (then the sums so far
+// are scaled).  Most steps need neither the row's maximum across lanes nor a
+// rescaling.  The p go to the second product in FP16, at most 2^(P_SHIFT +
+// SLACK) = 2^15 and normal down to 2^-24 of r's.  Their rounding (2^-11
+// relative at most, independent from position to position) is of the size of
+// the output's own rounding to FP16; the sum of the weights is taken from the
+// unrounded FP32 values.
+constexpr float P_SHIFT = 10.f, SLACK = 5.f;
 constexpr uint64_t WAIT_NS = 1000000000ull;
 
-template <int D>
+// NR tiles of eight query rows are taken together: positions (q . k) and
+// components (p . v) are the 16-wide operand, query rows the 8-wide one, so
+// that few rows cost few multiplications and the decoded codes serve 8 NR rows.
+template <int D, int NR>
 struct Cfg {
+    static constexpr int ROWS = NROW * NR;
     static constexpr int REC = sk::kv4_rec_bytes(D);
     static constexpr int STAGE = 2 * REC;
-    static constexpr int STAGES = D == 64 ? 4 : D == 128 ? 3 : 2;
-    static constexpr int KSTEPS = D / 16;
-    static constexpr int QBYTES = KSTEPS * 512;
+    static constexpr int KPAIRS = D / 32;            // pairs of k16 steps
+    static constexpr int QTILE = KPAIRS * 512;       // bytes of eight query rows
+    // accumulators are D / 4 NR registers a thread: CTAs per SM by what is left
+    static constexpr int ACC = D / 4 * NR;
+    static constexpr int CTAS = ACC >= 96 ? 2 : ACC >= 64 ? 3 : 4;
+    static constexpr int STAGES = D == 64 ? 4 : D == 128 ? (CTAS == 4 ? 2 : 3) : 2;
     static constexpr int RING = WARPS * STAGES * STAGE;
-    static constexpr int CTAS = D == 256 ? 2 : 3;
-    static constexpr int OSTRIDE = D + 4;        // floats between rows of a warp's sums at the merge
-    static constexpr size_t SMEM = RING + QBYTES + WARPS * STAGES * 8 + WARPS * ROWS * 8;
-    static_assert(WARPS * ROWS * OSTRIDE * 4 <= RING, "the merge reuses the ring");
+    static constexpr int OSTRIDE = D + 8;            // floats between rows of a warp's sums at the merge
+    static constexpr int MERGE = WARPS * ROWS * OSTRIDE * 4;
+    static constexpr int BODY = RING > MERGE ? RING : MERGE;      // the merge reuses the ring
+    static constexpr size_t SMEM = BODY + NR * QTILE + WARPS * STAGES * 8 + WARPS * ROWS * 8;
 };
 
 struct AttnParams {
@@ -60,6 +71,7 @@ struct AttnParams {
     int pages, heads, recs, width, cap;   // recs: records per page; cap: positions the table can hold
     int B, M, G, RT, ctas;     // G: query heads per kv head; RT: row tiles
     float scale2, vg;          // scale * key scale * log2 e; value scale
+    sk::Div by_recs;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -159,30 +171,28 @@ __device__ __forceinline__ Share share_of(const AttnParams &p, int per_len, long
     return s;
 }
 
-// Query rows [rt * 16, rt * 16 + 16) of (b, h) as A operands of the k16 steps:
-// step s of lane (g = lane / 4, t = lane % 4) takes components c..c+3 of rows g
-// and g + 8, where c = 128 (s / 8) + 32 t + 4 (s % 8) (D = 64: 16 t + 4 s):
-// the same order in which a lane's key bytes decode.  Rows past the last are zero.
+// Query rows [row0, row0 + 8 n) of (b, h) as B operands, two k16 steps in one
+// 16-byte word: word (pair w, tile r) of lane (g = lane / 4, t = lane % 4) holds
+// components c .. c + 7 of row row0 + 8 r + g, c = 128 (w / 4) + 32 t + 8 (w % 4)
+// (D = 64: 16 t + 8 w): the order in which a lane's key bytes decode.  Rows
+// past the last are zero.
 template <int D>
-__device__ __forceinline__ void load_q(const AttnParams &p, int b, int h, int rt, uint32_t qs) {
-    for (int i = threadIdx.x; i < Cfg<D>::KSTEPS * 32; i += blockDim.x) {
-        const int s = i >> 5, l = i & 31, g = l >> 2, t = l & 3;
-        const int c = D == 64 ? 16 * t + 4 * s : 128 * (s >> 3) + 32 * t + 4 * (s & 7);
-        uint2 v[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int r = rt * ROWS + g + 8 * k, m = r / p.G;
-            v[k] = make_uint2(0u, 0u);
-            if (m < p.M)
-                v[k] = *reinterpret_cast<const uint2 *>(p.q + ((long long)b * p.M + m) * p.q_stride +
-                                                         (long long)(h * p.G + r - m * p.G) * D + c);
-        }
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + i * 16), "r"(v[0].x), "r"(v[1].x),
-                     "r"(v[0].y), "r"(v[1].y) : "memory");
+__device__ __forceinline__ void load_q(const AttnParams &p, int b, int h, int row0, int n, uint32_t qs) {
+    constexpr int KPAIRS = D / 32;
+    for (int i = threadIdx.x; i < n * KPAIRS * 32; i += blockDim.x) {
+        const int l = i & 31, w = (i >> 5) % KPAIRS, r = (i >> 5) / KPAIRS, g = l >> 2, t = l & 3;
+        const int c = D == 64 ? 16 * t + 8 * w : 128 * (w >> 2) + 32 * t + 8 * (w & 3);
+        const int row = row0 + 8 * r + g, m = row / p.G;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (m < p.M)
+            v = *reinterpret_cast<const uint4 *>(p.q + ((long long)b * p.M + m) * p.q_stride +
+                                                  (long long)(h * p.G + row - m * p.G) * D + c);
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + i * 16), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                     : "memory");
     }
 }
 
-// Key bytes of one n8 tile's row for this lane, as loaded from a record at
+// Key bytes of one position for this lane, as loaded from a record at
 // `rec` (shared memory), row i = position in the record.
 template <int D>
 struct Keys {
@@ -211,26 +221,95 @@ __device__ __forceinline__ void load_keys(uint32_t rec, int i, int t, Keys<D> &k
     }
 }
 
-// s[j] += q . k over all D components for NT tiles of eight positions: each
-// key byte pair decodes to the B operand, scaled in FP16 first (exact: 2 x 4
-// significant bits, inside the FP16 normal range).
-template <int D, int NT>
-__device__ __forceinline__ void qk(const Keys<D> (&k)[NT], uint32_t qs, int lane, float (&s)[NT][4]) {
+// The same for four tiles straight from the cache, kept as loaded.
+template <int D>
+struct Raw {
+    uint32_t w[4][Keys<D>::PIECES * Keys<D>::WP];
+    uint32_t s[4][Keys<D>::PIECES];
+
+    __device__ __forceinline__ void load(const AttnParams &p, const int32_t *table, int step, int nrec, int h, int g, int t) {
 #pragma unroll
-    for (int w = 0; w < Keys<D>::PIECES * Keys<D>::WP; ++w) {
-        const uint4 a = sk::ld_shared_v4(qs + ((2 * w) * 32 + lane) * 16);
-        const uint4 c = sk::ld_shared_v4(qs + ((2 * w + 1) * 32 + lane) * 16);
+        for (int r = 0; r < 2; ++r) {
+            const uint8_t *rec = p.cache + size_t(sk::kv4_record(table, min(2 * step + r, nrec - 1), p.recs, p.by_recs,
+                                                                 p.pages, p.heads, h)) * sk::kv4_rec_bytes(D);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            uint32_t d[4];
-            sk::e2m1x8_to_f16x2x4(k[j].w[w], d);
-            const uint32_t sc = D == 64 ? k[j].s[0] : (w & 2) ? sk::bcast_hi(k[j].s[w / 4]) : sk::bcast_lo(k[j].s[w / 4]);
+            for (int jj = 0; jj < 2; ++jj) {
+                const int j = 2 * r + jj, i = jj * 8 + g;
+                if constexpr (D == 64) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(rec + i * 32 + t * 8);
+                    w[j][0] = v.x;
+                    w[j][1] = v.y;
+                    s[j][0] = rec[8 * D + i * 4 + t];
+                } else {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) d[x] = sk::hmul2(d[x], sc);
-            sk::mma_16816(s[j], a.x, a.y, a.z, a.w, d[0], d[1]);
-            sk::mma_16816(s[j], c.x, c.y, c.z, c.w, d[2], d[3]);
+                    for (int c = 0; c < Keys<D>::PIECES; ++c) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(rec + i * (D / 2) + c * 64 + t * 16);
+                        w[j][4 * c] = v.x;
+                        w[j][4 * c + 1] = v.y;
+                        w[j][4 * c + 2] = v.z;
+                        w[j][4 * c + 3] = v.w;
+                        s[j][c] = *reinterpret_cast<const uint16_t *>(rec + 8 * D + i * (D / 16) + c * 8 + t * 2);
+                    }
+                }
+            }
         }
     }
+    __device__ __forceinline__ void keys(Keys<D> (&k)[4]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int x = 0; x < Keys<D>::PIECES * Keys<D>::WP; ++x) k[j].w[x] = w[j][x];
+#pragma unroll
+            for (int c = 0; c < Keys<D>::PIECES; ++c)
+                k[j].s[c] = D == 64 ? sk::bcast_lo(scale_pair(s[j][c])) : scale_pair(s[j][c]);
+        }
+    }
+};
+
+// s[x][r] = q . k over all D components for NX records (16 positions each; the
+// lane holds positions g and g + 8 as k[2 x] and k[2 x + 1]) and NR tiles of
+// query rows: each key byte pair decodes to a pair of A elements, scaled in
+// FP16 first (exact: 2 x 4 significant bits, inside the FP16 normal range).
+// s[x][r] holds (g, 2 t), (g, 2 t + 1), (g + 8, 2 t), (g + 8, 2 t + 1) as
+// (position, row).
+template <int D, int NX, int NR>
+__device__ __forceinline__ void qk(const Keys<D> (&k)[2 * NX], uint32_t qs, int lane, float (&s)[NX][NR][4]) {
+#pragma unroll
+    for (int x = 0; x < NX; ++x)
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[x][r][e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+        uint4 q[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) q[r] = sk::ld_shared_v4(qs + ((r * (D / 32) + w) * 32 + lane) * 16);
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+            uint32_t d[2][4];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const Keys<D> &kk = k[2 * x + y];
+                sk::e2m1x8_to_f16x2x4(kk.w[w], d[y]);
+                const uint32_t sc = D == 64 ? kk.s[0] : (w & 2) ? sk::bcast_hi(kk.s[w / 4]) : sk::bcast_lo(kk.s[w / 4]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[y][e] = sk::hmul2(d[y][e], sc);
+            }
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                sk::mma_16816(s[x][r], d[0][0], d[1][0], d[0][1], d[1][1], q[r].x, q[r].y);
+                sk::mma_16816(s[x][r], d[0][2], d[1][2], d[0][3], d[1][3], q[r].z, q[r].w);
+            }
+        }
+    }
+}
+
+// An 8 x 8 tile of f16 pairs, transposed across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
 }
 
 // Codes of two neighbouring positions a, b (eight components each) -> f16x2
@@ -249,15 +328,17 @@ __device__ __forceinline__ void decode_pair(uint32_t a, uint32_t b, uint32_t (&d
     }
 }
 
-// o += p . v over the 16 positions of the record at `rec`; a[4] is the A
-// operand of p.
-template <int D>
-__device__ __forceinline__ void pv(uint32_t rec, const uint32_t (&a)[4], int g, int t, float (&o)[D / 8][4]) {
+// o += v^T . p^T over the 16 positions of the record at `rec`: b[r] is the B
+// operand of the weights of row tile r.  Lane g of a quad column decodes one
+// block (D = 64: half of one) of two neighbouring positions at a time; tile i
+// takes its components 2 i (rows g of the tile) and 2 i + 1 (rows g + 8).
+template <int D, int NR>
+__device__ __forceinline__ void pv(uint32_t rec, const uint32_t (&b)[NR][2], int g, int t, float (&o)[D / 16][NR][4]) {
     constexpr int NB = D == 64 ? 1 : D / 128, PER = D == 64 ? 8 : 16;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
         const int blk = D == 64 ? g >> 1 : g + 8 * nb;
-        uint32_t b[2][PER];
+        uint32_t a[2][PER];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint4 v = sk::ld_shared_v4(rec + 9 * D + j * 4 * D + blk * 64 + t * 16);
@@ -266,18 +347,22 @@ __device__ __forceinline__ void pv(uint32_t rec, const uint32_t (&a)[4], int g, 
             if constexpr (D == 64) {
                 decode_pair((g & 1) ? v.y : v.x, (g & 1) ? v.w : v.z, d);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) b[j][i] = sk::hmul2(d[i], sc);
+                for (int i = 0; i < 8; ++i) a[j][i] = sk::hmul2(d[i], sc);
             } else {
                 decode_pair(v.x, v.z, d);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) b[j][i] = sk::hmul2(d[i], sc);
+                for (int i = 0; i < 8; ++i) a[j][i] = sk::hmul2(d[i], sc);
                 decode_pair(v.y, v.w, d);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) b[j][8 + i] = sk::hmul2(d[i], sc);
+                for (int i = 0; i < 8; ++i) a[j][8 + i] = sk::hmul2(d[i], sc);
             }
         }
 #pragma unroll
-        for (int i = 0; i < PER; ++i) sk::mma_16816(o[nb * PER + i], a[0], a[1], a[2], a[3], b[0][i], b[1][i]);
+        for (int i = 0; i < PER / 2; ++i)
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                sk::mma_16816(o[nb * (PER / 2) + i][r], a[0][2 * i], a[0][2 * i + 1], a[1][2 * i], a[1][2 * i + 1],
+                              b[r][0], b[r][1]);
     }
 }
 
@@ -294,28 +379,29 @@ __device__ __forceinline__ void wait_full(uint32_t bar, uint32_t parity, unsigne
     }
 }
 
-// Few query rows per kv head: each warp streams its own steps of 32 positions
-// (bulk copies into a ring of its own, issued by one lane two or three steps
-// ahead) and keeps 16 query rows' maxima, sums and outputs in registers; the
-// four warps meet only at the end of a segment (sequence, head, row tile).
-template <int D>
-__global__ void __launch_bounds__(CT, Cfg<D>::CTAS) kv4_attention_kernel(const __grid_constant__ AttnParams p) {
-    using C = Cfg<D>;
+// Each warp streams its own steps of 32 positions (bulk copies into a ring of
+// its own, issued by one lane a ring's length ahead) and keeps 8 NR query rows'
+// references, sums and outputs in registers; the four warps meet only at the
+// end of a segment (sequence, head, row tile).
+template <int D, int NR>
+__global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(const __grid_constant__ AttnParams p) {
+    using C = Cfg<D, NR>;
+    constexpr int ROWS = C::ROWS, NX = C::ACC >= 64 || NR > 2 ? 1 : 2;       // records scored together
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long sm_share[WARPS + 4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t base = sk::smem_u32(smem);
-    const uint32_t qs = base + C::RING, bars = qs + C::QBYTES;
+    const uint32_t qs = base + C::BODY, bars = qs + NR * C::QTILE;
     const uint32_t ring = base + warp * C::STAGES * C::STAGE, bar = bars + warp * C::STAGES * 8;
     float *const obuf = reinterpret_cast<float *>(smem);
-    float2 *const mlbuf = reinterpret_cast<float2 *>(smem + C::RING + C::QBYTES + WARPS * C::STAGES * 8);
+    float2 *const mlbuf = reinterpret_cast<float2 *>(smem + C::BODY + NR * C::QTILE + WARPS * C::STAGES * 8);
     if (lane == 0)
         for (int s = 0; s < C::STAGES; ++s) sk::mbar_init(bar + s * 8, 1);
     sk::fence_barrier_init();
     sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
     Share sh = share_of(p, p.heads * p.RT, sm_share);
-    uint32_t it = 0;           // steps this warp has consumed: ring position and parity
+    uint32_t at = 0, parity = 0;   // this warp's ring position
     bool dead = false;
 
     while (sh.t < sh.end && sh.b < p.B) {
@@ -329,137 +415,166 @@ __global__ void __launch_bounds__(CT, Cfg<D>::CTAS) kv4_attention_kernel(const _
         const int h = hr / p.RT, rt = hr - h * p.RT, b = sh.b;
         const int32_t *table = p.table + (long long)b * p.width;
         const int nrec = (len + 15) / 16;
-        load_q<D>(p, b, h, rt, qs);
 
-        // this warp's steps: st = st_lo + warp, + WARPS, ... below st_hi
+        // this warp's steps: st0, st0 + WARPS, ... (n of them)
         const int st_hi = min(t_hi * WARPS, (len + STEP - 1) / STEP);
-        int st = t_lo * WARPS + warp;
-        const int n = st < st_hi ? (st_hi - st + WARPS - 1) / WARPS : 0;
-        auto record = [&](int rec) { return sk::kv4_record(table, min(rec, nrec - 1), p.recs, p.pages, p.heads, h); };
-        auto issue = [&](uint32_t slot, int step, size_t r0, size_t r1) {
-            const uint32_t dst = ring + (slot % C::STAGES) * C::STAGE, fb = bar + (slot % C::STAGES) * 8;
-            const bool two = 2 * step + 1 < nrec;
-            sk::mbar_arrive_expect_tx(fb, two ? 2 * C::REC : C::REC);
-            bulk_load(dst, p.cache + r0 * C::REC, C::REC, fb);
-            if (two) bulk_load(dst + C::REC, p.cache + r1 * C::REC, C::REC, fb);
+        const int st0 = t_lo * WARPS + warp;
+        const int n = st0 < st_hi ? (st_hi - st0 + WARPS - 1) / WARPS : 0;
+        // Record lookups, 16 steps at a time: lane l holds record l % 2 of step
+        // 16 k + l / 2; the next batch is fetched a whole batch early.
+        auto lookup = [&](int k) {
+            const int rec = 2 * (st0 + (16 * k + (lane >> 1)) * WARPS) + (lane & 1);
+            return sk::kv4_record(table, min(rec, nrec - 1), p.recs, p.by_recs, p.pages, p.heads, h);
         };
-        for (int i = 0; i < C::STAGES; ++i)
-            if (i < n && lane == 0) {
-                const int step = st + i * WARPS;
-                issue(it + i, step, record(2 * step), record(2 * step + 1));
+        uint32_t now = 0, soon = 0;
+        // copy step i of this warp into stage `slot`
+        auto issue = [&](int i, uint32_t slot) {
+            if ((i & 15) == 0) {
+                now = i == 0 ? lookup(0) : soon;
+                if (i + 16 < n) soon = lookup((i >> 4) + 1);
             }
-        // the records of the next step to issue, looked up one step ahead
-        size_t r0 = 0, r1 = 0;
-        if (C::STAGES < n) {
-            const int step = st + C::STAGES * WARPS;
-            r0 = record(2 * step);
-            r1 = record(2 * step + 1);
+            const uint32_t r0 = __shfl_sync(0xffffffffu, now, (2 * i) & 31), r1 = __shfl_sync(0xffffffffu, now, (2 * i + 1) & 31);
+            if (lane == 0) {
+                const uint32_t dst = ring + slot * C::STAGE, fb = bar + slot * 8;
+                const bool two = 2 * (st0 + i * WARPS) + 1 < nrec, one_copy = two && r1 == r0 + 1;
+                sk::mbar_arrive_expect_tx(fb, two ? 2 * C::REC : C::REC);
+                bulk_load(dst, p.cache + size_t(r0) * C::REC, one_copy ? 2 * C::REC : C::REC, fb);
+                if (two && !one_copy) bulk_load(dst + C::REC, p.cache + size_t(r1) * C::REC, C::REC, fb);
+            }
+        };
+        for (int i = 0; i < min(n, C::STAGES); ++i) {
+            uint32_t slot = at + i;
+            if (slot >= C::STAGES) slot -= C::STAGES;
+            issue(i, slot);
         }
+        load_q<D>(p, b, h, rt * ROWS, NR, qs);
         __syncthreads();       // the query rows are in shared memory
 
-        float o[D / 8][4], mx[2] = {NEG_INF, NEG_INF}, sum[2] = {0.f, 0.f};
+        float o[D / 16][NR][4];
+        // per row 2 t + e of tile r: the reference, P_SHIFT minus it, the score that passes it by SLACK, the sum
+        float ref[NR][2], off[NR][2], high[NR][2], sum[NR][2];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+        for (int r = 0; r < NR; ++r) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) o[i][x] = 0.f;
-        // rows g and g + 8 of the tile see positions below lim
-        int lim[2];
+            for (int e = 0; e < 2; ++e) {
+                ref[r][e] = high[r][e] = NEG_INF;
+                off[r][e] = sum[r][e] = 0.f;
+            }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) lim[k] = len - (p.M - 1 - min((rt * ROWS + g + 8 * k) / p.G, p.M - 1));
+            for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[x][r][e] = 0.f;
+        }
+        const int all_see = len - (p.M - 1);       // positions below it are seen by every row
 
-        for (int i = 0; i < n; ++i, ++it, st += WARPS) {
-            const uint32_t stage = ring + (it % C::STAGES) * C::STAGE;
-            wait_full(bar + (it % C::STAGES) * 8, (it / C::STAGES) & 1, p.err, dead);
-            float s[4][4];
-            {
-                Keys<D> k[4];
+        for (int i = 0; i < n; ++i) {
+            const uint32_t stage = ring + at * C::STAGE;
+            wait_full(bar + at * 8, parity, p.err, dead);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    load_keys<D>(stage + (j >> 1) * C::REC, (j & 1) * 8 + g, t, k[j]);
+            for (int x0 = 0; x0 < 2; x0 += NX) {
+                float s[NX][NR][4];
+                {
+                    Keys<D> k[2 * NX];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) s[j][x] = 0.f;
+                    for (int j = 0; j < 2 * NX; ++j)
+                        load_keys<D>(stage + (x0 + (j >> 1)) * C::REC, (j & 1) * 8 + g, t, k[j]);
+                    qk<D, NX, NR>(k, qs, lane, s);
                 }
-                qk<D, 4>(k, qs, lane, s);
-            }
-            const int pos = st * STEP;
-            const bool edge = pos + STEP > len - (p.M - 1);
-            if (edge) {
+                const int pos = (st0 + i * WARPS) * STEP + 16 * x0;
+                if (pos + 16 * NX > all_see) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                    for (int r = 0; r < NR; ++r)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (pos + j * 8 + 2 * t + (x & 1) >= lim[x >> 1]) s[j][x] = NEG_INF;
-            }
-            float off[2];
-            bool grown = false;
-            float alpha[2];
+                        for (int e = 0; e < 2; ++e) {
+                            const int row = rt * ROWS + 8 * r + 2 * t + e;
+                            const int lim = len - (p.M - 1 - min(row / p.G, p.M - 1));
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float m = s[0][2 * k];
+                            for (int x = 0; x < NX; ++x)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(s[j][2 * k], s[j][2 * k + 1]));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const float now = fmaxf(mx[k], m * p.scale2);
-                alpha[k] = mx[k] == now ? 1.f : ex2(mx[k] - now);
-                grown |= mx[k] != now;
-                mx[k] = now;
-                off[k] = now == NEG_INF ? 0.f : P_SHIFT - now;
-            }
-            if (__any_sync(0xffffffffu, grown)) {
-#pragma unroll
-                for (int x = 0; x < D / 8; ++x) {
-                    o[x][0] *= alpha[0];
-                    o[x][1] *= alpha[0];
-                    o[x][2] *= alpha[1];
-                    o[x][3] *= alpha[1];
+                                for (int y = 0; y < 2; ++y)
+                                    if (pos + 16 * x + 8 * y + g >= lim) s[x][r][2 * y + e] = NEG_INF;
+                        }
                 }
-                sum[0] *= alpha[0];
-                sum[1] *= alpha[1];
-            }
+                float top[NR][2];
+                bool rise = false;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                for (int r = 0; r < NR; ++r)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    s[j][x] = ex2(fmaf(s[j][x], p.scale2, off[x >> 1]));
-                    sum[x >> 1] += s[j][x];
+                    for (int e = 0; e < 2; ++e) {
+                        top[r][e] = fmaxf(s[0][r][e], s[0][r][2 + e]);
+                        if constexpr (NX == 2) top[r][e] = fmaxf(top[r][e], fmaxf(s[1][r][e], s[1][r][2 + e]));
+                        rise |= top[r][e] > high[r][e];
+                    }
+                if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float m = top[r][e];
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                            const float now_ref = fmaxf(ref[r][e], m * p.scale2);
+                            const float f = ref[r][e] == now_ref ? 1.f : ex2(ref[r][e] - now_ref);
+                            ref[r][e] = now_ref;
+                            off[r][e] = now_ref == NEG_INF ? 0.f : P_SHIFT - now_ref;
+                            high[r][e] = (now_ref + SLACK) / p.scale2;
+                            sum[r][e] *= f;
+#pragma unroll
+                            for (int x = 0; x < D / 16; ++x) {
+                                o[x][r][e] *= f;
+                                o[x][r][2 + e] *= f;
+                            }
+                        }
                 }
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint32_t a[4] = {pack_f16(s[2 * r][0], s[2 * r][1]), pack_f16(s[2 * r][2], s[2 * r][3]),
-                                       pack_f16(s[2 * r + 1][0], s[2 * r + 1][1]),
-                                       pack_f16(s[2 * r + 1][2], s[2 * r + 1][3])};
-                pv<D>(stage + r * C::REC, a, g, t, o);
+                for (int x = 0; x < NX; ++x) {
+                    uint32_t w[NR][2];
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float p0 = ex2(fmaf(s[x][r][2 * y], p.scale2, off[r][0]));
+                            const float p1 = ex2(fmaf(s[x][r][2 * y + 1], p.scale2, off[r][1]));
+                            sum[r][0] += p0;
+                            sum[r][1] += p1;
+                            w[r][y] = transpose8(pack_f16(p0, p1));
+                        }
+                    pv<D, NR>(stage + (x0 + x) * C::REC, w, g, t, o);
+                }
             }
             __syncwarp();      // every lane has read the stage
-            if (i + C::STAGES < n) {
-                if (lane == 0) issue(it + C::STAGES, st + C::STAGES * WARPS, r0, r1);
-                if (i + C::STAGES + 1 < n) {
-                    const int step = st + (C::STAGES + 1) * WARPS;
-                    r0 = record(2 * step);
-                    r1 = record(2 * step + 1);
-                }
+            if (i + C::STAGES < n) issue(i + C::STAGES, at);
+            if (++at == C::STAGES) {
+                at = 0;
+                parity ^= 1;
             }
         }
 
         // ---- the four warps' sums, in warp order
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
-            sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
-            if (t == 0) mlbuf[warp * ROWS + g + 8 * k] = make_float2(mx[k], sum[k]);
-        }
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                sum[r][e] += __shfl_xor_sync(0xffffffffu, sum[r][e], 4);
+                sum[r][e] += __shfl_xor_sync(0xffffffffu, sum[r][e], 8);
+                sum[r][e] += __shfl_xor_sync(0xffffffffu, sum[r][e], 16);
+                if (g == 0) mlbuf[warp * ROWS + 8 * r + 2 * t + e] = make_float2(ref[r][e], sum[r][e]);
+            }
         __syncthreads();       // every warp is done with its ring
         {
             float *dst = obuf + warp * ROWS * C::OSTRIDE;
+            constexpr int PER = D == 64 ? 8 : 16;
 #pragma unroll
-            for (int x = 0; x < D / 8; ++x)
+            for (int x = 0; x < D / 16; ++x)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int nn = 2 * t + (e & 1), row = g + 8 * (e >> 1);
-                    const int d = D == 64 ? 8 * nn + x : 16 * (nn + 8 * (x >> 4)) + (x & 15);
-                    dst[row * C::OSTRIDE + d] = o[x][e];
-                }
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int d = PER * (g + 8 * (x / (PER / 2))) + 2 * (x % (PER / 2));
+                        *reinterpret_cast<float2 *>(dst + (8 * r + 2 * t + e) * C::OSTRIDE + d) =
+                            make_float2(o[x][r][e], o[x][r][2 + e]);
+                    }
         }
         __syncthreads();
         const bool whole = t_lo == 0 && t_hi == nt;
@@ -487,12 +602,12 @@ __global__ void __launch_bounds__(CT, Cfg<D>::CTAS) kv4_attention_kernel(const _
             }
             if (whole) {
                 const int row = rt * ROWS + r, m = row / p.G;
-                const long long at = ((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G;
+                const long long to = ((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G;
                 const float f = l == 0.f ? 0.f : p.vg / l;
                 const __half2 y0 = __floats2half2_rn(v.x * f, v.y * f), y1 = __floats2half2_rn(v.z * f, v.w * f);
                 uint2 y = make_uint2(*reinterpret_cast<const uint32_t *>(&y0), *reinterpret_cast<const uint32_t *>(&y1));
-                *reinterpret_cast<uint2 *>(p.out + at * D + d) = y;
-                if (d == 0 && p.lse) p.lse[at] = l == 0.f ? NEG_INF : (top + __log2f(l) - P_SHIFT) * LN2;
+                *reinterpret_cast<uint2 *>(p.out + to * D + d) = y;
+                if (d == 0 && p.lse) p.lse[to] = l == 0.f ? NEG_INF : (top + __log2f(l) - P_SHIFT) * LN2;
             } else {
                 *reinterpret_cast<float4 *>(p.part_o + (slot * ROWS + r) * D + d) = v;
                 if (d == 0) *reinterpret_cast<float2 *>(p.part_ml + (slot * ROWS + r) * 2) = make_float2(top, l);
@@ -521,7 +636,7 @@ __global__ void __launch_bounds__(CT, Cfg<D>::CTAS) kv4_attention_kernel(const _
 constexpr int JT = 256;
 
 template <int D>
-__global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ AttnParams p, int max_parts) {
+__global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ AttnParams p, int max_parts, int tile_rows) {
     extern __shared__ float wgt[];                 // one weight per partial
     __shared__ float red[JT / 32], red_l[JT / 32];
     __shared__ float part[JT / 32][D];
@@ -529,7 +644,7 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
     sk::pdl_wait_primary();
     const int rows = p.M * p.G, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int bh = blockIdx.x / rows, row = blockIdx.x - bh * rows, b = bh / p.heads, h = bh - b * p.heads;
-    const int rt = row / ROWS, r = row - rt * ROWS, m = row / p.G;
+    const int rt = row / tile_rows, r = row - rt * tile_rows, m = row / p.G;
     const long long at = ((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G;
     const bool empty = length_of(p, b) == 0;
     if (empty) {
@@ -543,7 +658,7 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
     // slot of partial i: the first CTA's second slot, the first slot of the others
     auto slot = [&](int i) { return (size_t(seg.x) + i) * 2 + (i == 0 ? 1 : 0); };
     float top = NEG_INF;
-    for (int i = tid; i < n; i += JT) top = fmaxf(top, p.part_ml[(slot(i) * ROWS + r) * 2]);
+    for (int i = tid; i < n; i += JT) top = fmaxf(top, p.part_ml[(slot(i) * tile_rows + r) * 2]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) red[wid] = top;
@@ -552,7 +667,7 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
     for (int w = 0; w < JT / 32; ++w) top = fmaxf(top, red[w]);
     float l = 0.f;
     for (int i = tid; i < n; i += JT) {
-        const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + (slot(i) * ROWS + r) * 2);
+        const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + (slot(i) * tile_rows + r) * 2);
         const float f = ml.x == NEG_INF ? 0.f : ex2(ml.x - top);
         wgt[i] = f;
         l += ml.y * f;
@@ -570,7 +685,7 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
     for (int x = 0; x < PER; ++x) v[x] = 0.f;
 #pragma unroll 8
     for (int i = wid; i < n; i += JT / 32) {
-        const float *src = p.part_o + (slot(i) * ROWS + r) * D + lane * 2;
+        const float *src = p.part_o + (slot(i) * tile_rows + r) * D + lane * 2;
         const float f = wgt[i];
 #pragma unroll
         for (int x = 0; x < PER; x += 2) {
@@ -593,21 +708,23 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
 
 // acc_out = acc_in + the weights of all query rows, per position and kv head:
 // the scores once more (the keys alone are read), against the rows' final log
-// sums.  Each warp owns its positions, so the sum over rows has one order.
-constexpr int WT_WARPS = 8;
-constexpr int WT_TILES = 8;            // row tiles held in shared memory at a time
+// sums.  A warp owns the 32 positions of a step, whose sum over the rows is
+// taken in one order; the next step's keys are on their way meanwhile.
+constexpr int WT_TILES = 16;           // tiles of eight rows held in shared memory at a time
 
 template <int D>
-__global__ void __launch_bounds__(WT_WARPS * 32) kv4_weights_kernel(const __grid_constant__ AttnParams p, int held) {
-    using C = Cfg<D>;
+__global__ void __launch_bounds__(CT) kv4_weights_kernel(const __grid_constant__ AttnParams p, int tiles) {
+    constexpr int QTILE = D / 32 * 512;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long sm_share[WT_WARPS + 4];
-    __shared__ float lse2[WT_TILES * ROWS];
+    __shared__ long long sm_share[WARPS + 4];
+    __shared__ float lse2[WT_TILES * NROW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t qs = sk::smem_u32(smem);
     sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
     Share sh = share_of(p, p.heads, sm_share);
+    // this lane's position in a step once the sums are spread: record t / 2, half t % 2, position g
+    const int mine = (t >> 1) * 16 + (t & 1) * 8 + g;
     while (sh.t < sh.end && sh.b < p.B) {
         const int len = length_of(p, sh.b), nt = tiles_of(len);
         if (nt == 0) {
@@ -617,79 +734,65 @@ __global__ void __launch_bounds__(WT_WARPS * 32) kv4_weights_kernel(const __grid
         const int h = int(sh.off / nt), t_lo = int(sh.off - (long long)h * nt), b = sh.b;
         const int t_hi = int(min((long long)nt, t_lo + sh.end - sh.t));
         const int32_t *table = p.table + (long long)b * p.width;
-        const int rows = p.M * p.G;
-        for (int rt0 = 0; rt0 < p.RT; rt0 += held) {
-            const int nr = min(held, p.RT - rt0);
+        const int rows = p.M * p.G, nrec = (len + 15) / 16;
+        const size_t acc_at = (size_t(b) * p.heads + h) * size_t(p.cap);
+        const int st_hi = min(t_hi * WARPS, (len + STEP - 1) / STEP);
+        for (int r0 = 0; r0 < tiles; r0 += WT_TILES) {
+            const int nr = min(WT_TILES, tiles - r0);
             __syncthreads();
-            for (int x = 0; x < nr; ++x) load_q<D>(p, b, h, rt0 + x, qs + x * C::QBYTES);
-            for (int x = tid; x < nr * ROWS; x += WT_WARPS * 32) {
-                const int row = rt0 * ROWS + x, m = row / p.G;
+            load_q<D>(p, b, h, r0 * NROW, nr, qs);
+            for (int x = tid; x < nr * NROW; x += CT) {
+                const int row = r0 * NROW + x, m = row / p.G;
                 float v = NEG_INF;
                 if (row < rows) v = p.lse[((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G];
-                lse2[x] = v == NEG_INF ? -NEG_INF : v * LOG2E;     // no weight from rows that see nothing
+                // a row that sees nothing (or does not exist) gives no weight: 2^(z - huge) = 0
+                lse2[x] = v == NEG_INF ? 3e38f : v * LOG2E;
             }
             __syncthreads();
-            const int rec_hi = min(t_hi * (TILE / 16), (len + 15) / 16);
-            for (int rec = t_lo * (TILE / 16) + warp; rec < rec_hi; rec += WT_WARPS) {
-                const uint8_t *src = p.cache + sk::kv4_record(table, rec, p.recs, p.pages, p.heads, h) * C::REC;
-                Keys<D> k[2];
+            const float *old = r0 == 0 ? p.acc_in : p.acc_out;
+            Raw<D> raw;
+            float was = 0.f;
+            int st = t_lo * WARPS + warp;
+            auto fetch = [&](int step) {
+                raw.load(p, table, step, nrec, h, g, t);
+                was = old && step * STEP + mine < len ? old[acc_at + step * STEP + mine] : 0.f;
+            };
+            if (st < st_hi) fetch(st);
+            for (; st < st_hi; st += WARPS) {
+                Keys<D> k[4];
+                raw.keys(k);
+                const float before = was;
+                if (st + WARPS < st_hi) fetch(st + WARPS);
+                const int pos = st * STEP;
+                const bool edge = pos + STEP > len - (p.M - 1);
+                float w[4] = {0.f, 0.f, 0.f, 0.f};     // record x, half y: w[2 x + y], of position g
+                for (int r = 0; r < nr; ++r) {
+                    float s[2][1][4];
+                    qk<D, 2, 1>(k, qs + r * QTILE, lane, s);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int i = j * 8 + g;
-                    if constexpr (D == 64) {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(src + i * 32 + t * 8);
-                        k[j].w[0] = v.x;
-                        k[j].w[1] = v.y;
-                        k[j].s[0] = sk::bcast_lo(scale_pair(src[8 * D + i * 4 + t]));
-                    } else {
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = r * NROW + 2 * t + e;
+                        const float neg = -lse2[row];
+                        int lim = 0x7FFFFFFF;
+                        if (edge) lim = len - (p.M - 1 - min((r0 * NROW + row) / p.G, p.M - 1));
 #pragma unroll
-                        for (int c = 0; c < Keys<D>::PIECES; ++c) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(src + i * (D / 2) + c * 64 + t * 16);
-                            k[j].w[4 * c] = v.x;
-                            k[j].w[4 * c + 1] = v.y;
-                            k[j].w[4 * c + 2] = v.z;
-                            k[j].w[4 * c + 3] = v.w;
-                            k[j].s[c] =
-                                scale_pair(*reinterpret_cast<const uint16_t *>(src + 8 * D + i * (D / 16) + c * 8 + t * 2));
+                        for (int x = 0; x < 4; ++x) {
+                            const float v = ex2(fmaf(s[x >> 1][0][2 * (x & 1) + e], p.scale2, neg));
+                            w[x] += pos + 8 * x + g < lim ? v : 0.f;
                         }
                     }
                 }
-                float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-                for (int x = 0; x < nr; ++x) {
-                    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                    qk<D, 2>(k, qs + x * C::QBYTES, lane, s);
+                // sums over the four t, halving what a lane keeps
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const int row = x * ROWS + g + 8 * y;
-                        const float neg = -lse2[row];
-                        const int lim = len - (p.M - 1 - min((rt0 * ROWS + row) / p.G, p.M - 1));
+                for (int half = 2; half >= 1; half >>= 1) {
+                    const bool up = t & half;
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float z = fmaf(s[j][2 * y + e], p.scale2, neg);
-                                if (rec * 16 + j * 8 + 2 * t + e < lim) w[j][e] += neg == NEG_INF ? 0.f : ex2(z);
-                            }
+                    for (int x = 0; x < half; ++x) {
+                        const float give = up ? w[x] : w[x + half], keep = up ? w[x + half] : w[x];
+                        w[x] = keep + __shfl_xor_sync(0xffffffffu, give, half);
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        w[j][e] += __shfl_xor_sync(0xffffffffu, w[j][e], 4);
-                        w[j][e] += __shfl_xor_sync(0xffffffffu, w[j][e], 8);
-                        w[j][e] += __shfl_xor_sync(0xffffffffu, w[j][e], 16);
-                    }
-                // lane g = 0..3 of each t writes one of the four positions
-                if (g < 4) {
-                    const int pos = rec * 16 + (g >> 1) * 8 + 2 * t + (g & 1);
-                    const float mine = (g >> 1) ? ((g & 1) ? w[1][1] : w[1][0]) : ((g & 1) ? w[0][1] : w[0][0]);
-                    if (pos < len) {
-                        const size_t at = (size_t(b) * p.heads + h) * size_t(p.cap) + pos;
-                        const float *old = rt0 == 0 ? p.acc_in : p.acc_out;
-                        p.acc_out[at] = (old ? old[at] : 0.f) + mine;
-                    }
-                }
+                if (pos + mine < len) p.acc_out[acc_at + pos + mine] = before + w[0];
             }
         }
         sh.t += t_hi - t_lo;
@@ -705,29 +808,47 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int MAX_SEGMENTS = 131072;
 
-template <int D>
-sk_status run(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
-    using C = Cfg<D>;
+template <int D, int NR>
+sk_status attend(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
+    using C = Cfg<D, NR>;
     p.ctas = sms * C::CTAS;
     p.seg = reinterpret_cast<int2 *>(scratch);
     p.part_ml = reinterpret_cast<float *>(scratch + size_t(MAX_SEGMENTS) * sizeof(int2));
-    p.part_o = p.part_ml + size_t(p.ctas) * 2 * ROWS * 2;
-    if (size_t(reinterpret_cast<unsigned char *>(p.part_o + size_t(p.ctas) * 2 * ROWS * D) - scratch) > sk::SCRATCH_BYTES)
+    p.part_o = p.part_ml + size_t(p.ctas) * 2 * C::ROWS * 2;
+    if (size_t(reinterpret_cast<unsigned char *>(p.part_o + size_t(p.ctas) * 2 * C::ROWS * D) - scratch) >
+        sk::SCRATCH_BYTES)
         return SK_ERR_WORKSPACE;
-    if (sk::prepare_kernel<kv4_attention_kernel<D>>(C::SMEM) != cudaSuccess) return SK_ERR_CUDA;
-    if (sk::launch_pdl(kv4_attention_kernel<D>, dim3(p.ctas), dim3(CT), C::SMEM, s, p) != cudaSuccess) return SK_ERR_CUDA;
-    const long long rows = (long long)p.B * p.heads * p.M * p.G;
-    if (sk::launch_pdl(kv4_join_kernel<D>, dim3(unsigned(rows)), dim3(JT), size_t(p.ctas) * 4, s, p, p.ctas) != cudaSuccess)
+    if (sk::prepare_kernel<kv4_attention_kernel<D, NR>>(C::SMEM) != cudaSuccess) return SK_ERR_CUDA;
+    if (sk::launch_pdl(kv4_attention_kernel<D, NR>, dim3(p.ctas), dim3(CT), C::SMEM, s, p) != cudaSuccess)
         return SK_ERR_CUDA;
-    if (p.acc_out) {
-        const int held = p.RT < WT_TILES ? p.RT : WT_TILES;
-        const size_t bytes = size_t(held) * C::QBYTES;
-        p.ctas = sms * 4;
-        if (sk::prepare_kernel<kv4_weights_kernel<D>>(WT_TILES * C::QBYTES) != cudaSuccess) return SK_ERR_CUDA;
-        if (sk::launch_pdl(kv4_weights_kernel<D>, dim3(p.ctas), dim3(WT_WARPS * 32), bytes, s, p, held) != cudaSuccess)
-            return SK_ERR_CUDA;
-    }
-    return SK_OK;
+    const long long rows = (long long)p.B * p.heads * p.M * p.G;
+    return sk::launch_pdl(kv4_join_kernel<D>, dim3(unsigned(rows)), dim3(JT), size_t(p.ctas) * 4, s, p, p.ctas,
+                          int(C::ROWS)) == cudaSuccess
+               ? SK_OK
+               : SK_ERR_CUDA;
+}
+
+template <int D>
+sk_status run(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
+    // Query rows of a kv head in tiles of 8 NR rows, as even as they can be: NR
+    // up to 4 (the outputs are D / 4 NR registers a thread; D = 256: up to 2).
+    constexpr int MOST = D == 256 ? 2 : 4;
+    const int tiles = (p.M * p.G + NROW - 1) / NROW;       // of eight rows
+    p.RT = (tiles + MOST - 1) / MOST;
+    const int nr = (tiles + p.RT - 1) / p.RT;
+    sk_status st;
+    if (nr == 1) st = attend<D, 1>(p, scratch, sms, s);
+    else if (nr == 2) st = attend<D, 2>(p, scratch, sms, s);
+    else if constexpr (MOST == 4) st = nr == 3 ? attend<D, 3>(p, scratch, sms, s) : attend<D, 4>(p, scratch, sms, s);
+    else return SK_ERR_UNSUPPORTED_SHAPE;
+    if (st != SK_OK || !p.acc_out) return st;
+    const int held = tiles < WT_TILES ? tiles : WT_TILES;
+    p.ctas = sms * 4;
+    if (sk::prepare_kernel<kv4_weights_kernel<D>>(WT_TILES * (D / 32) * 512) != cudaSuccess) return SK_ERR_CUDA;
+    return sk::launch_pdl(kv4_weights_kernel<D>, dim3(p.ctas), dim3(CT), size_t(held) * (D / 32) * 512, s, p, tiles) ==
+                   cudaSuccess
+               ? SK_OK
+               : SK_ERR_CUDA;
 }
 
 }  // namespace
@@ -756,8 +877,9 @@ extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint
     p.M = rows;
     p.heads = kv_heads;
     p.G = q_heads / kv_heads;
-    p.RT = (rows * p.G + ROWS - 1) / ROWS;
-    if ((long long)seqs * kv_heads * p.RT > MAX_SEGMENTS || (long long)seqs * q_heads * rows > 0x7FFFFFFFLL)
+    // (sequence, kv head, tile of 16 rows) fit the segment list, whatever tiles the head size gets
+    if ((long long)seqs * kv_heads * ((rows * p.G + 15) / 16) > MAX_SEGMENTS ||
+        (long long)seqs * q_heads * rows > 0x7FFFFFFFLL)
         return SK_ERR_UNSUPPORTED_SHAPE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     sk::Scratch sc;
@@ -774,6 +896,7 @@ extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint
     p.err = sc.err;
     p.pages = pages;
     p.recs = page_size / sk::KV4_REC;
+    p.by_recs = sk::Div(p.recs);
     p.width = table_width;
     p.cap = table_width * page_size;
     p.scale2 = scale * k_scale * LOG2E;

@@ -30,6 +30,7 @@ struct EvictParams {
     int32_t *kept, *new_lens;
     int pages, heads, recs, width, dst_width, cap, dst_cap;
     int budget, recent;
+    sk::Div by_recs;
 };
 
 // Order of the weights as unsigned keys (larger weight, larger key; -0 = +0).
@@ -260,8 +261,8 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
             const int sp = src_pos[x], dp = int(j0) + x;
             kept[dp] = sp;
             if (acc_out) acc_out[dp] = acc[sp];
-            from_rec[x] = p.cache + sk::kv4_record(table, sp >> 4, p.recs, p.pages, p.heads, h) * sk::kv4_rec_bytes(D) + (sp & 15);
-            to_rec[x] = p.cache + sk::kv4_record(dtable, dp >> 4, p.recs, p.pages, p.heads, h) * sk::kv4_rec_bytes(D) + (dp & 15);
+            from_rec[x] = p.cache + size_t(sk::kv4_record(table, sp >> 4, p.recs, p.by_recs, p.pages, p.heads, h)) * sk::kv4_rec_bytes(D) + (sp & 15);
+            to_rec[x] = p.cache + size_t(sk::kv4_record(dtable, dp >> 4, p.recs, p.by_recs, p.pages, p.heads, h)) * sk::kv4_rec_bytes(D) + (dp & 15);
         }
         __syncthreads();
         // records start at multiples of 16: the low bits hold the position in one
@@ -317,6 +318,7 @@ extern "C" sk_status kv4_evict(uint8_t *cache, const int32_t *table, const int32
     p.pages = pages;
     p.heads = kv_heads;
     p.recs = page_size / sk::KV4_REC;
+    p.by_recs = sk::Div(p.recs);
     p.width = table_width;
     p.dst_width = dst_width;
     p.cap = table_width * page_size;

@@ -16,10 +16,12 @@ namespace sk {
 inline bool kv4_scale_ok(float g) { return g >= 1e-20f && g <= 1e20f; }
 
 // Head sizes the cache's kernels are built for, whole records per page, and
-// slot numbers that fit 31 bits.
+// slot numbers and record numbers (over all heads) that fit 31 bits: 2^31
+// records are more than 2 TB.
 inline bool kv4_shape_ok(int pages, int heads, int dim, int page) {
     return (dim == 64 || dim == 128 || dim == 256) && page % 16 == 0 &&
-           (long long)pages * page <= 0x7FFFFFFFLL && heads <= 4096;
+           (long long)pages * page <= 0x7FFFFFFFLL && heads <= 4096 &&
+           (long long)pages * (page / 16) * heads <= 0x7FFFFFFFLL;
 }
 
 // Launch with programmatic dependent launch (while sk_set_pdl allows it) and,

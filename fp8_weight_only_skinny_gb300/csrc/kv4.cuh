@@ -72,4 +72,28 @@ __device__ __forceinline__ uint32_t kv4_record(const int32_t *table, int rec, in
     return (uint32_t(id) * heads + head) * recs_per_page + (rec - pg * recs_per_page);
 }
 
+// Untiled bulk copy into this CTA's shared memory (16-byte aligned, bytes a
+// multiple of 16), completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+constexpr uint64_t KV4_WAIT_NS = 1000000000ull;
+
+// Wait, for a second at most, for the copies of a stage; when that runs out the
+// workspace's error word is set (where there is one) and no later wait is made.
+__device__ __forceinline__ void wait_full(uint32_t bar, uint32_t parity, unsigned int *err, bool &dead) {
+    if (dead) return;
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (globaltimer_ns() - t0 > KV4_WAIT_NS) {
+            dead = true;
+            if (err) atomicOr(err, 1u);
+            return;
+        }
+    }
+}
+
 }  // namespace sk

@@ -33,7 +33,6 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // the output's own rounding to FP16; the sum of the weights is taken from the
 // unrounded FP32 values.
 constexpr float P_SHIFT = 10.f, SLACK = 5.f;
-constexpr uint64_t WAIT_NS = 1000000000ull;
 
 // NR tiles of eight query rows are taken together: positions (q . k) and
 // components (p . v) are the 16-wide operand, query rows the 8-wide one, so
@@ -106,13 +105,6 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
     uint16_t v;
     asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
     return v;
-}
-
-// Untiled bulk copy into this CTA's shared memory (16-byte aligned, bytes a
-// multiple of 16), completing on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
 __device__ __forceinline__ int length_of(const AttnParams &p, int b) { return min(max(p.lens[b], 0), p.cap); }
@@ -221,51 +213,6 @@ __device__ __forceinline__ void load_keys(uint32_t rec, int i, int t, Keys<D> &k
     }
 }
 
-// The same for four tiles straight from the cache, kept as loaded.
-template <int D>
-struct Raw {
-    uint32_t w[4][Keys<D>::PIECES * Keys<D>::WP];
-    uint32_t s[4][Keys<D>::PIECES];
-
-    __device__ __forceinline__ void load(const AttnParams &p, const int32_t *table, int step, int nrec, int h, int g, int t) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint8_t *rec = p.cache + size_t(sk::kv4_record(table, min(2 * step + r, nrec - 1), p.recs, p.by_recs,
-                                                                 p.pages, p.heads, h)) * sk::kv4_rec_bytes(D);
-#pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-                const int j = 2 * r + jj, i = jj * 8 + g;
-                if constexpr (D == 64) {
-                    const uint2 v = *reinterpret_cast<const uint2 *>(rec + i * 32 + t * 8);
-                    w[j][0] = v.x;
-                    w[j][1] = v.y;
-                    s[j][0] = rec[8 * D + i * 4 + t];
-                } else {
-#pragma unroll
-                    for (int c = 0; c < Keys<D>::PIECES; ++c) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(rec + i * (D / 2) + c * 64 + t * 16);
-                        w[j][4 * c] = v.x;
-                        w[j][4 * c + 1] = v.y;
-                        w[j][4 * c + 2] = v.z;
-                        w[j][4 * c + 3] = v.w;
-                        s[j][c] = *reinterpret_cast<const uint16_t *>(rec + 8 * D + i * (D / 16) + c * 8 + t * 2);
-                    }
-                }
-            }
-        }
-    }
-    __device__ __forceinline__ void keys(Keys<D> (&k)[4]) const {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int x = 0; x < Keys<D>::PIECES * Keys<D>::WP; ++x) k[j].w[x] = w[j][x];
-#pragma unroll
-            for (int c = 0; c < Keys<D>::PIECES; ++c)
-                k[j].s[c] = D == 64 ? sk::bcast_lo(scale_pair(s[j][c])) : scale_pair(s[j][c]);
-        }
-    }
-};
-
 // s[x][r] = q . k over all D components for NX records (16 positions each; the
 // lane holds positions g and g + 8 as k[2 x] and k[2 x + 1]) and NR tiles of
 // query rows: each key byte pair decodes to a pair of A elements, scaled in
@@ -366,19 +313,6 @@ __device__ __forceinline__ void pv(uint32_t rec, const uint32_t (&b)[NR][2], int
     }
 }
 
-__device__ __forceinline__ void wait_full(uint32_t bar, uint32_t parity, unsigned int *err, bool &dead) {
-    if (dead) return;
-    if (sk::mbar_try_wait(bar, parity)) return;
-    const uint64_t t0 = sk::globaltimer_ns();
-    while (!sk::mbar_try_wait(bar, parity)) {
-        if (sk::globaltimer_ns() - t0 > WAIT_NS) {
-            dead = true;
-            atomicOr(err, 1u);
-            return;
-        }
-    }
-}
-
 // Each warp streams its own steps of 32 positions (bulk copies into a ring of
 // its own, issued by one lane a ring's length ahead) and keeps 8 NR query rows'
 // references, sums and outputs in registers; the four warps meet only at the
@@ -438,8 +372,8 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                 const uint32_t dst = ring + slot * C::STAGE, fb = bar + slot * 8;
                 const bool two = 2 * (st0 + i * WARPS) + 1 < nrec, one_copy = two && r1 == r0 + 1;
                 sk::mbar_arrive_expect_tx(fb, two ? 2 * C::REC : C::REC);
-                bulk_load(dst, p.cache + size_t(r0) * C::REC, one_copy ? 2 * C::REC : C::REC, fb);
-                if (two && !one_copy) bulk_load(dst + C::REC, p.cache + size_t(r1) * C::REC, C::REC, fb);
+                sk::bulk_load(dst, p.cache + size_t(r0) * C::REC, one_copy ? 2 * C::REC : C::REC, fb);
+                if (two && !one_copy) sk::bulk_load(dst + C::REC, p.cache + size_t(r1) * C::REC, C::REC, fb);
             }
         };
         for (int i = 0; i < min(n, C::STAGES); ++i) {
@@ -469,7 +403,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
 
         for (int i = 0; i < n; ++i) {
             const uint32_t stage = ring + at * C::STAGE;
-            wait_full(bar + at * 8, parity, p.err, dead);
+            sk::wait_full(bar + at * 8, parity, p.err, dead);
 #pragma unroll
             for (int x0 = 0; x0 < 2; x0 += NX) {
                 float s[NX][NR][4];
@@ -711,18 +645,36 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
 // sums.  A warp owns the 32 positions of a step, whose sum over the rows is
 // taken in one order; the next step's keys are on their way meanwhile.
 constexpr int WT_TILES = 16;           // tiles of eight rows held in shared memory at a time
+constexpr int WT_STAGES = 4;
 
 template <int D>
-__global__ void __launch_bounds__(CT) kv4_weights_kernel(const __grid_constant__ AttnParams p, int tiles) {
-    constexpr int QTILE = D / 32 * 512;
+struct WeightsCfg {
+    static constexpr int KEY = 9 * D;                // the keys' part of a record
+    static constexpr int STAGE = 2 * KEY;
+    static constexpr int RING = WARPS * WT_STAGES * STAGE;
+    static constexpr int QTILE = D / 32 * 512;
+    static constexpr int FIXED = RING + WARPS * WT_STAGES * 8;
+    static constexpr int CTAS = D == 256 ? 2 : 4;
+};
+
+template <int D>
+__global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
+    kv4_weights_kernel(const __grid_constant__ AttnParams p, int tiles) {
+    using C = WeightsCfg<D>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long sm_share[WARPS + 4];
     __shared__ float lse2[WT_TILES * NROW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const uint32_t qs = sk::smem_u32(smem);
+    const uint32_t base = sk::smem_u32(smem), qs = base + C::FIXED;
+    const uint32_t ring = base + warp * WT_STAGES * C::STAGE, bar = base + C::RING + warp * WT_STAGES * 8;
+    if (lane == 0)
+        for (int s = 0; s < WT_STAGES; ++s) sk::mbar_init(bar + s * 8, 1);
+    sk::fence_barrier_init();
     sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
     Share sh = share_of(p, p.heads, sm_share);
+    uint32_t it = 0;               // steps this warp has consumed
+    bool dead = false;
     // this lane's position in a step once the sums are spread: record t / 2, half t % 2, position g
     const int mine = (t >> 1) * 16 + (t & 1) * 8 + g;
     while (sh.t < sh.end && sh.b < p.B) {
@@ -737,8 +689,30 @@ __global__ void __launch_bounds__(CT) kv4_weights_kernel(const __grid_constant__
         const int rows = p.M * p.G, nrec = (len + 15) / 16;
         const size_t acc_at = (size_t(b) * p.heads + h) * size_t(p.cap);
         const int st_hi = min(t_hi * WARPS, (len + STEP - 1) / STEP);
+        const int st0 = t_lo * WARPS + warp;
+        const int n = st0 < st_hi ? (st_hi - st0 + WARPS - 1) / WARPS : 0;
         for (int r0 = 0; r0 < tiles; r0 += WT_TILES) {
             const int nr = min(WT_TILES, tiles - r0);
+            auto lookup = [&](int k) {
+                const int rec = 2 * (st0 + (16 * k + (lane >> 1)) * WARPS) + (lane & 1);
+                return sk::kv4_record(table, min(rec, nrec - 1), p.recs, p.by_recs, p.pages, p.heads, h);
+            };
+            uint32_t now = 0, soon = 0;
+            auto issue = [&](int i, uint32_t slot) {
+                if ((i & 15) == 0) {
+                    now = i == 0 ? lookup(0) : soon;
+                    if (i + 16 < n) soon = lookup((i >> 4) + 1);
+                }
+                const uint32_t a = __shfl_sync(0xffffffffu, now, (2 * i) & 31), c = __shfl_sync(0xffffffffu, now, (2 * i + 1) & 31);
+                if (lane == 0) {
+                    const uint32_t dst = ring + slot * C::STAGE, fb = bar + slot * 8;
+                    const bool two = 2 * (st0 + i * WARPS) + 1 < nrec;
+                    sk::mbar_arrive_expect_tx(fb, two ? 2 * C::KEY : C::KEY);
+                    sk::bulk_load(dst, p.cache + size_t(a) * sk::kv4_rec_bytes(D), C::KEY, fb);
+                    if (two) sk::bulk_load(dst + C::KEY, p.cache + size_t(c) * sk::kv4_rec_bytes(D), C::KEY, fb);
+                }
+            };
+            for (int i = 0; i < min(n, WT_STAGES); ++i) issue(i, (it + i) % WT_STAGES);
             __syncthreads();
             load_q<D>(p, b, h, r0 * NROW, nr, qs);
             for (int x = tid; x < nr * NROW; x += CT) {
@@ -750,38 +724,44 @@ __global__ void __launch_bounds__(CT) kv4_weights_kernel(const __grid_constant__
             }
             __syncthreads();
             const float *old = r0 == 0 ? p.acc_in : p.acc_out;
-            Raw<D> raw;
-            float was = 0.f;
-            int st = t_lo * WARPS + warp;
-            auto fetch = [&](int step) {
-                raw.load(p, table, step, nrec, h, g, t);
-                was = old && step * STEP + mine < len ? old[acc_at + step * STEP + mine] : 0.f;
+            auto fetch = [&](int i) {      // what the lane's position of step i had
+                const int pos = (st0 + i * WARPS) * STEP + mine;
+                return old && i < n && pos < len ? old[acc_at + pos] : 0.f;
             };
-            if (st < st_hi) fetch(st);
-            for (; st < st_hi; st += WARPS) {
+            float was = fetch(0), next = fetch(1);
+            for (int i = 0; i < n; ++i, ++it) {
+                const uint32_t slot = it % WT_STAGES, stage = ring + slot * C::STAGE;
+                sk::wait_full(bar + slot * 8, (it / WT_STAGES) & 1, p.err, dead);
                 Keys<D> k[4];
-                raw.keys(k);
-                const float before = was;
-                if (st + WARPS < st_hi) fetch(st + WARPS);
-                const int pos = st * STEP;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) load_keys<D>(stage + (j >> 1) * C::KEY, (j & 1) * 8 + g, t, k[j]);
+                const int pos = (st0 + i * WARPS) * STEP;
                 const bool edge = pos + STEP > len - (p.M - 1);
                 float w[4] = {0.f, 0.f, 0.f, 0.f};     // record x, half y: w[2 x + y], of position g
                 for (int r = 0; r < nr; ++r) {
                     float s[2][1][4];
-                    qk<D, 2, 1>(k, qs + r * QTILE, lane, s);
+                    qk<D, 2, 1>(k, qs + r * C::QTILE, lane, s);
+                    const float2 neg = *reinterpret_cast<const float2 *>(&lse2[r * NROW + 2 * t]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int row = r * NROW + 2 * t + e;
-                        const float neg = -lse2[row];
-                        int lim = 0x7FFFFFFF;
-                        if (edge) lim = len - (p.M - 1 - min((r0 * NROW + row) / p.G, p.M - 1));
+                    for (int x = 0; x < 4; ++x) {
+                        float *v = s[x >> 1][0] + 2 * (x & 1);
+                        v[0] = ex2(fmaf(v[0], p.scale2, -neg.x));
+                        v[1] = ex2(fmaf(v[1], p.scale2, -neg.y));
+                    }
+                    if (edge) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const float v = ex2(fmaf(s[x >> 1][0][2 * (x & 1) + e], p.scale2, neg));
-                            w[x] += pos + 8 * x + g < lim ? v : 0.f;
+                        for (int e = 0; e < 2; ++e) {
+                            const int lim = len - (p.M - 1 - min(((r0 + r) * NROW + 2 * t + e) / p.G, p.M - 1));
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                if (pos + 8 * x + g >= lim) s[x >> 1][0][2 * (x & 1) + e] = 0.f;
                         }
                     }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) w[x] += s[x >> 1][0][2 * (x & 1)] + s[x >> 1][0][2 * (x & 1) + 1];
                 }
+                __syncwarp();
+                if (i + WT_STAGES < n) issue(i + WT_STAGES, slot);
                 // sums over the four t, halving what a lane keeps
 #pragma unroll
                 for (int half = 2; half >= 1; half >>= 1) {
@@ -792,7 +772,9 @@ __global__ void __launch_bounds__(CT) kv4_weights_kernel(const __grid_constant__
                         w[x] = keep + __shfl_xor_sync(0xffffffffu, give, half);
                     }
                 }
-                if (pos + mine < len) p.acc_out[acc_at + pos + mine] = before + w[0];
+                if (pos + mine < len) p.acc_out[acc_at + pos + mine] = was + w[0];
+                was = next;
+                next = fetch(i + 2);
             }
         }
         sh.t += t_hi - t_lo;
@@ -843,10 +825,11 @@ sk_status run(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     else return SK_ERR_UNSUPPORTED_SHAPE;
     if (st != SK_OK || !p.acc_out) return st;
     const int held = tiles < WT_TILES ? tiles : WT_TILES;
-    p.ctas = sms * 4;
-    if (sk::prepare_kernel<kv4_weights_kernel<D>>(WT_TILES * (D / 32) * 512) != cudaSuccess) return SK_ERR_CUDA;
-    return sk::launch_pdl(kv4_weights_kernel<D>, dim3(p.ctas), dim3(CT), size_t(held) * (D / 32) * 512, s, p, tiles) ==
-                   cudaSuccess
+    using W = WeightsCfg<D>;
+    p.ctas = sms * W::CTAS;
+    if (sk::prepare_kernel<kv4_weights_kernel<D>>(W::FIXED + WT_TILES * W::QTILE) != cudaSuccess) return SK_ERR_CUDA;
+    return sk::launch_pdl(kv4_weights_kernel<D>, dim3(p.ctas), dim3(CT), size_t(W::FIXED) + size_t(held) * W::QTILE, s, p,
+                          tiles) == cudaSuccess
                ? SK_OK
                : SK_ERR_CUDA;
 }

@@ -18,9 +18,15 @@
 
 namespace {
 
-constexpr int ET = 512;            // threads per CTA
-constexpr int CHUNK = ET * 4;      // positions scanned at a time
+constexpr int ET = 256;            // threads per CTA
+constexpr int WARPS = ET / 32;
+constexpr int KEYS = 16384;        // keys kept in shared memory (the rest are read again)
+constexpr int BINS = 512;
+constexpr int FEW = 64;            // candidates left at which the selection ends by counting
+constexpr int CHUNK = 1024;        // records numbered at a time
 constexpr int MAX_CLUSTER = 16;
+constexpr int SLOTS = 2;           // source records in flight per warp
+constexpr int SOLO_MAX = 2 * KEYS; // positions up to which a CTA selects alone
 
 struct EvictParams {
     uint8_t *cache;
@@ -28,9 +34,30 @@ struct EvictParams {
     const float *acc;
     float *acc_out;
     int32_t *kept, *new_lens;
+    unsigned int *err;
     int pages, heads, recs, width, dst_width, cap, dst_cap;
     int budget, recent;
     sk::Div by_recs;
+};
+
+struct alignas(16) Shared {
+    unsigned int hist[2][BINS];
+    unsigned long long mine[FEW];      // this CTA's candidates
+    unsigned long long few[FEW];       // the cluster's
+    unsigned int range[2];             // this CTA's smallest and largest key
+    unsigned int counts[3];            // this CTA's: above the digits, equal to the threshold, candidates
+    unsigned int first[MAX_CLUSTER + 1];   // of each CTA's candidates among the cluster's
+    unsigned int gt[MAX_CLUSTER], eq[MAX_CLUSTER];
+    unsigned int scan[ET / 32];
+    unsigned int prefix, need, pop, above;
+    unsigned long long limit;
+    // records with something to keep: number in the sequence, positions kept, first destination slot
+    int list_rec[CHUNK];
+    uint32_t list_base[CHUNK];
+    uint16_t list_mask[CHUNK];
+    uint32_t masks[CHUNK];             // per record: kept for sure (low half), equal to the threshold (high half)
+    unsigned char nth[WARPS][16];      // the position of a record's n-th kept one
+    alignas(8) unsigned long long bar[WARPS][SLOTS];
 };
 
 // Order of the weights as unsigned keys (larger weight, larger key; -0 = +0).
@@ -39,16 +66,6 @@ __device__ __forceinline__ unsigned int key_of(float v) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ unsigned int cluster_rank() {
-    unsigned int r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ unsigned int cluster_size() {
-    unsigned int r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -59,12 +76,18 @@ __device__ __forceinline__ unsigned int ld_peer(const unsigned int *p, unsigned 
                  : "=r"(v) : "r"(a), "r"(rank) : "memory");
     return v;
 }
+__device__ __forceinline__ unsigned long long ld_peer64(const unsigned long long *p, unsigned int rank) {
+    const uint32_t a = sk::smem_u32(p);
+    unsigned long long v;
+    asm volatile("{ .reg .b32 r; mapa.shared::cluster.u32 r, %1, %2; ld.shared::cluster.u64 %0, [r]; }"
+                 : "=l"(v) : "r"(a), "r"(rank) : "memory");
+    return v;
+}
 
-// Exclusive prefix sum over the CTA in thread order of two counts packed as
-// (high << 16 | low), each total below 65536; *total gets the sum.
-__device__ __forceinline__ unsigned int scan2(unsigned int v, unsigned int *tmp, unsigned int *total) {
+// Inclusive prefix sum over the CTA in thread order (tmp: ET / 32 words); the
+// sum of all goes to *total.  Ends with a barrier before tmp is free again.
+__device__ __forceinline__ unsigned int inclusive(unsigned int x, unsigned int *tmp, unsigned int *total) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    unsigned int x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const unsigned int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -72,201 +95,357 @@ __device__ __forceinline__ unsigned int scan2(unsigned int v, unsigned int *tmp,
     }
     if (lane == 31) tmp[wid] = x;
     __syncthreads();
-    unsigned int before = 0, all = 0;
+    unsigned int all = 0;
 #pragma unroll
     for (int w = 0; w < ET / 32; ++w) {
-        if (w < wid) before += tmp[w];
+        if (w < wid) x += tmp[w];
         all += tmp[w];
     }
-    __syncthreads();
     *total = all;
-    return before + x - v;
+    __syncthreads();
+    return x;
 }
 
-// Copy m positions (from[x] -> to[x], each the address of a record plus the
-// position in it).  A lane always moves the same piece: eight code bytes of a
-// block, or its scale byte; a warp moves 32 / PIECES positions (D = 256: half
-// of one) at a time, eight in flight.
-template <int D>
-__device__ __forceinline__ void copy_rows(uint8_t *const *from, uint8_t *const *to, int m) {
-    constexpr int NB = D / 16, PIECES = 4 * NB;
-    const int piece = threadIdx.x % PIECES, blk = piece % NB, what = piece / NB;
-    constexpr int STRIDE = ET / PIECES, FLIGHT = 8;
-    auto at = [&](const uint8_t *r) {
-        const int i = int(reinterpret_cast<uintptr_t>(r) & 15u);
-        const int off = what == 0   ? sk::kv4_code_at<false>(D, i, blk)
-                        : what == 1 ? sk::kv4_code_at<true>(D, i, blk)
-                        : what == 2 ? sk::kv4_scale_at<false>(D, i, blk)
-                                    : sk::kv4_scale_at<true>(D, i, blk);
-        return off - i;
-    };
-    for (int x0 = threadIdx.x / PIECES; x0 < m; x0 += STRIDE * FLIGHT) {
-        uint2 v[FLIGHT];
-#pragma unroll
-        for (int f = 0; f < FLIGHT; ++f) {
-            const int x = x0 + f * STRIDE;
-            if (x < m) {
-                const uint8_t *s = from[x];
-                s += at(s);
-                if (what < 2) v[f] = *reinterpret_cast<const uint2 *>(s);
-                else v[f].x = *s;
-            }
-        }
-#pragma unroll
-        for (int f = 0; f < FLIGHT; ++f) {
-            const int x = x0 + f * STRIDE;
-            if (x < m) {
-                uint8_t *d = to[x];
-                d += at(d);
-                if (what < 2) *reinterpret_cast<uint2 *>(d) = v[f];
-                else *d = uint8_t(v[f].x);
-            }
-        }
-    }
+// A position as a candidate: larger weight first, then the lower position.
+__device__ __forceinline__ unsigned long long cand_of(unsigned int key, int pos) {
+    return (static_cast<unsigned long long>(key) << 32) | static_cast<unsigned int>(~pos);
 }
 
-// One cluster per (sequence, kv head); CTA r takes the r-th contiguous part of
-// the positions.  Selection is a radix select over the ordered weights, eight
-// bits a pass, on histograms summed over the cluster through distributed
-// shared memory; the kept positions of a chunk are then numbered by a scan and
-// their codes and scales copied.
-template <int D>
-__global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ unsigned int hist[2][256];
-    __shared__ unsigned int tot[256];
-    __shared__ unsigned int counts[2];           // this CTA's keys above / equal to the threshold
-    __shared__ unsigned int tmp[ET / 32];
-    __shared__ unsigned int s_prefix, s_need;
-    __shared__ int src_pos[CHUNK];
-    __shared__ uint8_t *from_rec[CHUNK], *to_rec[CHUNK];
+// C CTAs per (sequence, kv head); CTA r copies what is kept of the r-th
+// contiguous part of the records.  Up to a length every CTA selects over all
+// positions by itself (SOLO), which costs less than talking to the others;
+// beyond it the CTAs are a cluster, each selecting over its own part.
+//
+// The selection is a radix select, nine bits a pass from the highest bit in
+// which the weights differ, on histograms (summed over the cluster through
+// distributed shared memory).  As soon as the digit that holds the threshold
+// has few positions left, every CTA gathers them all and counts each one's
+// rank.  The copy streams the records that hold a kept position through shared
+// memory, a ring per warp: a position's value codes are eight-byte pieces and
+// its value scales single bytes, each in a 32-byte sector of its own, so
+// fetching only what is kept moves as many sectors (measured on 16 sequences
+// of up to 16411 positions, 2 heads of 256, 4096 kept: 47 us).
+template <int D, bool SOLO>
+__global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ EvictParams p, int ctas) {
+    constexpr int REC = sk::kv4_rec_bytes(D), NB = D / 16;
+    extern __shared__ __align__(128) unsigned char smem[];      // keys, later the records' ring
+    __shared__ Shared sh;
+    unsigned int *const keys = reinterpret_cast<unsigned int *>(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (lane == 0)
+        for (int s = 0; s < SLOTS; ++s) sk::mbar_init(sk::smem_u32(&sh.bar[warp][s]), 1);
+    sk::fence_barrier_init();
     sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
-    const int tid = threadIdx.x, lane = tid & 31;
-    const unsigned int rank = cluster_rank(), C = cluster_size();
+    const unsigned int C = unsigned(ctas), rank = blockIdx.x % C;      // in a cluster, the CTA's rank
     const int bh = blockIdx.x / C, b = bh / p.heads, h = bh - b * p.heads;
     const int n = min(max(p.lens[b], 0), p.cap);
     const int out_n = min(n, p.budget);
     const float *acc = p.acc + size_t(bh) * size_t(p.cap);
-    const bool all = n <= p.budget;
+    const bool all = n <= p.budget, none_old = !all && p.budget == p.recent, select = !all && !none_old;
     const int old = all ? n : n - p.recent;      // positions the selection decides on
-    const int part = (n + int(C) - 1) / int(C);
-    const int lo = min(n, int(rank) * part), hi = min(n, lo + part);
-    const int lo_old = min(lo, old), hi_old = min(hi, old);
+    const int nrec = (n + 15) / 16, part = (nrec + int(C) - 1) / int(C);
+    const int rec_lo = min(nrec, int(rank) * part), rec_hi = min(nrec, rec_lo + part);
+    const int lo = min(n, rec_lo * 16), hi = min(n, rec_hi * 16);
+    // the positions this CTA's selection reads
+    const int s_lo = SOLO ? 0 : lo, n_old = SOLO ? old : max(0, min(hi, old) - lo);
+    int cached = KEYS;
+    auto key_at = [&](int i) { return i < cached ? keys[i] : key_of(acc[s_lo + i]); };  // i counts from s_lo
 
-    // ---- threshold: the (budget - recent)-th largest key of the old positions
-    unsigned int prefix = 0, mask = 0, need = all ? 0u : unsigned(p.budget - p.recent);
-    if (!all && need > 0) {
-        for (int pass = 0; pass < 4; ++pass) {
-            const int shift = 24 - 8 * pass;
-            unsigned int *hh = hist[pass & 1];
-            if (tid < 256) hh[tid] = 0u;
-            __syncthreads();
-            for (int i = lo_old + tid; i < hi_old; i += ET) {
-                const unsigned int k = key_of(acc[i]);
-                if ((k & mask) == prefix) atomicAdd(&hh[(k >> shift) & 255u], 1u);
+    unsigned int low = 0, mask = 0, prefix = 0, need = select ? unsigned(p.budget - p.recent) : 0u;
+    unsigned int above = 0;                      // this CTA's keys above the digits found so far
+    unsigned long long limit = 0ull;             // with `few`: the threshold among candidates
+    bool few = false;
+    if (tid < 3) sh.counts[tid] = 0u;
+    if (select) {
+        // ---- keys, and the bits in which they differ
+        unsigned int mn = 0xFFFFFFFFu, mx = 0u;
+        if (tid == 0) {
+            sh.range[0] = 0xFFFFFFFFu;
+            sh.range[1] = 0u;
+        }
+        __syncthreads();
+        for (int i0 = tid; i0 < n_old; i0 += 8 * ET) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = i0 + j * ET < n_old ? acc[s_lo + i0 + j * ET] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int i = i0 + j * ET;
+                if (i < n_old) {
+                    const unsigned int k = key_of(v[j]);
+                    if (i < KEYS) keys[i] = k;
+                    mn = min(mn, k);
+                    mx = max(mx, k);
+                }
             }
+        }
+        mn = __reduce_min_sync(0xffffffffu, mn);
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        if (lane == 0) {
+            atomicMin(&sh.range[0], mn);
+            atomicMax(&sh.range[1], mx);
+        }
+        if constexpr (SOLO) {
+            __syncthreads();
+            mn = sh.range[0];
+            mx = sh.range[1];
+        } else {
             cluster_sync();
-            if (tid < 256) {
-                unsigned int t = 0;
-                for (unsigned int r = 0; r < C; ++r) t += ld_peer(hh + tid, r);
-                tot[tid] = t;
+            mn = 0xFFFFFFFFu;
+            mx = 0u;
+            for (unsigned int r = 0; r < C; ++r) {
+                mn = min(mn, ld_peer(&sh.range[0], r));
+                mx = max(mx, ld_peer(&sh.range[1], r));
             }
+        }
+        // digits of key - low, from its highest bit down (uniform in the cluster)
+        low = mn;
+        int top = 32 - __clz(mx - mn);           // bits still undecided
+        int pass = 0;
+        while (top > 0 && !few) {
+            const int bits = min(9, top), shift = top - bits;
+            const unsigned int bins = (1u << bits) - 1u;
+            unsigned int *hh = sh.hist[pass & 1];
+            hh[tid] = 0u;
+            hh[tid + ET] = 0u;
+            static_assert(BINS == 2 * ET, "two bins per thread");
             __syncthreads();
-            if (tid < 32) {
-                // lane l takes bins 255 - 8 l down; suffix sums from the top
-                unsigned int mine = 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) mine += tot[255 - (8 * lane + j)];
-                unsigned int x = mine;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const unsigned int y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += y;
-                }
-                unsigned int above = x - mine;
-                if (above < need && x >= need) {
-                    int bin = 255 - 8 * lane;
-                    while (above + tot[bin] < need) above += tot[bin--];
-                    s_prefix = prefix | (unsigned(bin) << shift);
-                    s_need = need - above;
+#pragma unroll 4
+            for (int i = tid; i < n_old; i += ET) {
+                const unsigned int k = key_at(i) - low;
+                if ((k & mask) == prefix) atomicAdd(&hh[(k >> shift) & bins], 1u);
+            }
+            // thread t takes bins 511 - 2 t and 510 - 2 t: an inclusive scan over t is the suffix sum over bins
+            unsigned int t0 = 0, t1 = 0;
+            if constexpr (SOLO) {
+                __syncthreads();
+                t0 = hh[BINS - 1 - 2 * tid];
+                t1 = hh[BINS - 2 - 2 * tid];
+            } else {
+                cluster_sync();
+#pragma unroll 4
+                for (unsigned int r = 0; r < C; ++r) {
+                    const unsigned long long w =
+                        ld_peer64(reinterpret_cast<const unsigned long long *>(hh + BINS - 2 - 2 * tid), r);
+                    t1 += static_cast<unsigned int>(w);
+                    t0 += static_cast<unsigned int>(w >> 32);
                 }
             }
+            unsigned int sum_all;
+            const unsigned int x = inclusive(t0 + t1, sh.scan, &sum_all);
+            // the digit: >= need keys at or above it, < need above it
+            const unsigned int over0 = x - t0 - t1, over1 = x - t1;
+            if (over1 >= need && over0 < need) {
+                sh.prefix = prefix | (unsigned(BINS - 1 - 2 * tid) << shift);
+                sh.need = need - over0;
+                sh.pop = t0;
+            } else if (x >= need && over1 < need) {
+                sh.prefix = prefix | (unsigned(BINS - 2 - 2 * tid) << shift);
+                sh.need = need - over1;
+                sh.pop = t1;
+            }
+            if (tid == 0) sh.above = 0u;
             __syncthreads();
-            prefix = s_prefix;
-            need = s_need;
-            mask |= 255u << shift;
+            prefix = sh.prefix;
+            need = sh.need;
+            few = sh.pop <= unsigned(FEW);
+            const unsigned int digit = (prefix >> shift) & bins;
+            unsigned int mine = (unsigned(2 * tid) > digit ? hh[2 * tid] : 0u) + (unsigned(2 * tid + 1) > digit ? hh[2 * tid + 1] : 0u);
+            mine = __reduce_add_sync(0xffffffffu, mine);
+            if (lane == 0 && mine) atomicAdd(&sh.above, mine);
+            __syncthreads();
+            above += sh.above;
+            mask |= bins << shift;
+            top = shift;
+            ++pass;
+        }
+        if (few) {
+            for (int i = tid; i < n_old; i += ET) {
+                const unsigned int k = key_at(i);
+                if (((k - low) & mask) == prefix) sh.mine[atomicAdd(&sh.counts[2], 1u)] = cand_of(k, s_lo + i);
+            }
+        } else if (!SOLO) {
+            unsigned int eq = 0;
+            for (int i = tid; i < n_old; i += ET) eq += key_at(i) - low == prefix;
+            eq = __reduce_add_sync(0xffffffffu, eq);
+            if (lane == 0 && eq) atomicAdd(&sh.counts[1], eq);
+        }
+        if (tid == 0) sh.counts[0] = above;
+    }
+
+    // ---- what the CTAs before this one keep
+    unsigned int gt_before = 0, eq_before = 0;
+    if (select && !SOLO) {
+        cluster_sync();
+        if (tid < 32) {
+            const bool in = unsigned(lane) < C;
+            const unsigned int c0 = in ? ld_peer(&sh.counts[0], unsigned(lane)) : 0u;
+            const unsigned int c1 = in ? ld_peer(&sh.counts[1], unsigned(lane)) : 0u;
+            unsigned int x = in ? ld_peer(&sh.counts[2], unsigned(lane)) : 0u;
+            if (in) {
+                sh.gt[lane] = c0;
+                sh.eq[lane] = c1;
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (in) sh.first[lane + 1] = x;
+            if (lane == 0) sh.first[0] = 0u;
+        }
+        __syncthreads();
+        for (unsigned int r = 0; r < rank; ++r) {
+            gt_before += sh.gt[r];
+            eq_before += sh.eq[r];
         }
     }
-    // kept: keys above `prefix`, and the first `need` equal to it; none of the old when need was 0
-    const bool none_old = !all && p.budget == p.recent;
-    auto kind = [&](int i) -> unsigned int {     // 2: kept for sure, 1: kept if among the first equal ones
+    if (few) {
+        // gather every CTA's candidates, and rank them by counting (four threads each)
+        const unsigned long long *list = SOLO ? sh.mine : sh.few;
+        unsigned int total;
+        if constexpr (SOLO) {
+            __syncthreads();
+            total = sh.counts[2];
+        } else {
+            total = sh.first[C];
+            if (unsigned(tid) < total) {
+                unsigned int r = 0;
+                while (sh.first[r + 1] <= unsigned(tid)) ++r;
+                sh.few[tid] = ld_peer64(&sh.mine[unsigned(tid) - sh.first[r]], r);
+            }
+            __syncthreads();
+        }
+        static_assert(ET == 4 * FEW, "four threads per candidate");
+        const unsigned int c = unsigned(tid) >> 2;
+        const unsigned long long v = c < total ? list[c] : 0ull;
+        unsigned int larger = 0;
+        for (unsigned int j = unsigned(tid) & 3u; j < total; j += 4) larger += list[j] > v;
+        larger += __shfl_xor_sync(0xffffffffu, larger, 1);
+        larger += __shfl_xor_sync(0xffffffffu, larger, 2);
+        if (c < total && larger == need - 1) sh.limit = v;
+        __syncthreads();
+        limit = sh.limit;
+        need = 0;
+        if constexpr (!SOLO)    // the candidates of the CTAs before this one that pass
+            gt_before += __syncthreads_count(unsigned(tid) < sh.first[rank] && list[tid & (FEW - 1)] >= limit);
+    }
+    if (select && !SOLO) cluster_sync();         // no CTA leaves while its counts and candidates are read
+    // 2: kept, 1: kept if among the first `need` equal to the threshold, 0: not
+    auto kind = [&](int i) -> unsigned int {
         if (all || i >= old) return 2u;
         if (none_old) return 0u;
-        const unsigned int k = key_of(acc[i]);
-        return k > prefix ? 2u : k == prefix ? 1u : 0u;
+        const unsigned int k = key_at(i - s_lo);
+        if (few) return cand_of(k, i) >= limit ? 2u : 0u;
+        return k - low > prefix ? 2u : k - low == prefix ? 1u : 0u;
     };
-    unsigned int gt = 0, eq = 0;
-    for (int i = lo + tid; i < hi; i += ET) {
-        const unsigned int k = kind(i);
-        gt += k == 2u;
-        eq += k == 1u;
+    if (SOLO && select) {
+        unsigned int gt = 0, eq = 0;
+        for (int i = tid; i < min(lo, old); i += ET) {
+            const unsigned int k = kind(i);
+            gt += k == 2u;
+            eq += k == 1u;
+        }
+        inclusive(gt, sh.scan, &gt_before);
+        inclusive(eq, sh.scan, &eq_before);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        gt += __shfl_xor_sync(0xffffffffu, gt, o);
-        eq += __shfl_xor_sync(0xffffffffu, eq, o);
-    }
-    if (tid < 2) counts[tid] = 0u;
-    __syncthreads();
-    if (lane == 0) {
-        atomicAdd(&counts[0], gt);
-        atomicAdd(&counts[1], eq);
-    }
-    cluster_sync();
-    unsigned int gt_before = 0, eq_before = 0;
-    for (unsigned int r = 0; r < rank; ++r) {
-        gt_before += ld_peer(&counts[0], r);
-        eq_before += ld_peer(&counts[1], r);
-    }
-    cluster_sync();                              // no CTA leaves while its counts are read
+    if (all) gt_before = lo;
+    else gt_before += max(0, lo - old);          // the recent positions follow the old ones
 
-    // ---- number the kept positions in order and copy them
+    // ---- number the kept positions in order and copy them, CHUNK records at a time
     const int32_t *table = p.table + size_t(b) * p.width;
     const int32_t *dtable = p.dst + size_t(b) * p.dst_width;
     int32_t *kept = p.kept + size_t(bh) * size_t(p.budget);
     float *acc_out = p.acc_out ? p.acc_out + size_t(bh) * size_t(p.dst_cap) : nullptr;
-    for (int c0 = lo; c0 < hi; c0 += CHUNK) {
-        unsigned int k4[4], v = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = c0 + tid * 4 + j;
-            k4[j] = i < hi ? kind(i) : 0u;
-            v += k4[j] == 2u ? 0x10000u : k4[j] == 1u ? 1u : 0u;
-        }
-        unsigned int total;
-        const unsigned int ex = scan2(v, tmp, &total);
-        unsigned int g = gt_before + (ex >> 16), e = eq_before + (ex & 0xFFFFu);
-        const unsigned int j0 = gt_before + min(eq_before, need);          // slot of the chunk's first kept position
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (k4[j] == 2u || (k4[j] == 1u && e < need)) src_pos[g + min(e, need) - j0] = c0 + tid * 4 + j;
-            g += k4[j] == 2u;
-            e += k4[j] == 1u;
-        }
-        gt_before += total >> 16;
-        eq_before += total & 0xFFFFu;
-        const int m = int(gt_before + min(eq_before, need) - j0);
-        __syncthreads();
-        for (int x = tid; x < m; x += ET) {
-            const int sp = src_pos[x], dp = int(j0) + x;
-            kept[dp] = sp;
-            if (acc_out) acc_out[dp] = acc[sp];
-            from_rec[x] = p.cache + size_t(sk::kv4_record(table, sp >> 4, p.recs, p.by_recs, p.pages, p.heads, h)) * sk::kv4_rec_bytes(D) + (sp & 15);
-            to_rec[x] = p.cache + size_t(sk::kv4_record(dtable, dp >> 4, p.recs, p.by_recs, p.pages, p.heads, h)) * sk::kv4_rec_bytes(D) + (dp & 15);
+    uint32_t done = 0;                           // records this warp has copied: ring position and parity
+    bool dead = false;
+    for (int r0 = rec_lo; r0 < rec_hi; r0 += CHUNK) {
+        const int nr = min(CHUNK, rec_hi - r0);
+        for (int i0 = 0; i0 < nr * 16; i0 += ET) {           // a lane a position: 32 positions are two records
+            const int i = r0 * 16 + i0 + tid;
+            const unsigned int k = i < hi && i0 + tid < nr * 16 ? kind(i) : 0u;
+            const unsigned int two = __ballot_sync(0xffffffffu, k == 2u), one = __ballot_sync(0xffffffffu, k == 1u);
+            const int r = (i0 + tid) >> 4;
+            if ((lane & 15) == 0 && r < nr) {
+                const int s = lane & 16;
+                sh.masks[r] = ((two >> s) & 0xFFFFu) | (((one >> s) & 0xFFFFu) << 16);
+            }
         }
         __syncthreads();
-        // records start at multiples of 16: the low bits hold the position in one
-        copy_rows<D>(from_rec, to_rec, m);
+        // base slot of each record, and the list of records with something kept (in order)
+        unsigned int listed = 0;
+        for (int x0 = 0; x0 < nr; x0 += ET) {
+            const unsigned int m = x0 + tid < nr ? sh.masks[x0 + tid] : 0u;
+            unsigned int two = m & 0xFFFFu, one = m >> 16, tg, te, tl;
+            const unsigned int c = (unsigned(__popc(two)) << 16) | unsigned(__popc(one));
+            const unsigned int x = inclusive(c, sh.scan, &tg) - c;             // at most 16 ET in each half
+            const unsigned int g = gt_before + (x >> 16), e = eq_before + (x & 0xFFFFu);
+            unsigned int keep_one = e < need ? need - e : 0u;                  // the first so many of `one`
+            while (unsigned(__popc(one)) > keep_one) one &= ~(0x80000000u >> __clz(one));
+            const unsigned int keep = two | one;
+            te = tg & 0xFFFFu;
+            const unsigned int at = inclusive(keep != 0u, sh.scan, &tl);
+            if (keep) {
+                const unsigned int y = listed + at - 1u;
+                sh.list_rec[y] = r0 + x0 + tid;
+                sh.list_base[y] = g + min(e, need);
+                sh.list_mask[y] = uint16_t(keep);
+            }
+            listed += tl;
+            gt_before += tg >> 16;
+            eq_before += te;
+        }
+        const int n_list = int(listed);
+        // the ring takes the keys' place (a later chunk reads them again)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+        cached = 0;
+        unsigned char *const own = smem + warp * SLOTS * REC;
+        const uint32_t ring = sk::smem_u32(own);
+        auto issue = [&](int y, uint32_t slot) {
+            if (lane == 0) {
+                const uint32_t bar = sk::smem_u32(&sh.bar[warp][slot]);
+                const uint32_t rec = sk::kv4_record(table, sh.list_rec[y], p.recs, p.by_recs, p.pages, p.heads, h);
+                sk::mbar_arrive_expect_tx(bar, REC);
+                sk::bulk_load(ring + slot * REC, p.cache + size_t(rec) * REC, REC, bar);
+            }
+        };
+        for (int k = 0; k < SLOTS; ++k)
+            if (warp + k * WARPS < n_list) issue(warp + k * WARPS, (done + k) % SLOTS);
+        for (int y = warp; y < n_list; y += WARPS, ++done) {
+            const uint32_t slot = done % SLOTS;
+            const unsigned int m = sh.list_mask[y], base = sh.list_base[y];
+            const int count = __popc(m), rec = sh.list_rec[y];
+            if (lane < 16 && (m >> lane & 1u)) {
+                const int q = __popc(m & ((1u << lane) - 1u)), from = rec * 16 + lane;
+                sh.nth[warp][q] = uint8_t(lane);
+                kept[base + q] = from;
+                if (acc_out) acc_out[base + q] = acc[from];
+            }
+            sk::wait_full(sk::smem_u32(&sh.bar[warp][slot]), (done / SLOTS) & 1, p.err, dead);
+            __syncwarp();
+            const unsigned char *src = own + slot * REC;
+            // four positions at a time: neighbouring lanes write neighbouring positions of a value block
+            for (int q0 = 0; q0 < count; q0 += 4) {
+                const int q = q0 + (lane & 3);
+                if (q < count) {
+                    const int i = sh.nth[warp][q], to = int(base) + q, j = to & 15;
+                    uint8_t *dst = p.cache + size_t(sk::kv4_record(dtable, to >> 4, p.recs, p.by_recs, p.pages, p.heads, h)) * REC;
+#pragma unroll
+                    for (int blk = lane >> 2; blk < NB; blk += 8) {
+                        *reinterpret_cast<uint2 *>(dst + sk::kv4_code_at<true>(D, j, blk)) =
+                            *reinterpret_cast<const uint2 *>(src + sk::kv4_code_at<true>(D, i, blk));
+                        *reinterpret_cast<uint2 *>(dst + sk::kv4_code_at<false>(D, j, blk)) =
+                            *reinterpret_cast<const uint2 *>(src + sk::kv4_code_at<false>(D, i, blk));
+                        dst[sk::kv4_scale_at<true>(D, j, blk)] = src[sk::kv4_scale_at<true>(D, i, blk)];
+                        dst[sk::kv4_scale_at<false>(D, j, blk)] = src[sk::kv4_scale_at<false>(D, i, blk)];
+                    }
+                }
+            }
+            __syncwarp();
+            if (y + SLOTS * WARPS < n_list) issue(y + SLOTS * WARPS, slot);
+        }
         __syncthreads();
     }
     for (int j = out_n + int(rank) * ET + tid; j < p.budget; j += int(C) * ET) kept[j] = -1;
@@ -275,13 +454,27 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
     if (h == 0 && rank == 0 && tid == 0) p.new_lens[b] = out_n;
 }
 
+// The keys, and later the records' ring in their place.
 template <int D>
-sk_status launch(const EvictParams &p, int bh, int cluster, cudaStream_t s) {
-    if (sk::prepare_kernel<kv4_evict_kernel<D>>(0, true) != cudaSuccess) return SK_ERR_CUDA;
-    return sk::launch_pdl_cluster(kv4_evict_kernel<D>, cluster, dim3(unsigned(bh) * unsigned(cluster)), dim3(ET), 0, s,
-                                  p) == cudaSuccess
-               ? SK_OK
-               : SK_ERR_CUDA;
+constexpr size_t smem_bytes() {
+    const size_t ring = size_t(WARPS) * SLOTS * sk::kv4_rec_bytes(D);
+    return ring > size_t(KEYS) * 4 ? ring : size_t(KEYS) * 4;
+}
+
+template <int D>
+sk_status launch(const EvictParams &p, int bh, int ctas, cudaStream_t s) {
+    const dim3 grid(unsigned(bh) * unsigned(ctas));
+    const size_t smem = smem_bytes<D>();
+    cudaError_t e;
+    if (p.cap <= SOLO_MAX) {
+        e = sk::prepare_kernel<kv4_evict_kernel<D, true>>(smem);
+        if (e == cudaSuccess) e = sk::launch_pdl(kv4_evict_kernel<D, true>, grid, dim3(ET), smem, s, p, ctas);
+    } else {
+        e = sk::prepare_kernel<kv4_evict_kernel<D, false>>(smem, true);
+        if (e == cudaSuccess)
+            e = sk::launch_pdl_cluster(kv4_evict_kernel<D, false>, ctas, grid, dim3(ET), smem, s, p, ctas);
+    }
+    return e == cudaSuccess ? SK_OK : SK_ERR_CUDA;
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -326,10 +519,12 @@ extern "C" sk_status kv4_evict(uint8_t *cache, const int32_t *table, const int32
     p.budget = budget;
     p.recent = recent;
     // CTAs per (sequence, head): as many as fill the GPU, at most a cluster
-    // of 16, and no more than the longest table can feed with a chunk each.
+    // of 16, and no more than the longest table can feed with a position a thread.
     const int bh = seqs * kv_heads;
+    sk::Scratch sc;                          // its error word, where the stream has a workspace
+    if (sk::scratch_for(reinterpret_cast<cudaStream_t>(stream), &sc)) p.err = sc.err;
     int cluster = 1;
-    while (cluster < MAX_CLUSTER && bh * cluster < sk::device_sm_count() && cluster * (CHUNK / 4) < p.cap) cluster *= 2;
+    while (cluster < MAX_CLUSTER && bh * cluster <= sk::device_sm_count() && cluster * ET < p.cap) cluster *= 2;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (head_dim) {
         case 64: return launch<64>(p, bh, cluster, s);

@@ -20,13 +20,13 @@ namespace {
 
 constexpr int ET = 256;            // threads per CTA
 constexpr int WARPS = ET / 32;
-constexpr int KEYS = 16384;        // keys kept in shared memory (the rest are read again)
+constexpr int KEYS = 8192;         // keys kept in shared memory (the rest are read again)
 constexpr int BINS = 512;
 constexpr int FEW = 64;            // candidates left at which the selection ends by counting
 constexpr int CHUNK = 1024;        // records numbered at a time
 constexpr int MAX_CLUSTER = 16;
 constexpr int SLOTS = 2;           // source records in flight per warp
-constexpr int SOLO_MAX = 2 * KEYS; // positions up to which a CTA selects alone
+constexpr int SOLO_MAX = KEYS;     // positions up to which a CTA selects alone
 
 struct EvictParams {
     uint8_t *cache;

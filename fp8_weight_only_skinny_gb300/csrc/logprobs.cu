@@ -26,6 +26,7 @@ constexpr int ROUND = LT * PER;
 constexpr int MAX_TOP = 64;
 constexpr int SOFT = 192;                // candidates that trigger a cut after a round
 constexpr int LIST = SOFT + ROUND + 2;   // a round can add all of its logits
+constexpr int GROUPS = 64;               // groups of threads whose maxima bound the n-th largest
 constexpr int MAX_CLUSTER = 16;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float LOWEST = -3.402823466e38f;
@@ -108,11 +109,21 @@ __device__ __forceinline__ Stats join(const Stats &a, const Stats &b, float c) {
     return r;
 }
 
+// Joined with lane ^ o's, the lower lane's first.
+__device__ __forceinline__ Stats join_across(const Stats &a, int o, int lane, float c) {
+    Stats x;
+    x.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+    x.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+    x.w = __shfl_xor_sync(0xffffffffu, a.w, o);
+    return (lane & o) ? join(x, a, c) : join(a, x, c);
+}
+
 struct Shared {
     unsigned long long list[LIST];
     unsigned long long best[MAX_TOP];
     unsigned long long maxima[LT];
-    unsigned int top32[LT];
+    alignas(16) unsigned int top[GROUPS];
+    unsigned long long all_best[MAX_CLUSTER * MAX_TOP];
     Stats stats[LT / 32];
     Stats mine, all;
     unsigned int above[LT / 32];
@@ -232,15 +243,18 @@ __device__ __forceinline__ float one(const __half *p) { return __half2float(*p);
 // takes the r-th contiguous part of the row, a round of 4096 logits at a time,
 // the next round's loads in flight while one is summed.
 template <typename T>
-__global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ LogprobParams p) {
+__global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ LogprobParams p, int first_row, int late) {
     extern __shared__ __align__(16) unsigned char raw_smem[];
     Shared &sh = *reinterpret_cast<Shared *>(raw_smem);
     constexpr int VEC = Raw<T>::VEC;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const unsigned int rank = cluster_rank(), C = cluster_size();
-    const int row = blockIdx.x / C;
+    const int row = first_row + blockIdx.x / C;
+    // The first of two launches lets the second start once all of its own CTAs
+    // are past their wait, so what the logits depend on is complete; the second
+    // (late) waits at its end, so that whatever follows it follows both.
+    if (!late) sk::pdl_wait_primary();
     sk::pdl_launch_dependents();
-    sk::pdl_wait_primary();
     const T *z0 = static_cast<const T *>(p.logits) + (long long)row * p.stride;
     // this CTA's part, and the 16-byte boundary at or below its first logit
     const int part = (p.N + int(C) - 1) / int(C);
@@ -251,6 +265,8 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
     const int tok = p.tokens ? p.tokens[row] : -1;
     const bool given = tok >= 0 && tok < p.N;
     const float ztok = given ? one(z0 + tok) : 0.f;
+    const float ztok_up = value_of(key_of(ztok) + 1u);       // the next larger value
+    const bool masked_token = ztok == -__builtin_huge_valf();
     const float c = p.inv_t2;
     const int n = min(p.top_n, p.N);
     if (tid == 0) sh.count = 0;
@@ -283,43 +299,66 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
             st.w = fmaf(e, d, st.w);
         }
         if (given && !(mx < ztok)) {
+            // logits before the token rank above it when they are at least its
+            // own, those after it when they exceed it; one word straddles it
 #pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                const int i = i0 + ((j / VEC) * LT + tid) * VEC + j % VEC;
-                above += i >= lo && i < hi && (z[j] > ztok || (z[j] == ztok && i < tok));
+            for (int v = 0; v < Raw<T>::NV; ++v) {
+                const int at = i0 + (v * LT + tid) * VEC;
+                if (masked_token || (at < tok && tok < at + VEC)) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j)
+                        above += at + j >= lo && at + j < hi &&
+                                 (z[v * VEC + j] > ztok || (z[v * VEC + j] == ztok && at + j < tok));
+                } else {
+                    const float t = at < tok ? ztok : ztok_up;
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) above += z[v * VEC + j] >= t;
+                }
             }
         }
         if (n > 0) {
             if (i0 == first) {
-                // the n-th largest of the threads' maxima bounds the n-th
-                // largest logit from below (the last byte holds the thread, so
-                // that they differ: at most a little lower)
-                const unsigned int mine = (key_of(mx) & ~255u) | unsigned(LT - 1 - tid);
-                sh.top32[tid] = mine;
+                // The n-th largest of the maxima of 64 groups of threads bounds
+                // the n-th largest logit from below (the last byte holds the
+                // group, so that they differ: at most a little lower).
+                float gm = mx;
+#pragma unroll
+                for (int o = 1; o < LT / GROUPS; o <<= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+                if (tid % (LT / GROUPS) == 0)
+                    sh.top[tid / (LT / GROUPS)] = (key_of(gm) & ~255u) | unsigned(GROUPS - 1 - tid / (LT / GROUPS));
                 __syncthreads();
-                int larger = 0;
-#pragma unroll 8
-                for (int j = 0; j < LT; j += 4) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(&sh.top32[j]);
-                    larger += (w.x > mine) + (w.y > mine) + (w.z > mine) + (w.w > mine);
+                if (wid == 0) {
+                    const unsigned int k0 = sh.top[lane], k1 = sh.top[lane + 32];
+                    int l0 = 0, l1 = 0;
+#pragma unroll
+                    for (int j = 0; j < GROUPS; j += 4) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(&sh.top[j]);
+                        l0 += (w.x > k0) + (w.y > k0) + (w.z > k0) + (w.w > k0);
+                        l1 += (w.x > k1) + (w.y > k1) + (w.z > k1) + (w.w > k1);
+                    }
+                    if (l0 == n - 1) sh.zfloor = value_of(k0 & ~255u);
+                    if (l1 == n - 1) sh.zfloor = value_of(k1 & ~255u);
                 }
-                if (larger == n - 1) sh.zfloor = value_of(mine & ~255u);
                 __syncthreads();
                 zfloor = sh.zfloor;
             }
             bool full = false;
             if (!(mx < zfloor)) {
 #pragma unroll
-                for (int j = 0; j < PER; ++j)
-                    if (!(z[j] < zfloor)) {
-                        const int i = i0 + ((j / VEC) * LT + tid) * VEC + j % VEC;
-                        const unsigned long long k = cand_of(z[j], i);
-                        if (k > floor && i >= lo && i < hi) {
-                            const int at = atomicAdd(&sh.count, 1);
-                            sh.list[at] = k;
-                            full |= at >= SOFT;
+                for (int q = 0; q < PER; q += 4) {
+                    if (fmaxf(fmaxf(z[q], z[q + 1]), fmaxf(z[q + 2], z[q + 3])) < zfloor) continue;
+#pragma unroll
+                    for (int j = q; j < q + 4; ++j)
+                        if (!(z[j] < zfloor)) {
+                            const int i = i0 + ((j / VEC) * LT + tid) * VEC + j % VEC;
+                            const unsigned long long k = cand_of(z[j], i);
+                            if (k > floor && i >= lo && i < hi) {
+                                const int at = atomicAdd(&sh.count, 1);
+                                sh.list[at] = k;
+                                full |= at >= SOFT;
+                            }
                         }
-                    }
+                }
             }
             if (__syncthreads_or(full)) {
                 pick_best(sh, sh.count, n);
@@ -335,11 +374,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
     // ---- the CTA's statistics and candidates, in a fixed order
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        Stats x;
-        x.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-        x.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-        x.w = __shfl_xor_sync(0xffffffffu, st.w, o);
-        st = (lane & o) ? join(x, st, c) : join(st, x, c);
+        st = join_across(st, o, lane, c);
         above += __shfl_xor_sync(0xffffffffu, above, o);
     }
     if (lane == 0) {
@@ -348,18 +383,21 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
     }
     __syncthreads();
     if (n > 0) pick_best(sh, sh.count, n);
-    if (tid == 0) {
-        Stats a = sh.stats[0];
-        unsigned int r = sh.above[0];
-        for (int w = 1; w < LT / 32; ++w) {
-            a = join(a, sh.stats[w], c);
-            r += sh.above[w];
+    if (wid == 0) {
+        Stats a = lane < LT / 32 ? sh.stats[lane] : Stats{LOWEST, 0.f, 0.f};
+        unsigned int r = lane < LT / 32 ? sh.above[lane] : 0u;
+#pragma unroll
+        for (int o = 1; o < LT / 32; o <<= 1) {
+            a = join_across(a, o, lane, c);
+            r += __shfl_xor_sync(0xffffffffu, r, o);
         }
-        sh.mine = a;
-        sh.above_mine = r;
-        if (C == 1) {
-            sh.all = a;
-            sh.above_all = r;
+        if (lane == 0) {
+            sh.mine = a;
+            sh.above_mine = r;
+            if (C == 1) {
+                sh.all = a;
+                sh.above_all = r;
+            }
         }
     }
     // ---- the cluster's: every CTA joins all the statistics, and places its
@@ -376,11 +414,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
             }
 #pragma unroll
             for (int o = 1; o < MAX_CLUSTER; o <<= 1) {
-                Stats x;
-                x.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-                x.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-                x.w = __shfl_xor_sync(0xffffffffu, a.w, o);
-                a = (lane & o) ? join(x, a, c) : join(a, x, c);
+                a = join_across(a, o, lane, c);
                 r += __shfl_xor_sync(0xffffffffu, r, o);
             }
             if (lane == 0) {
@@ -388,16 +422,21 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
                 sh.above_all = r;
             }
         }
-        // entry e of this CTA against the sorted entries of CTA k, both by thread
+        // everyone's entries, then entry e of this CTA against the sorted entries of CTA k, both by thread
+        for (int x = tid; x < int(C) * n; x += LT) {
+            const int k = x / n;
+            sh.all_best[x] = ld_peer_u64(peer(&sh.best[x - k * n], unsigned(k)));
+        }
+        __syncthreads();
         for (int x = tid; x < int(C) * n; x += LT) {
             const int k = x / n, e = x - k * n;
             if (unsigned(k) == rank) continue;
             const unsigned long long v = sh.best[e];
-            const uint32_t theirs = peer(sh.best, unsigned(k));
+            const unsigned long long *theirs = sh.all_best + k * n;
             int a = 0, b = n;                    // entries [0, a) are larger, [b, n) are not
             while (a < b) {
                 const int h = (a + b) >> 1;
-                if (ld_peer_u64(theirs + 8 * h) > v) a = h + 1;
+                if (theirs[h] > v) a = h + 1;
                 else b = h;
             }
             if (a) atomicAdd(&sh.place[e], unsigned(a));
@@ -424,6 +463,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
             p.top_logprobs[(long long)row * p.top_n + at] = logprob(value_of(static_cast<unsigned int>(k >> 32)));
         }
     }
+    if (late) sk::pdl_wait_primary();
     if (rank == 0)
         for (int e = n + tid; e < p.top_n; e += LT) {
             p.top_ids[(long long)row * p.top_n + e] = -1;
@@ -432,12 +472,40 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
 }
 
 template <typename T>
-sk_status launch(const LogprobParams &p, int rows, int cluster, cudaStream_t s) {
-    if (sk::prepare_kernel<logprobs_kernel<T>>(sizeof(Shared), true) != cudaSuccess) return SK_ERR_CUDA;
+cudaError_t launch(const LogprobParams &p, int first_row, int rows, int cluster, bool late, cudaStream_t s) {
+    const cudaError_t e = sk::prepare_kernel<logprobs_kernel<T>>(sizeof(Shared), true);
+    if (e != cudaSuccess) return e;
     return sk::launch_pdl_cluster(logprobs_kernel<T>, cluster, dim3(unsigned(rows) * unsigned(cluster)), dim3(LT),
-                                  sizeof(Shared), s, p) == cudaSuccess
-               ? SK_OK
-               : SK_ERR_CUDA;
+                                  sizeof(Shared), s, p, first_row, int(late));
+}
+
+// CTAs that run at a time, four to an SM (64 registers a thread).
+constexpr int PER_SM = 4;
+
+template <typename T>
+sk_status run(const LogprobParams &p, int rows, cudaStream_t s) {
+    const int slots = PER_SM * (sk::device_sm_count() > 0 ? sk::device_sm_count() : 1);
+    // CTAs per row: what fits, each with a round or more to read.
+    // (Clusters of fewer and larger CTAs, one round each, were slower: 1024
+    // threads took 10.5 against 9.8 us for one row of 151936, and eight
+    // clusters of 16 such CTAs do not fit the GPU at once.)
+    auto split = [&](int r) {
+        int c = 1;
+        while (c < MAX_CLUSTER && r * c * 2 <= slots && c * ROUND < p.N) c *= 2;
+        return c;
+    };
+    // Whole waves of one CTA per row, and what is left over split across the
+    // CTAs that fit, so that the last wave is short: 2048 rows of 151936 are
+    // 3.4 waves of 608 (measured: 265 us in one launch, 255 us in two).
+    const int left = rows > slots ? rows % slots : rows, cluster = split(left);
+    cudaError_t e;
+    if (rows <= slots || cluster == 1) {
+        e = launch<T>(p, 0, rows, rows <= slots ? cluster : 1, false, s);
+    } else {
+        e = launch<T>(p, 0, rows - left, 1, false, s);
+        if (e == cudaSuccess && left) e = launch<T>(p, rows - left, left, cluster, sk::pdl_enabled(), s);
+    }
+    return e == cudaSuccess ? SK_OK : SK_ERR_CUDA;
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -469,9 +537,6 @@ extern "C" sk_status token_logprobs(const void *logits, int f16, long long row_s
     p.inv_t2 = LOG2E / temperature;
     p.N = N;
     p.top_n = top_n;
-    // CTAs per row: enough to fill the GPU, at most a cluster of 16, each with a round or more to read
-    int cluster = 1;
-    while (cluster < MAX_CLUSTER && rows * cluster < 2 * sk::device_sm_count() && cluster * ROUND < N) cluster *= 2;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return f16 ? launch<__half>(p, rows, cluster, s) : launch<float>(p, rows, cluster, s);
+    return f16 ? run<__half>(p, rows, s) : run<float>(p, rows, s);
 }

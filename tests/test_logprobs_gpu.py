@@ -51,7 +51,7 @@ def _check(sk, z, tokens, T, n, stride_pad=0, offset=0):
 
 @pytest.mark.parametrize("dtype", [np.float32, np.float16])
 @pytest.mark.parametrize("M,N,n", [(1, 1, 1), (3, 2, 5), (2, 7, 7), (5, 255, 20), (4, 4095, 64), (2, 4097, 1), (3, 8193, 20),
-                                   (1, 65537, 5), (2, 151936, 20), (9, 10007, 0), (400, 1234, 8)])
+                                   (1, 65537, 5), (2, 151936, 20), (9, 10007, 0), (400, 1234, 8), (700, 5003, 5)])
 @pytest.mark.parametrize("T", [1.0, 0.6])
 def test_rows_of_all_lengths(sk, dtype, M, N, n, T):
     r = np.random.default_rng(M * N)

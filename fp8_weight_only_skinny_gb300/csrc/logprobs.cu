@@ -24,7 +24,7 @@ constexpr int LT = 256;                  // threads per CTA
 constexpr int PER = 16;                  // logits per thread and round
 constexpr int ROUND = LT * PER;
 constexpr int MAX_TOP = 64;
-constexpr int SOFT = 192;                // candidates that trigger a cut after a round
+constexpr int SOFT = 160;                // the most candidates that a round may start with
 constexpr int LIST = SOFT + ROUND + 2;   // a round can add all of its logits
 constexpr int GROUPS = 64;               // groups of threads whose maxima bound the n-th largest
 constexpr int MAX_CLUSTER = 16;
@@ -60,6 +60,11 @@ __device__ __forceinline__ unsigned int key_of(float v) {
 }
 __device__ __forceinline__ float value_of(unsigned int k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+// The value as a floor: everything passes one that is no number.
+__device__ __forceinline__ float floor_of(unsigned int k) {
+    const float v = value_of(k);
+    return v == v ? v : -__builtin_huge_valf();
 }
 __device__ __forceinline__ unsigned long long cand_of(float v, int i) {
     return (static_cast<unsigned long long>(key_of(v)) << 32) | static_cast<unsigned int>(~i);
@@ -264,18 +269,23 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
     next.load(z0, first, lo, hi);
     const int tok = p.tokens ? p.tokens[row] : -1;
     const bool given = tok >= 0 && tok < p.N;
-    const float ztok = given ? one(z0 + tok) : 0.f;
+    const float ztok = given ? one(z0 + tok) : 0.f, zrank = given ? ztok : __builtin_huge_valf();
     const float ztok_up = value_of(key_of(ztok) + 1u);       // the next larger value
     const bool masked_token = ztok == -__builtin_huge_valf();
     const float c = p.inv_t2;
     const int n = min(p.top_n, p.N);
+    // Candidates that trigger a cut after a round: few in a long part, so that
+    // the floor keeps up with what has been seen (2048 rows of 151936, top 20:
+    // 222 us, 237 us at 192 candidates); short parts end before that pays.
+    const int soft = hi - lo > 8 * ROUND ? 2 * n + 24 : SOFT;
+    static_assert(2 * MAX_TOP + 24 < SOFT, "the list holds them and a round");
     if (tid == 0) sh.count = 0;
     if (tid < MAX_TOP) sh.place[tid] = 0u;
 
     Stats st = {LOWEST, 0.f, 0.f};
     unsigned int above = 0;
     // a candidate is at least zfloor, and its key exceeds `floor`
-    float zfloor = -__builtin_huge_valf();
+    float zfloor = n > 0 ? -__builtin_huge_valf() : __builtin_huge_valf();
     unsigned long long floor = 0ull;
     for (int i0 = first; i0 < hi; i0 += ROUND) {
         float z[PER];
@@ -298,74 +308,74 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
             st.s += e;
             st.w = fmaf(e, d, st.w);
         }
-        if (given && !(mx < ztok)) {
-            // logits before the token rank above it when they are at least its
-            // own, those after it when they exceed it; one word straddles it
+        if (n > 0 && i0 == first) {
+            // The n-th largest of the maxima of 64 groups of threads bounds
+            // the n-th largest logit from below (the last byte holds the
+            // group, so that they differ: at most a little lower).
+            float gm = mx;
 #pragma unroll
-            for (int v = 0; v < Raw<T>::NV; ++v) {
-                const int at = i0 + (v * LT + tid) * VEC;
-                if (masked_token || (at < tok && tok < at + VEC)) {
+            for (int o = 1; o < LT / GROUPS; o <<= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+            if (tid % (LT / GROUPS) == 0)
+                sh.top[tid / (LT / GROUPS)] = (key_of(gm) & ~255u) | unsigned(GROUPS - 1 - tid / (LT / GROUPS));
+            __syncthreads();
+            if (wid == 0) {
+                const unsigned int k0 = sh.top[lane], k1 = sh.top[lane + 32];
+                int l0 = 0, l1 = 0;
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j)
-                        above += at + j >= lo && at + j < hi &&
-                                 (z[v * VEC + j] > ztok || (z[v * VEC + j] == ztok && at + j < tok));
-                } else {
-                    const float t = at < tok ? ztok : ztok_up;
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) above += z[v * VEC + j] >= t;
+                for (int j = 0; j < GROUPS; j += 4) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(&sh.top[j]);
+                    l0 += (w.x > k0) + (w.y > k0) + (w.z > k0) + (w.w > k0);
+                    l1 += (w.x > k1) + (w.y > k1) + (w.z > k1) + (w.w > k1);
                 }
+                if (l0 == n - 1) sh.zfloor = floor_of(k0 & ~255u);
+                if (l1 == n - 1) sh.zfloor = floor_of(k1 & ~255u);
+            }
+            __syncthreads();
+            zfloor = sh.zfloor;
+        }
+        // Four logits at a time that hold one to look at: at least the token's
+        // (for the rank), or at least the floor (for the list).
+        bool full = false;
+        const float least = fminf(zfloor, zrank);
+        if (!(mx < least)) {
+#pragma unroll
+            for (int q = 0; q < PER; q += 4) {
+                const float most = fmaxf(fmaxf(z[q], z[q + 1]), fmaxf(z[q + 2], z[q + 3]));
+                if (most < least) continue;
+                const int at = i0 + ((q / VEC) * LT + tid) * VEC + q % VEC;
+                if (!(most < zrank)) {
+                    // logits before the token rank above it when they are at
+                    // least its own, those after it when they exceed it
+                    if (masked_token || (at < tok && tok < at + 4)) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            above += at + j >= lo && at + j < hi && (z[q + j] > ztok || (z[q + j] == ztok && at + j < tok));
+                    } else {
+                        const float t = at < tok ? ztok : ztok_up;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) above += z[q + j] >= t;
+                    }
+                }
+                if (n == 0 || most < zfloor) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (!(z[q + j] < zfloor)) {
+                        const unsigned long long k = cand_of(z[q + j], at + j);
+                        if (k > floor && at + j >= lo && at + j < hi) {
+                            const int to = atomicAdd(&sh.count, 1);
+                            sh.list[to] = k;
+                            full |= to >= soft;
+                        }
+                    }
             }
         }
         if (n > 0) {
-            if (i0 == first) {
-                // The n-th largest of the maxima of 64 groups of threads bounds
-                // the n-th largest logit from below (the last byte holds the
-                // group, so that they differ: at most a little lower).
-                float gm = mx;
-#pragma unroll
-                for (int o = 1; o < LT / GROUPS; o <<= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
-                if (tid % (LT / GROUPS) == 0)
-                    sh.top[tid / (LT / GROUPS)] = (key_of(gm) & ~255u) | unsigned(GROUPS - 1 - tid / (LT / GROUPS));
-                __syncthreads();
-                if (wid == 0) {
-                    const unsigned int k0 = sh.top[lane], k1 = sh.top[lane + 32];
-                    int l0 = 0, l1 = 0;
-#pragma unroll
-                    for (int j = 0; j < GROUPS; j += 4) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(&sh.top[j]);
-                        l0 += (w.x > k0) + (w.y > k0) + (w.z > k0) + (w.w > k0);
-                        l1 += (w.x > k1) + (w.y > k1) + (w.z > k1) + (w.w > k1);
-                    }
-                    if (l0 == n - 1) sh.zfloor = value_of(k0 & ~255u);
-                    if (l1 == n - 1) sh.zfloor = value_of(k1 & ~255u);
-                }
-                __syncthreads();
-                zfloor = sh.zfloor;
-            }
-            bool full = false;
-            if (!(mx < zfloor)) {
-#pragma unroll
-                for (int q = 0; q < PER; q += 4) {
-                    if (fmaxf(fmaxf(z[q], z[q + 1]), fmaxf(z[q + 2], z[q + 3])) < zfloor) continue;
-#pragma unroll
-                    for (int j = q; j < q + 4; ++j)
-                        if (!(z[j] < zfloor)) {
-                            const int i = i0 + ((j / VEC) * LT + tid) * VEC + j % VEC;
-                            const unsigned long long k = cand_of(z[j], i);
-                            if (k > floor && i >= lo && i < hi) {
-                                const int at = atomicAdd(&sh.count, 1);
-                                sh.list[at] = k;
-                                full |= at >= SOFT;
-                            }
-                        }
-                }
-            }
             if (__syncthreads_or(full)) {
                 pick_best(sh, sh.count, n);
                 for (int i = tid; i < n; i += LT) sh.list[i] = sh.best[i];
                 if (tid == 0) sh.count = n;
                 floor = sh.best[n - 1];
-                zfloor = value_of(static_cast<unsigned int>(floor >> 32));
+                zfloor = floor_of(static_cast<unsigned int>(floor >> 32));
                 __syncthreads();
             }
         }

@@ -11,28 +11,12 @@
 
 #include "../../include/skinny.h"
 #include "internal.h"
-#include "kv4.cuh"
+#include "kv4_attention.cuh"
 #include "launch_util.cuh"
 
 namespace {
 
-constexpr int WARPS = 4;
-constexpr int CT = WARPS * 32;
-constexpr int STEP = 32;               // positions per warp step: two records
-constexpr int TILE = WARPS * STEP;     // positions per CTA step, the unit of the work split
-constexpr int NROW = 8;                // query rows per n8 tile
-constexpr float NEG_INF = -__builtin_huge_valf();
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-// Each row's weights are taken against a reference r, p = 2^(z - r + P_SHIFT):
-// any r gives the same quotient, so r is a maximum the row had earlier and is
-// moved only when a score passes it by more than SLACK (then the sums so far
-// are scaled).  Most steps need neither the row's maximum across lanes nor a
-// rescaling.  The p go to the second product in FP16, at most 2^(P_SHIFT +
-// SLACK) = 2^15 and normal down to 2^-24 of r's.  Their rounding (2^-11
-// relative at most, independent from position to position) is of the size of
-// the output's own rounding to FP16; the sum of the weights is taken from the
-// unrounded FP32 values.
-constexpr float P_SHIFT = 10.f, SLACK = 5.f;
+using namespace sk::attn;
 
 // NR tiles of eight query rows are taken together: positions (q . k) and
 // components (p . v) are the 16-wide operand, query rows the 8-wide one, so
@@ -55,46 +39,6 @@ struct Cfg {
     static constexpr size_t SMEM = BODY + NR * QTILE + WARPS * STAGES * 8 + WARPS * ROWS * 8;
 };
 
-struct AttnParams {
-    const __half *q;
-    long long q_stride;        // elements between query rows
-    const uint8_t *cache;
-    const int32_t *table, *lens;
-    __half *out;
-    float *lse;
-    const float *acc_in;
-    float *acc_out;
-    float *part_o, *part_ml;   // per partial slot: [ROWS][D] sums, [ROWS][2] (maximum, sum)
-    int2 *seg;                 // per segment: first CTA, partial slots (0: written whole)
-    unsigned int *err;
-    int pages, heads, recs, width, cap;   // recs: records per page; cap: positions the table can hold
-    int B, M, G, RT, ctas;     // G: query heads per kv head; RT: row tiles
-    float scale2, vg;          // scale * key scale * log2 e; value scale
-    sk::Div by_recs;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-
-// Two scale codes -> f16x2.  Scales are written non-negative; a NaN code (only
-// memory that no position was written to can hold one) becomes zero, so that a
-// weight of zero times what lies there is zero.
-__device__ __forceinline__ uint32_t scale_pair(uint32_t codes) {
-    const uint32_t s = sk::e4m3x2_h_to_f16x2(uint16_t(codes));
-    uint32_t d;
-    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(s), "r"(0u));
-    return d;
-}
-
 __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
@@ -105,62 +49,6 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
     uint16_t v;
     asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
     return v;
-}
-
-__device__ __forceinline__ int length_of(const AttnParams &p, int b) { return min(max(p.lens[b], 0), p.cap); }
-__device__ __forceinline__ int tiles_of(int len) { return (len + TILE - 1) / TILE; }
-
-// The CTA's share of all (sequence, head, row tile, position tile) in that
-// order: tiles [T c / P, T (c + 1) / P) of T for CTA c of P = min(ctas, T),
-// so every CTA reads the same number of positions whatever the lengths.
-struct Share {
-    long long total, t, end;   // tiles in all, this CTA's next and end
-    int parts, b;              // P; the sequence of tile t
-    long long off;             // tile t's index among the tiles of sequence b
-};
-
-__device__ __forceinline__ Share share_of(const AttnParams &p, int per_len, long long *sm /* CT / 32 + 4 */) {
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, nw = blockDim.x >> 5;
-    const int each = (p.B + int(blockDim.x) - 1) / int(blockDim.x);
-    const int lo = min(p.B, tid * each), hi = min(p.B, lo + each);
-    long long mine = 0;
-    for (int b = lo; b < hi; ++b) mine += (long long)tiles_of(length_of(p, b)) * per_len;
-    long long x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) sm[wid] = x;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < nw; ++w) {
-        if (w < wid) before += sm[w];
-        total += sm[w];
-    }
-    __syncthreads();
-    Share s;
-    s.total = total;
-    s.parts = int(total < p.ctas ? total : p.ctas);
-    const bool in = int(blockIdx.x) < s.parts;
-    s.t = in ? total * blockIdx.x / s.parts : 0;
-    s.end = in ? total * (blockIdx.x + 1) / s.parts : 0;
-    before += x - mine;
-    if (in && s.t >= before && s.t < before + mine) {
-        int b = lo;
-        long long left = s.t - before;
-        for (; b + 1 < hi; ++b) {
-            const long long n = (long long)tiles_of(length_of(p, b)) * per_len;
-            if (left < n) break;
-            left -= n;
-        }
-        sm[0] = b;
-        sm[1] = left;
-    }
-    __syncthreads();
-    s.b = int(sm[0]);
-    s.off = sm[1];
-    return s;
 }
 
 // Query rows [row0, row0 + 8 n) of (b, h) as B operands, two k16 steps in one
@@ -789,25 +677,43 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 constexpr int MAX_SEGMENTS = 131072;
+constexpr int TC_ABOVE = 16;           // more query rows of a kv head than these go to the tensor-core kernel
+
+// The scratch memory's segment list and partial sums for `rows` per tile.
+bool place_partials(AttnParams &p, unsigned char *scratch, int rows, int D) {
+    p.seg = reinterpret_cast<int2 *>(scratch);
+    p.part_ml = reinterpret_cast<float *>(scratch + size_t(MAX_SEGMENTS) * sizeof(int2));
+    p.part_o = p.part_ml + size_t(p.ctas) * 2 * rows * 2;
+    return size_t(reinterpret_cast<unsigned char *>(p.part_o + size_t(p.ctas) * 2 * rows * D) - scratch) <=
+           sk::SCRATCH_BYTES;
+}
+
+template <int D>
+sk_status join(const AttnParams &p, int tile_rows, cudaStream_t s) {
+    const long long rows = (long long)p.B * p.heads * p.M * p.G;
+    return sk::launch_pdl(kv4_join_kernel<D>, dim3(unsigned(rows)), dim3(JT), size_t(p.ctas) * 4, s, p, p.ctas,
+                          tile_rows) == cudaSuccess
+               ? SK_OK
+               : SK_ERR_CUDA;
+}
 
 template <int D, int NR>
 sk_status attend(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     using C = Cfg<D, NR>;
     p.ctas = sms * C::CTAS;
-    p.seg = reinterpret_cast<int2 *>(scratch);
-    p.part_ml = reinterpret_cast<float *>(scratch + size_t(MAX_SEGMENTS) * sizeof(int2));
-    p.part_o = p.part_ml + size_t(p.ctas) * 2 * C::ROWS * 2;
-    if (size_t(reinterpret_cast<unsigned char *>(p.part_o + size_t(p.ctas) * 2 * C::ROWS * D) - scratch) >
-        sk::SCRATCH_BYTES)
-        return SK_ERR_WORKSPACE;
+    if (!place_partials(p, scratch, C::ROWS, D)) return SK_ERR_WORKSPACE;
     if (sk::prepare_kernel<kv4_attention_kernel<D, NR>>(C::SMEM) != cudaSuccess) return SK_ERR_CUDA;
     if (sk::launch_pdl(kv4_attention_kernel<D, NR>, dim3(p.ctas), dim3(CT), C::SMEM, s, p) != cudaSuccess)
         return SK_ERR_CUDA;
-    const long long rows = (long long)p.B * p.heads * p.M * p.G;
-    return sk::launch_pdl(kv4_join_kernel<D>, dim3(unsigned(rows)), dim3(JT), size_t(p.ctas) * 4, s, p, p.ctas,
-                          int(C::ROWS)) == cudaSuccess
-               ? SK_OK
-               : SK_ERR_CUDA;
+    return join<D>(p, C::ROWS, s);
+}
+
+sk_status attend_tc(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
+    const int n = tc_rows(p.M * p.G, &p.RT), rows = n < 32 ? 32 : n;
+    p.ctas = sms * TC_CTAS;
+    if (!place_partials(p, scratch, rows, 128)) return SK_ERR_WORKSPACE;
+    if (launch_tc(p, rows, s) != cudaSuccess) return SK_ERR_CUDA;
+    return join<128>(p, rows, s);
 }
 
 template <int D>
@@ -819,7 +725,8 @@ sk_status run(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     p.RT = (tiles + MOST - 1) / MOST;
     const int nr = (tiles + p.RT - 1) / p.RT;
     sk_status st;
-    if (nr == 1) st = attend<D, 1>(p, scratch, sms, s);
+    if (D == 128 && p.M * p.G > TC_ABOVE) st = attend_tc(p, scratch, sms, s);
+    else if (nr == 1) st = attend<D, 1>(p, scratch, sms, s);
     else if (nr == 2) st = attend<D, 2>(p, scratch, sms, s);
     else if constexpr (MOST == 4) st = nr == 3 ? attend<D, 3>(p, scratch, sms, s) : attend<D, 4>(p, scratch, sms, s);
     else return SK_ERR_UNSUPPORTED_SHAPE;

@@ -1,0 +1,472 @@
+// kv4_attention_tc.cu -- the attention over the 4-bit cache for many query rows
+// per kv head (verify rounds over grouped heads), on the fifth-generation
+// tensor cores.  Head size 128.
+//
+// With the positions as the 128-wide operand and the N query rows as the
+// narrow one, a tile of 128 positions is two products:
+//     S (128 x N, TMEM)  = K (128 x 128) . q^T       A: keys decoded into TMEM
+//     O (128 x N, TMEM) += V^T (128 x 128) . p^T     A: values decoded into
+//                                                    shared memory, read along d
+// so decoded keys never pass through shared memory, and both accumulators are
+// N columns.  A thread of the softmax holds one position: the row references
+// are the same for all threads and move rarely (kv4_attention.cuh), and the sums
+// of the weights are added up across positions once per segment.  Two CTAs
+// share an SM: one's decoding covers the other's products and softmax.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/skinny.h"
+#include "internal.h"
+#include "kv4_attention.cuh"
+#include "launch_util.cuh"
+
+namespace {
+
+using namespace sk::attn;
+
+constexpr int D = 128;
+constexpr int TT = 256;                // threads: eight warps
+constexpr int REC = sk::kv4_rec_bytes(D);
+constexpr int HALF = 4 * REC;          // half a tile's records: the unit of the ring
+
+template <int N>
+struct Tc {
+    static constexpr int HALVES = N <= 64 ? 4 : 3;
+    static constexpr int V = 0, Q = V + 128 * D * 2, P = Q + N * D * 2, RAW = P + N * 128 * 2, SMALL = RAW + HALVES * HALF;
+    // per row: reference, P_SHIFT minus it, the score that passes it, a factor, the first unseen position; four
+    // warps' values of each row; barriers of the ring and of the two products; the TMEM address
+    static constexpr int REF = SMALL, OFF = REF + 4 * N, HIGH = OFF + 4 * N, FAC = HIGH + 4 * N, LIM = FAC + 4 * N,
+                         WARP = LIM + 4 * N, BARS = WARP + 16 * N, TMEM = BARS + 8 * (HALVES + 2);
+    static constexpr size_t SMEM = 1024 + TMEM + 16;
+    static constexpr int S_COL = 64, O_COL = 64 + N;         // TMEM columns: keys 0..63, S, O
+    static_assert(O_COL + N <= 256, "half of the TMEM");
+};
+
+// ------------------------------------------------------- tcgen05 ----------
+
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Shared-memory operand: start address, the two strides, swizzle (0 none, 2 of
+// 128 bytes).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride, uint64_t swizzle) {
+    return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((lead >> 4) & 0x3FFFu) << 16) |
+           (uint64_t((stride >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (swizzle << 61);
+}
+// D (FP32) of M = 128, N columns, FP16 operands; bits 15 and 16: A and B stored
+// along M and N.
+__host__ __device__ constexpr uint32_t shape(int n, bool a_along_m, bool b_along_n) {
+    return (1u << 4) | (uint32_t(a_along_m) << 15) | (uint32_t(b_along_n) << 16) | (uint32_t(n >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)) : "memory");
+}
+__device__ __forceinline__ void mma_smem_a(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)) : "memory");
+}
+// Arrive on `bar` when the products issued so far by this thread are done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Eight columns of this warp's 32 lanes.
+__device__ __forceinline__ void ld8(uint32_t addr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr) : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void st8(uint32_t addr, const float (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};"
+                 ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "r"(addr)
+                 : "memory");
+}
+// Sixteen lanes x 64 columns: lane (g, t) of the warp gives columns 8 j + 2 t and
+// 8 j + 2 t + 1 of rows g (v[4 j], v[4 j + 1]) and g + 8 (v[4 j + 2], v[4 j + 3]).
+__device__ __forceinline__ void st_16x64(uint32_t addr, const uint32_t (&v)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x8.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+                 ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+                 "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
+                 "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
+                 "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ uint32_t scale_pair(uint32_t codes) {      // as in kv4_attention.cu: NaN becomes zero
+    const uint32_t s = sk::e4m3x2_h_to_f16x2(uint16_t(codes));
+    uint32_t d;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(s), "r"(0u));
+    return d;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Keys of the record at `rec` (shared memory) into 16 lanes of TMEM.  A lane
+// decodes 32 components of positions g and g + 8 (components 32 t on); column
+// 8 j + 2 t + x takes components 32 t + 4 j + 2 x and the next, the order in
+// which load_q places the query rows.
+__device__ __forceinline__ void decode_keys(uint32_t rec, uint32_t tmem, int g, int t) {
+    uint32_t v[32];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const int i = g + 8 * y;
+        const uint4 k = sk::ld_shared_v4(rec + i * 64 + t * 16);
+        const uint32_t s = scale_pair(sk::ld_shared_u16(rec + 8 * D + i * 8 + t * 2));
+        const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t d[4];
+            sk::e2m1x8_to_f16x2x4(w[q], d);
+            const uint32_t sc = q < 2 ? sk::bcast_lo(s) : sk::bcast_hi(s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int pair = 4 * q + e;                  // = 2 j + x
+                v[4 * (pair >> 1) + 2 * y + (pair & 1)] = sk::hmul2(d[e], sc);
+            }
+        }
+    }
+    st_16x64(tmem, v);
+}
+
+// Values of a record (positions pos0 .. pos0 + 15 of the tile) to the operand
+// of the second product: 64 components (128 bytes) of a position in a row, eight
+// positions an atom of 1024 bytes whose 16-byte pieces are swizzled, the upper
+// 64 components 16 KB further.
+__device__ __forceinline__ void decode_values(uint32_t rec, uint32_t vbase, int pos0, int lane) {
+    const int blk = lane >> 2, pair = (lane & 3) * 2;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+        const uint4 c = sk::ld_shared_v4(rec + 9 * D + hf * 4 * D + lane * 16);
+        const uint32_t s = scale_pair(sk::ld_shared_u16(rec + 17 * D + blk * 16 + hf * 8 + pair));
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {                        // the two positions
+            const uint32_t sc = y ? sk::bcast_hi(s) : sk::bcast_lo(s);
+            const int row = pair + y;
+            const uint32_t at = vbase + (blk >> 2) * 16384 + ((pos0 >> 3) + hf) * 1024 + row * 128;
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                uint32_t d[4];
+                sk::e2m1x8_to_f16x2x4(w[2 * y + z], d);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[e] = sk::hmul2(d[e], sc);
+                st_shared_v4(at + ((((blk & 3) * 2 + z) ^ row) << 4), d[0], d[1], d[2], d[3]);
+            }
+        }
+    }
+}
+
+template <int N>
+__global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_constant__ AttnParams p) {
+    using C = Tc<N>;
+    constexpr int NH = N / 2, HALVES = C::HALVES;            // columns per thread; halves in the ring
+    extern __shared__ unsigned char dyn[];
+    __shared__ long long sm_share[TT / 32 + 4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int quad = warp & 3, side = warp >> 2;             // this warp's TMEM lanes and its half of the columns
+    const uint32_t base = (sk::smem_u32(dyn) + 1023u) & ~1023u;
+    unsigned char *const smem = dyn + (base - sk::smem_u32(dyn));
+    float *const ref = reinterpret_cast<float *>(smem + C::REF), *const off = reinterpret_cast<float *>(smem + C::OFF);
+    float *const high = reinterpret_cast<float *>(smem + C::HIGH), *const fac = reinterpret_cast<float *>(smem + C::FAC);
+    int *const lim = reinterpret_cast<int *>(smem + C::LIM);
+    float *const of_warp = reinterpret_cast<float *>(smem + C::WARP);
+    const uint32_t bars = base + C::BARS, bar_s = bars + 8 * HALVES, bar_o = bar_s + 8;
+
+    if (warp == 0) tmem_alloc(base + C::TMEM, 256);
+    if (tid == 0) {
+        for (int i = 0; i < HALVES + 2; ++i) sk::mbar_init(bars + 8 * i, 1);
+        sk::fence_barrier_init();
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::TMEM);
+    const uint32_t my_lanes = tmem + (uint32_t(quad * 32) << 16);
+    sk::pdl_launch_dependents();
+    sk::pdl_wait_primary();
+    Share sh = share_of(p, p.heads * p.RT, sm_share);
+    uint32_t half0 = 0, ph_s = 0, ph_o = 0;                  // halves consumed; parities of the two products' barriers
+    bool dead = false;
+
+    while (sh.t < sh.end && sh.b < p.B) {
+        const int len = length_of(p, sh.b), nt = tiles_of(len);
+        if (nt == 0) {
+            ++sh.b;
+            continue;
+        }
+        const int hr = int(sh.off / nt), t_lo = int(sh.off - (long long)hr * nt);
+        const int t_hi = int(min((long long)nt, t_lo + sh.end - sh.t));
+        const int h = hr / p.RT, rt = hr - h * p.RT, b = sh.b, tiles = t_hi - t_lo;
+        const int32_t *table = p.table + (long long)b * p.width;
+        const int nrec = (len + 15) / 16, rec0 = t_lo * 8;
+
+        // Records of halves j0 and on, a lane a record (warp 0).
+        auto lookup = [&](int j0) {
+            const int rec = rec0 + 4 * (j0 + (lane >> 2)) + (lane & 3);
+            return sk::kv4_record(table, min(rec, nrec - 1), p.recs, p.by_recs, p.pages, p.heads, h);
+        };
+        auto issue = [&](int j0, int n, uint32_t idx) {      // n halves from j0 on, records idx
+            const int j = j0 + (lane >> 2), rec = rec0 + 4 * j + (lane & 3);
+            const bool in = lane < 4 * n && j < 2 * tiles, load = in && rec < nrec;
+            const uint32_t slot = (half0 + uint32_t(j)) % HALVES, bar = bars + 8 * slot;
+            const unsigned int mask = __ballot_sync(0xffffffffu, load);
+            if (in && (lane & 3) == 0) sk::mbar_arrive_expect_tx(bar, __popc((mask >> lane) & 15u) * REC);
+            __syncwarp();
+            if (load)
+                sk::bulk_load(base + C::RAW + slot * HALF + (lane & 3) * REC, p.cache + size_t(idx) * REC, REC, bar);
+        };
+        uint32_t soon = 0;
+        if (warp == 0) {
+            issue(0, HALVES, lookup(0));
+            soon = lookup(HALVES);
+        }
+        // rows: query, reference, first unseen position
+        for (int i = tid; i < N * 32; i += TT) {
+            const int n = i >> 5, c = i & 31, row = rt * N + n, m = row / p.G;      // eight bytes: j = c / 4, t = c % 4
+            uint2 v = make_uint2(0u, 0u);
+            if (m < p.M)
+                v = *reinterpret_cast<const uint2 *>(p.q + ((long long)b * p.M + m) * p.q_stride +
+                                                      (long long)(h * p.G + row - m * p.G) * D + 32 * (c & 3) + 4 * (c >> 2));
+            const int kb = 8 * c, w = kb & 127;
+            *reinterpret_cast<uint2 *>(smem + C::Q + (kb >> 7) * (N * 128) + (n >> 3) * 1024 + (n & 7) * 128 +
+                                       ((((w >> 4) ^ (n & 7)) << 4) | (w & 15))) = v;
+        }
+        for (int n = tid; n < N; n += TT) {
+            ref[n] = high[n] = NEG_INF;
+            off[n] = 0.f;
+            lim[n] = len - (p.M - 1 - min((rt * N + n) / p.G, p.M - 1));
+        }
+        float l[NH];
+#pragma unroll
+        for (int i = 0; i < NH; ++i) l[i] = 0.f;
+        fence_async_smem();
+        __syncthreads();
+
+        for (int i = 0; i < tiles; ++i) {
+            const uint32_t h0 = half0 + 2 * i, h1 = h0 + 1;
+            const uint32_t raw0 = base + C::RAW + (h0 % HALVES) * HALF, raw1 = base + C::RAW + (h1 % HALVES) * HALF;
+            sk::wait_full(bars + 8 * (h0 % HALVES), (h0 / HALVES) & 1, p.err, dead);
+            sk::wait_full(bars + 8 * (h1 % HALVES), (h1 / HALVES) & 1, p.err, dead);
+            // ---- S = K . q^T
+            {
+                const int r = 2 * quad + side;               // record, in this warp's lanes
+                decode_keys((r < 4 ? raw0 : raw1) + (r & 3) * REC, tmem + (uint32_t(16 * r) << 16), g, t);
+                wait_st();
+            }
+            fence_before();
+            __syncthreads();
+            if (tid == 0) {
+                fence_after();
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_tmem_a(tmem + C::S_COL, tmem + 8 * s,
+                               operand(base + C::Q + (s >> 2) * (N * 128) + (s & 3) * 32, 16, 1024, 2), shape(N, false, false),
+                               s > 0);
+                commit(bar_s);
+            }
+            // ---- V, once the last tile's second product has read its own
+            if (i > 0) {
+                sk::wait_full(bar_o, ph_o, p.err, dead);
+                ph_o ^= 1;
+                fence_after();
+            }
+            decode_values((warp < 4 ? raw0 : raw1) + (warp & 3) * REC, base + C::V, warp * 16, lane);
+            // ---- has any score passed its row's reference?
+            sk::wait_full(bar_s, ph_s, p.err, dead);
+            ph_s ^= 1;
+            fence_after();
+            const int at = quad * 32 + lane, pos = (t_lo + i) * TILE + at;
+            const bool edge = (t_lo + i + 1) * TILE > len - (p.M - 1);
+            const uint32_t s_addr = my_lanes + C::S_COL + side * NH;
+            bool rise = false;
+#pragma unroll
+            for (int c = 0; c < NH; c += 8) {
+                float s[8];
+                ld8(s_addr + c, s);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int n = side * NH + c + e;
+                    rise |= s[e] > high[n] && (!edge || pos < lim[n]);
+                }
+            }
+            const bool any = __syncthreads_or(rise);         // the ring's records are decoded, too
+            if (warp == 0) {
+                issue(2 * i + HALVES, 2, soon);
+                soon = lookup(2 * (i + 1) + HALVES);
+            }
+            if (any) {
+#pragma unroll
+                for (int c = 0; c < NH; c += 8) {
+                    float s[8];
+                    ld8(s_addr + c, s);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int n = side * NH + c + e;
+                        float m = edge && pos >= lim[n] ? NEG_INF : s[e];
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        if (lane == 0) of_warp[quad * N + n] = m;
+                    }
+                }
+                __syncthreads();
+                for (int n = tid; n < N; n += TT) {
+                    const float m = fmaxf(fmaxf(of_warp[n], of_warp[N + n]), fmaxf(of_warp[2 * N + n], of_warp[3 * N + n]));
+                    const float r = fmaxf(ref[n], m * p.scale2);
+                    fac[n] = ref[n] == r ? 1.f : ex2(ref[n] - r);
+                    ref[n] = r;
+                    off[n] = r == NEG_INF ? 0.f : P_SHIFT - r;
+                    high[n] = (r + SLACK) / p.scale2;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int c = 0; c < NH; c += 8) {
+                    float f[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        f[e] = fac[side * NH + c + e];
+                        l[c + e] *= f[e];
+                    }
+                    if (i > 0) {
+                        float o[8];
+                        ld8(my_lanes + C::O_COL + side * NH + c, o);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] *= f[e];
+                        st8(my_lanes + C::O_COL + side * NH + c, o);
+                    }
+                }
+                wait_st();
+            }
+            // ---- the weights, to the operand of the second product: eight rows
+            // of a position in 16 bytes, positions 16 bytes apart
+#pragma unroll
+            for (int c = 0; c < NH; c += 8) {
+                float s[8];
+                ld8(s_addr + c, s);
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int n = side * NH + c + e;
+                    s[e] = ex2(fmaf(s[e], p.scale2, off[n]));
+                    if (edge && pos >= lim[n]) s[e] = 0.f;
+                    l[c + e] += s[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = pack_f16(s[2 * e], s[2 * e + 1]);
+                st_shared_v4(base + C::P + (side * NH + c) / 8 * 2048 + at * 16, w[0], w[1], w[2], w[3]);
+            }
+            fence_async_smem();
+            fence_before();
+            __syncthreads();
+            if (tid == 0) {
+                fence_after();
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_smem_a(tmem + C::O_COL, operand(base + C::V + s * 2048, 16384, 1024, 2),
+                               operand(base + C::P + s * 256, 128, 2048, 0), shape(N, true, true), i > 0 || s > 0);
+                commit(bar_o);
+            }
+        }
+        half0 += 2 * tiles;
+
+        // ---- the rows' sums over the positions, then the outputs
+#pragma unroll
+        for (int c = 0; c < NH; ++c) {
+            float v = l[c];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == 0) of_warp[quad * N + side * NH + c] = v;
+        }
+        sk::wait_full(bar_o, ph_o, p.err, dead);
+        ph_o ^= 1;
+        fence_after();
+        __syncthreads();
+        const bool whole = t_lo == 0 && t_hi == nt;
+        const int rows = min(N, p.M * p.G - rt * N), d = quad * 32 + lane;
+        const size_t slot = size_t(blockIdx.x) * 2 + (t_lo == 0 ? 1 : 0);
+#pragma unroll
+        for (int c = 0; c < NH; c += 8) {
+            float o[8];
+            ld8(my_lanes + C::O_COL + side * NH + c, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int n = side * NH + c + e;
+                if (n >= rows) continue;
+                const float sum = (of_warp[n] + of_warp[N + n]) + (of_warp[2 * N + n] + of_warp[3 * N + n]);
+                if (whole) {
+                    const int row = rt * N + n, m = row / p.G;
+                    const long long to = ((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G;
+                    p.out[to * D + d] = __float2half_rn(sum == 0.f ? 0.f : o[e] * (p.vg / sum));
+                    if (d == 0 && p.lse) p.lse[to] = sum == 0.f ? NEG_INF : (ref[n] + __log2f(sum) - P_SHIFT) * LN2;
+                } else {
+                    p.part_o[(slot * N + n) * D + d] = o[e];
+                    if (d == 0) *reinterpret_cast<float2 *>(p.part_ml + (slot * N + n) * 2) = make_float2(ref[n], sum);
+                }
+            }
+        }
+        if (tid == 0 && t_lo == 0) {
+            const long long last = sh.t + nt - 1;     // the segment's last tile
+            const int c1 = int(((last + 1) * sh.parts - 1) / sh.total);
+            p.seg[((long long)b * p.heads + h) * p.RT + rt] = make_int2(int(blockIdx.x), whole ? 0 : c1 - int(blockIdx.x) + 1);
+        }
+        fence_before();
+        __syncthreads();
+        fence_after();
+        sh.t += t_hi - t_lo;
+        sh.off += t_hi - t_lo;
+        if (sh.off == (long long)nt * p.heads * p.RT) {
+            ++sh.b;
+            sh.off = 0;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) tmem_free(tmem, 256);
+}
+
+template <int N>
+cudaError_t launch(AttnParams &p, cudaStream_t s) {
+    const cudaError_t e = sk::prepare_kernel<kv4_attention_tc_kernel<N>>(Tc<N>::SMEM);
+    if (e != cudaSuccess) return e;
+    return sk::launch_pdl(kv4_attention_tc_kernel<N>, dim3(p.ctas), dim3(TT), Tc<N>::SMEM, s, p);
+}
+
+}  // namespace
+
+namespace sk {
+namespace attn {
+
+int tc_rows(int rows, int *tiles) {
+    *tiles = (rows + TC_MOST - 1) / TC_MOST;
+    const int each = (rows + *tiles - 1) / *tiles;
+    return (each + 15) / 16 * 16;
+}
+
+cudaError_t launch_tc(AttnParams &p, int n, cudaStream_t s) {
+    switch (n) {
+        case 16: case 32: return launch<32>(p, s);
+        case 48: return launch<48>(p, s);
+        case 64: return launch<64>(p, s);
+        case 80: return launch<80>(p, s);
+        default: return launch<96>(p, s);
+    }
+}
+
+}  // namespace attn
+}  // namespace sk

@@ -22,11 +22,11 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // moved only when a score passes it by more than SLACK (then the sums so far
 // are scaled).  Most steps need neither the row's maximum across lanes nor a
 // rescaling.  The p go to the second product in FP16, at most 2^(P_SHIFT +
-// SLACK) = 2^15 and normal down to 2^-24 of r's.  Their rounding (2^-11
-// relative at most, independent from position to position) is of the size of
-// the output's own rounding to FP16; the sum of the weights is taken from the
-// unrounded FP32 values.
-constexpr float P_SHIFT = 10.f, SLACK = 5.f;
+// SLACK) = 2^15 and normal down to 2^-21 of r's (2^-32 is the rounding of the
+// smaller ones).  Their rounding (2^-11 relative at most, independent from
+// position to position) is of the size of the output's own rounding to FP16;
+// the sum of the weights is taken from the unrounded FP32 values.
+constexpr float P_SHIFT = 7.f, SLACK = 8.f;
 
 struct AttnParams {
     const __half *q;

@@ -109,6 +109,19 @@ __device__ __forceinline__ void st_16x64(uint32_t addr, const uint32_t (&v)[32])
                  "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(addr) : "memory");
 }
 
+// Eight rows' numbers from shared memory.
+__device__ __forceinline__ void row8(const float *p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = a.z;
+    v[3] = a.w;
+    v[4] = b.x;
+    v[5] = b.y;
+    v[6] = b.z;
+    v[7] = b.w;
+}
+
 __device__ __forceinline__ uint32_t scale_pair(uint32_t codes) {      // as in kv4_attention.cu: NaN becomes zero
     const uint32_t s = sk::e4m3x2_h_to_f16x2(uint16_t(codes));
     uint32_t d;
@@ -294,18 +307,28 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             ph_s ^= 1;
             fence_after();
             const int at = quad * 32 + lane, pos = (t_lo + i) * TILE + at;
-            const bool edge = (t_lo + i + 1) * TILE > len - (p.M - 1);
             const uint32_t s_addr = my_lanes + C::S_COL + side * NH;
-            bool rise = false;
+            if ((t_lo + i + 1) * TILE > len - (p.M - 1)) {
+                // the tile's end: scores that their rows do not see, in place
+#pragma unroll 1
+                for (int c = 0; c < NH; c += 8) {
+                    float s[8];
+                    ld8(s_addr + c, s);
 #pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (pos >= lim[side * NH + c + e]) s[e] = NEG_INF;
+                    st8(s_addr + c, s);
+                }
+                wait_st();
+            }
+            bool rise = false;
+#pragma unroll 1
             for (int c = 0; c < NH; c += 8) {
-                float s[8];
+                float s[8], hi[8];
+                row8(high + side * NH + c, hi);
                 ld8(s_addr + c, s);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int n = side * NH + c + e;
-                    rise |= s[e] > high[n] && (!edge || pos < lim[n]);
-                }
+                for (int e = 0; e < 8; ++e) rise |= s[e] > hi[e];
             }
             const bool any = __syncthreads_or(rise);         // the ring's records are decoded, too
             if (warp == 0) {
@@ -313,17 +336,15 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                 soon = lookup(2 * (i + 1) + HALVES);
             }
             if (any) {
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < NH; c += 8) {
                     float s[8];
                     ld8(s_addr + c, s);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const int n = side * NH + c + e;
-                        float m = edge && pos >= lim[n] ? NEG_INF : s[e];
 #pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        if (lane == 0) of_warp[quad * N + n] = m;
+                        for (int o = 1; o < 32; o <<= 1) s[e] = fmaxf(s[e], __shfl_xor_sync(0xffffffffu, s[e], o));
+                        if (lane == 0) of_warp[quad * N + side * NH + c + e] = s[e];
                     }
                 }
                 __syncthreads();
@@ -336,36 +357,31 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                     high[n] = (r + SLACK) / p.scale2;
                 }
                 __syncthreads();
+                if (i > 0) {
 #pragma unroll
-                for (int c = 0; c < NH; c += 8) {
-                    float f[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        f[e] = fac[side * NH + c + e];
-                        l[c + e] *= f[e];
-                    }
-                    if (i > 0) {
+                    for (int c = 0; c < NH; ++c) l[c] *= fac[side * NH + c];
+#pragma unroll 1
+                    for (int c = 0; c < NH; c += 8) {
                         float o[8];
                         ld8(my_lanes + C::O_COL + side * NH + c, o);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] *= f[e];
+                        for (int e = 0; e < 8; ++e) o[e] *= fac[side * NH + c + e];
                         st8(my_lanes + C::O_COL + side * NH + c, o);
                     }
+                    wait_st();
                 }
-                wait_st();
             }
             // ---- the weights, to the operand of the second product: eight rows
             // of a position in 16 bytes, positions 16 bytes apart
 #pragma unroll
             for (int c = 0; c < NH; c += 8) {
-                float s[8];
+                float s[8], of[8];
+                row8(off + side * NH + c, of);
                 ld8(s_addr + c, s);
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int n = side * NH + c + e;
-                    s[e] = ex2(fmaf(s[e], p.scale2, off[n]));
-                    if (edge && pos >= lim[n]) s[e] = 0.f;
+                    s[e] = ex2(fmaf(s[e], p.scale2, of[e]));
                     l[c + e] += s[e];
                 }
 #pragma unroll
@@ -387,12 +403,25 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
         half0 += 2 * tiles;
 
         // ---- the rows' sums over the positions, then the outputs
+        // (a warp's 32 positions, eight rows at a time, halving what a lane
+        // keeps: lanes 4 i .. 4 i + 3 end with row i)
 #pragma unroll
-        for (int c = 0; c < NH; ++c) {
-            float v = l[c];
+        for (int c = 0; c < NH; c += 8) {
+            float v[8];
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (lane == 0) of_warp[quad * N + side * NH + c] = v;
+            for (int e = 0; e < 8; ++e) v[e] = l[c + e];
+#pragma unroll
+            for (int half = 4, o = 16; half >= 1; half >>= 1, o >>= 1) {
+                const bool up = lane & o;
+#pragma unroll
+                for (int e = 0; e < half; ++e) {
+                    const float give = up ? v[e] : v[e + half], keep = up ? v[e + half] : v[e];
+                    v[e] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+            }
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+            if ((lane & 3) == 0) of_warp[quad * N + side * NH + c + (lane >> 2)] = v[0];
         }
         sk::wait_full(bar_o, ph_o, p.err, dead);
         ph_o ^= 1;
@@ -401,24 +430,32 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
         const bool whole = t_lo == 0 && t_hi == nt;
         const int rows = min(N, p.M * p.G - rt * N), d = quad * 32 + lane;
         const size_t slot = size_t(blockIdx.x) * 2 + (t_lo == 0 ? 1 : 0);
-#pragma unroll
+        // row n's sum, and what its output is multiplied by
+        for (int n = tid; n < rows; n += TT) {
+            const float sum = (of_warp[n] + of_warp[N + n]) + (of_warp[2 * N + n] + of_warp[3 * N + n]);
+            fac[n] = sum == 0.f ? 0.f : p.vg / sum;
+            if (whole) {
+                const int row = rt * N + n, m = row / p.G;
+                const long long to = ((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G;
+                lim[n] = int(to - ((long long)b * p.M * p.heads * p.G));       // the row within its sequence
+                if (p.lse) p.lse[to] = sum == 0.f ? NEG_INF : (ref[n] + __log2f(sum) - P_SHIFT) * LN2;
+            } else {
+                *reinterpret_cast<float2 *>(p.part_ml + (slot * N + n) * 2) = make_float2(ref[n], sum);
+            }
+        }
+        __syncthreads();
+        __half *const out = p.out + (long long)b * p.M * p.heads * p.G * D + d;
+        float *const part = p.part_o + slot * N * D + d;
+#pragma unroll 1
         for (int c = 0; c < NH; c += 8) {
             float o[8];
             ld8(my_lanes + C::O_COL + side * NH + c, o);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int n = side * NH + c + e;
-                if (n >= rows) continue;
-                const float sum = (of_warp[n] + of_warp[N + n]) + (of_warp[2 * N + n] + of_warp[3 * N + n]);
-                if (whole) {
-                    const int row = rt * N + n, m = row / p.G;
-                    const long long to = ((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G;
-                    p.out[to * D + d] = __float2half_rn(sum == 0.f ? 0.f : o[e] * (p.vg / sum));
-                    if (d == 0 && p.lse) p.lse[to] = sum == 0.f ? NEG_INF : (ref[n] + __log2f(sum) - P_SHIFT) * LN2;
-                } else {
-                    p.part_o[(slot * N + n) * D + d] = o[e];
-                    if (d == 0) *reinterpret_cast<float2 *>(p.part_ml + (slot * N + n) * 2) = make_float2(ref[n], sum);
-                }
+                if (n >= rows) break;
+                if (whole) out[(long long)lim[n] * D] = __float2half_rn(o[e] * fac[n]);
+                else part[n * D] = o[e];
             }
         }
         if (tid == 0 && t_lo == 0) {

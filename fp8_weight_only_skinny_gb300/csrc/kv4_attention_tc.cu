@@ -83,6 +83,22 @@ __device__ __forceinline__ void mma_smem_a(uint32_t d, uint64_t a, uint64_t b, u
 __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+// NH columns of this warp's 32 lanes, all loads in flight together.
+template <int NH>
+__device__ __forceinline__ void ld_row(uint32_t addr, float (&v)[NH]) {
+#pragma unroll
+    for (int c = 0; c < NH; c += 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=f"(v[c]), "=f"(v[c + 1]), "=f"(v[c + 2]), "=f"(v[c + 3]), "=f"(v[c + 4]), "=f"(v[c + 5]),
+                       "=f"(v[c + 6]), "=f"(v[c + 7])
+                     : "r"(addr + c) : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    // no use of the values is moved ahead of the wait
+#pragma unroll
+    for (int c = 0; c < NH; c += 8)
+        asm volatile("" : "+f"(v[c]), "+f"(v[c + 1]), "+f"(v[c + 2]), "+f"(v[c + 3]), "+f"(v[c + 4]), "+f"(v[c + 5]),
+                          "+f"(v[c + 6]), "+f"(v[c + 7]));
+}
 // Eight columns of this warp's 32 lanes.
 __device__ __forceinline__ void ld8(uint32_t addr, float (&v)[8]) {
     uint32_t r[8];
@@ -307,28 +323,21 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             ph_s ^= 1;
             fence_after();
             const int at = quad * 32 + lane, pos = (t_lo + i) * TILE + at;
-            const uint32_t s_addr = my_lanes + C::S_COL + side * NH;
+            float s[NH];
+            ld_row<NH>(my_lanes + C::S_COL + side * NH, s);
             if ((t_lo + i + 1) * TILE > len - (p.M - 1)) {
-                // the tile's end: scores that their rows do not see, in place
-#pragma unroll 1
-                for (int c = 0; c < NH; c += 8) {
-                    float s[8];
-                    ld8(s_addr + c, s);
+                // the tile's end: scores that their rows do not see
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (pos >= lim[side * NH + c + e]) s[e] = NEG_INF;
-                    st8(s_addr + c, s);
-                }
-                wait_st();
+                for (int c = 0; c < NH; ++c)
+                    if (pos >= lim[side * NH + c]) s[c] = NEG_INF;
             }
             bool rise = false;
-#pragma unroll 1
-            for (int c = 0; c < NH; c += 8) {
-                float s[8], hi[8];
-                row8(high + side * NH + c, hi);
-                ld8(s_addr + c, s);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) rise |= s[e] > hi[e];
+            for (int c = 0; c < NH; c += 8) {
+                float hi[8];
+                row8(high + side * NH + c, hi);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) rise |= s[c + e] > hi[e];
             }
             const bool any = __syncthreads_or(rise);         // the ring's records are decoded, too
             if (warp == 0) {
@@ -336,16 +345,25 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                 soon = lookup(2 * (i + 1) + HALVES);
             }
             if (any) {
-#pragma unroll 1
+                // each row's maximum over this warp's positions, eight rows at a
+                // time, halving what a lane keeps: lanes 4 i .. 4 i + 3 end with row i
+#pragma unroll
                 for (int c = 0; c < NH; c += 8) {
-                    float s[8];
-                    ld8(s_addr + c, s);
+                    float v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < 8; ++e) v[e] = s[c + e];
 #pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) s[e] = fmaxf(s[e], __shfl_xor_sync(0xffffffffu, s[e], o));
-                        if (lane == 0) of_warp[quad * N + side * NH + c + e] = s[e];
+                    for (int half = 4, o = 16; half >= 1; half >>= 1, o >>= 1) {
+                        const bool up = lane & o;
+#pragma unroll
+                        for (int e = 0; e < half; ++e) {
+                            const float give = up ? v[e] : v[e + half], keep = up ? v[e + half] : v[e];
+                            v[e] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
+                        }
                     }
+                    v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
+                    v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+                    if ((lane & 3) == 0) of_warp[quad * N + side * NH + c + (lane >> 2)] = v[0];
                 }
                 __syncthreads();
                 for (int n = tid; n < N; n += TT) {
@@ -375,17 +393,16 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             // of a position in 16 bytes, positions 16 bytes apart
 #pragma unroll
             for (int c = 0; c < NH; c += 8) {
-                float s[8], of[8];
+                float of[8];
                 row8(off + side * NH + c, of);
-                ld8(s_addr + c, s);
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    s[e] = ex2(fmaf(s[e], p.scale2, of[e]));
-                    l[c + e] += s[e];
+                    s[c + e] = ex2(fmaf(s[c + e], p.scale2, of[e]));
+                    l[c + e] += s[c + e];
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = pack_f16(s[2 * e], s[2 * e + 1]);
+                for (int e = 0; e < 4; ++e) w[e] = pack_f16(s[c + 2 * e], s[c + 2 * e + 1]);
                 st_shared_v4(base + C::P + (side * NH + c) / 8 * 2048 + at * 16, w[0], w[1], w[2], w[3]);
             }
             fence_async_smem();

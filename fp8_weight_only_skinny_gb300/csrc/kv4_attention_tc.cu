@@ -29,16 +29,19 @@ using namespace sk::attn;
 constexpr int D = 128;
 constexpr int TT = 256;                // threads: eight warps
 constexpr int REC = sk::kv4_rec_bytes(D);
-constexpr int HALF = 4 * REC;          // half a tile's records: the unit of the ring
+constexpr int PART = REC / 2;          // the keys' or the values' half of a record
+constexpr int UNIT = 8 * PART;         // of a tile's eight records: the unit of the ring
+constexpr float MOST_WEIGHT = 32768.f; // 2^(P_SHIFT + SLACK): a larger weight moves its row's reference
+static_assert(P_SHIFT + SLACK == 15.f, "MOST_WEIGHT");
 
 template <int N>
 struct Tc {
-    static constexpr int HALVES = N <= 64 ? 4 : 3;
-    static constexpr int V = 0, Q = V + 128 * D * 2, P = Q + N * D * 2, RAW = P + N * 128 * 2, SMALL = RAW + HALVES * HALF;
-    // per row: reference, P_SHIFT minus it, the score that passes it, a factor, the first unseen position; four
+    static constexpr int UNITS = N <= 64 ? 4 : 3;
+    static constexpr int V = 0, Q = V + 128 * D * 2, P = Q + N * D * 2, RAW = P + N * 128 * 2, SMALL = RAW + UNITS * UNIT;
+    // per row: reference, P_SHIFT minus it, a factor, the first unseen position; four
     // warps' values of each row; barriers of the ring and of the two products; the TMEM address
-    static constexpr int REF = SMALL, OFF = REF + 4 * N, HIGH = OFF + 4 * N, FAC = HIGH + 4 * N, LIM = FAC + 4 * N,
-                         WARP = LIM + 4 * N, BARS = WARP + 16 * N, TMEM = BARS + 8 * (HALVES + 2);
+    static constexpr int REF = SMALL, OFF = REF + 4 * N, FAC = OFF + 4 * N, LIM = FAC + 4 * N,
+                         WARP = LIM + 4 * N, BARS = WARP + 16 * N, TMEM = BARS + 8 * (UNITS + 2);
     static constexpr size_t SMEM = 1024 + TMEM + 16;
     static constexpr int S_COL = 64, O_COL = 64 + N;         // TMEM columns: keys 0..63, S, O
     static_assert(O_COL + N <= 256, "half of the TMEM");
@@ -175,7 +178,7 @@ __device__ __forceinline__ void decode_keys(uint32_t rec, uint32_t tmem, int g, 
     st_16x64(tmem, v);
 }
 
-// Values of a record (positions pos0 .. pos0 + 15 of the tile) to the operand
+// Values of a record (their half of it; positions pos0 .. pos0 + 15 of the tile) to the operand
 // of the second product: 64 components (128 bytes) of a position in a row, eight
 // positions an atom of 1024 bytes whose 16-byte pieces are swizzled, the upper
 // 64 components 16 KB further.
@@ -183,8 +186,8 @@ __device__ __forceinline__ void decode_values(uint32_t rec, uint32_t vbase, int 
     const int blk = lane >> 2, pair = (lane & 3) * 2;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-        const uint4 c = sk::ld_shared_v4(rec + 9 * D + hf * 4 * D + lane * 16);
-        const uint32_t s = scale_pair(sk::ld_shared_u16(rec + 17 * D + blk * 16 + hf * 8 + pair));
+        const uint4 c = sk::ld_shared_v4(rec + hf * 4 * D + lane * 16);
+        const uint32_t s = scale_pair(sk::ld_shared_u16(rec + 8 * D + blk * 16 + hf * 8 + pair));
         const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
         for (int y = 0; y < 2; ++y) {                        // the two positions
@@ -206,7 +209,7 @@ __device__ __forceinline__ void decode_values(uint32_t rec, uint32_t vbase, int 
 template <int N>
 __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_constant__ AttnParams p) {
     using C = Tc<N>;
-    constexpr int NH = N / 2, HALVES = C::HALVES;            // columns per thread; halves in the ring
+    constexpr int NH = N / 2, UNITS = C::UNITS;              // columns per thread; units in the ring
     extern __shared__ unsigned char dyn[];
     __shared__ long long sm_share[TT / 32 + 4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -214,14 +217,14 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
     const uint32_t base = (sk::smem_u32(dyn) + 1023u) & ~1023u;
     unsigned char *const smem = dyn + (base - sk::smem_u32(dyn));
     float *const ref = reinterpret_cast<float *>(smem + C::REF), *const off = reinterpret_cast<float *>(smem + C::OFF);
-    float *const high = reinterpret_cast<float *>(smem + C::HIGH), *const fac = reinterpret_cast<float *>(smem + C::FAC);
+    float *const fac = reinterpret_cast<float *>(smem + C::FAC);
     int *const lim = reinterpret_cast<int *>(smem + C::LIM);
     float *const of_warp = reinterpret_cast<float *>(smem + C::WARP);
-    const uint32_t bars = base + C::BARS, bar_s = bars + 8 * HALVES, bar_o = bar_s + 8;
+    const uint32_t bars = base + C::BARS, bar_s = bars + 8 * UNITS, bar_o = bar_s + 8;
 
     if (warp == 0) tmem_alloc(base + C::TMEM, 256);
     if (tid == 0) {
-        for (int i = 0; i < HALVES + 2; ++i) sk::mbar_init(bars + 8 * i, 1);
+        for (int i = 0; i < UNITS + 2; ++i) sk::mbar_init(bars + 8 * i, 1);
         sk::fence_barrier_init();
     }
     fence_before();
@@ -232,7 +235,10 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
     sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
     Share sh = share_of(p, p.heads * p.RT, sm_share);
-    uint32_t half0 = 0, ph_s = 0, ph_o = 0;                  // halves consumed; parities of the two products' barriers
+    // the products' shared-memory operands at their first k16 step
+    const uint64_t q_op = operand(base + C::Q, 16, 1024, 2), v_op = operand(base + C::V, 16384, 1024, 2),
+                   p_op = operand(base + C::P, 128, 2048, 0);
+    uint32_t unit0 = 0, ph_s = 0, ph_o = 0;                  // units consumed; parities of the two products' barriers
     bool dead = false;
 
     while (sh.t < sh.end && sh.b < p.B) {
@@ -247,25 +253,32 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
         const int32_t *table = p.table + (long long)b * p.width;
         const int nrec = (len + 15) / 16, rec0 = t_lo * 8;
 
-        // Records of halves j0 and on, a lane a record (warp 0).
-        auto lookup = [&](int j0) {
-            const int rec = rec0 + 4 * (j0 + (lane >> 2)) + (lane & 3);
+        // Unit u is the keys (even) or the values (odd) of tile u / 2, whose slot
+        // is free again after the barrier that ends their decoding: every copy
+        // has a tile's time to arrive.  Warp 1 issues them, a lane a record.
+        auto lookup = [&](int tile) {
+            const int rec = rec0 + 8 * tile + (lane & 7);
             return sk::kv4_record(table, min(rec, nrec - 1), p.recs, p.by_recs, p.pages, p.heads, h);
         };
-        auto issue = [&](int j0, int n, uint32_t idx) {      // n halves from j0 on, records idx
-            const int j = j0 + (lane >> 2), rec = rec0 + 4 * j + (lane & 3);
-            const bool in = lane < 4 * n && j < 2 * tiles, load = in && rec < nrec;
-            const uint32_t slot = (half0 + uint32_t(j)) % HALVES, bar = bars + 8 * slot;
+        auto issue = [&](int u, uint32_t idx) {              // idx: the tile's records
+            if (u >= 2 * tiles) return;
+            const bool load = lane < 8 && rec0 + 8 * (u >> 1) + lane < nrec;
+            const uint32_t slot = (unit0 + uint32_t(u)) % UNITS, bar = bars + 8 * slot;
             const unsigned int mask = __ballot_sync(0xffffffffu, load);
-            if (in && (lane & 3) == 0) sk::mbar_arrive_expect_tx(bar, __popc((mask >> lane) & 15u) * REC);
+            if (lane == 0) sk::mbar_arrive_expect_tx(bar, __popc(mask) * PART);
             __syncwarp();
             if (load)
-                sk::bulk_load(base + C::RAW + slot * HALF + (lane & 3) * REC, p.cache + size_t(idx) * REC, REC, bar);
+                sk::bulk_load(base + C::RAW + slot * UNIT + lane * PART, p.cache + size_t(idx) * REC + (u & 1) * PART, PART, bar);
         };
-        uint32_t soon = 0;
-        if (warp == 0) {
-            issue(0, HALVES, lookup(0));
-            soon = lookup(HALVES);
+        uint32_t idx1 = 0, idx2 = 0, idx3 = 0;               // records of the next three tiles
+        if (warp == 1) {
+            const uint32_t idx0 = lookup(0);
+            idx1 = lookup(1);
+            idx2 = lookup(2);
+            issue(0, idx0);
+            issue(1, idx0);
+            issue(2, idx1);
+            if (UNITS == 4) issue(3, idx1);
         }
         // rows: query, reference, first unseen position
         for (int i = tid; i < N * 32; i += TT) {
@@ -279,7 +292,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                                        ((((w >> 4) ^ (n & 7)) << 4) | (w & 15))) = v;
         }
         for (int n = tid; n < N; n += TT) {
-            ref[n] = high[n] = NEG_INF;
+            ref[n] = NEG_INF;
             off[n] = 0.f;
             lim[n] = len - (p.M - 1 - min((rt * N + n) / p.G, p.M - 1));
         }
@@ -290,14 +303,13 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
         __syncthreads();
 
         for (int i = 0; i < tiles; ++i) {
-            const uint32_t h0 = half0 + 2 * i, h1 = h0 + 1;
-            const uint32_t raw0 = base + C::RAW + (h0 % HALVES) * HALF, raw1 = base + C::RAW + (h1 % HALVES) * HALF;
-            sk::wait_full(bars + 8 * (h0 % HALVES), (h0 / HALVES) & 1, p.err, dead);
-            sk::wait_full(bars + 8 * (h1 % HALVES), (h1 / HALVES) & 1, p.err, dead);
+            const uint32_t uk = unit0 + 2 * i, uv = uk + 1;
+            const uint32_t keys = base + C::RAW + (uk % UNITS) * UNIT, vals = base + C::RAW + (uv % UNITS) * UNIT;
             // ---- S = K . q^T
+            sk::wait_full(bars + 8 * (uk % UNITS), (uk / UNITS) & 1, p.err, dead);
             {
                 const int r = 2 * quad + side;               // record, in this warp's lanes
-                decode_keys((r < 4 ? raw0 : raw1) + (r & 3) * REC, tmem + (uint32_t(16 * r) << 16), g, t);
+                decode_keys(keys + r * PART, tmem + (uint32_t(16 * r) << 16), g, t);
                 wait_st();
             }
             fence_before();
@@ -306,10 +318,13 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                 fence_after();
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                    mma_tmem_a(tmem + C::S_COL, tmem + 8 * s,
-                               operand(base + C::Q + (s >> 2) * (N * 128) + (s & 3) * 32, 16, 1024, 2), shape(N, false, false),
-                               s > 0);
+                    mma_tmem_a(tmem + C::S_COL, tmem + 8 * s, q_op + ((s >> 2) * (N * 128) + (s & 3) * 32) / 16,
+                               shape(N, false, false), s > 0);
                 commit(bar_s);
+            }
+            if (warp == 1) {
+                idx3 = lookup(i + 3);
+                issue(2 * i + UNITS, UNITS == 4 ? idx2 : idx1);
             }
             // ---- V, once the last tile's second product has read its own
             if (i > 0) {
@@ -317,36 +332,62 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                 ph_o ^= 1;
                 fence_after();
             }
-            decode_values((warp < 4 ? raw0 : raw1) + (warp & 3) * REC, base + C::V, warp * 16, lane);
-            // ---- has any score passed its row's reference?
+            sk::wait_full(bars + 8 * (uv % UNITS), (uv / UNITS) & 1, p.err, dead);
+            decode_values(vals + warp * PART, base + C::V, warp * 16, lane);
+            // ---- the weights, to the operand of the second product: eight rows
+            // of a position in 16 bytes, positions 16 bytes apart
             sk::wait_full(bar_s, ph_s, p.err, dead);
             ph_s ^= 1;
             fence_after();
             const int at = quad * 32 + lane, pos = (t_lo + i) * TILE + at;
+            const bool edge = (t_lo + i + 1) * TILE > len - (p.M - 1);
             float s[NH];
-            ld_row<NH>(my_lanes + C::S_COL + side * NH, s);
-            if ((t_lo + i + 1) * TILE > len - (p.M - 1)) {
-                // the tile's end: scores that their rows do not see
+            auto scores = [&] {
+                ld_row<NH>(my_lanes + C::S_COL + side * NH, s);
+                if (edge) {
+                    // the tile's end: scores that their rows do not see
 #pragma unroll
-                for (int c = 0; c < NH; ++c)
-                    if (pos >= lim[side * NH + c]) s[c] = NEG_INF;
-            }
-            bool rise = false;
+                    for (int c = 0; c < NH; ++c)
+                        if (pos >= lim[side * NH + c]) s[c] = NEG_INF;
+                }
+            };
+            bool rise = false;                               // whether a score has passed its row's reference
+            auto weigh = [&] {
 #pragma unroll
-            for (int c = 0; c < NH; c += 8) {
-                float hi[8];
-                row8(high + side * NH + c, hi);
+                for (int c = 0; c < NH; c += 8) {
+                    float of[8];
+                    row8(off + side * NH + c, of);
+                    uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) rise |= s[c + e] > hi[e];
+                    for (int e = 0; e < 8; ++e) {
+                        s[c + e] = ex2(fmaf(s[c + e], p.scale2, of[e]));
+                        rise |= s[c + e] > MOST_WEIGHT;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = pack_f16(s[c + 2 * e], s[c + 2 * e + 1]);
+                    st_shared_v4(base + C::P + (side * NH + c) / 8 * 2048 + at * 16, w[0], w[1], w[2], w[3]);
+                }
+                fence_async_smem();
+                fence_before();
+            };
+            scores();
+            if (i > 0) {
+                weigh();
+            } else {
+                rise = true;                                 // no reference yet
             }
             const bool any = __syncthreads_or(rise);         // the ring's records are decoded, too
-            if (warp == 0) {
-                issue(2 * i + HALVES, 2, soon);
-                soon = lookup(2 * (i + 1) + HALVES);
+            if (warp == 1) {
+                issue(2 * i + 1 + UNITS, idx2);
+                idx1 = idx2;
+                idx2 = idx3;
             }
             if (any) {
-                // each row's maximum over this warp's positions, eight rows at a
-                // time, halving what a lane keeps: lanes 4 i .. 4 i + 3 end with row i
+                // move the references: each row's maximum over this warp's
+                // positions first, eight rows at a time, halving what a lane
+                // keeps (lanes 4 i .. 4 i + 3 end with row i)
+                fence_after();
+                if (i > 0) scores();
 #pragma unroll
                 for (int c = 0; c < NH; c += 8) {
                     float v[8];
@@ -368,11 +409,10 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                 __syncthreads();
                 for (int n = tid; n < N; n += TT) {
                     const float m = fmaxf(fmaxf(of_warp[n], of_warp[N + n]), fmaxf(of_warp[2 * N + n], of_warp[3 * N + n]));
-                    const float r = fmaxf(ref[n], m * p.scale2);
+                    const float z = m * p.scale2, r = z > ref[n] + SLACK ? z : ref[n];
                     fac[n] = ref[n] == r ? 1.f : ex2(ref[n] - r);
                     ref[n] = r;
                     off[n] = r == NEG_INF ? 0.f : P_SHIFT - r;
-                    high[n] = (r + SLACK) / p.scale2;
                 }
                 __syncthreads();
                 if (i > 0) {
@@ -388,36 +428,21 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                     }
                     wait_st();
                 }
+                weigh();
+                __syncthreads();
             }
-            // ---- the weights, to the operand of the second product: eight rows
-            // of a position in 16 bytes, positions 16 bytes apart
 #pragma unroll
-            for (int c = 0; c < NH; c += 8) {
-                float of[8];
-                row8(off + side * NH + c, of);
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    s[c + e] = ex2(fmaf(s[c + e], p.scale2, of[e]));
-                    l[c + e] += s[c + e];
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = pack_f16(s[c + 2 * e], s[c + 2 * e + 1]);
-                st_shared_v4(base + C::P + (side * NH + c) / 8 * 2048 + at * 16, w[0], w[1], w[2], w[3]);
-            }
-            fence_async_smem();
-            fence_before();
-            __syncthreads();
+            for (int c = 0; c < NH; ++c) l[c] += s[c];
             if (tid == 0) {
                 fence_after();
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                    mma_smem_a(tmem + C::O_COL, operand(base + C::V + s * 2048, 16384, 1024, 2),
-                               operand(base + C::P + s * 256, 128, 2048, 0), shape(N, true, true), i > 0 || s > 0);
+                    mma_smem_a(tmem + C::O_COL, v_op + s * 2048 / 16, p_op + s * 256 / 16, shape(N, true, true),
+                               i > 0 || s > 0);
                 commit(bar_o);
             }
         }
-        half0 += 2 * tiles;
+        unit0 += 2 * tiles;
 
         // ---- the rows' sums over the positions, then the outputs
         // (a warp's 32 positions, eight rows at a time, halving what a lane

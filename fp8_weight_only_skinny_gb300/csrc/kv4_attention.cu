@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
     using C = Cfg<D, NR>;
     constexpr int ROWS = C::ROWS, NX = C::ACC >= 64 || NR > 2 ? 1 : 2;       // records scored together
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long sm_share[WARPS + 4];
+    __shared__ int sm_share[WARPS + 2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t base = sk::smem_u32(smem);
     const uint32_t qs = base + C::BODY, bars = qs + NR * C::QTILE;
@@ -232,15 +232,14 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
             ++sh.b;
             continue;
         }
-        const int hr = int(sh.off / nt), t_lo = int(sh.off - (long long)hr * nt);
-        const int t_hi = int(min((long long)nt, t_lo + sh.end - sh.t));
+        const int hr = sh.off / nt, t_lo = sh.off - hr * nt;
+        const int t_hi = min(nt, t_lo + sh.end - sh.t);
         const int h = hr / p.RT, rt = hr - h * p.RT, b = sh.b;
         const int32_t *table = p.table + (long long)b * p.width;
         const int nrec = (len + 15) / 16;
 
         // this warp's steps: st0, st0 + WARPS, ... (n of them)
-        const int st_hi = min(t_hi * WARPS, (len + STEP - 1) / STEP);
-        const int st0 = t_lo * WARPS + warp;
+        const int st0 = t_lo * WARPS + warp, st_hi = min(t_hi * WARPS, (len + STEP - 1) / STEP);
         const int n = st0 < st_hi ? (st_hi - st0 + WARPS - 1) / WARPS : 0;
         // Record lookups, 16 steps at a time: lane l holds record l % 2 of step
         // 16 k + l / 2; the next batch is fetched a whole batch early.
@@ -436,51 +435,57 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
             }
         }
         if (tid == 0 && t_lo == 0) {
-            const long long last = sh.t + nt - 1;     // the segment's last tile
-            const int c1 = int(((last + 1) * sh.parts - 1) / sh.total);
-            p.seg[((long long)b * p.heads + h) * p.RT + rt] = make_int2(int(blockIdx.x), whole ? 0 : c1 - int(blockIdx.x) + 1);
+            const int c1 = cta_of(sh, sh.t + nt - 1);     // of the segment's last tile
+            p.seg[(b * p.heads + h) * p.RT + rt] = make_int2(int(blockIdx.x), whole ? 0 : c1 - int(blockIdx.x) + 1);
         }
         // the ring's next copies come after these reads and writes of it
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();
         sh.t += t_hi - t_lo;
         sh.off += t_hi - t_lo;
-        if (sh.off == (long long)nt * p.heads * p.RT) {
+        if (sh.off == nt * p.heads * p.RT) {
             ++sh.b;
             sh.off = 0;
         }
     }
 }
 
-// One CTA per query row: the partial sums of its segment, in the order of the
-// CTAs that wrote them, joined under the common maximum.  Rows of an empty
+// DC components of a query row per CTA: the partial sums of its segment, in the
+// order of the CTAs that wrote them, joined under the common reference.  DC / 4
+// threads take a part at a time, 1024 / DC parts together.  Rows of an empty
 // sequence are written here too (zero, with a log sum of minus infinity).
 constexpr int JT = 256;
 
-template <int D>
-__global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ AttnParams p, int max_parts, int tile_rows) {
-    extern __shared__ float wgt[];                 // one weight per partial
+template <int D, int DC>
+__global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ AttnParams p, int tile_rows) {
+    constexpr int COLS = DC / 4, GROUPS = JT / COLS, CHUNKS = D / DC;
+    extern __shared__ float2 ml[];                 // (reference, sum) of each part, then (weight, -)
     __shared__ float red[JT / 32], red_l[JT / 32];
-    __shared__ float part[JT / 32][D];
+    __shared__ float4 part[GROUPS][COLS];
     sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
     const int rows = p.M * p.G, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const int bh = blockIdx.x / rows, row = blockIdx.x - bh * rows, b = bh / p.heads, h = bh - b * p.heads;
+    const int which = blockIdx.x / CHUNKS, d0 = (blockIdx.x - which * CHUNKS) * DC;
+    const int bh = which / rows, row = which - bh * rows, b = bh / p.heads, h = bh - b * p.heads;
     const int rt = row / tile_rows, r = row - rt * tile_rows, m = row / p.G;
-    const long long at = ((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G;
+    const int2 seg = p.seg[bh * p.RT + rt];        // of an earlier call where the sequence is empty
     const bool empty = length_of(p, b) == 0;
+    if (!empty && seg.y == 0) return;
+    const long long at = ((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G;
     if (empty) {
-        for (int d = tid; d < D; d += JT) p.out[at * D + d] = __float2half_rn(0.f);
-        if (tid == 0 && p.lse) p.lse[at] = NEG_INF;
+        for (int d = tid; d < DC; d += JT) p.out[at * D + d0 + d] = __float2half_rn(0.f);
+        if (tid == 0 && d0 == 0 && p.lse) p.lse[at] = NEG_INF;
         return;
     }
-    const int2 seg = p.seg[(long long)bh * p.RT + rt];
-    if (seg.y == 0) return;
-    const int n = min(seg.y, max_parts);
-    // slot of partial i: the first CTA's second slot, the first slot of the others
+    const int n = seg.y;
+    // slot of part i: the first CTA's second slot, the first slot of the others
     auto slot = [&](int i) { return (size_t(seg.x) + i) * 2 + (i == 0 ? 1 : 0); };
     float top = NEG_INF;
-    for (int i = tid; i < n; i += JT) top = fmaxf(top, p.part_ml[(slot(i) * tile_rows + r) * 2]);
+    for (int i = tid; i < n; i += JT) {
+        const float2 v = *reinterpret_cast<const float2 *>(p.part_ml + (slot(i) * tile_rows + r) * 2);
+        ml[i] = v;
+        top = fmaxf(top, v.x);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) red[wid] = top;
@@ -489,10 +494,9 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
     for (int w = 0; w < JT / 32; ++w) top = fmaxf(top, red[w]);
     float l = 0.f;
     for (int i = tid; i < n; i += JT) {
-        const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + (slot(i) * tile_rows + r) * 2);
-        const float f = ml.x == NEG_INF ? 0.f : ex2(ml.x - top);
-        wgt[i] = f;
-        l += ml.y * f;
+        const float f = ml[i].x == NEG_INF ? 0.f : ex2(ml[i].x - top);
+        l += ml[i].y * f;
+        ml[i].x = f;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -501,31 +505,27 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
     l = 0.f;
 #pragma unroll
     for (int w = 0; w < JT / 32; ++w) l += red_l[w];
-    constexpr int PER = D / 32;
-    float v[PER];
-#pragma unroll
-    for (int x = 0; x < PER; ++x) v[x] = 0.f;
+    const int grp = tid / COLS, col = tid - grp * COLS;
+    const float *src = p.part_o + size_t(r) * D + d0 + col * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int i = wid; i < n; i += JT / 32) {
-        const float *src = p.part_o + (slot(i) * tile_rows + r) * D + lane * 2;
-        const float f = wgt[i];
-#pragma unroll
-        for (int x = 0; x < PER; x += 2) {
-            const float2 y = *reinterpret_cast<const float2 *>(src + x * 32);
-            v[x] += y.x * f;
-            v[x + 1] += y.y * f;
-        }
+    for (int i = grp; i < n; i += GROUPS) {
+        const float4 y = *reinterpret_cast<const float4 *>(src + slot(i) * tile_rows * D);
+        const float f = ml[i].x;
+        v.x += y.x * f;
+        v.y += y.y * f;
+        v.z += y.z * f;
+        v.w += y.w * f;
     }
-#pragma unroll
-    for (int x = 0; x < PER; x += 2) *reinterpret_cast<float2 *>(&part[wid][x * 32 + lane * 2]) = make_float2(v[x], v[x + 1]);
+    part[grp][col] = v;
     __syncthreads();
-    for (int d = tid; d < D; d += JT) {
+    for (int d = tid; d < DC; d += JT) {
         float y = 0.f;
 #pragma unroll
-        for (int w = 0; w < JT / 32; ++w) y += part[w][d];
-        p.out[at * D + d] = __float2half_rn(l == 0.f ? 0.f : y * (p.vg / l));
+        for (int w = 0; w < GROUPS; ++w) y += reinterpret_cast<const float *>(part[w])[d];
+        p.out[at * D + d0 + d] = __float2half_rn(l == 0.f ? 0.f : y * (p.vg / l));
     }
-    if (tid == 0 && p.lse) p.lse[at] = l == 0.f ? NEG_INF : (top + __log2f(l) - P_SHIFT) * LN2;
+    if (tid == 0 && d0 == 0 && p.lse) p.lse[at] = l == 0.f ? NEG_INF : (top + __log2f(l) - P_SHIFT) * LN2;
 }
 
 // acc_out = acc_in + the weights of all query rows, per position and kv head:
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
     kv4_weights_kernel(const __grid_constant__ AttnParams p, int tiles) {
     using C = WeightsCfg<D>;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long sm_share[WARPS + 4];
+    __shared__ int sm_share[WARPS + 2];
     __shared__ float lse2[WT_TILES * NROW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t base = sk::smem_u32(smem), qs = base + C::FIXED;
@@ -571,13 +571,12 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
             ++sh.b;
             continue;
         }
-        const int h = int(sh.off / nt), t_lo = int(sh.off - (long long)h * nt), b = sh.b;
-        const int t_hi = int(min((long long)nt, t_lo + sh.end - sh.t));
+        const int h = sh.off / nt, t_lo = sh.off - h * nt, b = sh.b;
+        const int t_hi = min(nt, t_lo + sh.end - sh.t);
         const int32_t *table = p.table + (long long)b * p.width;
         const int rows = p.M * p.G, nrec = (len + 15) / 16;
         const size_t acc_at = (size_t(b) * p.heads + h) * size_t(p.cap);
-        const int st_hi = min(t_hi * WARPS, (len + STEP - 1) / STEP);
-        const int st0 = t_lo * WARPS + warp;
+        const int st0 = t_lo * WARPS + warp, st_hi = min(t_hi * WARPS, (len + STEP - 1) / STEP);
         const int n = st0 < st_hi ? (st_hi - st0 + WARPS - 1) / WARPS : 0;
         for (int r0 = 0; r0 < tiles; r0 += WT_TILES) {
             const int nr = min(WT_TILES, tiles - r0);
@@ -667,7 +666,7 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
         }
         sh.t += t_hi - t_lo;
         sh.off += t_hi - t_lo;
-        if (sh.off == (long long)nt * p.heads) {
+        if (sh.off == nt * p.heads) {
             ++sh.b;
             sh.off = 0;
         }
@@ -677,7 +676,7 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 constexpr int MAX_SEGMENTS = 131072;
-constexpr int TC_ABOVE = 16;           // more query rows of a kv head than these go to the tensor-core kernel
+constexpr int TC_ABOVE = 32;           // more query rows of a kv head than these go to the tensor-core kernel
 
 // The scratch memory's segment list and partial sums for `rows` per tile.
 bool place_partials(AttnParams &p, unsigned char *scratch, int rows, int D) {
@@ -689,12 +688,17 @@ bool place_partials(AttnParams &p, unsigned char *scratch, int rows, int D) {
 }
 
 template <int D>
-sk_status join(const AttnParams &p, int tile_rows, cudaStream_t s) {
+sk_status join(const AttnParams &p, int tile_rows, int sms, cudaStream_t s) {
+    // Few rows (one long sequence): each split over CTAs, 32 components each, so
+    // that a thread's parts are all in flight.  Measured on ten rows over 60000
+    // positions (456 parts): JOIN_US.
     const long long rows = (long long)p.B * p.heads * p.M * p.G;
-    return sk::launch_pdl(kv4_join_kernel<D>, dim3(unsigned(rows)), dim3(JT), size_t(p.ctas) * 4, s, p, p.ctas,
-                          tile_rows) == cudaSuccess
-               ? SK_OK
-               : SK_ERR_CUDA;
+    const size_t smem = size_t(p.ctas) * sizeof(float2);
+    const cudaError_t e =
+        rows <= sms
+            ? sk::launch_pdl(kv4_join_kernel<D, 32>, dim3(unsigned(rows) * (D / 32)), dim3(JT), smem, s, p, tile_rows)
+            : sk::launch_pdl(kv4_join_kernel<D, D>, dim3(unsigned(rows)), dim3(JT), smem, s, p, tile_rows);
+    return e == cudaSuccess ? SK_OK : SK_ERR_CUDA;
 }
 
 template <int D, int NR>
@@ -705,7 +709,7 @@ sk_status attend(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s)
     if (sk::prepare_kernel<kv4_attention_kernel<D, NR>>(C::SMEM) != cudaSuccess) return SK_ERR_CUDA;
     if (sk::launch_pdl(kv4_attention_kernel<D, NR>, dim3(p.ctas), dim3(CT), C::SMEM, s, p) != cudaSuccess)
         return SK_ERR_CUDA;
-    return join<D>(p, C::ROWS, s);
+    return join<D>(p, C::ROWS, sms, s);
 }
 
 sk_status attend_tc(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
@@ -713,7 +717,7 @@ sk_status attend_tc(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t
     p.ctas = sms * TC_CTAS;
     if (!place_partials(p, scratch, rows, 128)) return SK_ERR_WORKSPACE;
     if (launch_tc(p, rows, s) != cudaSuccess) return SK_ERR_CUDA;
-    return join<128>(p, rows, s);
+    return join<128>(p, rows, sms, s);
 }
 
 template <int D>
@@ -769,7 +773,10 @@ extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint
     p.G = q_heads / kv_heads;
     // (sequence, kv head, tile of 16 rows) fit the segment list, whatever tiles the head size gets
     if ((long long)seqs * kv_heads * ((rows * p.G + 15) / 16) > MAX_SEGMENTS ||
-        (long long)seqs * q_heads * rows > 0x7FFFFFFFLL)
+        (long long)seqs * q_heads * rows > 0x7FFFFFFLL)
+        return SK_ERR_UNSUPPORTED_SHAPE;
+    // tiles of positions, over all segments, fit 31 bits
+    if ((long long)seqs * kv_heads * ((rows * p.G + 7) / 8) * (((long long)table_width * page_size + TILE - 1) / TILE) > 0x7FFFFFFFLL)
         return SK_ERR_UNSUPPORTED_SHAPE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     sk::Scratch sc;

@@ -27,6 +27,7 @@ namespace {
 using namespace sk::attn;
 
 constexpr int D = 128;
+static_assert(TILE == 128, "positions per tile");
 constexpr int TT = 256;                // threads: eight warps
 constexpr int REC = sk::kv4_rec_bytes(D);
 constexpr int PART = REC / 2;          // the keys' or the values' half of a record
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
     using C = Tc<N>;
     constexpr int NH = N / 2, UNITS = C::UNITS;              // columns per thread; units in the ring
     extern __shared__ unsigned char dyn[];
-    __shared__ long long sm_share[TT / 32 + 4];
+    __shared__ int sm_share[TT / 32 + 2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int quad = warp & 3, side = warp >> 2;             // this warp's TMEM lanes and its half of the columns
     const uint32_t base = (sk::smem_u32(dyn) + 1023u) & ~1023u;
@@ -247,8 +248,8 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             ++sh.b;
             continue;
         }
-        const int hr = int(sh.off / nt), t_lo = int(sh.off - (long long)hr * nt);
-        const int t_hi = int(min((long long)nt, t_lo + sh.end - sh.t));
+        const int hr = sh.off / nt, t_lo = sh.off - hr * nt;
+        const int t_hi = min(nt, t_lo + sh.end - sh.t);
         const int h = hr / p.RT, rt = hr - h * p.RT, b = sh.b, tiles = t_hi - t_lo;
         const int32_t *table = p.table + (long long)b * p.width;
         const int nrec = (len + 15) / 16, rec0 = t_lo * 8;
@@ -501,16 +502,15 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             }
         }
         if (tid == 0 && t_lo == 0) {
-            const long long last = sh.t + nt - 1;     // the segment's last tile
-            const int c1 = int(((last + 1) * sh.parts - 1) / sh.total);
-            p.seg[((long long)b * p.heads + h) * p.RT + rt] = make_int2(int(blockIdx.x), whole ? 0 : c1 - int(blockIdx.x) + 1);
+            const int c1 = cta_of(sh, sh.t + nt - 1);     // of the segment's last tile
+            p.seg[(b * p.heads + h) * p.RT + rt] = make_int2(int(blockIdx.x), whole ? 0 : c1 - int(blockIdx.x) + 1);
         }
         fence_before();
         __syncthreads();
         fence_after();
         sh.t += t_hi - t_lo;
         sh.off += t_hi - t_lo;
-        if (sh.off == (long long)nt * p.heads * p.RT) {
+        if (sh.off == nt * p.heads * p.RT) {
             ++sh.b;
             sh.off = 0;
         }

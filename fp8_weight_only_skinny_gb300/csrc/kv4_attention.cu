@@ -528,6 +528,67 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
     if (tid == 0 && d0 == 0 && p.lse) p.lse[at] = l == 0.f ? NEG_INF : (top + __log2f(l) - P_SHIFT) * LN2;
 }
 
+// The same with a warp per row, for segments of few parts: no barriers.
+template <int D>
+__global__ void __launch_bounds__(JT) kv4_join_rows_kernel(const __grid_constant__ AttnParams p, int tile_rows) {
+    constexpr int PER = D / 32;                    // components per lane: two neighbouring ones, 64 apart
+    sk::pdl_launch_dependents();
+    sk::pdl_wait_primary();
+    const int rows = p.M * p.G, lane = threadIdx.x & 31;
+    const int which = blockIdx.x * (JT / 32) + (threadIdx.x >> 5);
+    const int bh = which / rows, row = which - bh * rows, b = bh / p.heads, h = bh - b * p.heads;
+    if (b >= p.B) return;
+    const int rt = row / tile_rows, r = row - rt * tile_rows, m = row / p.G;
+    const int2 seg = p.seg[bh * p.RT + rt];        // of an earlier call where the sequence is empty
+    const bool empty = length_of(p, b) == 0;
+    if (!empty && seg.y == 0) return;
+    const long long at = ((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G;
+    __half2 *const out = reinterpret_cast<__half2 *>(p.out + at * D) + lane;
+    if (empty) {
+#pragma unroll
+        for (int x = 0; x < PER / 2; ++x) out[32 * x] = __floats2half2_rn(0.f, 0.f);
+        if (lane == 0 && p.lse) p.lse[at] = NEG_INF;
+        return;
+    }
+    const int n = seg.y;
+    auto slot = [&](int i) { return (size_t(seg.x) + i) * 2 + (i == 0 ? 1 : 0); };
+    float top = NEG_INF, l = 0.f, v[PER];
+#pragma unroll
+    for (int x = 0; x < PER; ++x) v[x] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {           // 32 parts at a time, under the reference so far
+        float2 ml = make_float2(NEG_INF, 0.f);
+        if (i0 + lane < n) ml = *reinterpret_cast<const float2 *>(p.part_ml + (slot(i0 + lane) * tile_rows + r) * 2);
+        float now = ml.x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+        now = fmaxf(now, top);
+        const float old = top == now ? 1.f : ex2(top - now), f = ml.x == NEG_INF ? 0.f : ex2(ml.x - now);
+        top = now;
+        float add = ml.y * f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
+        l = l * old + add;
+#pragma unroll
+        for (int x = 0; x < PER; ++x) v[x] *= old;
+        const int k = min(32, n - i0);
+#pragma unroll 4
+        for (int i = 0; i < k; ++i) {
+            const float w = __shfl_sync(0xffffffffu, f, i);
+            const float2 *src = reinterpret_cast<const float2 *>(p.part_o + (slot(i0 + i) * tile_rows + r) * D) + lane;
+#pragma unroll
+            for (int x = 0; x < PER / 2; ++x) {
+                const float2 y = src[32 * x];
+                v[2 * x] += y.x * w;
+                v[2 * x + 1] += y.y * w;
+            }
+        }
+    }
+    const float f = l == 0.f ? 0.f : p.vg / l;
+#pragma unroll
+    for (int x = 0; x < PER / 2; ++x) out[32 * x] = __floats2half2_rn(v[2 * x] * f, v[2 * x + 1] * f);
+    if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? NEG_INF : (top + __log2f(l) - P_SHIFT) * LN2;
+}
+
 // acc_out = acc_in + the weights of all query rows, per position and kv head:
 // the scores once more (the keys alone are read), against the rows' final log
 // sums.  A warp owns the 32 positions of a step, whose sum over the rows is
@@ -689,15 +750,21 @@ bool place_partials(AttnParams &p, unsigned char *scratch, int rows, int D) {
 
 template <int D>
 sk_status join(const AttnParams &p, int tile_rows, int sms, cudaStream_t s) {
-    // Few rows (one long sequence): each split over CTAs, 32 components each, so
-    // that a thread's parts are all in flight.  Measured on ten rows over 60000
-    // positions (456 parts): JOIN_US.
-    const long long rows = (long long)p.B * p.heads * p.M * p.G;
+    // By how many parts a segment has on average: few, a warp per row (64
+    // sequences of 2 heads, 3 parts: 9.6 -> WARP_US); many, a CTA per row, and
+    // where the rows are few as well, each split over CTAs of 32 components, so
+    // that a thread's parts are all in flight (ten rows of 456 parts: the call
+    // 24 -> 15 us).
+    const long long rows = (long long)p.B * p.heads * p.M * p.G, segments = (long long)p.B * p.heads * p.RT;
     const size_t smem = size_t(p.ctas) * sizeof(float2);
-    const cudaError_t e =
-        rows <= sms
-            ? sk::launch_pdl(kv4_join_kernel<D, 32>, dim3(unsigned(rows) * (D / 32)), dim3(JT), smem, s, p, tile_rows)
-            : sk::launch_pdl(kv4_join_kernel<D, D>, dim3(unsigned(rows)), dim3(JT), smem, s, p, tile_rows);
+    cudaError_t e;
+    if (p.ctas <= 8 * segments)
+        e = sk::launch_pdl(kv4_join_rows_kernel<D>, dim3(unsigned((rows + JT / 32 - 1) / (JT / 32))), dim3(JT), 0, s, p,
+                           tile_rows);
+    else if (rows <= sms)
+        e = sk::launch_pdl(kv4_join_kernel<D, 32>, dim3(unsigned(rows) * (D / 32)), dim3(JT), smem, s, p, tile_rows);
+    else
+        e = sk::launch_pdl(kv4_join_kernel<D, D>, dim3(unsigned(rows)), dim3(JT), smem, s, p, tile_rows);
     return e == cudaSuccess ? SK_OK : SK_ERR_CUDA;
 }
 

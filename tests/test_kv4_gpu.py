@@ -162,6 +162,45 @@ def test_attention_head_groups(sk, Hq, H, rows):
     _check_attention(sk, cache, table, lens, q, rows, Hq, D, acc=False)
 
 
+@pytest.mark.parametrize("Hq,H,rows", [(33, 1, 1), (17, 1, 2), (12, 1, 4), (48, 1, 1), (10, 1, 5), (16, 1, 4), (16, 1, 5), (12, 1, 7),
+                                        (12, 1, 8), (13, 1, 8), (25, 1, 8), (32, 2, 6)])
+@pytest.mark.parametrize("lens", [[0, 1, 7, 128], [129, 300, 64, 5]])
+def test_attention_of_many_rows_per_kv_head(sk, Hq, H, rows, lens):
+    """Head size 128: row counts on both sides of the tensor-core kernel's tiles (48, 64, 80, 96 rows, and two tiles)."""
+    cache, table, lens, q = _case(Hq * rows + lens[0], lens, rows, Hq, H, 128, 32, q_gap=128)
+    _check_attention(sk, cache, table, lens, q, rows, Hq, 128, acc=False)
+
+
+@pytest.mark.parametrize("order", ["rising", "falling"])
+@pytest.mark.parametrize("Hq,rows", [(12, 1), (12, 3), (12, 8)])
+def test_attention_references_move_across_tiles(sk, order, Hq, rows):
+    """Head size 128, scores that rise by far more than the slack from tile to tile of one CTA (a batch that gives each
+    CTA several tiles of a sequence), or fall as far."""
+    import torch
+
+    D, n, page, H = 128, 1100, 64, 2
+    r = np.random.default_rng(rows)
+    pages = (n + page - 1) // page
+    cache = np.full((pages, H, page // 16, 18 * D), 0xFF, np.uint8)
+    for j in range(n):
+        for h in range(H):
+            k = np.full(D, (j if order == "rising" else n - j) / n * 6, np.float16)
+            kv4.write(cache, j, h, k, r.standard_normal(D).astype(np.float16), KG, VG)
+    B = 70                                         # the same sequence many times: over 1200 tiles
+    table = np.tile(np.arange(pages, dtype=np.int32), (B, 1))
+    q = (r.random((rows, Hq * H * D)) + 0.5).astype(np.float16)
+    lens = np.full(B, n, np.int32)
+    ref = kv4.attention(q.reshape(rows, Hq * H, D), cache, table[:1], lens[:1], KG, VG, 0.1, rows)
+    out, lse = sk.kv4_attention(dev(np.tile(q, (B, 1))).unflatten(1, (Hq * H, D)), dev(cache), dev(table), dev(lens), KG, VG,
+                                0.1, rows=rows)
+    out, lse = host(out).reshape(B, rows, Hq * H, D), host(lse).reshape(B, rows, Hq * H)
+    e = (D / 16 + 16) * 2.0 ** -23 * ref["zmax"] + 2.0 ** -22 * np.abs(ref["lse"])
+    tol = (2.0 ** -11 + 4 * e[..., None] + 2.0 ** -15) * ref["absum"] + 2.0 ** -11 * np.abs(ref["out"]) + 2.0 ** -25
+    for b in range(B):
+        assert np.all(np.abs(out[b] - ref["out"]) <= tol), b
+        assert np.all(np.abs(lse[b] - ref["lse"]) <= e + 2.0 ** -16 + 2.0 ** -22 * np.abs(ref["lse"])), b
+
+
 @pytest.mark.parametrize("page", [16, 48, 64, 80, 256])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attention_page_sizes(sk, page, D):
@@ -317,7 +356,7 @@ def test_a_captured_decode_step_follows_changing_lengths(sk):
 @pytest.mark.parametrize("lens,budget,recent,H,D,page", [
     ([0, 1, 5, 40], 16, 4, 2, 64, 16), ([100, 33, 64, 65], 33, 0, 1, 128, 32), ([300, 17], 17, 17, 3, 64, 16),
     ([257, 256, 255], 100, 31, 1, 256, 64), ([50], 200, 3, 2, 128, 48), ([5000, 4097, 1], 1000, 10, 1, 64, 16),
-    ([3000], 1, 0, 1, 64, 16), ([9000], 2049, 1, 2, 64, 16)])
+    ([3000], 1, 0, 1, 64, 16), ([9000], 2049, 1, 2, 64, 16), ([8193, 8192, 20000], 3000, 100, 1, 64, 16), ([40000], 20000, 0, 1, 64, 32)])
 @pytest.mark.parametrize("kind", ["random", "ties", "zeros"])
 def test_evict_moves_the_oracles_positions(sk, lens, budget, recent, H, D, page, kind):
     import torch
@@ -373,6 +412,26 @@ def test_evicted_cache_serves_attention_over_the_kept_positions(sk):
     assert np.array_equal(host(kept)[0, 0], hot) and int(new[0]) == 25
     out2, _ = sk.kv4_attention(q, c, dst, new, KG, VG, 0.125, acc=acc2, acc_out=acc2)
     assert np.abs(host(out) - host(out2)).max() <= 2.0 ** -9
+
+
+def test_example_of_a_decode_round(sk):
+    """The example's rounds: its picks are greedy (rank 1, the first alternative), its cache stays within bounds
+    through several evictions, and every position holds keys of the sequence's own pages."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_round.py")
+    spec = importlib.util.spec_from_file_location("decode_round", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    got = example.decode(rounds=120, rows=4, page=16, high_water=64, budget=32, recent=8)
+    assert got["evictions"] >= 3 and 0 < got["length"] <= 64
+    for token, lp, rank, entropy, ids, top in got["report"]:
+        assert rank == 1 and ids[0] == token and abs(top[0] - lp) < 1e-6 and lp < 0 < entropy
+    acc = host(got["acc"])[0, :, :got["length"]]
+    assert np.all(acc >= 0) and acc.sum() > 0
+    k, _ = kv4.read(got["cache"].cpu().numpy(), int(got["table"][0, 0]) * 16, 0, 0.002, 0.002)
+    assert np.abs(k).max() > 0
 
 
 def test_binding_refuses_what_the_library_cannot_see(sk):

@@ -25,7 +25,6 @@ constexpr int BINS = 512;
 constexpr int FEW = 64;            // candidates left at which the selection ends by counting
 constexpr int CHUNK = 1024;        // records numbered at a time
 constexpr int MAX_CLUSTER = 16;
-constexpr int SLOTS = 2;           // source records in flight per warp
 constexpr int SOLO_MAX = KEYS;     // positions up to which a CTA selects alone
 
 struct EvictParams {
@@ -40,7 +39,21 @@ struct EvictParams {
     sk::Div by_recs;
 };
 
+// Records with something to keep.
+struct List {
+    uint32_t src[CHUNK], dst[CHUNK][2];    // record in the cache; those of the first kept position and the next
+    int rec[CHUNK];                        // number in the sequence
+    uint32_t base[CHUNK];                  // slot of the first kept position
+    uint16_t mask[CHUNK];                  // positions kept
+    uint32_t masks[CHUNK];                 // per record: kept for sure (low half), equal to the threshold (high half)
+};
+
+template <int SLOTS>
 struct alignas(16) Shared {
+    union {
+        unsigned int bins[BINS];       // while selecting
+        List list;                     // afterwards
+    };
     unsigned int hist[2][BINS];
     unsigned long long mine[FEW];      // this CTA's candidates
     unsigned long long few[FEW];       // the cluster's
@@ -51,14 +64,12 @@ struct alignas(16) Shared {
     unsigned int scan[ET / 32];
     unsigned int prefix, need, pop, above;
     unsigned long long limit;
-    // records with something to keep: number in the sequence, positions kept, first destination slot
-    int list_rec[CHUNK];
-    uint32_t list_base[CHUNK];
-    uint16_t list_mask[CHUNK];
-    uint32_t masks[CHUNK];             // per record: kept for sure (low half), equal to the threshold (high half)
     unsigned char nth[WARPS][16];      // the position of a record's n-th kept one
     alignas(8) unsigned long long bar[WARPS][SLOTS];
 };
+
+// Source records in flight per warp.
+__host__ __device__ constexpr int ring_slots(int d) { return d == 256 ? 2 : 4; }
 
 // Order of the weights as unsigned keys (larger weight, larger key; -0 = +0).
 __device__ __forceinline__ unsigned int key_of(float v) {
@@ -123,13 +134,18 @@ __device__ __forceinline__ unsigned long long cand_of(unsigned int key, int pos)
 // rank.  The copy streams the records that hold a kept position through shared
 // memory, a ring per warp: a position's value codes are eight-byte pieces and
 // its value scales single bytes, each in a 32-byte sector of its own, so
-// fetching only what is kept moves as many sectors (measured on 16 sequences
-// of up to 16411 positions, 2 heads of 256, 4096 kept: 47 us).
+// fetching only what is kept moves as many sectors and costs a load for each
+// (a kernel of its own for the copies, a warp gathering a record's 16
+// positions: 34 us where this takes 30, 19 us where this takes 15).
+//
+// Bound by latency, and by what the longest sequence's cluster copies: 16
+// sequences of up to 16411 positions, 2 heads of 256, 4096 kept, 30 us (59 MB
+// read and written at least, 8.8 us); one of 1500 positions, 4 heads of 128, 7 us.
 template <int D, bool SOLO>
 __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ EvictParams p, int ctas) {
-    constexpr int REC = sk::kv4_rec_bytes(D), NB = D / 16;
+    constexpr int REC = sk::kv4_rec_bytes(D), NB = D / 16, SLOTS = ring_slots(D);
     extern __shared__ __align__(128) unsigned char smem[];      // keys, later the records' ring
-    __shared__ Shared sh;
+    __shared__ Shared<SLOTS> sh;
     unsigned int *const keys = reinterpret_cast<unsigned int *>(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (lane == 0)
@@ -165,12 +181,15 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
             sh.range[1] = 0u;
         }
         __syncthreads();
-        for (int i0 = tid; i0 < n_old; i0 += 8 * ET) {
-            float v[8];
+        sh.bins[tid] = 0u;
+        sh.bins[tid + ET] = 0u;
+        static_assert(BINS == 2 * ET, "two bins per thread");
+        for (int i0 = tid; i0 < n_old; i0 += 16 * ET) {
+            float v[16];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = i0 + j * ET < n_old ? acc[s_lo + i0 + j * ET] : 0.f;
+            for (int j = 0; j < 16; ++j) v[j] = i0 + j * ET < n_old ? acc[s_lo + i0 + j * ET] : 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 16; ++j) {
                 const int i = i0 + j * ET;
                 if (i < n_old) {
                     const unsigned int k = key_of(v[j]);
@@ -192,12 +211,9 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
             mx = sh.range[1];
         } else {
             cluster_sync();
-            mn = 0xFFFFFFFFu;
-            mx = 0u;
-            for (unsigned int r = 0; r < C; ++r) {
-                mn = min(mn, ld_peer(&sh.range[0], r));
-                mx = max(mx, ld_peer(&sh.range[1], r));
-            }
+            const unsigned int peer = unsigned(lane) & (C - 1u);
+            mn = __reduce_min_sync(0xffffffffu, ld_peer(&sh.range[0], peer));
+            mx = __reduce_max_sync(0xffffffffu, ld_peer(&sh.range[1], peer));
         }
         // digits of key - low, from its highest bit down (uniform in the cluster)
         low = mn;
@@ -206,30 +222,31 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
         while (top > 0 && !few) {
             const int bits = min(9, top), shift = top - bits;
             const unsigned int bins = (1u << bits) - 1u;
-            unsigned int *hh = sh.hist[pass & 1];
-            hh[tid] = 0u;
-            hh[tid + ET] = 0u;
-            static_assert(BINS == 2 * ET, "two bins per thread");
-            __syncthreads();
 #pragma unroll 4
             for (int i = tid; i < n_old; i += ET) {
                 const unsigned int k = key_at(i) - low;
-                if ((k & mask) == prefix) atomicAdd(&hh[(k >> shift) & bins], 1u);
+                if ((k & mask) == prefix) atomicAdd(&sh.bins[(k >> shift) & bins], 1u);
             }
-            // thread t takes bins 511 - 2 t and 510 - 2 t: an inclusive scan over t is the suffix sum over bins
-            unsigned int t0 = 0, t1 = 0;
-            if constexpr (SOLO) {
-                __syncthreads();
-                t0 = hh[BINS - 1 - 2 * tid];
-                t1 = hh[BINS - 2 - 2 * tid];
-            } else {
+            __syncthreads();
+            // thread t takes bins 511 - 2 t and 510 - 2 t, and clears them: an
+            // inclusive scan over t is the suffix sum over bins
+            uint2 *const two = reinterpret_cast<uint2 *>(&sh.bins[BINS - 2 - 2 * tid]);
+            unsigned int t0 = two->y, t1 = two->x;
+            *two = make_uint2(0u, 0u);
+            unsigned int *const hh = sh.hist[pass & 1];
+            if constexpr (!SOLO) {
+                hh[BINS - 1 - 2 * tid] = t0;
+                hh[BINS - 2 - 2 * tid] = t1;
                 cluster_sync();
-#pragma unroll 4
-                for (unsigned int r = 0; r < C; ++r) {
-                    const unsigned long long w =
-                        ld_peer64(reinterpret_cast<const unsigned long long *>(hh + BINS - 2 - 2 * tid), r);
-                    t1 += static_cast<unsigned int>(w);
-                    t0 += static_cast<unsigned int>(w >> 32);
+                unsigned long long w[MAX_CLUSTER];       // all in flight, each CTA beginning with its own
+#pragma unroll
+                for (unsigned int r = 0; r < MAX_CLUSTER; ++r)
+                    w[r] = r < C ? ld_peer64(reinterpret_cast<const unsigned long long *>(hh + BINS - 2 - 2 * tid), (rank + r) & (C - 1u)) : 0ull;
+                t0 = t1 = 0;
+#pragma unroll
+                for (unsigned int r = 0; r < MAX_CLUSTER; ++r) {
+                    t1 += static_cast<unsigned int>(w[r]);
+                    t0 += static_cast<unsigned int>(w[r] >> 32);
                 }
             }
             unsigned int sum_all;
@@ -245,17 +262,19 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
                 sh.need = need - over1;
                 sh.pop = t1;
             }
-            if (tid == 0) sh.above = 0u;
+            if (!SOLO && tid == 0) sh.above = 0u;
             __syncthreads();
             prefix = sh.prefix;
             need = sh.need;
             few = sh.pop <= unsigned(FEW);
-            const unsigned int digit = (prefix >> shift) & bins;
-            unsigned int mine = (unsigned(2 * tid) > digit ? hh[2 * tid] : 0u) + (unsigned(2 * tid + 1) > digit ? hh[2 * tid + 1] : 0u);
-            mine = __reduce_add_sync(0xffffffffu, mine);
-            if (lane == 0 && mine) atomicAdd(&sh.above, mine);
-            __syncthreads();
-            above += sh.above;
+            if constexpr (!SOLO) {
+                const unsigned int digit = (prefix >> shift) & bins;
+                unsigned int mine = (unsigned(2 * tid) > digit ? hh[2 * tid] : 0u) + (unsigned(2 * tid + 1) > digit ? hh[2 * tid + 1] : 0u);
+                mine = __reduce_add_sync(0xffffffffu, mine);
+                if (lane == 0 && mine) atomicAdd(&sh.above, mine);
+                __syncthreads();
+                above += sh.above;
+            }
             mask |= bins << shift;
             top = shift;
             ++pass;
@@ -369,14 +388,14 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
             const int r = (i0 + tid) >> 4;
             if ((lane & 15) == 0 && r < nr) {
                 const int s = lane & 16;
-                sh.masks[r] = ((two >> s) & 0xFFFFu) | (((one >> s) & 0xFFFFu) << 16);
+                sh.list.masks[r] = ((two >> s) & 0xFFFFu) | (((one >> s) & 0xFFFFu) << 16);
             }
         }
         __syncthreads();
         // base slot of each record, and the list of records with something kept (in order)
         unsigned int listed = 0;
         for (int x0 = 0; x0 < nr; x0 += ET) {
-            const unsigned int m = x0 + tid < nr ? sh.masks[x0 + tid] : 0u;
+            const unsigned int m = x0 + tid < nr ? sh.list.masks[x0 + tid] : 0u;
             unsigned int two = m & 0xFFFFu, one = m >> 16, tg, te, tl;
             const unsigned int c = (unsigned(__popc(two)) << 16) | unsigned(__popc(one));
             const unsigned int x = inclusive(c, sh.scan, &tg) - c;             // at most 16 ET in each half
@@ -387,10 +406,14 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
             te = tg & 0xFFFFu;
             const unsigned int at = inclusive(keep != 0u, sh.scan, &tl);
             if (keep) {
-                const unsigned int y = listed + at - 1u;
-                sh.list_rec[y] = r0 + x0 + tid;
-                sh.list_base[y] = g + min(e, need);
-                sh.list_mask[y] = uint16_t(keep);
+                const unsigned int y = listed + at - 1u, to = g + min(e, need);
+                const int rec = r0 + x0 + tid;
+                sh.list.rec[y] = rec;
+                sh.list.base[y] = to;
+                sh.list.mask[y] = uint16_t(keep);
+                sh.list.src[y] = sk::kv4_record(table, rec, p.recs, p.by_recs, p.pages, p.heads, h);
+                sh.list.dst[y][0] = sk::kv4_record(dtable, int(to >> 4), p.recs, p.by_recs, p.pages, p.heads, h);
+                sh.list.dst[y][1] = sk::kv4_record(dtable, int((to + __popc(keep) - 1u) >> 4), p.recs, p.by_recs, p.pages, p.heads, h);
             }
             listed += tl;
             gt_before += tg >> 16;
@@ -406,23 +429,40 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
         auto issue = [&](int y, uint32_t slot) {
             if (lane == 0) {
                 const uint32_t bar = sk::smem_u32(&sh.bar[warp][slot]);
-                const uint32_t rec = sk::kv4_record(table, sh.list_rec[y], p.recs, p.by_recs, p.pages, p.heads, h);
                 sk::mbar_arrive_expect_tx(bar, REC);
-                sk::bulk_load(ring + slot * REC, p.cache + size_t(rec) * REC, REC, bar);
+                sk::bulk_load(ring + slot * REC, p.cache + size_t(sh.list.src[y]) * REC, REC, bar);
             }
         };
         for (int k = 0; k < SLOTS; ++k)
             if (warp + k * WARPS < n_list) issue(warp + k * WARPS, (done + k) % SLOTS);
+        // meanwhile, the kept positions' numbers and weights, eight to a thread in flight
+        for (int i0 = tid; i0 < n_list * 16; i0 += 8 * ET) {
+            int to[8], from[8];
+            float v[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int y = (i0 + x * ET) >> 4, j = tid & 15;
+                const unsigned int m = y < n_list ? sh.list.mask[y] : 0u;
+                to[x] = -1;
+                v[x] = 0.f;
+                if (m >> j & 1u) {
+                    to[x] = int(sh.list.base[y]) + __popc(m & ((1u << j) - 1u));
+                    from[x] = sh.list.rec[y] * 16 + j;
+                    if (acc_out) v[x] = acc[from[x]];
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                if (to[x] >= 0) {
+                    kept[to[x]] = from[x];
+                    if (acc_out) acc_out[to[x]] = v[x];
+                }
+        }
         for (int y = warp; y < n_list; y += WARPS, ++done) {
             const uint32_t slot = done % SLOTS;
-            const unsigned int m = sh.list_mask[y], base = sh.list_base[y];
-            const int count = __popc(m), rec = sh.list_rec[y];
-            if (lane < 16 && (m >> lane & 1u)) {
-                const int q = __popc(m & ((1u << lane) - 1u)), from = rec * 16 + lane;
-                sh.nth[warp][q] = uint8_t(lane);
-                kept[base + q] = from;
-                if (acc_out) acc_out[base + q] = acc[from];
-            }
+            const unsigned int m = sh.list.mask[y], base = sh.list.base[y];
+            const int count = __popc(m);
+            if (lane < 16 && (m >> lane & 1u)) sh.nth[warp][__popc(m & ((1u << lane) - 1u))] = uint8_t(lane);
             sk::wait_full(sk::smem_u32(&sh.bar[warp][slot]), (done / SLOTS) & 1, p.err, dead);
             __syncwarp();
             const unsigned char *src = own + slot * REC;
@@ -431,7 +471,7 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
                 const int q = q0 + (lane & 3);
                 if (q < count) {
                     const int i = sh.nth[warp][q], to = int(base) + q, j = to & 15;
-                    uint8_t *dst = p.cache + size_t(sk::kv4_record(dtable, to >> 4, p.recs, p.by_recs, p.pages, p.heads, h)) * REC;
+                    uint8_t *dst = p.cache + size_t(sh.list.dst[y][(to >> 4) != int(base >> 4)]) * REC;
 #pragma unroll
                     for (int blk = lane >> 2; blk < NB; blk += 8) {
                         *reinterpret_cast<uint2 *>(dst + sk::kv4_code_at<true>(D, j, blk)) =
@@ -457,7 +497,7 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
 // The keys, and later the records' ring in their place.
 template <int D>
 constexpr size_t smem_bytes() {
-    const size_t ring = size_t(WARPS) * SLOTS * sk::kv4_rec_bytes(D);
+    const size_t ring = size_t(WARPS) * ring_slots(D) * sk::kv4_rec_bytes(D);
     return ring > size_t(KEYS) * 4 ? ring : size_t(KEYS) * 4;
 }
 

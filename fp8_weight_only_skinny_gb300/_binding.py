@@ -347,6 +347,15 @@ def _raw_stream(stream, device):
     return torch.cuda.current_stream(device).cuda_stream if number is None else number(device)
 
 
+def _new(shape, dtype, device, stream):
+    """An output's memory, from the pool of the stream that will write it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def kv4_append(k, v, slots, cache, k_scale: float, v_scale: float, k_held=None, v_held=None, stream=None) -> None:
     """Write keys and values (FP16 [T][kv_heads][head_dim], row stride free) to the cache's slots
     (int32 [T], page * page_size + offset; negative: skipped).
@@ -386,9 +395,9 @@ def kv4_attention(q, cache, table, lens, k_scale: float, v_scale: float, scale: 
     tp = _need(table, torch.int32, (seqs, width), "table")
     lp = _need(lens, torch.int32, (seqs,), "lens")
     if out is None:
-        out = torch.empty((n, hq, dim), dtype=torch.float16, device=q.device)
+        out = _new((n, hq, dim), torch.float16, q.device, stream)
     if lse is None:
-        lse = torch.empty((n, hq), dtype=torch.float32, device=q.device)
+        lse = _new((n, hq), torch.float32, q.device, stream)
     ap = None if acc is None else _need(acc, torch.float32, (seqs, heads, width * page), "acc")
     op = None if acc_out is None else _need(acc_out, torch.float32, (seqs, heads, width * page), "acc_out")
     _check(lib.kv4_attention(q.data_ptr(), qs, cache.data_ptr(), tp, lp, k_scale, v_scale, scale,
@@ -413,11 +422,11 @@ def kv4_evict(cache, table, lens, acc, dst_table, budget: int, recent: int, kept
     seqs, width = table.shape
     dwidth = dst_table.shape[1]
     if new_lens is None:
-        new_lens = torch.empty((seqs,), dtype=torch.int32, device=cache.device)
+        new_lens = _new((seqs,), torch.int32, cache.device, stream)
     if kept is None:
-        kept = torch.empty((seqs, heads, budget), dtype=torch.int32, device=cache.device)
+        kept = _new((seqs, heads, budget), torch.int32, cache.device, stream)
     if acc_out is None:
-        acc_out = torch.empty((seqs, heads, dwidth * page), dtype=torch.float32, device=cache.device)
+        acc_out = _new((seqs, heads, dwidth * page), torch.float32, cache.device, stream)
     i32, f32 = torch.int32, torch.float32
     _check(lib.kv4_evict(cache.data_ptr(), _need(table, i32, (seqs, width), "table"), _need(lens, i32, (seqs,), "lens"),
                          _need(acc, f32, (seqs, heads, width * page), "acc"),
@@ -448,18 +457,18 @@ def token_logprobs(logits, tokens=None, top_n: int = 0, temperature: float = 1.0
     if tokens is not None:
         tp = _need(tokens, i32, (M,), "tokens")
         if logprob is None:
-            logprob = torch.empty((M,), dtype=f32, device=dev)
+            logprob = _new((M,), f32, dev, stream)
         if rank is None:
-            rank = torch.empty((M,), dtype=i32, device=dev)
+            rank = _new((M,), i32, dev, stream)
         lp, rp = _need(logprob, f32, (M,), "logprob"), _need(rank, i32, (M,), "rank")
     else:
         logprob = rank = None
     if entropy is None:
-        entropy = torch.empty((M,), dtype=f32, device=dev)
+        entropy = _new((M,), f32, dev, stream)
     if top_ids is None:
-        top_ids = torch.empty((M, top_n), dtype=i32, device=dev)
+        top_ids = _new((M, top_n), i32, dev, stream)
     if top_logprobs is None:
-        top_logprobs = torch.empty((M, top_n), dtype=f32, device=dev)
+        top_logprobs = _new((M, top_n), f32, dev, stream)
     _check(lib.token_logprobs(logits.data_ptr(), 0 if logits.dtype == f32 else 1, stride if M > 1 else max(stride, N),
                               tp, temperature, top_n, lp, rp, _need(entropy, f32, (M,), "entropy"),
                               _need(top_ids, i32, (M, top_n), "top_ids"),

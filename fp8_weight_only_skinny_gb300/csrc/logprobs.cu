@@ -20,12 +20,10 @@
 
 namespace {
 
-constexpr int LT = 256;                  // threads per CTA
+constexpr int WIDE = 256, NARROW = 64;   // threads per CTA (LT below)
 constexpr int PER = 16;                  // logits per thread and round
-constexpr int ROUND = LT * PER;
 constexpr int MAX_TOP = 64;
 constexpr int SOFT = 160;                // the most candidates that a round may start with
-constexpr int LIST = SOFT + ROUND + 2;   // a round can add all of its logits
 constexpr int GROUPS = 64;               // groups of threads whose maxima bound the n-th largest
 constexpr int MAX_CLUSTER = 16;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
@@ -123,12 +121,14 @@ __device__ __forceinline__ Stats join_across(const Stats &a, int o, int lane, fl
     return (lane & o) ? join(x, a, c) : join(a, x, c);
 }
 
+// A CTA of few threads has a row to itself: it joins no cluster.
+template <int LT>
 struct Shared {
-    unsigned long long list[LIST];
+    unsigned long long list[SOFT + LT * PER + 2];         // a round can add all of its logits
     unsigned long long best[MAX_TOP];
     unsigned long long maxima[LT];
     alignas(16) unsigned int top[GROUPS];
-    unsigned long long all_best[MAX_CLUSTER * MAX_TOP];
+    unsigned long long all_best[LT == NARROW ? 1 : MAX_CLUSTER * MAX_TOP];
     Stats stats[LT / 32];
     Stats mine, all;
     unsigned int above[LT / 32];
@@ -143,7 +143,8 @@ struct Shared {
 // counting for each how many are larger (the entries differ: each holds its
 // index).  With many candidates, those below the n-th largest of the threads'
 // maxima go first: at least n are at or above it.
-__device__ __forceinline__ void pick_best(Shared &sh, int count, int n) {
+template <int LT>
+__device__ __forceinline__ void pick_best(Shared<LT> &sh, int count, int n) {
     const int tid = threadIdx.x;
     __syncthreads();
     if (count > 2 * LT) {
@@ -184,9 +185,9 @@ __device__ __forceinline__ void pick_best(Shared &sh, int count, int n) {
 
 // Sixteen logits of a thread as loaded: NV words of 16 bytes, the v-th holding
 // logits i0 + (v LT + tid) VEC and on.
-template <typename T>
+template <typename T, int LT>
 struct Raw {
-    static constexpr int VEC = 16 / int(sizeof(T)), NV = PER / VEC;
+    static constexpr int VEC = 16 / int(sizeof(T)), NV = PER / VEC, ROUND = LT * PER;
     uint4 w[NV];
 
     // whole: all of the round's logits belong to [lo, hi); the others are read
@@ -245,15 +246,18 @@ __device__ __forceinline__ float one(const float *p) { return *p; }
 __device__ __forceinline__ float one(const __half *p) { return __half2float(*p); }
 
 // One cluster per row (a single CTA where the rows alone fill the GPU); CTA r
-// takes the r-th contiguous part of the row, a round of 4096 logits at a time,
-// the next round's loads in flight while one is summed.
-template <typename T>
+// takes the r-th contiguous part of the row, a round of 16 logits a thread at
+// a time, the next round's loads in flight while one is summed.  Many long
+// rows are bound by the reads (2048 of 151936, FP32, top 20: 220 us, 5.7 TB/s);
+// few or short ones by the latency of a read, the cut of the candidates and
+// the exchange in the cluster (one row of 151936: 8.6 us).
+template <typename T, int LT>
 __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ LogprobParams p, int first_row, int late) {
     extern __shared__ __align__(16) unsigned char raw_smem[];
-    Shared &sh = *reinterpret_cast<Shared *>(raw_smem);
-    constexpr int VEC = Raw<T>::VEC;
+    Shared<LT> &sh = *reinterpret_cast<Shared<LT> *>(raw_smem);
+    constexpr int VEC = Raw<T, LT>::VEC, ROUND = LT * PER;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const unsigned int rank = cluster_rank(), C = cluster_size();
+    const unsigned int rank = LT == NARROW ? 0u : cluster_rank(), C = LT == NARROW ? 1u : cluster_size();
     const int row = first_row + blockIdx.x / C;
     // The first of two launches lets the second start once all of its own CTAs
     // are past their wait, so what the logits depend on is complete; the second
@@ -265,7 +269,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
     const int part = (p.N + int(C) - 1) / int(C);
     const int lo = min(p.N, int(rank) * part), hi = min(p.N, lo + part);
     const int first = lo - int((reinterpret_cast<uintptr_t>(z0 + lo) & 15u) / sizeof(T));
-    Raw<T> next;
+    Raw<T, LT> next;
     next.load(z0, first, lo, hi);
     const int tok = p.tokens ? p.tokens[row] : -1;
     const bool given = tok >= 0 && tok < p.N;
@@ -281,6 +285,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
     static_assert(2 * MAX_TOP + 24 < SOFT, "the list holds them and a round");
     if (tid == 0) sh.count = 0;
     if (tid < MAX_TOP) sh.place[tid] = 0u;
+    static_assert(LT >= MAX_TOP && LT >= GROUPS, "a thread a place, and a group's threads");
 
     Stats st = {LOWEST, 0.f, 0.f};
     unsigned int above = 0;
@@ -371,7 +376,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
         }
         if (n > 0) {
             if (__syncthreads_or(full)) {
-                pick_best(sh, sh.count, n);
+                pick_best<LT>(sh, sh.count, n);
                 for (int i = tid; i < n; i += LT) sh.list[i] = sh.best[i];
                 if (tid == 0) sh.count = n;
                 floor = sh.best[n - 1];
@@ -392,7 +397,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
         sh.above[wid] = above;
     }
     __syncthreads();
-    if (n > 0) pick_best(sh, sh.count, n);
+    if (n > 0) pick_best<LT>(sh, sh.count, n);
     if (wid == 0) {
         Stats a = lane < LT / 32 ? sh.stats[lane] : Stats{LOWEST, 0.f, 0.f};
         unsigned int r = lane < LT / 32 ? sh.above[lane] : 0u;
@@ -481,12 +486,12 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
         }
 }
 
-template <typename T>
+template <typename T, int LT>
 cudaError_t launch(const LogprobParams &p, int first_row, int rows, int cluster, bool late, cudaStream_t s) {
-    const cudaError_t e = sk::prepare_kernel<logprobs_kernel<T>>(sizeof(Shared), true);
+    const cudaError_t e = sk::prepare_kernel<logprobs_kernel<T, LT>>(sizeof(Shared<LT>), LT == WIDE);
     if (e != cudaSuccess) return e;
-    return sk::launch_pdl_cluster(logprobs_kernel<T>, cluster, dim3(unsigned(rows) * unsigned(cluster)), dim3(LT),
-                                  sizeof(Shared), s, p, first_row, int(late));
+    return sk::launch_pdl_cluster(logprobs_kernel<T, LT>, cluster, dim3(unsigned(rows) * unsigned(cluster)), dim3(LT),
+                                  sizeof(Shared<LT>), s, p, first_row, int(late));
 }
 
 // CTAs that run at a time, four to an SM (64 registers a thread).
@@ -495,10 +500,18 @@ constexpr int PER_SM = 4;
 template <typename T>
 sk_status run(const LogprobParams &p, int rows, cudaStream_t s) {
     const int slots = PER_SM * (sk::device_sm_count() > 0 ? sk::device_sm_count() : 1);
+    // Short rows: a CTA of 64 threads for each, where one round holds the row,
+    // or where two do and the rows exceed the wide CTAs that run at a time.
+    // (2048 rows of 300, FP32, top 20: 11 us, 58 with wide CTAs, whose idle
+    // threads leave no floor to the candidates; 1000 of 2000: 10.4 and 12.6;
+    // one row of 1000: 5.7 and 5.1; 300 of 2000: 8.8 and 6.0.)
+    if (p.N <= (rows > slots ? 2 : 1) * NARROW * PER)
+        return launch<T, NARROW>(p, 0, rows, 1, false, s) == cudaSuccess ? SK_OK : SK_ERR_CUDA;
     // CTAs per row: what fits, each with a round or more to read.
     // (Clusters of fewer and larger CTAs, one round each, were slower: 1024
     // threads took 10.5 against 9.8 us for one row of 151936, and eight
     // clusters of 16 such CTAs do not fit the GPU at once.)
+    constexpr int ROUND = WIDE * PER;
     auto split = [&](int r) {
         int c = 1;
         while (c < MAX_CLUSTER && r * c * 2 <= slots && c * ROUND < p.N) c *= 2;
@@ -510,10 +523,10 @@ sk_status run(const LogprobParams &p, int rows, cudaStream_t s) {
     const int left = rows > slots ? rows % slots : rows, cluster = split(left);
     cudaError_t e;
     if (rows <= slots || cluster == 1) {
-        e = launch<T>(p, 0, rows, rows <= slots ? cluster : 1, false, s);
+        e = launch<T, WIDE>(p, 0, rows, rows <= slots ? cluster : 1, false, s);
     } else {
-        e = launch<T>(p, 0, rows - left, 1, false, s);
-        if (e == cudaSuccess && left) e = launch<T>(p, rows - left, left, cluster, sk::pdl_enabled(), s);
+        e = launch<T, WIDE>(p, 0, rows - left, 1, false, s);
+        if (e == cudaSuccess && left) e = launch<T, WIDE>(p, rows - left, left, cluster, sk::pdl_enabled(), s);
     }
     return e == cudaSuccess ? SK_OK : SK_ERR_CUDA;
 }

@@ -107,6 +107,45 @@ def test_masked_rows(sk):
     _check(sk, h, [1, 0], 0.8, 6)
 
 
+@pytest.mark.parametrize("dtype", [np.float32, np.float16])
+@pytest.mark.parametrize("M,N,n", [(700, 300, 20), (3, 1023, 20), (5, 1024, 64), (5, 1025, 64), (700, 1025, 20),
+                                   (650, 2048, 33), (650, 2049, 5), (620, 19, 40), (640, 1, 2)])
+def test_short_rows(sk, dtype, M, N, n):
+    """One round of a narrow CTA, two of them, and the lengths on either side."""
+    r = np.random.default_rng(M + N)
+    z = (r.standard_normal((M, N)) * 3).astype(dtype)
+    z[M // 2] = np.sort(z[M // 2])
+    z[M // 3] = 1.0
+    z[M - 1, : N // 2] = -np.inf
+    _check(sk, z, r.integers(N // 2, N, M), 1.0, n)
+    if N > 2:
+        _check(sk, z[:, 1:], r.integers(N // 2, N - 1, M), 0.7, n, 3, 1)
+
+
+@pytest.mark.parametrize("order", [1, -1])
+def test_sorted_short_rows(sk, order):
+    z = np.tile(np.linspace(-20, 20, 2000, dtype=np.float32)[::order], (640, 1))
+    _check(sk, z, np.full(640, 1999), 1.0, 64)
+
+
+def test_outputs_belong_to_the_given_stream(sk):
+    """Outputs made by a call on a stream come from that stream's memory: freed, they go to it and to no other."""
+    import torch
+
+    s = torch.cuda.Stream()
+    z = torch.randn((3, 70000), device="cuda")
+    torch.cuda.synchronize()
+    got = sk.token_logprobs(z, top_n=4, stream=s)
+    s.synchronize()
+    at = {t.data_ptr() for t in got if t is not None}
+    want = sk.token_logprobs(z, top_n=4)
+    torch.cuda.synchronize()
+    assert torch.equal(got[3], want[3])
+    del got
+    other = [torch.empty(3, 4, device="cuda") for _ in range(8)]
+    assert at.isdisjoint({t.data_ptr() for t in other})
+
+
 def test_tokens_outside_the_row_and_calls_without_tokens(sk):
     z = np.random.default_rng(9).standard_normal((3, 1000)).astype(np.float32)
     _check(sk, z, [-1, 1000, -100], 1.0, 4)

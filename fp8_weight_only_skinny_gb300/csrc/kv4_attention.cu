@@ -201,16 +201,65 @@ __device__ __forceinline__ void pv(uint32_t rec, const uint32_t (&b)[NR][2], int
     }
 }
 
+constexpr int MAX_CLUSTER = 16;
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float2 ld_peer_v2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_peer_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// Four components of query row r of a segment, and its log sum, from the sums
+// under the reference `top`.
+template <int D>
+__device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int row, int d, const float4 &v, float top, float l) {
+    const int m = row / p.G;
+    const long long to = ((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G;
+    const float f = l == 0.f ? 0.f : p.vg / l;
+    const __half2 y0 = __floats2half2_rn(v.x * f, v.y * f), y1 = __floats2half2_rn(v.z * f, v.w * f);
+    uint2 y = make_uint2(*reinterpret_cast<const uint32_t *>(&y0), *reinterpret_cast<const uint32_t *>(&y1));
+    *reinterpret_cast<uint2 *>(p.out + to * D + d) = y;
+    if (d == 0 && p.lse) p.lse[to] = l == 0.f ? NEG_INF : (top + __log2f(l) - P_SHIFT) * LN2;
+}
+
 // Each warp streams its own steps of 32 positions (bulk copies into a ring of
 // its own, issued by one lane a ring's length ahead) and keeps 8 NR query rows'
 // references, sums and outputs in registers; the four warps meet only at the
 // end of a segment (sequence, head, row tile).
-template <int D, int NR>
+//
+// SHORT: a cluster per segment, each CTA the same number of the table's tiles,
+// joined through distributed shared memory.  Otherwise the CTAs share all tiles
+// evenly, and kv4_join_kernel joins what they leave in the scratch memory.
+//
+// Bound by the issue of decoding (conversion, scaling) and products, which add
+// up: 64 sequences of up to 16411 positions, 24 query over 2 kv heads of 256,
+// the call 82 us (281 MB, 3.4 TB/s).  One sequence of
+// 1031 positions, 48 over 4 heads of 128: 6.5 us, all of it latency.
+template <int D, int NR, bool SHORT>
 __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(const __grid_constant__ AttnParams p) {
     using C = Cfg<D, NR>;
     constexpr int ROWS = C::ROWS, NX = C::ACC >= 64 || NR > 2 ? 1 : 2;       // records scored together
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int sm_share[WARPS + 2];
+    __shared__ __align__(16) float2 all_ml[SHORT ? ROWS : 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t base = sk::smem_u32(smem);
     const uint32_t qs = base + C::BODY, bars = qs + NR * C::QTILE;
@@ -222,19 +271,37 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
     sk::fence_barrier_init();
     sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
-    Share sh = share_of(p, p.heads * p.RT, sm_share);
+    Share sh;
+    if constexpr (!SHORT) sh = share_of(p, p.heads * p.RT, sm_share);
+    const uint32_t CL = SHORT ? cluster_size() : 1u;
     uint32_t at = 0, parity = 0;   // this warp's ring position
     bool dead = false;
 
-    while (sh.t < sh.end && sh.b < p.B) {
-        const int len = length_of(p, sh.b), nt = tiles_of(len);
-        if (nt == 0) {
-            ++sh.b;
-            continue;
+    for (;;) {
+        int b, hr, len, nt, t_lo, t_hi;
+        if constexpr (SHORT) {
+            const int which = int(blockIdx.x / CL), rank = int(blockIdx.x % CL);
+            b = which / (p.heads * p.RT);
+            hr = which - b * (p.heads * p.RT);
+            len = length_of(p, b);
+            nt = tiles_of(len);
+            const int each = (nt + int(CL) - 1) / int(CL);
+            t_lo = min(nt, rank * each);
+            t_hi = min(nt, t_lo + each);
+        } else {
+            if (sh.t >= sh.end || sh.b >= p.B) break;
+            b = sh.b;
+            len = length_of(p, b);
+            nt = tiles_of(len);
+            if (nt == 0) {
+                ++sh.b;
+                continue;
+            }
+            hr = sh.off / nt;
+            t_lo = sh.off - hr * nt;
+            t_hi = min(nt, t_lo + sh.end - sh.t);
         }
-        const int hr = sh.off / nt, t_lo = sh.off - hr * nt;
-        const int t_hi = min(nt, t_lo + sh.end - sh.t);
-        const int h = hr / p.RT, rt = hr - h * p.RT, b = sh.b;
+        const int h = hr / p.RT, rt = hr - h * p.RT;
         const int32_t *table = p.table + (long long)b * p.width;
         const int nrec = (len + 15) / 16;
 
@@ -398,7 +465,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                     }
         }
         __syncthreads();
-        const bool whole = t_lo == 0 && t_hi == nt;
+        const bool whole = SHORT ? CL == 1u : t_lo == 0 && t_hi == nt;
         const int rows = min(ROWS, p.M * p.G - rt * ROWS);
         const size_t slot = size_t(blockIdx.x) * 2 + (t_lo == 0 ? 1 : 0);
         for (int i = tid; i < rows * (D / 4); i += CT) {
@@ -422,18 +489,52 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                 v.w += x.w * f;
             }
             if (whole) {
-                const int row = rt * ROWS + r, m = row / p.G;
-                const long long to = ((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G;
-                const float f = l == 0.f ? 0.f : p.vg / l;
-                const __half2 y0 = __floats2half2_rn(v.x * f, v.y * f), y1 = __floats2half2_rn(v.z * f, v.w * f);
-                uint2 y = make_uint2(*reinterpret_cast<const uint32_t *>(&y0), *reinterpret_cast<const uint32_t *>(&y1));
-                *reinterpret_cast<uint2 *>(p.out + to * D + d) = y;
-                if (d == 0 && p.lse) p.lse[to] = l == 0.f ? NEG_INF : (top + __log2f(l) - P_SHIFT) * LN2;
+                write_row<D>(p, b, h, rt * ROWS + r, d, v, top, l);
+            } else if constexpr (SHORT) {
+                // in warp 0's place: no other thread reads it
+                *reinterpret_cast<float4 *>(obuf + r * C::OSTRIDE + d) = v;
+                if (d == 0) all_ml[r] = make_float2(top, l);
             } else {
                 *reinterpret_cast<float4 *>(p.part_o + (slot * ROWS + r) * D + d) = v;
                 if (d == 0) *reinterpret_cast<float2 *>(p.part_ml + (slot * ROWS + r) * 2) = make_float2(top, l);
             }
         }
+        if constexpr (SHORT) {
+            if (CL == 1u) break;
+            cluster_sync();
+            // the cluster's, in its order, every CTA a part of the rows and components
+            const uint32_t ml_at = sk::smem_u32(all_ml);
+            for (int i = int(blockIdx.x % CL) * CT + tid; i < rows * (D / 4); i += int(CL) * CT) {
+                const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+                float2 ml[MAX_CLUSTER];
+                float4 x[MAX_CLUSTER];
+#pragma unroll
+                for (uint32_t k = 0; k < MAX_CLUSTER; ++k) {
+                    ml[k] = make_float2(NEG_INF, 0.f);
+                    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k < CL) {
+                        ml[k] = ld_peer_v2(peer(ml_at + r * 8, k));
+                        x[k] = ld_peer_v4(peer(base + (r * C::OSTRIDE + d) * 4, k));
+                    }
+                }
+                float top = NEG_INF, l = 0.f;
+#pragma unroll
+                for (int k = 0; k < MAX_CLUSTER; ++k) top = fmaxf(top, ml[k].x);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < MAX_CLUSTER; ++k) {
+                    const float f = ml[k].x == NEG_INF ? 0.f : ex2(ml[k].x - top);
+                    l += ml[k].y * f;
+                    v.x += x[k].x * f;
+                    v.y += x[k].y * f;
+                    v.z += x[k].z * f;
+                    v.w += x[k].w * f;
+                }
+                write_row<D>(p, b, h, rt * ROWS + r, d, v, top, l);
+            }
+            cluster_sync();                      // no CTA leaves while its sums are read
+            break;
+        } else {
         if (tid == 0 && t_lo == 0) {
             const int c1 = cta_of(sh, sh.t + nt - 1);     // of the segment's last tile
             p.seg[(b * p.heads + h) * p.RT + rt] = make_int2(int(blockIdx.x), whole ? 0 : c1 - int(blockIdx.x) + 1);
@@ -446,6 +547,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
         if (sh.off == nt * p.heads * p.RT) {
             ++sh.b;
             sh.off = 0;
+        }
         }
     }
 }
@@ -592,7 +694,11 @@ __global__ void __launch_bounds__(JT) kv4_join_rows_kernel(const __grid_constant
 // acc_out = acc_in + the weights of all query rows, per position and kv head:
 // the scores once more (the keys alone are read), against the rows' final log
 // sums.  A warp owns the 32 positions of a step, whose sum over the rows is
-// taken in one order; the next step's keys are on their way meanwhile.
+// taken in one order; the next step's keys are on their way meanwhile.  (Taken
+// during the attention the weights would need each row's final sum, which is
+// not known until its last position.)  Bound like the attention by decoding and
+// products: 23 sequences of up to 9001 positions, 2 rows, 32 over 8 heads of 64,
+// the whole call 50 us.
 constexpr int WT_TILES = 16;           // tiles of eight rows held in shared memory at a time
 constexpr int WT_STAGES = 4;
 
@@ -737,7 +843,13 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 constexpr int MAX_SEGMENTS = 131072;
-constexpr int TC_ABOVE = 32;           // more query rows of a kv head than these go to the tensor-core kernel
+// More query rows of a kv head than these go to the tensor-core kernel, which
+// decodes a tile once for up to 96 rows where the registers hold 24 to 32:
+// 60000 positions, 4 heads of 128, 96 rows 39 us against 53, 36 rows 28 against
+// 33, 24 rows 25.0 against 23.6; 8 heads, 28 rows, 64 sequences of 300 29.5
+// against 34.5 and 16 of 20000 143 against 148, 24 rows 28 against 30 and 142
+// against 122.
+constexpr int TC_ABOVE = 24;
 
 // The scratch memory's segment list and partial sums for `rows` per tile.
 bool place_partials(AttnParams &p, unsigned char *scratch, int rows, int D) {
@@ -751,7 +863,7 @@ bool place_partials(AttnParams &p, unsigned char *scratch, int rows, int D) {
 template <int D>
 sk_status join(const AttnParams &p, int tile_rows, int sms, cudaStream_t s) {
     // By how many parts a segment has on average: few, a warp per row (64
-    // sequences of 2 heads, 3 parts: 9.6 -> WARP_US); many, a CTA per row, and
+    // sequences of 2 heads, 3 parts: the call 84 -> 82 us); many, a CTA per row, and
     // where the rows are few as well, each split over CTAs of 32 components, so
     // that a thread's parts are all in flight (ten rows of 456 parts: the call
     // 24 -> 15 us).
@@ -768,13 +880,48 @@ sk_status join(const AttnParams &p, int tile_rows, int sms, cudaStream_t s) {
     return e == cudaSuccess ? SK_OK : SK_ERR_CUDA;
 }
 
+// CTAs per segment with which all segments run at a time, each CTA with few of
+// the table's tiles; 0 where there is no such number.
+// Few: one launch then takes less than two and the scratch memory's round trip
+// (48 query over 4 heads of 128, one sequence of 1031 positions 6.5 us against
+// 8.3, of 7900 9.8 against 11.1; 50 of 500 11.0 against 12.7); with eight tiles
+// each one of 16000 takes 14.1 against 13.0.  In place of the tensor cores (rows
+// above TC_ABOVE) half as many: 32 rows, one of 4000 12.0 against 12.3, of 7900
+// 15.5 against 14.6.
+constexpr int SHORT_TILES = 4;
+template <int D, int NR>
+int short_cluster(const AttnParams &p, int few) {
+    using C = Cfg<D, NR>;
+    constexpr auto kernel = kv4_attention_kernel<D, NR, true>;
+    if (sk::prepare_kernel<kernel>(C::SMEM, true) != cudaSuccess) return 0;
+    const long long segments = (long long)p.B * p.heads * p.RT, tiles = ((long long)p.cap + TILE - 1) / TILE;
+    int c = 1;
+    while (c < MAX_CLUSTER && c < tiles && segments <= sk::resident_clusters<kernel>(c * 2, CT, C::SMEM)) c *= 2;
+    return tiles <= (long long)c * few && segments <= sk::resident_clusters<kernel>(c, CT, C::SMEM) ? c : 0;
+}
+
+// The launch of that form, where there is one.
+template <int D, int NR>
+bool attend_short(const AttnParams &p, int few, cudaStream_t s, sk_status *st) {
+    const int cluster = short_cluster<D, NR>(p, few);
+    if (!cluster) return false;
+    const dim3 grid(unsigned(cluster) * unsigned(p.B * p.heads * p.RT));
+    *st = sk::launch_pdl_cluster(kv4_attention_kernel<D, NR, true>, cluster, grid, dim3(CT), Cfg<D, NR>::SMEM, s, p) ==
+                  cudaSuccess
+              ? SK_OK
+              : SK_ERR_CUDA;
+    return true;
+}
+
 template <int D, int NR>
 sk_status attend(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     using C = Cfg<D, NR>;
+    sk_status st;
+    if (attend_short<D, NR>(p, SHORT_TILES, s, &st)) return st;
     p.ctas = sms * C::CTAS;
     if (!place_partials(p, scratch, C::ROWS, D)) return SK_ERR_WORKSPACE;
-    if (sk::prepare_kernel<kv4_attention_kernel<D, NR>>(C::SMEM) != cudaSuccess) return SK_ERR_CUDA;
-    if (sk::launch_pdl(kv4_attention_kernel<D, NR>, dim3(p.ctas), dim3(CT), C::SMEM, s, p) != cudaSuccess)
+    if (sk::prepare_kernel<kv4_attention_kernel<D, NR, false>>(C::SMEM) != cudaSuccess) return SK_ERR_CUDA;
+    if (sk::launch_pdl(kv4_attention_kernel<D, NR, false>, dim3(p.ctas), dim3(CT), C::SMEM, s, p) != cudaSuccess)
         return SK_ERR_CUDA;
     return join<D>(p, C::ROWS, sms, s);
 }
@@ -790,16 +937,21 @@ sk_status attend_tc(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t
 template <int D>
 sk_status run(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     // Query rows of a kv head in tiles of 8 NR rows, as even as they can be: NR
-    // up to 4 (the outputs are D / 4 NR registers a thread; D = 256: up to 2).
-    constexpr int MOST = D == 256 ? 2 : 4;
+    // up to 4 (the outputs are D / 4 NR registers a thread; D = 256: up to 2;
+    // D = 128: up to 3, more rows go to the tensor cores).
+    constexpr int MOST = D == 256 ? 2 : D == 128 ? TC_ABOVE / NROW : 4;
     const int tiles = (p.M * p.G + NROW - 1) / NROW;       // of eight rows
     p.RT = (tiles + MOST - 1) / MOST;
     const int nr = (tiles + p.RT - 1) / p.RT;
     sk_status st;
-    if (D == 128 && p.M * p.G > TC_ABOVE) st = attend_tc(p, scratch, sms, s);
-    else if (nr == 1) st = attend<D, 1>(p, scratch, sms, s);
+    if (D == 128 && p.M * p.G > TC_ABOVE) {
+        const bool done = nr == 3 ? attend_short<128, 3>(p, SHORT_TILES / 2, s, &st)
+                                  : attend_short<128, 2>(p, SHORT_TILES / 2, s, &st);
+        if (!done) st = attend_tc(p, scratch, sms, s);
+    } else if (nr == 1) st = attend<D, 1>(p, scratch, sms, s);
     else if (nr == 2) st = attend<D, 2>(p, scratch, sms, s);
     else if constexpr (MOST == 4) st = nr == 3 ? attend<D, 3>(p, scratch, sms, s) : attend<D, 4>(p, scratch, sms, s);
+    else if constexpr (MOST == 3) st = attend<D, 3>(p, scratch, sms, s);
     else return SK_ERR_UNSUPPORTED_SHAPE;
     if (st != SK_OK || !p.acc_out) return st;
     const int held = tiles < WT_TILES ? tiles : WT_TILES;

@@ -71,4 +71,33 @@ cudaError_t prepare_kernel(size_t smem, bool wide_clusters = false) {
     return e;
 }
 
+// How many clusters of `cluster` CTAs (a power of two up to 16) of this kernel
+// the current device runs at a time, after prepare_kernel.  Asked once.
+template <auto Kernel>
+long long resident_clusters(int cluster, int threads, size_t smem) {
+    static std::atomic<int> known[64][5] = {};       // number + 1
+    int dev = 0, log2 = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    while ((1 << log2) < cluster) ++log2;
+    if (dev < 64) {
+        const int v = known[dev][log2].load(std::memory_order_relaxed);
+        if (v) return v - 1;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(cluster));
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) return 0;
+    if (dev < 64) known[dev][log2].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
 }  // namespace sk

@@ -201,6 +201,39 @@ def test_attention_references_move_across_tiles(sk, order, Hq, rows):
         assert np.all(np.abs(lse[b] - ref["lse"]) <= e + 2.0 ** -16 + 2.0 ** -22 * np.abs(ref["lse"])), b
 
 
+@pytest.mark.parametrize("D,Hq,H,rows", [(64, 6, 2, 1), (64, 12, 1, 1), (64, 10, 1, 2), (64, 8, 1, 4), (64, 7, 1, 7),
+                                         (128, 4, 2, 2), (128, 12, 1, 1), (128, 12, 1, 2), (128, 5, 1, 5), (128, 12, 1, 3),
+                                         (128, 8, 1, 6), (128, 16, 1, 4), (128, 10, 1, 8), (128, 12, 1, 8), (128, 13, 1, 8),
+                                         (256, 3, 1, 2), (256, 12, 1, 1), (256, 5, 1, 5)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_attention_does_not_depend_on_the_tables_width(sk, D, Hq, H, rows, wide):
+    """A table of few positions (a cluster per segment, one launch) and one with room for more (shares of all tiles, joined
+    in a second launch; many rows of 128 on the tensor cores), over the same sequences."""
+    lens = [0, 1, 3, rows, 131, 300, 40, 64]
+    cache, table, lens, q = _case(rows + D + Hq, lens, rows, Hq, H, D, 32, width=300 if wide else None, q_gap=64)
+    acc = np.random.default_rng(1).random((len(lens), H, table.shape[1] * 32)).astype(np.float32)
+    _check_attention(sk, cache, table, lens, q, rows, Hq, D, acc=acc)
+
+
+@pytest.mark.parametrize("D,Hq,H,rows,lens", [(64, 4, 2, 1, [2000]), (128, 12, 1, 2, [1999, 17]), (256, 8, 1, 1, [1030, 0]),
+                                              (128, 12, 1, 8, [700, 1025]), (64, 8, 1, 4, [513, 1, 64, 385]),
+                                              (128, 2, 1, 1, [129, 4000]), (64, 4, 1, 1, [7300])])
+def test_attention_clusters(sk, D, Hq, H, rows, lens):
+    """Segments over clusters of every size, whole and partial tiles, CTAs without positions."""
+    cache, table, lens, q = _case(sum(lens), lens, rows, Hq, H, D, 64)
+    _check_attention(sk, cache, table, lens, q, rows, Hq, D, acc=False)
+
+
+@pytest.mark.parametrize("B", [75, 150, 200, 320])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_many_short_sequences(sk, D, B):
+    r = np.random.default_rng(B)
+    lens = [int(x) for x in r.integers(0, 20, B)]
+    lens[5] = 200
+    cache, table, lens, q = _case(B, lens, 1, 4, 2, D, 16)
+    _check_attention(sk, cache, table, lens, q, 1, 4, D)
+
+
 @pytest.mark.parametrize("page", [16, 48, 64, 80, 256])
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_attention_page_sizes(sk, page, D):

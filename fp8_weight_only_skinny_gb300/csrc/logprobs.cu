@@ -20,7 +20,7 @@
 
 namespace {
 
-constexpr int WIDE = 256, NARROW = 64;   // threads per CTA (LT below)
+constexpr int NARROW = 64, WIDE = 256, WIDER = 512;   // threads per CTA (LT below)
 constexpr int PER = 16;                  // logits per thread and round
 constexpr int MAX_TOP = 64;
 constexpr int SOFT = 160;                // the most candidates that a round may start with
@@ -250,7 +250,7 @@ __device__ __forceinline__ float one(const __half *p) { return __half2float(*p);
 // a time, the next round's loads in flight while one is summed.  Many long
 // rows are bound by the reads (2048 of 151936, FP32, top 20: 220 us, 5.7 TB/s);
 // few or short ones by the latency of a read, the cut of the candidates and
-// the exchange in the cluster (one row of 151936: 8.6 us).
+// the exchange in the cluster (one row of 151936, top 5: 8.4 us).
 template <typename T, int LT>
 __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ LogprobParams p, int first_row, int late) {
     extern __shared__ __align__(16) unsigned char raw_smem[];
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
 
 template <typename T, int LT>
 cudaError_t launch(const LogprobParams &p, int first_row, int rows, int cluster, bool late, cudaStream_t s) {
-    const cudaError_t e = sk::prepare_kernel<logprobs_kernel<T, LT>>(sizeof(Shared<LT>), LT == WIDE);
+    const cudaError_t e = sk::prepare_kernel<logprobs_kernel<T, LT>>(sizeof(Shared<LT>), LT != NARROW);
     if (e != cudaSuccess) return e;
     return sk::launch_pdl_cluster(logprobs_kernel<T, LT>, cluster, dim3(unsigned(rows) * unsigned(cluster)), dim3(LT),
                                   sizeof(Shared<LT>), s, p, first_row, int(late));
@@ -508,9 +508,6 @@ sk_status run(const LogprobParams &p, int rows, cudaStream_t s) {
     if (p.N <= (rows > slots ? 2 : 1) * NARROW * PER)
         return launch<T, NARROW>(p, 0, rows, 1, false, s) == cudaSuccess ? SK_OK : SK_ERR_CUDA;
     // CTAs per row: what fits, each with a round or more to read.
-    // (Clusters of fewer and larger CTAs, one round each, were slower: 1024
-    // threads took 10.5 against 9.8 us for one row of 151936, and eight
-    // clusters of 16 such CTAs do not fit the GPU at once.)
     constexpr int ROUND = WIDE * PER;
     auto split = [&](int r) {
         int c = 1;
@@ -522,7 +519,14 @@ sk_status run(const LogprobParams &p, int rows, cudaStream_t s) {
     // 3.4 waves of 608 (measured: 265 us in one launch, 255 us in two).
     const int left = rows > slots ? rows % slots : rows, cluster = split(left);
     cudaError_t e;
-    if (rows <= slots || cluster == 1) {
+    if (rows * cluster <= slots / PER_SM && p.N > 2 * cluster * ROUND) {
+        // Few rows of more than two rounds a CTA, an SM to each: twice the
+        // threads, and the rounds' reads are in flight together (rows of
+        // 151936, FP32, top 20: one 10.6 -> 9.1 us, four 11.4 -> 9.3, eight
+        // 12.3 -> 11.6; of 32000, one round each, 7.3 -> 7.7 were they to take
+        // it).  With 1024 threads one row takes 10.5.
+        e = launch<T, WIDER>(p, 0, rows, cluster, false, s);
+    } else if (rows <= slots || cluster == 1) {
         e = launch<T, WIDE>(p, 0, rows, rows <= slots ? cluster : 1, false, s);
     } else {
         e = launch<T, WIDE>(p, 0, rows - left, 1, false, s);

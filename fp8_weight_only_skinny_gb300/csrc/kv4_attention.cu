@@ -29,9 +29,11 @@ struct Cfg {
     static constexpr int KPAIRS = D / 32;            // pairs of k16 steps
     static constexpr int QTILE = KPAIRS * 512;       // bytes of eight query rows
     // accumulators are D / 4 NR registers a thread: CTAs per SM by what is left
+    // (six of D = 64, NR = 1: 8 sequences of 30000, 8 heads, one row 46 -> 43 us;
+    // five of 32 accumulators spill: 33 -> 37 us at D = 128)
     static constexpr int ACC = D / 4 * NR;
-    static constexpr int CTAS = ACC >= 96 ? 2 : ACC >= 64 ? 3 : 4;
-    static constexpr int STAGES = D == 64 ? 4 : D == 128 ? (CTAS == 4 ? 2 : 3) : 2;
+    static constexpr int CTAS = ACC >= 96 ? 2 : ACC >= 64 ? 3 : ACC <= 16 ? 6 : 4;
+    static constexpr int STAGES = D == 64 ? (CTAS == 6 ? 3 : 4) : D == 128 ? (CTAS == 4 ? 2 : 3) : 2;
     static constexpr int RING = WARPS * STAGES * STAGE;
     static constexpr int OSTRIDE = D + 8;            // floats between rows of a warp's sums at the merge
     static constexpr int MERGE = WARPS * ROWS * OSTRIDE * 4;
@@ -698,9 +700,10 @@ __global__ void __launch_bounds__(JT) kv4_join_rows_kernel(const __grid_constant
 // during the attention the weights would need each row's final sum, which is
 // not known until its last position.)  Bound like the attention by decoding and
 // products: 23 sequences of up to 9001 positions, 2 rows, 32 over 8 heads of 64,
-// the whole call 50 us.
+// the whole call 47 us.
 constexpr int WT_TILES = 16;           // tiles of eight rows held in shared memory at a time
 constexpr int WT_STAGES = 4;
+constexpr int ACC_STEPS = 4;           // steps whose accumulated weights are on their way
 
 template <int D>
 struct WeightsCfg {
@@ -782,53 +785,60 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
                 const int pos = (st0 + i * WARPS) * STEP + mine;
                 return old && i < n && pos < len ? old[acc_at + pos] : 0.f;
             };
-            float was = fetch(0), next = fetch(1);
-            for (int i = 0; i < n; ++i, ++it) {
-                const uint32_t slot = it % WT_STAGES, stage = ring + slot * C::STAGE;
-                sk::wait_full(bar + slot * 8, (it / WT_STAGES) & 1, p.err, dead);
-                Keys<D> k[4];
+            float had[ACC_STEPS];              // (a rotation through moves would wait for each)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) load_keys<D>(stage + (j >> 1) * C::KEY, (j & 1) * 8 + g, t, k[j]);
-                const int pos = (st0 + i * WARPS) * STEP;
-                const bool edge = pos + STEP > len - (p.M - 1);
-                float w[4] = {0.f, 0.f, 0.f, 0.f};     // record x, half y: w[2 x + y], of position g
-                for (int r = 0; r < nr; ++r) {
-                    float s[2][1][4];
-                    qk<D, 2, 1>(k, qs + r * C::QTILE, lane, s);
-                    const float2 neg = *reinterpret_cast<const float2 *>(&lse2[r * NROW + 2 * t]);
+            for (int j = 0; j < ACC_STEPS; ++j) had[j] = fetch(j);
+            for (int i0 = 0; i0 < n; i0 += ACC_STEPS) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        float *v = s[x >> 1][0] + 2 * (x & 1);
-                        v[0] = ex2(fmaf(v[0], p.scale2, -neg.x));
-                        v[1] = ex2(fmaf(v[1], p.scale2, -neg.y));
+                for (int j = 0; j < ACC_STEPS; ++j) {
+                    const int i = i0 + j;
+                    if (i >= n) break;
+                    const uint32_t slot = it % WT_STAGES, stage = ring + slot * C::STAGE;
+                    sk::wait_full(bar + slot * 8, (it / WT_STAGES) & 1, p.err, dead);
+                    Keys<D> k[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) load_keys<D>(stage + (x >> 1) * C::KEY, (x & 1) * 8 + g, t, k[x]);
+                    const int pos = (st0 + i * WARPS) * STEP;
+                    const bool edge = pos + STEP > len - (p.M - 1);
+                    float w[4] = {0.f, 0.f, 0.f, 0.f};     // record x, half y: w[2 x + y], of position g
+                    for (int r = 0; r < nr; ++r) {
+                        float s[2][1][4];
+                        qk<D, 2, 1>(k, qs + r * C::QTILE, lane, s);
+                        const float2 neg = *reinterpret_cast<const float2 *>(&lse2[r * NROW + 2 * t]);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            float *v = s[x >> 1][0] + 2 * (x & 1);
+                            v[0] = ex2(fmaf(v[0], p.scale2, -neg.x));
+                            v[1] = ex2(fmaf(v[1], p.scale2, -neg.y));
+                        }
+                        if (edge) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int lim = len - (p.M - 1 - min(((r0 + r) * NROW + 2 * t + e) / p.G, p.M - 1));
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    if (pos + 8 * x + g >= lim) s[x >> 1][0][2 * (x & 1) + e] = 0.f;
+                            }
+                        }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) w[x] += s[x >> 1][0][2 * (x & 1)] + s[x >> 1][0][2 * (x & 1) + 1];
                     }
-                    if (edge) {
+                    __syncwarp();
+                    if (i + WT_STAGES < n) issue(i + WT_STAGES, slot);
+                    // sums over the four t, halving what a lane keeps
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int lim = len - (p.M - 1 - min(((r0 + r) * NROW + 2 * t + e) / p.G, p.M - 1));
+                    for (int half = 2; half >= 1; half >>= 1) {
+                        const bool up = t & half;
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                if (pos + 8 * x + g >= lim) s[x >> 1][0][2 * (x & 1) + e] = 0.f;
+                        for (int x = 0; x < half; ++x) {
+                            const float give = up ? w[x] : w[x + half], keep = up ? w[x + half] : w[x];
+                            w[x] = keep + __shfl_xor_sync(0xffffffffu, give, half);
                         }
                     }
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) w[x] += s[x >> 1][0][2 * (x & 1)] + s[x >> 1][0][2 * (x & 1) + 1];
+                    if (pos + mine < len) p.acc_out[acc_at + pos + mine] = had[j] + w[0];
+                    had[j] = fetch(i + ACC_STEPS);
+                    ++it;
                 }
-                __syncwarp();
-                if (i + WT_STAGES < n) issue(i + WT_STAGES, slot);
-                // sums over the four t, halving what a lane keeps
-#pragma unroll
-                for (int half = 2; half >= 1; half >>= 1) {
-                    const bool up = t & half;
-#pragma unroll
-                    for (int x = 0; x < half; ++x) {
-                        const float give = up ? w[x] : w[x + half], keep = up ? w[x + half] : w[x];
-                        w[x] = keep + __shfl_xor_sync(0xffffffffu, give, half);
-                    }
-                }
-                if (pos + mine < len) p.acc_out[acc_at + pos + mine] = was + w[0];
-                was = next;
-                next = fetch(i + 2);
             }
         }
         sh.t += t_hi - t_lo;

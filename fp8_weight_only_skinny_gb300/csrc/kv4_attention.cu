@@ -54,24 +54,22 @@ __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
 }
 
 // Query rows [row0, row0 + 8 n) of (b, h) as B operands, two k16 steps in one
-// 16-byte word: word (pair w, tile r) of lane (g = lane / 4, t = lane % 4) holds
+// 16-byte word: word i (pair w, tile r) of lane (g = lane / 4, t = lane % 4) holds
 // components c .. c + 7 of row row0 + 8 r + g, c = 128 (w / 4) + 32 t + 8 (w % 4)
 // (D = 64: 16 t + 8 w): the order in which a lane's key bytes decode.  Rows
 // past the last are zero.
 template <int D>
-__device__ __forceinline__ void load_q(const AttnParams &p, int b, int h, int row0, int n, uint32_t qs) {
+__device__ __forceinline__ uint4 fetch_q(const AttnParams &p, int b, int h, int row0, int i) {
     constexpr int KPAIRS = D / 32;
-    for (int i = threadIdx.x; i < n * KPAIRS * 32; i += blockDim.x) {
-        const int l = i & 31, w = (i >> 5) % KPAIRS, r = (i >> 5) / KPAIRS, g = l >> 2, t = l & 3;
-        const int c = D == 64 ? 16 * t + 8 * w : 128 * (w >> 2) + 32 * t + 8 * (w & 3);
-        const int row = row0 + 8 * r + g, m = row / p.G;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (m < p.M)
-            v = *reinterpret_cast<const uint4 *>(p.q + ((long long)b * p.M + m) * p.q_stride +
-                                                  (long long)(h * p.G + row - m * p.G) * D + c);
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + i * 16), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                     : "memory");
-    }
+    const int l = i & 31, w = (i >> 5) % KPAIRS, r = (i >> 5) / KPAIRS, g = l >> 2, t = l & 3;
+    const int c = D == 64 ? 16 * t + 8 * w : 128 * (w >> 2) + 32 * t + 8 * (w & 3);
+    const int row = row0 + 8 * r + g, m = row / p.G;
+    if (m >= p.M) return make_uint4(0u, 0u, 0u, 0u);
+    return *reinterpret_cast<const uint4 *>(p.q + ((long long)b * p.M + m) * p.q_stride +
+                                             (long long)(h * p.G + row - m * p.G) * D + c);
+}
+__device__ __forceinline__ void store_q(uint32_t qs, int i, const uint4 &v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qs + i * 16), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // Key bytes of one position for this lane, as loaded from a record at
@@ -253,8 +251,8 @@ __device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int
 //
 // Bound by the issue of decoding (conversion, scaling) and products, which add
 // up: 64 sequences of up to 16411 positions, 24 query over 2 kv heads of 256,
-// the call 82 us (281 MB, 3.4 TB/s).  One sequence of
-// 1031 positions, 48 over 4 heads of 128: 6.5 us, all of it latency.
+// the call 78 us (281 MB, 3.6 TB/s).  One sequence of
+// 1031 positions, 48 over 4 heads of 128: 5.7 us, all of it latency.
 template <int D, int NR, bool SHORT>
 __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(const __grid_constant__ AttnParams p) {
     using C = Cfg<D, NR>;
@@ -332,12 +330,21 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                 if (two && !one_copy) sk::bulk_load(dst + C::REC, p.cache + size_t(r1) * C::REC, C::REC, fb);
             }
         };
+        // The query rows are asked for before the first copies: behind those of
+        // all CTAs they arrive microseconds later (64 sequences of up to 16411, 24
+        // over 2 heads of 256: the call 82 us, 78.4 this way).
+        constexpr int QPER = (NR * C::KPAIRS * 32 + CT - 1) / CT;
+        uint4 qv[QPER];
+#pragma unroll
+        for (int x = 0; x < QPER; ++x) qv[x] = fetch_q<D>(p, b, h, rt * ROWS, x * CT + tid);
         for (int i = 0; i < min(n, C::STAGES); ++i) {
             uint32_t slot = at + i;
             if (slot >= C::STAGES) slot -= C::STAGES;
             issue(i, slot);
         }
-        load_q<D>(p, b, h, rt * ROWS, NR, qs);
+#pragma unroll
+        for (int x = 0; x < QPER; ++x)
+            if (x * CT + tid < NR * C::KPAIRS * 32) store_q(qs, x * CT + tid, qv[x]);
         __syncthreads();       // the query rows are in shared memory
 
         float o[D / 16][NR][4];
@@ -566,7 +573,12 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
     extern __shared__ float2 ml[];                 // (reference, sum) of each part, then (weight, -)
     __shared__ float red[JT / 32], red_l[JT / 32];
     __shared__ float4 part[GROUPS][COLS];
-    sk::pdl_launch_dependents();
+    // Only this call's own weights kernel may be placed early.  The next call's
+    // attention fills an SM's registers to the last block, and CTAs of it placed
+    // around this kernel's leave a hole that is too small for the last one, which
+    // then runs after the others (64 sequences of 3000, 48 query over 4 heads of
+    // 128, calls in a row: 58 us each, 42 without).
+    if (p.acc_out) sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
     const int rows = p.M * p.G, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int which = blockIdx.x / CHUNKS, d0 = (blockIdx.x - which * CHUNKS) * DC;
@@ -636,7 +648,7 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
 template <int D>
 __global__ void __launch_bounds__(JT) kv4_join_rows_kernel(const __grid_constant__ AttnParams p, int tile_rows) {
     constexpr int PER = D / 32;                    // components per lane: two neighbouring ones, 64 apart
-    sk::pdl_launch_dependents();
+    if (p.acc_out) sk::pdl_launch_dependents();    // as above
     sk::pdl_wait_primary();
     const int rows = p.M * p.G, lane = threadIdx.x & 31;
     const int which = blockIdx.x * (JT / 32) + (threadIdx.x >> 5);
@@ -771,7 +783,7 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
             };
             for (int i = 0; i < min(n, WT_STAGES); ++i) issue(i, (it + i) % WT_STAGES);
             __syncthreads();
-            load_q<D>(p, b, h, r0 * NROW, nr, qs);
+            for (int x = tid; x < nr * (D / 32) * 32; x += CT) store_q(qs, x, fetch_q<D>(p, b, h, r0 * NROW, x));
             for (int x = tid; x < nr * NROW; x += CT) {
                 const int row = r0 * NROW + x, m = row / p.G;
                 float v = NEG_INF;

@@ -15,9 +15,10 @@
 //
 // Bound by the softmax's and the decoding's instructions between barriers, not
 // by the products: 100003 positions of 4 heads, 8 rows of 48 query heads (96
-// rows a kv head), 53 us with the join, 370 TFLOP/s (58 MB read); with 32-row
-// tiles in registers 90 us.  (A ninth warp for products and copies leaves 96
-// registers a thread: spills, 62 us.)
+// rows a kv head), 47 us with the join, 420 TFLOP/s (58 MB read); with 24-row
+// tiles in registers 90 us.  The scores of a position are read from TMEM a few
+// rows at a time: all 48 at once leave the sums no registers (52 us).  (A ninth
+// warp for products and copies leaves 96 registers a thread: spills, 62 us.)
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -45,9 +46,9 @@ template <int N>
 struct Tc {
     static constexpr int UNITS = N <= 64 ? 4 : 3;
     static constexpr int V = 0, Q = V + 128 * D * 2, P = Q + N * D * 2, RAW = P + N * 128 * 2, SMALL = RAW + UNITS * UNIT;
-    // per row: reference, P_SHIFT minus it, a factor, the first unseen position; four
+    // per row: reference, P_SHIFT minus it, that before it moved, a factor, the first unseen position; four
     // warps' values of each row; barriers of the ring and of the two products; the TMEM address
-    static constexpr int REF = SMALL, OFF = REF + 4 * N, FAC = OFF + 4 * N, LIM = FAC + 4 * N,
+    static constexpr int REF = SMALL, OFF = REF + 4 * N, OLD = OFF + 4 * N, FAC = OLD + 4 * N, LIM = FAC + 4 * N,
                          WARP = LIM + 4 * N, BARS = WARP + 16 * N, TMEM = BARS + 8 * (UNITS + 2);
     static constexpr size_t SMEM = 1024 + TMEM + 16;
     static constexpr int S_COL = 64, O_COL = 64 + N;         // TMEM columns: keys 0..63, S, O
@@ -124,15 +125,12 @@ __device__ __forceinline__ void st8(uint32_t addr, const float (&v)[8]) {
                  ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "r"(addr)
                  : "memory");
 }
-// Sixteen lanes x 64 columns: lane (g, t) of the warp gives columns 8 j + 2 t and
+// Sixteen lanes x 32 columns: lane (g, t) of the warp gives columns 8 j + 2 t and
 // 8 j + 2 t + 1 of rows g (v[4 j], v[4 j + 1]) and g + 8 (v[4 j + 2], v[4 j + 3]).
-__device__ __forceinline__ void st_16x64(uint32_t addr, const uint32_t (&v)[32]) {
-    asm volatile("tcgen05.st.sync.aligned.16x256b.x8.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+__device__ __forceinline__ void st_16x32(uint32_t addr, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
                  ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-                 "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
-                 "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
-                 "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(addr) : "memory");
+                 "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(addr) : "memory");
 }
 
 // Eight rows' numbers from shared memory.
@@ -163,26 +161,34 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 // 8 j + 2 t + x takes components 32 t + 4 j + 2 x and the next, the order in
 // which load_q places the query rows.
 __device__ __forceinline__ void decode_keys(uint32_t rec, uint32_t tmem, int g, int t) {
-    uint32_t v[32];
+    uint4 k[2];
+    uint32_t sc[2];
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
         const int i = g + 8 * y;
-        const uint4 k = sk::ld_shared_v4(rec + i * 64 + t * 16);
-        const uint32_t s = scale_pair(sk::ld_shared_u16(rec + 8 * D + i * 8 + t * 2));
-        const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+        k[y] = sk::ld_shared_v4(rec + i * 64 + t * 16);
+        sc[y] = scale_pair(sk::ld_shared_u16(rec + 8 * D + i * 8 + t * 2));
+    }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t d[4];
-            sk::e2m1x8_to_f16x2x4(w[q], d);
-            const uint32_t sc = q < 2 ? sk::bcast_lo(s) : sk::bcast_hi(s);
+    for (int hf = 0; hf < 2; ++hf) {                         // a block of 16 components: 32 columns
+        uint32_t v[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int pair = 4 * q + e;                  // = 2 j + x
-                v[4 * (pair >> 1) + 2 * y + (pair & 1)] = sk::hmul2(d[e], sc);
+        for (int y = 0; y < 2; ++y) {
+            const uint32_t w[2] = {hf ? k[y].z : k[y].x, hf ? k[y].w : k[y].y};
+            const uint32_t s = hf ? sk::bcast_hi(sc[y]) : sk::bcast_lo(sc[y]);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t d[4];
+                sk::e2m1x8_to_f16x2x4(w[q], d);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int pair = 4 * q + e;              // = 2 j + x
+                    v[4 * (pair >> 1) + 2 * y + (pair & 1)] = sk::hmul2(d[e], s);
+                }
             }
         }
+        st_16x32(tmem + 32 * hf, v);
     }
-    st_16x64(tmem, v);
 }
 
 // Values of a record (their half of it; positions pos0 .. pos0 + 15 of the tile) to the operand
@@ -224,7 +230,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
     const uint32_t base = (sk::smem_u32(dyn) + 1023u) & ~1023u;
     unsigned char *const smem = dyn + (base - sk::smem_u32(dyn));
     float *const ref = reinterpret_cast<float *>(smem + C::REF), *const off = reinterpret_cast<float *>(smem + C::OFF);
-    float *const fac = reinterpret_cast<float *>(smem + C::FAC);
+    float *const old = reinterpret_cast<float *>(smem + C::OLD), *const fac = reinterpret_cast<float *>(smem + C::FAC);
     int *const lim = reinterpret_cast<int *>(smem + C::LIM);
     float *const of_warp = reinterpret_cast<float *>(smem + C::WARP);
     const uint32_t bars = base + C::BARS, bar_s = bars + 8 * UNITS, bar_o = bar_s + 8;
@@ -277,6 +283,17 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             if (load)
                 sk::bulk_load(base + C::RAW + slot * UNIT + lane * PART, p.cache + size_t(idx) * REC + (u & 1) * PART, PART, bar);
         };
+        // rows: query, reference, first unseen position
+        uint2 qv[N / 8];                                     // on their way before the first copies
+        const int qc = tid & 31;                             // eight bytes: j = c / 4, t = c % 4
+#pragma unroll
+        for (int x = 0; x < N / 8; ++x) {
+            const int row = rt * N + 8 * x + (tid >> 5), m = row / p.G;
+            qv[x] = make_uint2(0u, 0u);
+            if (m < p.M)
+                qv[x] = *reinterpret_cast<const uint2 *>(p.q + ((long long)b * p.M + m) * p.q_stride +
+                                                        (long long)(h * p.G + row - m * p.G) * D + 32 * (qc & 3) + 4 * (qc >> 2));
+        }
         uint32_t idx1 = 0, idx2 = 0, idx3 = 0;               // records of the next three tiles
         if (warp == 1) {
             const uint32_t idx0 = lookup(0);
@@ -287,17 +304,11 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             issue(2, idx1);
             if (UNITS == 4) issue(3, idx1);
         }
-        // rows: query, reference, first unseen position
-        for (int i = tid; i < N * 32; i += TT) {
-            const int n = i >> 5, c = i & 31, row = rt * N + n, m = row / p.G;      // eight bytes: j = c / 4, t = c % 4
-            uint2 v = make_uint2(0u, 0u);
-            if (m < p.M)
-                v = *reinterpret_cast<const uint2 *>(p.q + ((long long)b * p.M + m) * p.q_stride +
-                                                      (long long)(h * p.G + row - m * p.G) * D + 32 * (c & 3) + 4 * (c >> 2));
-            const int kb = 8 * c, w = kb & 127;
-            *reinterpret_cast<uint2 *>(smem + C::Q + (kb >> 7) * (N * 128) + (n >> 3) * 1024 + (n & 7) * 128 +
-                                       ((((w >> 4) ^ (n & 7)) << 4) | (w & 15))) = v;
-        }
+        static_assert(TT == 256, "eight rows at a time");
+        const int q_at = (qc >> 4) * (N * 128) + warp * 128 + (((((8 * qc & 127) >> 4) ^ warp) << 4) | (8 * qc & 15));
+#pragma unroll
+        for (int x = 0; x < N / 8; ++x)
+            *reinterpret_cast<uint2 *>(smem + C::Q + q_at + x * 1024) = qv[x];
         for (int n = tid; n < N; n += TT) {
             ref[n] = NEG_INF;
             off[n] = 0.f;
@@ -348,40 +359,48 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             fence_after();
             const int at = quad * 32 + lane, pos = (t_lo + i) * TILE + at;
             const bool edge = (t_lo + i + 1) * TILE > len - (p.M - 1);
-            float s[NH];
-            auto scores = [&] {
-                ld_row<NH>(my_lanes + C::S_COL + side * NH, s);
+            // CH scores of this position, rows side * NH + c and on
+            constexpr int CH = NH % 24 == 0 ? 24 : NH % 16 == 0 ? 16 : 8;
+            auto scores = [&](int c, float (&s)[CH]) {
+                ld_row<CH>(my_lanes + C::S_COL + side * NH + c, s);
                 if (edge) {
                     // the tile's end: scores that their rows do not see
 #pragma unroll
-                    for (int c = 0; c < NH; ++c)
-                        if (pos >= lim[side * NH + c]) s[c] = NEG_INF;
+                    for (int e = 0; e < CH; ++e)
+                        if (pos >= lim[side * NH + c + e]) s[e] = NEG_INF;
                 }
             };
-            bool rise = false;                               // whether a score has passed its row's reference
-            auto weigh = [&] {
+            auto store_weights = [&](int c, const float (&s)[CH]) {
 #pragma unroll
-                for (int c = 0; c < NH; c += 8) {
-                    float of[8];
-                    row8(off + side * NH + c, of);
+                for (int x = 0; x < CH; x += 8) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        s[c + e] = ex2(fmaf(s[c + e], p.scale2, of[e]));
-                        rise |= s[c + e] > MOST_WEIGHT;
-                    }
+                    for (int e = 0; e < 4; ++e) w[e] = pack_f16(s[x + 2 * e], s[x + 2 * e + 1]);
+                    st_shared_v4(base + C::P + (side * NH + c + x) / 8 * 2048 + at * 16, w[0], w[1], w[2], w[3]);
+                }
+            };
+            bool rise = i == 0;                              // whether a score has passed its row's reference
+            if (i > 0) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = pack_f16(s[c + 2 * e], s[c + 2 * e + 1]);
-                    st_shared_v4(base + C::P + (side * NH + c) / 8 * 2048 + at * 16, w[0], w[1], w[2], w[3]);
+                for (int c = 0; c < NH; c += CH) {
+                    float s[CH];
+                    scores(c, s);
+#pragma unroll
+                    for (int x = 0; x < CH; x += 8) {
+                        float of[8];
+                        row8(off + side * NH + c + x, of);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float y = ex2(fmaf(s[x + e], p.scale2, of[e]));
+                            rise |= y > MOST_WEIGHT;
+                            l[c + x + e] += y;
+                            s[x + e] = y;
+                        }
+                    }
+                    store_weights(c, s);
                 }
                 fence_async_smem();
                 fence_before();
-            };
-            scores();
-            if (i > 0) {
-                weigh();
-            } else {
-                rise = true;                                 // no reference yet
             }
             const bool any = __syncthreads_or(rise);         // the ring's records are decoded, too
             if (warp == 1) {
@@ -394,24 +413,28 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                 // positions first, eight rows at a time, halving what a lane
                 // keeps (lanes 4 i .. 4 i + 3 end with row i)
                 fence_after();
-                if (i > 0) scores();
 #pragma unroll
-                for (int c = 0; c < NH; c += 8) {
-                    float v[8];
+                for (int c = 0; c < NH; c += CH) {
+                    float s[CH];
+                    scores(c, s);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = s[c + e];
+                    for (int x = 0; x < CH; x += 8) {
+                        float v[8];
 #pragma unroll
-                    for (int half = 4, o = 16; half >= 1; half >>= 1, o >>= 1) {
-                        const bool up = lane & o;
+                        for (int e = 0; e < 8; ++e) v[e] = s[x + e];
 #pragma unroll
-                        for (int e = 0; e < half; ++e) {
-                            const float give = up ? v[e] : v[e + half], keep = up ? v[e + half] : v[e];
-                            v[e] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
+                        for (int half = 4, o = 16; half >= 1; half >>= 1, o >>= 1) {
+                            const bool up = lane & o;
+#pragma unroll
+                            for (int e = 0; e < half; ++e) {
+                                const float give = up ? v[e] : v[e + half], keep = up ? v[e + half] : v[e];
+                                v[e] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
+                            }
                         }
+                        v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
+                        v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+                        if ((lane & 3) == 0) of_warp[quad * N + side * NH + c + x + (lane >> 2)] = v[0];
                     }
-                    v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
-                    v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
-                    if ((lane & 3) == 0) of_warp[quad * N + side * NH + c + (lane >> 2)] = v[0];
                 }
                 __syncthreads();
                 for (int n = tid; n < N; n += TT) {
@@ -419,12 +442,30 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                     const float z = m * p.scale2, r = z > ref[n] + SLACK ? z : ref[n];
                     fac[n] = ref[n] == r ? 1.f : ex2(ref[n] - r);
                     ref[n] = r;
+                    old[n] = off[n];
                     off[n] = r == NEG_INF ? 0.f : P_SHIFT - r;
                 }
                 __syncthreads();
-                if (i > 0) {
+                // The weights again.  A sum already holds this tile's weight
+                // under the old reference: it is taken out (the rounding that
+                // leaves is of the size of the new weight's own) unless the
+                // reference rose so far that what was summed before vanishes
+                // beside the position it rose to.
 #pragma unroll
-                    for (int c = 0; c < NH; ++c) l[c] *= fac[side * NH + c];
+                for (int c = 0; c < NH; c += CH) {
+                    float s[CH];
+                    scores(c, s);
+#pragma unroll
+                    for (int e = 0; e < CH; ++e) {
+                        const int n = side * NH + c + e;
+                        const float f = fac[n], y = ex2(fmaf(s[e], p.scale2, off[n]));
+                        const float both = (l[c + e] - ex2(fmaf(s[e], p.scale2, old[n]))) * f + y;
+                        l[c + e] = f < 0x1p-64f ? y : f == 1.f && i > 0 ? l[c + e] : both;
+                        s[e] = y;
+                    }
+                    store_weights(c, s);
+                }
+                if (i > 0) {
 #pragma unroll 1
                     for (int c = 0; c < NH; c += 8) {
                         float o[8];
@@ -435,11 +476,10 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                     }
                     wait_st();
                 }
-                weigh();
+                fence_async_smem();
+                fence_before();
                 __syncthreads();
             }
-#pragma unroll
-            for (int c = 0; c < NH; ++c) l[c] += s[c];
             if (tid == 0) {
                 fence_after();
 #pragma unroll

@@ -35,7 +35,7 @@ struct Cfg {
     static constexpr int CTAS = ACC >= 96 ? 2 : ACC >= 64 ? 3 : ACC <= 16 ? 6 : 4;
     static constexpr int STAGES = D == 64 ? (CTAS == 6 ? 3 : 4) : D == 128 ? (CTAS == 4 ? 2 : 3) : 2;
     static constexpr int RING = WARPS * STAGES * STAGE;
-    static constexpr int OSTRIDE = D + 8;            // floats between rows of a warp's sums at the merge
+    static constexpr int OSTRIDE = D == 256 ? D + 8 : D;          // floats between rows of a warp's sums at the merge
     static constexpr int MERGE = WARPS * ROWS * OSTRIDE * 4;
     static constexpr int BODY = RING > MERGE ? RING : MERGE;      // the merge reuses the ring
     static constexpr size_t SMEM = BODY + NR * QTILE + WARPS * STAGES * 8 + WARPS * ROWS * 8;
@@ -201,6 +201,17 @@ __device__ __forceinline__ void pv(uint32_t rec, const uint32_t (&b)[NR][2], int
     }
 }
 
+// Where a warp's sums lie at the merge: component pairs of a row are permuted
+// so that the 16 lanes of a store (four rows, four groups of components) meet 16
+// different pairs of banks (one sequence of 60000, 12 rows a head of 128: 18.8 ->
+// 17.7 us).  With the accumulators of D = 256 the permutation's registers cost
+// more than the conflicts of padded rows (64 sequences to 16411: 78.6 -> 79.7 us).
+template <int D>
+__device__ __forceinline__ int merge_swizzle(int row, int d) {
+    const int t = (row >> 1) & 3;
+    return D == 256 ? 0 : D == 64 ? t : 2 * t | ((d >> 5) & 1);
+}
+
 constexpr int MAX_CLUSTER = 16;
 
 __device__ __forceinline__ void cluster_sync() {
@@ -252,7 +263,7 @@ __device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int
 // Bound by the issue of decoding (conversion, scaling) and products, which add
 // up: 64 sequences of up to 16411 positions, 24 query over 2 kv heads of 256,
 // the call 78 us (281 MB, 3.6 TB/s).  One sequence of
-// 1031 positions, 48 over 4 heads of 128: 5.7 us, all of it latency.
+// 1031 positions, 48 over 4 heads of 128: 5.3 us, all of it latency.
 template <int D, int NR, bool SHORT>
 __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(const __grid_constant__ AttnParams p) {
     using C = Cfg<D, NR>;
@@ -468,8 +479,8 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                 for (int r = 0; r < NR; ++r)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int d = PER * (g + 8 * (x / (PER / 2))) + 2 * (x % (PER / 2));
-                        *reinterpret_cast<float2 *>(dst + (8 * r + 2 * t + e) * C::OSTRIDE + d) =
+                        const int d = PER * (g + 8 * (x / (PER / 2))) + 2 * (x % (PER / 2)), row = 8 * r + 2 * t + e;
+                        *reinterpret_cast<float2 *>(dst + row * C::OSTRIDE + (d ^ (2 * merge_swizzle<D>(row, d)))) =
                             make_float2(o[x][r][e], o[x][r][2 + e]);
                     }
         }
@@ -486,22 +497,24 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                 ml[w] = mlbuf[w * ROWS + r];
                 top = fmaxf(top, ml[w].x);
             }
+            const int sw = merge_swizzle<D>(r, d), at_r = d ^ (2 * (sw & ~1));     // the four of d: pairs change places if sw is odd
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
                 const float f = ml[w].x == NEG_INF ? 0.f : ex2(ml[w].x - top);
-                const float4 x = *reinterpret_cast<const float4 *>(obuf + (w * ROWS + r) * C::OSTRIDE + d);
+                const float4 x = *reinterpret_cast<const float4 *>(obuf + (w * ROWS + r) * C::OSTRIDE + at_r);
                 l += ml[w].y * f;
                 v.x += x.x * f;
                 v.y += x.y * f;
                 v.z += x.z * f;
                 v.w += x.w * f;
             }
+            if (sw & 1) v = make_float4(v.z, v.w, v.x, v.y);
             if (whole) {
                 write_row<D>(p, b, h, rt * ROWS + r, d, v, top, l);
             } else if constexpr (SHORT) {
                 // in warp 0's place: no other thread reads it
-                *reinterpret_cast<float4 *>(obuf + r * C::OSTRIDE + d) = v;
+                *reinterpret_cast<float4 *>(obuf + r * C::OSTRIDE + at_r) = v;
                 if (d == 0) all_ml[r] = make_float2(top, l);
             } else {
                 *reinterpret_cast<float4 *>(p.part_o + (slot * ROWS + r) * D + d) = v;
@@ -523,7 +536,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                     x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (k < CL) {
                         ml[k] = ld_peer_v2(peer(ml_at + r * 8, k));
-                        x[k] = ld_peer_v4(peer(base + (r * C::OSTRIDE + d) * 4, k));
+                        x[k] = ld_peer_v4(peer(base + (r * C::OSTRIDE + (d ^ (2 * (merge_swizzle<D>(r, d) & ~1)))) * 4, k));
                     }
                 }
                 float top = NEG_INF, l = 0.f;

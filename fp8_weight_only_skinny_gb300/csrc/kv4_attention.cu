@@ -586,12 +586,11 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
     extern __shared__ float2 ml[];                 // (reference, sum) of each part, then (weight, -)
     __shared__ float red[JT / 32], red_l[JT / 32];
     __shared__ float4 part[GROUPS][COLS];
-    // Only this call's own weights kernel may be placed early.  The next call's
-    // attention fills an SM's registers to the last block, and CTAs of it placed
-    // around this kernel's leave a hole that is too small for the last one, which
-    // then runs after the others (64 sequences of 3000, 48 query over 4 heads of
-    // 128, calls in a row: 58 us each, 42 without).
-    if (p.acc_out) sk::pdl_launch_dependents();
+    // (Here and in the weights' kernel nothing is let in early.  The kernel after
+    // it fills an SM's registers to the last block, and CTAs of it placed around
+    // this kernel's leave a hole that is too small for the last one, which then
+    // runs after the others: 64 sequences of 3000, 48 query over 4 heads of 128,
+    // calls in a row 58 us each, 42 without, with the weights 90 and 62.)
     sk::pdl_wait_primary();
     const int rows = p.M * p.G, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int which = blockIdx.x / CHUNKS, d0 = (blockIdx.x - which * CHUNKS) * DC;
@@ -661,7 +660,6 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
 template <int D>
 __global__ void __launch_bounds__(JT) kv4_join_rows_kernel(const __grid_constant__ AttnParams p, int tile_rows) {
     constexpr int PER = D / 32;                    // components per lane: two neighbouring ones, 64 apart
-    if (p.acc_out) sk::pdl_launch_dependents();    // as above
     sk::pdl_wait_primary();
     const int rows = p.M * p.G, lane = threadIdx.x & 31;
     const int which = blockIdx.x * (JT / 32) + (threadIdx.x >> 5);
@@ -725,7 +723,7 @@ __global__ void __launch_bounds__(JT) kv4_join_rows_kernel(const __grid_constant
 // during the attention the weights would need each row's final sum, which is
 // not known until its last position.)  Bound like the attention by decoding and
 // products: 23 sequences of up to 9001 positions, 2 rows, 32 over 8 heads of 64,
-// the whole call 47 us.
+// the whole call 46 us.
 constexpr int WT_TILES = 16;           // tiles of eight rows held in shared memory at a time
 constexpr int WT_STAGES = 4;
 constexpr int ACC_STEPS = 4;           // steps whose accumulated weights are on their way
@@ -753,7 +751,6 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
     if (lane == 0)
         for (int s = 0; s < WT_STAGES; ++s) sk::mbar_init(bar + s * 8, 1);
     sk::fence_barrier_init();
-    sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
     Share sh = share_of(p, p.heads, sm_share);
     uint32_t it = 0;               // steps this warp has consumed

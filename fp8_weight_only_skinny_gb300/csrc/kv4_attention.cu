@@ -877,10 +877,10 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 constexpr int MAX_SEGMENTS = 131072;
 // More query rows of a kv head than these go to the tensor-core kernel, which
 // decodes a tile once for up to 96 rows where the registers hold 24 to 32:
-// 60000 positions, 4 heads of 128, 96 rows 39 us against 53, 36 rows 28 against
-// 33, 24 rows 25.0 against 23.6; 8 heads, 28 rows, 64 sequences of 300 29.5
-// against 34.5 and 16 of 20000 143 against 148, 24 rows 28 against 30 and 142
-// against 122.
+// 60000 positions, 4 heads of 128, 96 rows 36 us against 52, 36 rows 26.6
+// against 30.3, 24 rows 24.2 against 21.4; 8 heads, 28 rows, 64 sequences of 300
+// 28 against 30 and 16 of 20000 139 against 153, 24 rows 27 against 25 and 139
+// against 118.
 constexpr int TC_ABOVE = 24;
 
 // The scratch memory's segment list and partial sums for `rows` per tile.
@@ -915,11 +915,10 @@ sk_status join(const AttnParams &p, int tile_rows, int sms, cudaStream_t s) {
 // CTAs per segment with which all segments run at a time, each CTA with few of
 // the table's tiles; 0 where there is no such number.
 // Few: one launch then takes less than two and the scratch memory's round trip
-// (48 query over 4 heads of 128, one sequence of 1031 positions 6.5 us against
-// 8.3, of 7900 9.8 against 11.1; 50 of 500 11.0 against 12.7); with eight tiles
-// each one of 16000 takes 14.1 against 13.0.  In place of the tensor cores (rows
-// above TC_ABOVE) half as many: 32 rows, one of 4000 12.0 against 12.3, of 7900
-// 15.5 against 14.6.
+// (48 query over 4 heads of 128, one sequence of 1031 positions 5.4 us against
+// 7.7, of 7900 8.4 against 9.5; 50 of up to 500 9.5 against 11.5); with eight
+// tiles each one of 16000 takes 12.5 against 11.3.  In place of the tensor cores
+// (rows above TC_ABOVE) half as many: 32 rows, one of 4000 10.1 against 12.5.
 constexpr int SHORT_TILES = 4;
 template <int D, int NR>
 int short_cluster(const AttnParams &p, int few) {

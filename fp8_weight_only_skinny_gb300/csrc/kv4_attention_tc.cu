@@ -15,8 +15,8 @@
 //
 // Bound by the softmax's and the decoding's instructions between barriers, not
 // by the products: 100003 positions of 4 heads, 8 rows of 48 query heads (96
-// rows a kv head), 47 us with the join, 420 TFLOP/s (58 MB read); with 24-row
-// tiles in registers 90 us.  The scores of a position are read from TMEM a few
+// rows a kv head), 46 us with the join, 420 TFLOP/s (58 MB read); with 24-row
+// tiles in registers 79 us.  The scores of a position are read from TMEM a few
 // rows at a time: all 48 at once leave the sums no registers (52 us).  (A ninth
 // warp for products and copies leaves 96 registers a thread: spills, 62 us.)
 #include <cuda_fp16.h>

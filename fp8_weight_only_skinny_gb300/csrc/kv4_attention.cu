@@ -958,7 +958,7 @@ sk_status attend(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s)
 }
 
 sk_status attend_tc(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
-    const int n = tc_rows(p.M * p.G, &p.RT), rows = n < 32 ? 32 : n;
+    const int rows = tc_rows(p.M * p.G, &p.RT);
     p.ctas = sms * TC_CTAS;
     if (!place_partials(p, scratch, rows, 128)) return SK_ERR_WORKSPACE;
     if (launch_tc(p, rows, s) != cudaSuccess) return SK_ERR_CUDA;

@@ -585,7 +585,7 @@ int tc_rows(int rows, int *tiles) {
 
 cudaError_t launch_tc(AttnParams &p, int n, cudaStream_t s) {
     switch (n) {
-        case 16: case 32: return launch<32>(p, s);
+        case 32: return launch<32>(p, s);
         case 48: return launch<48>(p, s);
         case 64: return launch<64>(p, s);
         case 80: return launch<80>(p, s);

@@ -26,6 +26,10 @@ constexpr int MAX_TOP = 64;
 constexpr int SOFT = 160;                // the most candidates that a round may start with
 constexpr int GROUPS = 64;               // groups of threads whose maxima bound the n-th largest
 constexpr int MAX_CLUSTER = 16;
+// Logits a row may have: indices run up to two rounds of the widest CTA past a
+// row's end, and a row is cut in MAX_CLUSTER parts rounded up, all in 31 bits.
+constexpr int MAX_N = 0x7FFF0000;
+static_assert(0x7FFFFFFF - MAX_N > 2 * WIDER * PER + MAX_CLUSTER, "indices past a row's end");
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float LOWEST = -3.402823466e38f;
 
@@ -544,7 +548,7 @@ extern "C" sk_status token_logprobs(const void *logits, int f16, long long row_s
                                     int32_t *top_ids, float *top_logprobs, int rows, int N, void *stream) {
     if (rows < 0 || N < 1 || top_n < 0 || (f16 != 0 && f16 != 1) || row_stride < N) return SK_ERR_INVALID_ARG;
     if (!(temperature >= 1e-6f && temperature <= 1e6f)) return SK_ERR_INVALID_ARG;
-    if (top_n > MAX_TOP || rows > (1 << 26)) return SK_ERR_UNSUPPORTED_SHAPE;
+    if (top_n > MAX_TOP || rows > (1 << 26) || N > MAX_N) return SK_ERR_UNSUPPORTED_SHAPE;
     if (rows == 0) return SK_OK;
     if (!logits || (top_n > 0 && (!top_ids || !top_logprobs))) return SK_ERR_INVALID_ARG;
     if (!tokens && (logprob || rank)) return SK_ERR_INVALID_ARG;

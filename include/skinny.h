@@ -381,7 +381,8 @@ SK_API sk_status kv4_evict(uint8_t *cache, const int32_t *table, const int32_t *
  *            faster)
  *   tokens   const i32 [rows], or NULL (then logprob and rank are NULL too)
  *   logprob, rank and entropy may each be NULL; 1e-6 <= temperature <= 1e6;
- *   0 <= top_n <= 64 (larger: SK_ERR_UNSUPPORTED_SHAPE).
+ *   0 <= top_n <= 64, N <= 2^31 - 65536, rows <= 2^26 (larger:
+ *   SK_ERR_UNSUPPORTED_SHAPE).
  *   Masked logits may be minus infinity or the type's lowest value: their
  *   probability is zero.  A row of only minus infinity gives log probabilities
  *   of minus infinity and entropy 0.  A NaN or plus infinity in a row makes its

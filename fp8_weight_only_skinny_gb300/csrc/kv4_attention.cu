@@ -1007,6 +1007,10 @@ extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint
         return SK_ERR_INVALID_ARG;
     if (q_heads % kv_heads) return SK_ERR_INVALID_ARG;
     if (!sk::kv4_scale_ok(k_scale) || !sk::kv4_scale_ok(v_scale) || !(scale > 0.f && scale < 1e20f)) return SK_ERR_INVALID_ARG;
+    // The kernels use the product: it neither vanishes nor is infinite, nor is
+    // SLACK divided by it or the largest score (256 65504 2688) multiplied.
+    const double product = double(scale) * double(k_scale);
+    if (!(product >= 1e-37 && product <= 1e27)) return SK_ERR_INVALID_ARG;
     if (!sk::kv4_shape_ok(pages, kv_heads, head_dim, page_size)) return SK_ERR_UNSUPPORTED_SHAPE;
     if ((long long)table_width * page_size > 0x7FFFFF00LL) return SK_ERR_UNSUPPORTED_SHAPE;
     if (seqs == 0) return SK_OK;
@@ -1046,7 +1050,7 @@ extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint
     p.by_recs = sk::Div(p.recs);
     p.width = table_width;
     p.cap = table_width * page_size;
-    p.scale2 = scale * k_scale * LOG2E;
+    p.scale2 = float(product * double(LOG2E));
     p.vg = v_scale;
     switch (head_dim) {
         case 64: return run<64>(p, sc.base, sc.num_sms, s);

@@ -239,7 +239,7 @@ __device__ __forceinline__ float4 ld_peer_v4(uint32_t addr) {
 }
 
 // Four components of query row r of a segment, and its log sum, from the sums
-// under the reference `top`.
+// under the base `top`.
 template <int D>
 __device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int row, int d, const float4 &v, float top, float l) {
     const int m = row / p.G;
@@ -248,12 +248,12 @@ __device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int
     const __half2 y0 = __floats2half2_rn(v.x * f, v.y * f), y1 = __floats2half2_rn(v.z * f, v.w * f);
     uint2 y = make_uint2(*reinterpret_cast<const uint32_t *>(&y0), *reinterpret_cast<const uint32_t *>(&y1));
     *reinterpret_cast<uint2 *>(p.out + to * D + d) = y;
-    if (d == 0 && p.lse) p.lse[to] = l == 0.f ? NEG_INF : (top + __log2f(l) - P_SHIFT) * LN2;
+    if (d == 0 && p.lse) p.lse[to] = log_sum(p, top, l);
 }
 
 // Each warp streams its own steps of 32 positions (bulk copies into a ring of
 // its own, issued by one lane a ring's length ahead) and keeps 8 NR query rows'
-// references, sums and outputs in registers; the four warps meet only at the
+// bases, sums and outputs in registers; the four warps meet only at the
 // end of a segment (sequence, head, row tile).
 //
 // SHORT: a cluster per segment, each CTA the same number of the table's tiles,
@@ -359,14 +359,13 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
         __syncthreads();       // the query rows are in shared memory
 
         float o[D / 16][NR][4];
-        // per row 2 t + e of tile r: the reference, P_SHIFT minus it, the score that passes it by SLACK, the sum
-        float ref[NR][2], off[NR][2], high[NR][2], sum[NR][2];
+        float neg[NR][2], sum[NR][2];              // per row 2 t + e of tile r: minus the base, the sum
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                ref[r][e] = high[r][e] = NEG_INF;
-                off[r][e] = sum[r][e] = 0.f;
+                neg[r][e] = NO_BASE;
+                sum[r][e] = 0.f;
             }
 #pragma unroll
             for (int x = 0; x < D / 16; ++x)
@@ -411,7 +410,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                     for (int e = 0; e < 2; ++e) {
                         top[r][e] = fmaxf(s[0][r][e], s[0][r][2 + e]);
                         if constexpr (NX == 2) top[r][e] = fmaxf(top[r][e], fmaxf(s[1][r][e], s[1][r][2 + e]));
-                        rise |= top[r][e] > high[r][e];
+                        rise |= passes(p, top[r][e], neg[r][e]);
                     }
                 if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
@@ -422,11 +421,9 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                            const float now_ref = fmaxf(ref[r][e], m * p.scale2);
-                            const float f = ref[r][e] == now_ref ? 1.f : ex2(ref[r][e] - now_ref);
-                            ref[r][e] = now_ref;
-                            off[r][e] = now_ref == NEG_INF ? 0.f : P_SHIFT - now_ref;
-                            high[r][e] = (now_ref + SLACK) / p.scale2;
+                            const float had = neg[r][e];
+                            neg[r][e] = fminf(had, neg_base(p, m));
+                            const float f = rebase(p, neg[r][e], had);
                             sum[r][e] *= f;
 #pragma unroll
                             for (int x = 0; x < D / 16; ++x) {
@@ -442,8 +439,8 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                     for (int r = 0; r < NR; ++r)
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            const float p0 = ex2(fmaf(s[x][r][2 * y], p.scale2, off[r][0]));
-                            const float p1 = ex2(fmaf(s[x][r][2 * y + 1], p.scale2, off[r][1]));
+                            const float2 w2 = weights2(p, s[x][r][2 * y], s[x][r][2 * y + 1], neg[r][0], neg[r][1]);
+                            const float p0 = w2.x, p1 = w2.y;
                             sum[r][0] += p0;
                             sum[r][1] += p1;
                             w[r][y] = transpose8(pack_f16(p0, p1));
@@ -467,7 +464,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                 sum[r][e] += __shfl_xor_sync(0xffffffffu, sum[r][e], 4);
                 sum[r][e] += __shfl_xor_sync(0xffffffffu, sum[r][e], 8);
                 sum[r][e] += __shfl_xor_sync(0xffffffffu, sum[r][e], 16);
-                if (g == 0) mlbuf[warp * ROWS + 8 * r + 2 * t + e] = make_float2(ref[r][e], sum[r][e]);
+                if (g == 0) mlbuf[warp * ROWS + 8 * r + 2 * t + e] = make_float2(-neg[r][e], sum[r][e]);
             }
         __syncthreads();       // every warp is done with its ring
         {
@@ -501,7 +498,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
-                const float f = ml[w].x == NEG_INF ? 0.f : ex2(ml[w].x - top);
+                const float f = rebase(p, ml[w].x, top);
                 const float4 x = *reinterpret_cast<const float4 *>(obuf + (w * ROWS + r) * C::OSTRIDE + at_r);
                 l += ml[w].y * f;
                 v.x += x.x * f;
@@ -545,7 +542,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < MAX_CLUSTER; ++k) {
-                    const float f = ml[k].x == NEG_INF ? 0.f : ex2(ml[k].x - top);
+                    const float f = rebase(p, ml[k].x, top);
                     l += ml[k].y * f;
                     v.x += x[k].x * f;
                     v.y += x[k].y * f;
@@ -575,7 +572,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
 }
 
 // DC components of a query row per CTA: the partial sums of its segment, in the
-// order of the CTAs that wrote them, joined under the common reference.  DC / 4
+// order of the CTAs that wrote them, joined under the largest base.  DC / 4
 // threads take a part at a time, 1024 / DC parts together.  Rows of an empty
 // sequence are written here too (zero, with a log sum of minus infinity).
 constexpr int JT = 256;
@@ -583,7 +580,7 @@ constexpr int JT = 256;
 template <int D, int DC>
 __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ AttnParams p, int tile_rows) {
     constexpr int COLS = DC / 4, GROUPS = JT / COLS, CHUNKS = D / DC;
-    extern __shared__ float2 ml[];                 // (reference, sum) of each part, then (weight, -)
+    extern __shared__ float2 ml[];                 // (base, sum) of each part, then (factor, -)
     __shared__ float red[JT / 32], red_l[JT / 32];
     __shared__ float4 part[GROUPS][COLS];
     // (Here and in the weights' kernel nothing is let in early.  The kernel after
@@ -622,7 +619,7 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
     for (int w = 0; w < JT / 32; ++w) top = fmaxf(top, red[w]);
     float l = 0.f;
     for (int i = tid; i < n; i += JT) {
-        const float f = ml[i].x == NEG_INF ? 0.f : ex2(ml[i].x - top);
+        const float f = rebase(p, ml[i].x, top);
         l += ml[i].y * f;
         ml[i].x = f;
     }
@@ -653,7 +650,7 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
         for (int w = 0; w < GROUPS; ++w) y += reinterpret_cast<const float *>(part[w])[d];
         p.out[at * D + d0 + d] = __float2half_rn(l == 0.f ? 0.f : y * (p.vg / l));
     }
-    if (tid == 0 && d0 == 0 && p.lse) p.lse[at] = l == 0.f ? NEG_INF : (top + __log2f(l) - P_SHIFT) * LN2;
+    if (tid == 0 && d0 == 0 && p.lse) p.lse[at] = log_sum(p, top, l);
 }
 
 // The same with a warp per row, for segments of few parts: no barriers.
@@ -682,14 +679,14 @@ __global__ void __launch_bounds__(JT) kv4_join_rows_kernel(const __grid_constant
     float top = NEG_INF, l = 0.f, v[PER];
 #pragma unroll
     for (int x = 0; x < PER; ++x) v[x] = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 32) {           // 32 parts at a time, under the reference so far
+    for (int i0 = 0; i0 < n; i0 += 32) {           // 32 parts at a time, under the largest base so far
         float2 ml = make_float2(NEG_INF, 0.f);
         if (i0 + lane < n) ml = *reinterpret_cast<const float2 *>(p.part_ml + (slot(i0 + lane) * tile_rows + r) * 2);
         float now = ml.x;
 #pragma unroll
         for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
         now = fmaxf(now, top);
-        const float old = top == now ? 1.f : ex2(top - now), f = ml.x == NEG_INF ? 0.f : ex2(ml.x - now);
+        const float old = rebase(p, top, now), f = rebase(p, ml.x, now);
         top = now;
         float add = ml.y * f;
 #pragma unroll
@@ -713,7 +710,7 @@ __global__ void __launch_bounds__(JT) kv4_join_rows_kernel(const __grid_constant
     const float f = l == 0.f ? 0.f : p.vg / l;
 #pragma unroll
     for (int x = 0; x < PER / 2; ++x) out[32 * x] = __floats2half2_rn(v[2 * x] * f, v[2 * x + 1] * f);
-    if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? NEG_INF : (top + __log2f(l) - P_SHIFT) * LN2;
+    if (lane == 0 && p.lse) p.lse[at] = log_sum(p, top, l);
 }
 
 // acc_out = acc_in + the weights of all query rows, per position and kv head:
@@ -830,8 +827,8 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             float *v = s[x >> 1][0] + 2 * (x & 1);
-                            v[0] = ex2(fmaf(v[0], p.scale2, -neg.x));
-                            v[1] = ex2(fmaf(v[1], p.scale2, -neg.y));
+                            v[0] = ex2(fmaf(v[0], p.c, -neg.x));
+                            v[1] = ex2(fmaf(v[1], p.c, -neg.y));
                         }
                         if (edge) {
 #pragma unroll
@@ -1008,7 +1005,7 @@ extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint
     if (q_heads % kv_heads) return SK_ERR_INVALID_ARG;
     if (!sk::kv4_scale_ok(k_scale) || !sk::kv4_scale_ok(v_scale) || !(scale > 0.f && scale < 1e20f)) return SK_ERR_INVALID_ARG;
     // The kernels use the product: it neither vanishes nor is infinite, nor is
-    // SLACK divided by it or the largest score (256 65504 2688) multiplied.
+    // P_SHIFT + SLACK divided by it or the largest score (256 65504 2688) multiplied.
     const double product = double(scale) * double(k_scale);
     if (!(product >= 1e-37 && product <= 1e27)) return SK_ERR_INVALID_ARG;
     if (!sk::kv4_shape_ok(pages, kv_heads, head_dim, page_size)) return SK_ERR_UNSUPPORTED_SHAPE;
@@ -1050,7 +1047,9 @@ extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint
     p.by_recs = sk::Div(p.recs);
     p.width = table_width;
     p.cap = table_width * page_size;
-    p.scale2 = float(product * double(LOG2E));
+    p.c = float(product * double(LOG2E));
+    p.shift = P_SHIFT / p.c;
+    p.reach = (P_SHIFT + SLACK) / p.c;
     p.vg = v_scale;
     switch (head_dim) {
         case 64: return run<64>(p, sc.base, sc.num_sms, s);

@@ -20,12 +20,20 @@ constexpr int TILE = WARPS * STEP;
 constexpr int NROW = 8;                // query rows per n8 tile
 constexpr float NEG_INF = -__builtin_huge_valf();
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-// Each row's weights are taken against a reference r, p = 2^(z - r + P_SHIFT):
-// any r gives the same quotient, so r is a maximum the row had earlier and is
-// moved only when a score passes it by more than SLACK (then the sums so far
-// are scaled).  Most steps need neither the row's maximum across lanes nor a
-// rescaling.  The p go to the second product in FP16, at most 2^(P_SHIFT +
-// SLACK) = 2^15 and normal down to 2^-21 of r's (2^-32 is the rounding of the
+// Each row's weights are taken against a base, a score in the units of q . k:
+// p = 2^((s - base) c) with c = scale * key scale * log2 e.  Any base gives the
+// same quotient, so it is P_SHIFT / c below a maximum the row had earlier and is
+// moved only when a score passes that maximum by more than SLACK / c (then the
+// sums so far are scaled).  Most steps need neither the row's maximum across
+// lanes nor a rescaling.  The base is subtracted before anything is scaled: the
+// difference of neighbouring numbers is exact, so that weights near the maximum
+// are right whatever the scores' size (c s - c base, each rounded by itself, is
+// off by up to 2^5 where the scores are 2^28, and the FP16 weights overflow or
+// vanish); two scores at a time, an add and a multiply of f32x2, that costs what
+// an fma each did (0.98 to 1.02 of it, over eighteen shapes).  A base is rounded
+// such that (s - base) c is between 0 and P_SHIFT for the maximum, and moves when
+// that exceeds P_SHIFT + SLACK.  The p go to the second product in FP16, at most
+// 2^15 and normal down to 2^-21 of the maximum's (2^-32 is the rounding of the
 // smaller ones).  Their rounding (2^-11 relative at most, independent from
 // position to position) is of the size of the output's own rounding to FP16;
 // the sum of the weights is taken from the unrounded FP32 values.
@@ -45,7 +53,7 @@ struct AttnParams {
     unsigned int *err;
     int pages, heads, recs, width, cap;   // recs: records per page; cap: positions the table can hold
     int B, M, G, RT, ctas;     // G: query heads per kv head; RT: row tiles
-    float scale2, vg;          // scale * key scale * log2 e; value scale
+    float c, shift, reach, vg; // scale * key scale * log2 e; P_SHIFT / c; (P_SHIFT + SLACK) / c; value scale
     sk::Div by_recs;
 };
 
@@ -53,6 +61,31 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Rows keep minus their base.  NO_BASE: no score seen yet; any score passes it,
+// and the sums under it are zero.
+constexpr float NO_BASE = 3.402823466e38f;
+// Minus the base for a maximum of m, rounded so that the base is at or above
+// P_SHIFT / c below m (and at most m: m itself is among the numbers rounded to).
+__device__ __forceinline__ float neg_base(const AttnParams &p, float m) { return __fadd_rd(p.shift, -m); }
+// Whether the score s makes its row's base move.
+__device__ __forceinline__ bool passes(const AttnParams &p, float s, float neg) { return s + neg > p.reach; }
+// A weight of the score s.
+__device__ __forceinline__ float weight(const AttnParams &p, float s, float neg) { return ex2((s + neg) * p.c); }
+// Two weights at a time.
+__device__ __forceinline__ float2 weights2(const AttnParams &p, float s0, float s1, float n0, float n1) {
+    float2 d;
+    asm("{ .reg .b64 s, n, c; mov.b64 s, {%2, %3}; mov.b64 n, {%4, %5}; mov.b64 c, {%6, %6};\n\t"
+        "add.rn.f32x2 s, s, n; mul.rn.f32x2 s, s, c; mov.b64 {%0, %1}, s; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(s0), "f"(s1), "f"(n0), "f"(n1), "f"(p.c));
+    return make_float2(ex2(d.x), ex2(d.y));
+}
+// What sums under one base are multiplied by to stand under another.
+__device__ __forceinline__ float rebase(const AttnParams &p, float from, float to) { return ex2((from - to) * p.c); }
+// The natural log of a row's sum l of weights under a base.
+__device__ __forceinline__ float log_sum(const AttnParams &p, float base, float l) {
+    return l == 0.f ? NEG_INF : fmaf(base, p.c, __log2f(l)) * LN2;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {

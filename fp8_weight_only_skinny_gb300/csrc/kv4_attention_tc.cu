@@ -8,7 +8,7 @@
 //     O (128 x N, TMEM) += V^T (128 x 128) . p^T     A: values decoded into
 //                                                    shared memory, read along d
 // so decoded keys never pass through shared memory, and both accumulators are
-// N columns.  A thread of the softmax holds one position: the row references
+// N columns.  A thread of the softmax holds one position: the row bases
 // are the same for all threads and move rarely (kv4_attention.cuh), and the sums
 // of the weights are added up across positions once per segment.  Two CTAs
 // share an SM: one's decoding covers the other's products and softmax.
@@ -39,16 +39,16 @@ constexpr int TT = 256;                // threads: eight warps
 constexpr int REC = sk::kv4_rec_bytes(D);
 constexpr int PART = REC / 2;          // the keys' or the values' half of a record
 constexpr int UNIT = 8 * PART;         // of a tile's eight records: the unit of the ring
-constexpr float MOST_WEIGHT = 32768.f; // 2^(P_SHIFT + SLACK): a larger weight moves its row's reference
+constexpr float MOST_WEIGHT = 32768.f; // 2^(P_SHIFT + SLACK): a larger weight moves its row's base
 static_assert(P_SHIFT + SLACK == 15.f, "MOST_WEIGHT");
 
 template <int N>
 struct Tc {
     static constexpr int UNITS = N <= 64 ? 4 : 3;
     static constexpr int V = 0, Q = V + 128 * D * 2, P = Q + N * D * 2, RAW = P + N * 128 * 2, SMALL = RAW + UNITS * UNIT;
-    // per row: reference, P_SHIFT minus it, that before it moved, a factor, the first unseen position; four
-    // warps' values of each row; barriers of the ring and of the two products; the TMEM address
-    static constexpr int REF = SMALL, OFF = REF + 4 * N, OLD = OFF + 4 * N, FAC = OLD + 4 * N, LIM = FAC + 4 * N,
+    // per row: minus its base, that before it moved, a factor, the first unseen position; four warps' values of each
+    // row; barriers of the ring and of the two products; the TMEM address
+    static constexpr int NEG = SMALL, OLD = NEG + 4 * N, FAC = OLD + 4 * N, LIM = FAC + 4 * N,
                          WARP = LIM + 4 * N, BARS = WARP + 16 * N, TMEM = BARS + 8 * (UNITS + 2);
     static constexpr size_t SMEM = 1024 + TMEM + 16;
     static constexpr int S_COL = 64, O_COL = 64 + N;         // TMEM columns: keys 0..63, S, O
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
     const int quad = warp & 3, side = warp >> 2;             // this warp's TMEM lanes and its half of the columns
     const uint32_t base = (sk::smem_u32(dyn) + 1023u) & ~1023u;
     unsigned char *const smem = dyn + (base - sk::smem_u32(dyn));
-    float *const ref = reinterpret_cast<float *>(smem + C::REF), *const off = reinterpret_cast<float *>(smem + C::OFF);
+    float *const neg = reinterpret_cast<float *>(smem + C::NEG);
     float *const old = reinterpret_cast<float *>(smem + C::OLD), *const fac = reinterpret_cast<float *>(smem + C::FAC);
     int *const lim = reinterpret_cast<int *>(smem + C::LIM);
     float *const of_warp = reinterpret_cast<float *>(smem + C::WARP);
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             if (load)
                 sk::bulk_load(base + C::RAW + slot * UNIT + lane * PART, p.cache + size_t(idx) * REC + (u & 1) * PART, PART, bar);
         };
-        // rows: query, reference, first unseen position
+        // rows: query, base, first unseen position
         uint2 qv[N / 8];                                     // on their way before the first copies
         const int qc = tid & 31;                             // eight bytes: j = c / 4, t = c % 4
 #pragma unroll
@@ -310,8 +310,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
         for (int x = 0; x < N / 8; ++x)
             *reinterpret_cast<uint2 *>(smem + C::Q + q_at + x * 1024) = qv[x];
         for (int n = tid; n < N; n += TT) {
-            ref[n] = NEG_INF;
-            off[n] = 0.f;
+            neg[n] = NO_BASE;
             lim[n] = len - (p.M - 1 - min((rt * N + n) / p.G, p.M - 1));
         }
         float l[NH];
@@ -379,7 +378,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                     st_shared_v4(base + C::P + (side * NH + c + x) / 8 * 2048 + at * 16, w[0], w[1], w[2], w[3]);
                 }
             };
-            bool rise = i == 0;                              // whether a score has passed its row's reference
+            bool rise = i == 0;                              // whether a score has passed its row's base
             if (i > 0) {
 #pragma unroll
                 for (int c = 0; c < NH; c += CH) {
@@ -387,14 +386,16 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                     scores(c, s);
 #pragma unroll
                     for (int x = 0; x < CH; x += 8) {
-                        float of[8];
-                        row8(off + side * NH + c + x, of);
+                        float m[8];
+                        row8(neg + side * NH + c + x, m);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float y = ex2(fmaf(s[x + e], p.scale2, of[e]));
-                            rise |= y > MOST_WEIGHT;
-                            l[c + x + e] += y;
-                            s[x + e] = y;
+                        for (int e = 0; e < 8; e += 2) {
+                            const float2 y = weights2(p, s[x + e], s[x + e + 1], m[e], m[e + 1]);
+                            rise |= y.x > MOST_WEIGHT || y.y > MOST_WEIGHT;
+                            l[c + x + e] += y.x;
+                            l[c + x + e + 1] += y.y;
+                            s[x + e] = y.x;
+                            s[x + e + 1] = y.y;
                         }
                     }
                     store_weights(c, s);
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                 idx2 = idx3;
             }
             if (any) {
-                // move the references: each row's maximum over this warp's
+                // move the bases: each row's maximum over this warp's
                 // positions first, eight rows at a time, halving what a lane
                 // keeps (lanes 4 i .. 4 i + 3 end with row i)
                 fence_after();
@@ -439,17 +440,16 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                 __syncthreads();
                 for (int n = tid; n < N; n += TT) {
                     const float m = fmaxf(fmaxf(of_warp[n], of_warp[N + n]), fmaxf(of_warp[2 * N + n], of_warp[3 * N + n]));
-                    const float z = m * p.scale2, r = z > ref[n] + SLACK ? z : ref[n];
-                    fac[n] = ref[n] == r ? 1.f : ex2(ref[n] - r);
-                    ref[n] = r;
-                    old[n] = off[n];
-                    off[n] = r == NEG_INF ? 0.f : P_SHIFT - r;
+                    const float had = neg[n], now = passes(p, m, had) ? fminf(had, neg_base(p, m)) : had;
+                    fac[n] = rebase(p, now, had);
+                    old[n] = had;
+                    neg[n] = now;
                 }
                 __syncthreads();
                 // The weights again.  A sum already holds this tile's weight
-                // under the old reference: it is taken out (the rounding that
+                // under the old base: it is taken out (the rounding that
                 // leaves is of the size of the new weight's own) unless the
-                // reference rose so far that what was summed before vanishes
+                // base rose so far that what was summed before vanishes
                 // beside the position it rose to.
 #pragma unroll
                 for (int c = 0; c < NH; c += CH) {
@@ -458,9 +458,9 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
 #pragma unroll
                     for (int e = 0; e < CH; ++e) {
                         const int n = side * NH + c + e;
-                        const float f = fac[n], y = ex2(fmaf(s[e], p.scale2, off[n]));
-                        const float both = (l[c + e] - ex2(fmaf(s[e], p.scale2, old[n]))) * f + y;
-                        l[c + e] = f < 0x1p-64f ? y : f == 1.f && i > 0 ? l[c + e] : both;
+                        const float f = fac[n], y = weight(p, s[e], neg[n]);
+                        const float both = (l[c + e] - weight(p, s[e], old[n])) * f + y;
+                        l[c + e] = i == 0 || f < 0x1p-64f ? y : f == 1.f ? l[c + e] : both;
                         s[e] = y;
                     }
                     store_weights(c, s);
@@ -527,9 +527,9 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                 const int row = rt * N + n, m = row / p.G;
                 const long long to = ((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G;
                 lim[n] = int(to - ((long long)b * p.M * p.heads * p.G));       // the row within its sequence
-                if (p.lse) p.lse[to] = sum == 0.f ? NEG_INF : (ref[n] + __log2f(sum) - P_SHIFT) * LN2;
+                if (p.lse) p.lse[to] = log_sum(p, -neg[n], sum);
             } else {
-                *reinterpret_cast<float2 *>(p.part_ml + (slot * N + n) * 2) = make_float2(ref[n], sum);
+                *reinterpret_cast<float2 *>(p.part_ml + (slot * N + n) * 2) = make_float2(-neg[n], sum);
             }
         }
         __syncthreads();

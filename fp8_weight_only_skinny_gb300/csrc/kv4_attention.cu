@@ -1005,9 +1005,11 @@ extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint
     if (q_heads % kv_heads) return SK_ERR_INVALID_ARG;
     if (!sk::kv4_scale_ok(k_scale) || !sk::kv4_scale_ok(v_scale) || !(scale > 0.f && scale < 1e20f)) return SK_ERR_INVALID_ARG;
     // The kernels use the product: it neither vanishes nor is infinite, nor is
-    // P_SHIFT + SLACK divided by it or the largest score (256 65504 2688) multiplied.
+    // the largest score (256 65504 2688) times it, nor P_SHIFT + SLACK divided by
+    // it; and it takes NO_BASE far enough from any base that a sum under NO_BASE
+    // counts for nothing (2^-64).
     const double product = double(scale) * double(k_scale);
-    if (!(product >= 1e-37 && product <= 1e27)) return SK_ERR_INVALID_ARG;
+    if (!(product >= 5e-37 && product <= 1e27)) return SK_ERR_INVALID_ARG;
     if (!sk::kv4_shape_ok(pages, kv_heads, head_dim, page_size)) return SK_ERR_UNSUPPORTED_SHAPE;
     if ((long long)table_width * page_size > 0x7FFFFF00LL) return SK_ERR_UNSUPPORTED_SHAPE;
     if (seqs == 0) return SK_OK;

@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                         const int n = side * NH + c + e;
                         const float f = fac[n], y = weight(p, s[e], neg[n]);
                         const float both = (l[c + e] - weight(p, s[e], old[n])) * f + y;
-                        l[c + e] = i == 0 || f < 0x1p-64f ? y : f == 1.f ? l[c + e] : both;
+                        l[c + e] = f < 0x1p-64f ? y : f == 1.f && i > 0 ? l[c + e] : both;
                         s[e] = y;
                     }
                     store_weights(c, s);

@@ -321,7 +321,7 @@ SK_API sk_status kv4_append(const void *k, long long k_stride, const void *v, lo
  *     p = softmax_j(scale * q . k_j),  out = sum_j p_j v_j,  lse = ln sum_j exp(scale * q . k_j)
  *   q       const f16 [seqs * M][q_heads][D], q_stride elements from row to row
  *           (a multiple of 8, >= q_heads * D), 16-byte aligned
- *   scale   0 < scale < 1e20 (usually 1 / sqrt(D)), 1e-37 <= scale * k_scale <= 1e27
+ *   scale   0 < scale < 1e20 (usually 1 / sqrt(D)), 5e-37 <= scale * k_scale <= 1e27
  *   out     f16 [seqs * M][q_heads][D], 16-byte aligned
  *   lse     f32 [seqs * M][q_heads], or NULL
  *   acc_in  const f32 [seqs][kv_heads][table_width * page_size], or NULL (zeros)

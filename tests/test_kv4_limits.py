@@ -25,7 +25,7 @@ def _attn(scale, kg, B=1):
     return sk.lib.kv4_attention(A, 6144, A, A, A, kg, 0.02, scale, A, A, None, None, B, 1, 48, 4, 128, 4, 64, 2, None)
 
 
-@pytest.mark.parametrize("scale,kg", [(1e-30, 1e-20), (1e-24, 1e-20), (1e-18, 1e-20), (1e-37, 0.02), (1e19, 1e20), (1e8, 1e20),
+@pytest.mark.parametrize("scale,kg", [(1e-30, 1e-20), (1e-24, 1e-20), (1e-18, 1e-20), (1e-37, 0.02), (1e-37, 4.0), (1e19, 1e20), (1e8, 1e20),
                                       (9e19, 2e7)])
 def test_scale_times_key_scale_out_of_range(scale, kg):
     """Their product, by which scores are multiplied and the softmax's slack divided, is neither lost nor infinite, nor

@@ -238,7 +238,7 @@ __device__ __forceinline__ float4 ld_peer_v4(uint32_t addr) {
     return v;
 }
 
-// Four components of query row r of a segment, and its log sum, from the sums
+// Four components of query row r of a segment, and its statistics, from the sums
 // under the base `top`.
 template <int D>
 __device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int row, int d, const float4 &v, float top, float l) {
@@ -248,7 +248,7 @@ __device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int
     const __half2 y0 = __floats2half2_rn(v.x * f, v.y * f), y1 = __floats2half2_rn(v.z * f, v.w * f);
     uint2 y = make_uint2(*reinterpret_cast<const uint32_t *>(&y0), *reinterpret_cast<const uint32_t *>(&y1));
     *reinterpret_cast<uint2 *>(p.out + to * D + d) = y;
-    if (d == 0 && p.lse) p.lse[to] = log_sum(p, top, l);
+    if (d == 0) write_stats(p, to, top, l);
 }
 
 // Each warp streams its own steps of 32 positions (bulk copies into a ring of
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const __grid_constant__ At
         for (int w = 0; w < GROUPS; ++w) y += reinterpret_cast<const float *>(part[w])[d];
         p.out[at * D + d0 + d] = __float2half_rn(l == 0.f ? 0.f : y * (p.vg / l));
     }
-    if (tid == 0 && d0 == 0 && p.lse) p.lse[at] = log_sum(p, top, l);
+    if (tid == 0 && d0 == 0) write_stats(p, at, top, l);
 }
 
 // The same with a warp per row, for segments of few parts: no barriers.
@@ -710,12 +710,12 @@ __global__ void __launch_bounds__(JT) kv4_join_rows_kernel(const __grid_constant
     const float f = l == 0.f ? 0.f : p.vg / l;
 #pragma unroll
     for (int x = 0; x < PER / 2; ++x) out[32 * x] = __floats2half2_rn(v[2 * x] * f, v[2 * x + 1] * f);
-    if (lane == 0 && p.lse) p.lse[at] = log_sum(p, top, l);
+    if (lane == 0) write_stats(p, at, top, l);
 }
 
 // acc_out = acc_in + the weights of all query rows, per position and kv head:
-// the scores once more (the keys alone are read), against the rows' final log
-// sums.  A warp owns the 32 positions of a step, whose sum over the rows is
+// the scores once more (the keys alone are read), against the rows' final bases
+// and sums.  A warp owns the 32 positions of a step, whose sum over the rows is
 // taken in one order; the next step's keys are on their way meanwhile.  (Taken
 // during the attention the weights would need each row's final sum, which is
 // not known until its last position.)  Bound like the attention by decoding and
@@ -741,7 +741,8 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
     using C = WeightsCfg<D>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int sm_share[WARPS + 2];
-    __shared__ float lse2[WT_TILES * NROW];
+    // minus each row's base, and minus log2 of its sum
+    __shared__ __align__(8) float neg[WT_TILES * NROW], neg_g[WT_TILES * NROW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t base = sk::smem_u32(smem), qs = base + C::FIXED;
     const uint32_t ring = base + warp * WT_STAGES * C::STAGE, bar = base + C::RING + warp * WT_STAGES * 8;
@@ -793,10 +794,11 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
             for (int x = tid; x < nr * (D / 32) * 32; x += CT) store_q(qs, x, fetch_q<D>(p, b, h, r0 * NROW, x));
             for (int x = tid; x < nr * NROW; x += CT) {
                 const int row = r0 * NROW + x, m = row / p.G;
-                float v = NEG_INF;
-                if (row < rows) v = p.lse[((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G];
-                // a row that sees nothing (or does not exist) gives no weight: 2^(z - huge) = 0
-                lse2[x] = v == NEG_INF ? 3e38f : v * LOG2E;
+                // a row that sees nothing (or does not exist) gives no weight: 2^-inf
+                float2 v = make_float2(0.f, -NEG_INF);
+                if (row < rows) v = p.norm[((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G];
+                neg[x] = v.x;
+                neg_g[x] = -v.y;
             }
             __syncthreads();
             const float *old = r0 == 0 ? p.acc_in : p.acc_out;
@@ -823,12 +825,14 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
                     for (int r = 0; r < nr; ++r) {
                         float s[2][1][4];
                         qk<D, 2, 1>(k, qs + r * C::QTILE, lane, s);
-                        const float2 neg = *reinterpret_cast<const float2 *>(&lse2[r * NROW + 2 * t]);
+                        const float2 n = *reinterpret_cast<const float2 *>(&neg[r * NROW + 2 * t]);
+                        const float2 ng = *reinterpret_cast<const float2 *>(&neg_g[r * NROW + 2 * t]);
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
                             float *v = s[x >> 1][0] + 2 * (x & 1);
-                            v[0] = ex2(fmaf(v[0], p.c, -neg.x));
-                            v[1] = ex2(fmaf(v[1], p.c, -neg.y));
+                            const float2 y = weights2(p, v[0], v[1], n, ng);
+                            v[0] = y.x;
+                            v[1] = y.y;
                         }
                         if (edge) {
 #pragma unroll
@@ -880,13 +884,21 @@ constexpr int MAX_SEGMENTS = 131072;
 // against 118.
 constexpr int TC_ABOVE = 24;
 
-// The scratch memory's segment list and partial sums for `rows` per tile.
-bool place_partials(AttnParams &p, unsigned char *scratch, int rows, int D) {
+// The scratch memory: the segment list, the rows' statistics where weights are
+// accumulated (16 MiB at most: MAX_SEGMENTS tiles of 16 rows), and in the rest
+// the partial sums for `rows` per tile.
+unsigned char *place_rows(AttnParams &p, unsigned char *scratch) {
     p.seg = reinterpret_cast<int2 *>(scratch);
-    p.part_ml = reinterpret_cast<float *>(scratch + size_t(MAX_SEGMENTS) * sizeof(int2));
+    scratch += size_t(MAX_SEGMENTS) * sizeof(int2);
+    if (!p.acc_out) return scratch;
+    p.norm = reinterpret_cast<float2 *>(scratch);
+    return scratch + (size_t(p.B) * p.heads * p.M * p.G * sizeof(float2) + 255) / 256 * 256;
+}
+bool place_partials(AttnParams &p, unsigned char *rest, int rows, int D) {
+    p.part_ml = reinterpret_cast<float *>(rest);
     p.part_o = p.part_ml + size_t(p.ctas) * 2 * rows * 2;
-    return size_t(reinterpret_cast<unsigned char *>(p.part_o + size_t(p.ctas) * 2 * rows * D) - scratch) <=
-           sk::SCRATCH_BYTES;
+    return size_t(reinterpret_cast<unsigned char *>(p.part_o + size_t(p.ctas) * 2 * rows * D) -
+                  reinterpret_cast<unsigned char *>(p.seg)) <= sk::SCRATCH_BYTES;
 }
 
 template <int D>
@@ -942,22 +954,22 @@ bool attend_short(const AttnParams &p, int few, cudaStream_t s, sk_status *st) {
 }
 
 template <int D, int NR>
-sk_status attend(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
+sk_status attend(AttnParams &p, unsigned char *rest, int sms, cudaStream_t s) {
     using C = Cfg<D, NR>;
     sk_status st;
     if (attend_short<D, NR>(p, SHORT_TILES, s, &st)) return st;
     p.ctas = sms * C::CTAS;
-    if (!place_partials(p, scratch, C::ROWS, D)) return SK_ERR_WORKSPACE;
+    if (!place_partials(p, rest, C::ROWS, D)) return SK_ERR_WORKSPACE;
     if (sk::prepare_kernel<kv4_attention_kernel<D, NR, false>>(C::SMEM) != cudaSuccess) return SK_ERR_CUDA;
     if (sk::launch_pdl(kv4_attention_kernel<D, NR, false>, dim3(p.ctas), dim3(CT), C::SMEM, s, p) != cudaSuccess)
         return SK_ERR_CUDA;
     return join<D>(p, C::ROWS, sms, s);
 }
 
-sk_status attend_tc(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
+sk_status attend_tc(AttnParams &p, unsigned char *rest, int sms, cudaStream_t s) {
     const int rows = tc_rows(p.M * p.G, &p.RT);
     p.ctas = sms * TC_CTAS;
-    if (!place_partials(p, scratch, rows, 128)) return SK_ERR_WORKSPACE;
+    if (!place_partials(p, rest, rows, 128)) return SK_ERR_WORKSPACE;
     if (launch_tc(p, rows, s) != cudaSuccess) return SK_ERR_CUDA;
     return join<128>(p, rows, sms, s);
 }
@@ -971,15 +983,16 @@ sk_status run(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     const int tiles = (p.M * p.G + NROW - 1) / NROW;       // of eight rows
     p.RT = (tiles + MOST - 1) / MOST;
     const int nr = (tiles + p.RT - 1) / p.RT;
+    unsigned char *const rest = place_rows(p, scratch);
     sk_status st;
     if (D == 128 && p.M * p.G > TC_ABOVE) {
         const bool done = nr == 3 ? attend_short<128, 3>(p, SHORT_TILES / 2, s, &st)
                                   : attend_short<128, 2>(p, SHORT_TILES / 2, s, &st);
-        if (!done) st = attend_tc(p, scratch, sms, s);
-    } else if (nr == 1) st = attend<D, 1>(p, scratch, sms, s);
-    else if (nr == 2) st = attend<D, 2>(p, scratch, sms, s);
-    else if constexpr (MOST == 4) st = nr == 3 ? attend<D, 3>(p, scratch, sms, s) : attend<D, 4>(p, scratch, sms, s);
-    else if constexpr (MOST == 3) st = attend<D, 3>(p, scratch, sms, s);
+        if (!done) st = attend_tc(p, rest, sms, s);
+    } else if (nr == 1) st = attend<D, 1>(p, rest, sms, s);
+    else if (nr == 2) st = attend<D, 2>(p, rest, sms, s);
+    else if constexpr (MOST == 4) st = nr == 3 ? attend<D, 3>(p, rest, sms, s) : attend<D, 4>(p, rest, sms, s);
+    else if constexpr (MOST == 3) st = attend<D, 3>(p, rest, sms, s);
     else return SK_ERR_UNSUPPORTED_SHAPE;
     if (st != SK_OK || !p.acc_out) return st;
     const int held = tiles < WT_TILES ? tiles : WT_TILES;

@@ -50,6 +50,7 @@ struct AttnParams {
     float *acc_out;
     float *part_o, *part_ml;   // per partial slot: [ROWS][D] sums, [ROWS][2] (maximum, sum)
     int2 *seg;                 // per segment: first CTA, partial slots (0: written whole)
+    float2 *norm;              // per row, where weights are accumulated: minus its base, log2 of the sum under it
     unsigned int *err;
     int pages, heads, recs, width, cap;   // recs: records per page; cap: positions the table can hold
     int B, M, G, RT, ctas;     // G: query heads per kv head; RT: row tiles
@@ -73,7 +74,7 @@ __device__ __forceinline__ float neg_base(const AttnParams &p, float m) { return
 __device__ __forceinline__ bool passes(const AttnParams &p, float s, float neg) { return s + neg > p.reach; }
 // A weight of the score s.
 __device__ __forceinline__ float weight(const AttnParams &p, float s, float neg) { return ex2((s + neg) * p.c); }
-// Two weights at a time.
+// Two weights at a time, and two with a factor of 2^-g each.
 __device__ __forceinline__ float2 weights2(const AttnParams &p, float s0, float s1, float n0, float n1) {
     float2 d;
     asm("{ .reg .b64 s, n, c; mov.b64 s, {%2, %3}; mov.b64 n, {%4, %5}; mov.b64 c, {%6, %6};\n\t"
@@ -81,11 +82,22 @@ __device__ __forceinline__ float2 weights2(const AttnParams &p, float s0, float 
         : "=f"(d.x), "=f"(d.y) : "f"(s0), "f"(s1), "f"(n0), "f"(n1), "f"(p.c));
     return make_float2(ex2(d.x), ex2(d.y));
 }
+__device__ __forceinline__ float2 weights2(const AttnParams &p, float s0, float s1, const float2 &n, const float2 &neg_g) {
+    float2 d;
+    asm("{ .reg .b64 s, n, c, g; mov.b64 s, {%2, %3}; mov.b64 n, {%4, %5}; mov.b64 c, {%6, %6}; mov.b64 g, {%7, %8};\n\t"
+        "add.rn.f32x2 s, s, n; fma.rn.f32x2 s, s, c, g; mov.b64 {%0, %1}, s; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(s0), "f"(s1), "f"(n.x), "f"(n.y), "f"(p.c), "f"(neg_g.x), "f"(neg_g.y));
+    return make_float2(ex2(d.x), ex2(d.y));
+}
 // What sums under one base are multiplied by to stand under another.
 __device__ __forceinline__ float rebase(const AttnParams &p, float from, float to) { return ex2((from - to) * p.c); }
-// The natural log of a row's sum l of weights under a base.
-__device__ __forceinline__ float log_sum(const AttnParams &p, float base, float l) {
-    return l == 0.f ? NEG_INF : fmaf(base, p.c, __log2f(l)) * LN2;
+// What a row's statistics, the sum l of its weights under a base, are needed
+// for later: the natural log of the sum, and for the accumulated weights base
+// and sum apart (the log holds no fraction where it is large).
+__device__ __forceinline__ void write_stats(const AttnParams &p, long long row, float base, float l) {
+    const float lg = __log2f(l);
+    if (p.lse) p.lse[row] = l == 0.f ? NEG_INF : fmaf(base, p.c, lg) * LN2;
+    if (p.norm) p.norm[row] = l == 0.f ? make_float2(0.f, -NEG_INF) : make_float2(-base, lg);
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {

@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                 const int row = rt * N + n, m = row / p.G;
                 const long long to = ((long long)b * p.M + m) * (p.heads * p.G) + h * p.G + row - m * p.G;
                 lim[n] = int(to - ((long long)b * p.M * p.heads * p.G));       // the row within its sequence
-                if (p.lse) p.lse[to] = log_sum(p, -neg[n], sum);
+                write_stats(p, to, -neg[n], sum);
             } else {
                 *reinterpret_cast<float2 *>(p.part_ml + (slot * N + n) * 2) = make_float2(-neg[n], sum);
             }

@@ -130,3 +130,24 @@ def test_small_differences_of_large_scores(sk, D, Hq, H, rows, wide):
     q = np.full((len(lens) * rows, Hq, D), 16384.0 / D, np.float16)
     q[..., 0] = 1 / 64
     _run(sk, cache, tables, lens, q, rows, Hq, D, 0.7, 300 if wide else 5)
+
+
+@pytest.mark.parametrize("D,Hq,H,rows", FORMS)
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("tied", [False, True])
+def test_weights_of_large_scores(sk, D, Hq, H, rows, wide, tied):
+    """What positions get is what the outputs were made of, whatever the scores' size."""
+    r = np.random.default_rng(D * Hq + 1)
+    lens, page = [150, 0, 41, 1], 32
+    keys = []
+    for n in lens:
+        k = np.full((n, D), 768.0)
+        k[:, 0] = 64.0 * r.choice([0, 1, 2, 3, 4, 6, 8, 12], n)
+        keys.append(_tied_keys(r, n, D) if tied and n else k.astype(np.float16))
+    cache, tables = _cache(r, keys, H, D, page)
+    q = np.full((len(lens) * rows, Hq, D), 32768.0 if tied else 16384.0 / D, np.float16)
+    if tied:
+        q[..., 1::3] = 16384.0
+    else:
+        q[..., 0] = 1 / 64
+    _run(sk, cache, tables, lens, q, rows, Hq, D, 0.7, 300 if wide else 5, weights=True)

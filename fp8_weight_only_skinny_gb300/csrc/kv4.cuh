@@ -81,19 +81,41 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 constexpr uint64_t KV4_WAIT_NS = 1000000000ull;
 
-// Wait, for a second at most, for the copies of a stage; when that runs out the
-// workspace's error word is set (where there is one) and no later wait is made.
-__device__ __forceinline__ void wait_full(uint32_t bar, uint32_t parity, unsigned int *err, bool &dead) {
-    if (dead) return;
-    if (mbar_try_wait(bar, parity)) return;
+// Wait until `bar`'s phase of this parity is complete, for a second at most.
+__device__ __forceinline__ bool wait_limited(uint32_t bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (globaltimer_ns() - t0 > KV4_WAIT_NS) {
-            dead = true;
-            if (err) atomicOr(err, 1u);
-            return;
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > KV4_WAIT_NS) return false;
+    return true;
+}
+
+// Let the copies land that a ring of SLOTS barriers at `bars` may still have in
+// flight: those of the next SLOTS uses from `slot` on, whose parity is `parity`
+// (a use that was never issued takes the rest of the second).
+template <int SLOTS>
+__device__ __forceinline__ void drain_ring(uint32_t bars, uint32_t slot, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    for (int k = 0; k < SLOTS; ++k) {
+        while (!mbar_try_wait(bars + slot * 8, parity))
+            if (globaltimer_ns() - t0 > KV4_WAIT_NS) return;
+        if (++slot == SLOTS) {
+            slot = 0;
+            parity ^= 1u;
         }
     }
+}
+
+// Wait for a ring's copies into `slot`.  When the second runs out the
+// workspace's error word is set (where there is one), the copies in flight are
+// let land, and the thread is dead: it makes no later wait and issues no copy.
+template <int SLOTS>
+__device__ __forceinline__ void wait_ring(uint32_t bars, uint32_t slot, uint32_t parity, unsigned int *err, bool &dead) {
+    if (dead || wait_limited(bars + slot * 8, parity)) return;
+    dead = true;
+    if (err) atomicOr(err, 1u);
+    drain_ring<SLOTS>(bars, slot, parity);
 }
 
 }  // namespace sk

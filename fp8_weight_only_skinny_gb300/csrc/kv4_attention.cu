@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
     if constexpr (!SHORT) sh = share_of(p, p.heads * p.RT, sm_share);
     const uint32_t CL = SHORT ? cluster_size() : 1u;
     uint32_t at = 0, parity = 0;   // this warp's ring position
+    const bool issuer = lane == 0 && !p.stall;
     bool dead = false;
 
     for (;;) {
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                 if (i + 16 < n) soon = lookup((i >> 4) + 1);
             }
             const uint32_t r0 = __shfl_sync(0xffffffffu, now, (2 * i) & 31), r1 = __shfl_sync(0xffffffffu, now, (2 * i + 1) & 31);
-            if (lane == 0) {
+            if (issuer && !dead) {
                 const uint32_t dst = ring + slot * C::STAGE, fb = bar + slot * 8;
                 const bool two = 2 * (st0 + i * WARPS) + 1 < nrec, one_copy = two && r1 == r0 + 1;
                 sk::mbar_arrive_expect_tx(fb, two ? 2 * C::REC : C::REC);
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
 
         for (int i = 0; i < n; ++i) {
             const uint32_t stage = ring + at * C::STAGE;
-            sk::wait_full(bar + at * 8, parity, p.err, dead);
+            sk::wait_ring<C::STAGES>(bar, at, parity, p.err, dead);
 #pragma unroll
             for (int x0 = 0; x0 < 2; x0 += NX) {
                 float s[NX][NR][4];
@@ -752,6 +753,7 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
     sk::pdl_wait_primary();
     Share sh = share_of(p, p.heads, sm_share);
     uint32_t it = 0;               // steps this warp has consumed
+    const bool issuer = lane == 0 && !p.stall;
     bool dead = false;
     // this lane's position in a step once the sums are spread: record t / 2, half t % 2, position g
     const int mine = (t >> 1) * 16 + (t & 1) * 8 + g;
@@ -781,7 +783,7 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
                     if (i + 16 < n) soon = lookup((i >> 4) + 1);
                 }
                 const uint32_t a = __shfl_sync(0xffffffffu, now, (2 * i) & 31), c = __shfl_sync(0xffffffffu, now, (2 * i + 1) & 31);
-                if (lane == 0) {
+                if (issuer && !dead) {
                     const uint32_t dst = ring + slot * C::STAGE, fb = bar + slot * 8;
                     const bool two = 2 * (st0 + i * WARPS) + 1 < nrec;
                     sk::mbar_arrive_expect_tx(fb, two ? 2 * C::KEY : C::KEY);
@@ -815,7 +817,7 @@ __global__ void __launch_bounds__(CT, WeightsCfg<D>::CTAS)
                     const int i = i0 + j;
                     if (i >= n) break;
                     const uint32_t slot = it % WT_STAGES, stage = ring + slot * C::STAGE;
-                    sk::wait_full(bar + slot * 8, (it / WT_STAGES) & 1, p.err, dead);
+                    sk::wait_ring<WT_STAGES>(bar, slot, (it / WT_STAGES) & 1, p.err, dead);
                     Keys<D> k[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) load_keys<D>(stage + (x >> 1) * C::KEY, (x & 1) * 8 + g, t, k[x]);
@@ -1066,6 +1068,7 @@ extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint
     p.shift = P_SHIFT / p.c;
     p.reach = (P_SHIFT + SLACK) / p.c;
     p.vg = v_scale;
+    p.stall = sk::take_inject_stall();
     switch (head_dim) {
         case 64: return run<64>(p, sc.base, sc.num_sms, s);
         case 128: return run<128>(p, sc.base, sc.num_sms, s);

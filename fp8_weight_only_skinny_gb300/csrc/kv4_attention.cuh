@@ -52,6 +52,7 @@ struct AttnParams {
     int2 *seg;                 // per segment: first CTA, partial slots (0: written whole)
     float2 *norm;              // per row, where weights are accumulated: minus its base, log2 of the sum under it
     unsigned int *err;
+    int stall;                 // issue no copies (sk_inject_wait_timeout)
     int pages, heads, recs, width, cap;   // recs: records per page; cap: positions the table can hold
     int B, M, G, RT, ctas;     // G: query heads per kv head; RT: row tiles
     float c, shift, reach, vg; // scale * key scale * log2 e; P_SHIFT / c; (P_SHIFT + SLACK) / c; value scale

@@ -47,9 +47,10 @@ struct Tc {
     static constexpr int UNITS = N <= 64 ? 4 : 3;
     static constexpr int V = 0, Q = V + 128 * D * 2, P = Q + N * D * 2, RAW = P + N * 128 * 2, SMALL = RAW + UNITS * UNIT;
     // per row: minus its base, that before it moved, a factor, the first unseen position; four warps' values of each
-    // row; barriers of the ring and of the two products; the TMEM address
+    // row; barriers of the ring, of the two products and of the end; the TMEM
+    // address
     static constexpr int NEG = SMALL, OLD = NEG + 4 * N, FAC = OLD + 4 * N, LIM = FAC + 4 * N,
-                         WARP = LIM + 4 * N, BARS = WARP + 16 * N, TMEM = BARS + 8 * (UNITS + 2);
+                         WARP = LIM + 4 * N, BARS = WARP + 16 * N, TMEM = BARS + 8 * (UNITS + 3);
     static constexpr size_t SMEM = 1024 + TMEM + 16;
     static constexpr int S_COL = 64, O_COL = 64 + N;         // TMEM columns: keys 0..63, S, O
     static_assert(O_COL + N <= 256, "half of the TMEM");
@@ -233,11 +234,11 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
     float *const old = reinterpret_cast<float *>(smem + C::OLD), *const fac = reinterpret_cast<float *>(smem + C::FAC);
     int *const lim = reinterpret_cast<int *>(smem + C::LIM);
     float *const of_warp = reinterpret_cast<float *>(smem + C::WARP);
-    const uint32_t bars = base + C::BARS, bar_s = bars + 8 * UNITS, bar_o = bar_s + 8;
+    const uint32_t bars = base + C::BARS, bar_s = bars + 8 * UNITS, bar_o = bar_s + 8, bar_end = bar_o + 8;
 
     if (warp == 0) tmem_alloc(base + C::TMEM, 256);
     if (tid == 0) {
-        for (int i = 0; i < UNITS + 2; ++i) sk::mbar_init(bars + 8 * i, 1);
+        for (int i = 0; i < UNITS + 3; ++i) sk::mbar_init(bars + 8 * i, 1);
         sk::fence_barrier_init();
     }
     fence_before();
@@ -253,6 +254,14 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                    p_op = operand(base + C::P, 128, 2048, 0);
     uint32_t unit0 = 0, ph_s = 0, ph_o = 0;                  // units consumed; parities of the two products' barriers
     bool dead = false;
+    // Copies of unit u (counted from the kernel's start), and a product beside which the units from u on are in flight.
+    auto wait_unit = [&](uint32_t u) { sk::wait_ring<UNITS>(bars, u % UNITS, (u / UNITS) & 1, p.err, dead); };
+    auto wait_product = [&](uint32_t bar, uint32_t parity, uint32_t u) {
+        if (dead || sk::wait_limited(bar, parity)) return;
+        dead = true;
+        if (p.err) atomicOr(p.err, 1u);
+        sk::drain_ring<UNITS>(bars, u % UNITS, (u / UNITS) & 1);
+    };
 
     while (sh.t < sh.end && sh.b < p.B) {
         const int len = length_of(p, sh.b), nt = tiles_of(len);
@@ -274,7 +283,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             return sk::kv4_record(table, min(rec, nrec - 1), p.recs, p.by_recs, p.pages, p.heads, h);
         };
         auto issue = [&](int u, uint32_t idx) {              // idx: the tile's records
-            if (u >= 2 * tiles) return;
+            if (u >= 2 * tiles || p.stall || __any_sync(0xffffffffu, dead)) return;
             const bool load = lane < 8 && rec0 + 8 * (u >> 1) + lane < nrec;
             const uint32_t slot = (unit0 + uint32_t(u)) % UNITS, bar = bars + 8 * slot;
             const unsigned int mask = __ballot_sync(0xffffffffu, load);
@@ -323,7 +332,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             const uint32_t uk = unit0 + 2 * i, uv = uk + 1;
             const uint32_t keys = base + C::RAW + (uk % UNITS) * UNIT, vals = base + C::RAW + (uv % UNITS) * UNIT;
             // ---- S = K . q^T
-            sk::wait_full(bars + 8 * (uk % UNITS), (uk / UNITS) & 1, p.err, dead);
+            wait_unit(uk);
             {
                 const int r = 2 * quad + side;               // record, in this warp's lanes
                 decode_keys(keys + r * PART, tmem + (uint32_t(16 * r) << 16), g, t);
@@ -345,15 +354,15 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             }
             // ---- V, once the last tile's second product has read its own
             if (i > 0) {
-                sk::wait_full(bar_o, ph_o, p.err, dead);
+                wait_product(bar_o, ph_o, uv);
                 ph_o ^= 1;
                 fence_after();
             }
-            sk::wait_full(bars + 8 * (uv % UNITS), (uv / UNITS) & 1, p.err, dead);
+            wait_unit(uv);
             decode_values(vals + warp * PART, base + C::V, warp * 16, lane);
             // ---- the weights, to the operand of the second product: eight rows
             // of a position in 16 bytes, positions 16 bytes apart
-            sk::wait_full(bar_s, ph_s, p.err, dead);
+            wait_product(bar_s, ph_s, uv + 1);
             ph_s ^= 1;
             fence_after();
             const int at = quad * 32 + lane, pos = (t_lo + i) * TILE + at;
@@ -512,7 +521,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
             if ((lane & 3) == 0) of_warp[quad * N + side * NH + c + (lane >> 2)] = v[0];
         }
-        sk::wait_full(bar_o, ph_o, p.err, dead);
+        wait_product(bar_o, ph_o, unit0);
         ph_o ^= 1;
         fence_after();
         __syncthreads();
@@ -561,7 +570,13 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             sh.off = 0;
         }
     }
-    __syncthreads();
+    if (__syncthreads_or(dead)) {
+        // a product may still be under way: its end, too, is waited for
+        if (tid == 0) commit(bar_end);
+        sk::wait_limited(bar_end, 0);
+        fence_after();
+        __syncthreads();
+    }
     if (warp == 0) tmem_free(tmem, 256);
 }
 

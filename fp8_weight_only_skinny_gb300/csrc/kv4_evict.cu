@@ -34,6 +34,7 @@ struct EvictParams {
     float *acc_out;
     int32_t *kept, *new_lens;
     unsigned int *err;
+    int stall;                         // issue no copies (sk_inject_wait_timeout)
     int pages, heads, recs, width, dst_width, cap, dst_cap;
     int budget, recent;
     sk::Div by_recs;
@@ -378,6 +379,7 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
     int32_t *kept = p.kept + size_t(bh) * size_t(p.budget);
     float *acc_out = p.acc_out ? p.acc_out + size_t(bh) * size_t(p.dst_cap) : nullptr;
     uint32_t done = 0;                           // records this warp has copied: ring position and parity
+    const bool issuer = lane == 0 && !p.stall;
     bool dead = false;
     for (int r0 = rec_lo; r0 < rec_hi; r0 += CHUNK) {
         const int nr = min(CHUNK, rec_hi - r0);
@@ -427,7 +429,7 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
         unsigned char *const own = smem + warp * SLOTS * REC;
         const uint32_t ring = sk::smem_u32(own);
         auto issue = [&](int y, uint32_t slot) {
-            if (lane == 0) {
+            if (issuer && !dead) {
                 const uint32_t bar = sk::smem_u32(&sh.bar[warp][slot]);
                 sk::mbar_arrive_expect_tx(bar, REC);
                 sk::bulk_load(ring + slot * REC, p.cache + size_t(sh.list.src[y]) * REC, REC, bar);
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
             const unsigned int m = sh.list.mask[y], base = sh.list.base[y];
             const int count = __popc(m);
             if (lane < 16 && (m >> lane & 1u)) sh.nth[warp][__popc(m & ((1u << lane) - 1u))] = uint8_t(lane);
-            sk::wait_full(sk::smem_u32(&sh.bar[warp][slot]), (done / SLOTS) & 1, p.err, dead);
+            sk::wait_ring<SLOTS>(sk::smem_u32(&sh.bar[warp][0]), slot, (done / SLOTS) & 1, p.err, dead);
             __syncwarp();
             const unsigned char *src = own + slot * REC;
             // four positions at a time: neighbouring lanes write neighbouring positions of a value block
@@ -565,6 +567,7 @@ extern "C" sk_status kv4_evict(uint8_t *cache, const int32_t *table, const int32
     if (sk::scratch_for(reinterpret_cast<cudaStream_t>(stream), &sc)) p.err = sc.err;
     int cluster = 1;
     while (cluster < MAX_CLUSTER && bh * cluster <= sk::device_sm_count() && cluster * ET < p.cap) cluster *= 2;
+    p.stall = sk::take_inject_stall();
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (head_dim) {
         case 64: return launch<64>(p, bh, cluster, s);

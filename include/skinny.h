@@ -360,7 +360,9 @@ SK_API sk_status kv4_attention(const void *q, long long q_stride, const uint8_t 
  *   acc_out   f32 [seqs][kv_heads][dst_width * page_size], or NULL: acc of the
  *             kept positions, zeros after them; must not be acc
  *   budget >= 1, 0 <= recent <= budget.  Slots of dst_table from new_lens on are
- *   not written.  seqs = 0: nothing is launched.  Needs no workspace.
+ *   not written.  seqs = 0: nothing is launched.  Needs no workspace; where the
+ *   stream or the device has one, a bounded wait that ran out is reported by
+ *   sk_last_device_error.
  */
 SK_API sk_status kv4_evict(uint8_t *cache, const int32_t *table, const int32_t *lens, const float *acc,
                            const int32_t *dst_table, int32_t *kept, int32_t *new_lens, float *acc_out, int seqs,
@@ -427,12 +429,12 @@ enum { SK_VARIANT_AUTO = 0, SK_VARIANT_TENSOR = 1, SK_VARIANT_SIMT = 2 };
 SK_API int sk_set_variant(int variant);
 
 /*
- * Failure-injection hook for tests: with enable = 1 the next kernel launched
- * by this process on any device issues no weight copies, so its consumers'
- * bounded waits run out (about one second); the kernel then finishes without
- * further waiting and records SK_ERR_TIMEOUT, which sk_last_device_error()
- * returns.  The hook clears itself after that one launch.  No fault, trap or
- * unbounded wait is involved.
+ * Failure-injection hook for tests: with enable = 1 the next linear-layer,
+ * kv4_attention or kv4_evict call of this process on any device issues no bulk
+ * copies, so that its kernels' bounded waits run out (about one second, twice
+ * that in the cache kernels); they then finish without further waiting and
+ * record SK_ERR_TIMEOUT, which sk_last_device_error() returns.  The hook clears
+ * itself after that one call.  No fault, trap or unbounded wait is involved.
  */
 SK_API void sk_inject_wait_timeout(int enable);
 

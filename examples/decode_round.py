@@ -1,10 +1,10 @@
 """Speculative decode rounds of one layer with its cache in 4 bits.
 
 Each round projects M rows (the last token and M - 1 drafted ones), appends their keys and values
-to the cache, attends over it with the weight of every position accumulated, projects back, and
-verifies the drafts against the vocabulary projection, whose picks are reported with their log
-probability, rank, entropy and alternatives.  When the cache reaches its high-water mark it is
-trimmed to the positions with the most weight (and the latest), in other pages.
+to the cache, attends over it, projects back, and verifies the drafts against the vocabulary
+projection, whose picks are reported with their log probability, rank, entropy and alternatives.
+The weight that the accepted rows give to each position is accumulated.  When the cache reaches its
+high-water mark it is trimmed to the positions with the most weight (and the latest), in other pages.
 
     python examples/decode_round.py [rounds]
 
@@ -61,7 +61,7 @@ def decode(rounds=40, rows=4, page=32, high_water=256, budget=96, recent=32, top
         at = torch.arange(n, n + rows, device="cuda")
         sk.kv4_append(k, v, (table[0, at // page] * page + at % page).int(), cache, K_SCALE, V_SCALE)
         lens.fill_(n + rows)
-        heads, _ = sk.kv4_attention(q, cache, table, lens, K_SCALE, V_SCALE, DIM ** -0.5, rows=rows, acc=acc, acc_out=acc)
+        heads, _ = sk.kv4_attention(q, cache, table, lens, K_SCALE, V_SCALE, DIM ** -0.5, rows=rows)
         y = x + sk.fp8_gemm(heads.flatten(1), *out_w, f16_out=True)
         logits, picks, accept = sk.lm_head_verify(y, head_codes, head_scales, head_g, draft)
         logprob, rank, entropy, ids, top = sk.token_logprobs(logits, picks, top_n=top_n)
@@ -71,7 +71,11 @@ def decode(rounds=40, rows=4, page=32, high_water=256, budget=96, recent=32, top
             report.append((token, float(logprob[i]), int(rank[i]), float(entropy[i]), ids[i].tolist(), top[i].tolist()))
         tokens += committed
         n += agreed + 1
-        acc[:, :, n:] = 0                          # what the rejected rows gave and got goes with them
+        # The weight of each position, from the accepted rows alone: which they are is known only now, so those rows
+        # attend once more, as the last ones of a sequence that ends with them.
+        lens.fill_(n)
+        sk.kv4_attention(q[:agreed + 1], cache, table, lens, K_SCALE, V_SCALE, DIM ** -0.5, rows=agreed + 1, acc=acc,
+                         acc_out=acc)
     assert sk.last_device_error() == sk.SK_OK
     return {"tokens": tokens, "report": report, "length": n, "evictions": evictions, "cache": cache, "table": table,
             "acc": acc}

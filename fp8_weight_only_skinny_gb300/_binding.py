@@ -322,7 +322,7 @@ def _rows_f16(t, heads, dim, what):
     if one != 1 or (head != dim and heads > 1):
         raise ValueError(f"{what}: heads and components must be contiguous (only the row stride is free)")
     n = shape[0]
-    return n, row if n > 1 else max(row, heads * dim)
+    return n, row if n > 1 else heads * dim            # a single row has no stride to keep to
 
 
 _TORCH = None

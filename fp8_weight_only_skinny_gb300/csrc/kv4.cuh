@@ -29,11 +29,8 @@ namespace sk {
 
 constexpr int KV4_REC = 16;   // positions per record
 
-// Byte offsets inside a record of a head of size D.
+// Bytes of a record of a head of size D.
 __host__ __device__ constexpr int kv4_rec_bytes(int D) { return 18 * D; }
-__host__ __device__ constexpr int kv4_key_scales(int D) { return 8 * D; }
-__host__ __device__ constexpr int kv4_val_codes(int D) { return 9 * D; }
-__host__ __device__ constexpr int kv4_val_scales(int D) { return 17 * D; }
 
 // Where position i (< 16) of a record keeps block b (16 components): the
 // eight code bytes and the scale byte, for keys (VALUE = false) and values.

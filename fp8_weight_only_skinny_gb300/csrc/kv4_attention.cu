@@ -214,30 +214,6 @@ __device__ __forceinline__ int merge_swizzle(int row, int d) {
 
 constexpr int MAX_CLUSTER = 16;
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ float2 ld_peer_v2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_peer_v4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
 // Four components of query row r of a segment, and its statistics, from the sums
 // under the base `top`.
 template <int D>
@@ -284,7 +260,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
     sk::pdl_wait_primary();
     Share sh;
     if constexpr (!SHORT) sh = share_of(p, p.heads * p.RT, sm_share);
-    const uint32_t CL = SHORT ? cluster_size() : 1u;
+    const uint32_t CL = SHORT ? sk::cluster_size() : 1u;
     uint32_t at = 0, parity = 0;   // this warp's ring position
     const bool issuer = lane == 0 && !p.stall;
     bool dead = false;
@@ -521,7 +497,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
         }
         if constexpr (SHORT) {
             if (CL == 1u) break;
-            cluster_sync();
+            sk::cluster_sync();
             // the cluster's, in its order, every CTA a part of the rows and components
             const uint32_t ml_at = sk::smem_u32(all_ml);
             for (int i = int(blockIdx.x % CL) * CT + tid; i < rows * (D / 4); i += int(CL) * CT) {
@@ -533,8 +509,8 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                     ml[k] = make_float2(NEG_INF, 0.f);
                     x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (k < CL) {
-                        ml[k] = ld_peer_v2(peer(ml_at + r * 8, k));
-                        x[k] = ld_peer_v4(peer(base + (r * C::OSTRIDE + (d ^ (2 * (merge_swizzle<D>(r, d) & ~1)))) * 4, k));
+                        ml[k] = sk::ld_peer_v2(sk::peer(ml_at + r * 8, k));
+                        x[k] = sk::ld_peer_v4(sk::peer(base + (r * C::OSTRIDE + (d ^ (2 * (merge_swizzle<D>(r, d) & ~1)))) * 4, k));
                     }
                 }
                 float top = NEG_INF, l = 0.f;
@@ -552,7 +528,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                 }
                 write_row<D>(p, b, h, rt * ROWS + r, d, v, top, l);
             }
-            cluster_sync();                      // no CTA leaves while its sums are read
+            sk::cluster_sync();                      // no CTA leaves while its sums are read
             break;
         } else {
         if (tid == 0 && t_lo == 0) {

@@ -5,6 +5,7 @@
 
 #include <cstdint>
 
+#include "cluster.cuh"
 #include "kv4.cuh"
 
 namespace sk {
@@ -58,12 +59,6 @@ struct AttnParams {
     float c, shift, reach, vg; // scale * key scale * log2 e; P_SHIFT / c; (P_SHIFT + SLACK) / c; value scale
     sk::Div by_recs;
 };
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Rows keep minus their base.  NO_BASE: no score seen yet; any score passes it,
 // and the sums under it are zero.

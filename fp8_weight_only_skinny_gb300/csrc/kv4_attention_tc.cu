@@ -147,12 +147,6 @@ __device__ __forceinline__ void row8(const float *p, float (&v)[8]) {
     v[7] = b.w;
 }
 
-__device__ __forceinline__ uint32_t scale_pair(uint32_t codes) {      // as in kv4_attention.cu: NaN becomes zero
-    const uint32_t s = sk::e4m3x2_h_to_f16x2(uint16_t(codes));
-    uint32_t d;
-    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(s), "r"(0u));
-    return d;
-}
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }

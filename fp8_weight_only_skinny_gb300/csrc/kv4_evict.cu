@@ -12,6 +12,7 @@
 #include <cstdint>
 
 #include "../../include/skinny.h"
+#include "cluster.cuh"
 #include "internal.h"
 #include "kv4.cuh"
 #include "launch_util.cuh"
@@ -71,30 +72,6 @@ struct alignas(16) Shared {
 
 // Source records in flight per warp.
 __host__ __device__ constexpr int ring_slots(int d) { return d == 256 ? 2 : 4; }
-
-// Order of the weights as unsigned keys (larger weight, larger key; -0 = +0).
-__device__ __forceinline__ unsigned int key_of(float v) {
-    const unsigned int u = __float_as_uint(v + 0.f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ unsigned int ld_peer(const unsigned int *p, unsigned int rank) {
-    const uint32_t a = sk::smem_u32(p);
-    unsigned int v;
-    asm volatile("{ .reg .b32 r; mapa.shared::cluster.u32 r, %1, %2; ld.shared::cluster.u32 %0, [r]; }"
-                 : "=r"(v) : "r"(a), "r"(rank) : "memory");
-    return v;
-}
-__device__ __forceinline__ unsigned long long ld_peer64(const unsigned long long *p, unsigned int rank) {
-    const uint32_t a = sk::smem_u32(p);
-    unsigned long long v;
-    asm volatile("{ .reg .b32 r; mapa.shared::cluster.u32 r, %1, %2; ld.shared::cluster.u64 %0, [r]; }"
-                 : "=l"(v) : "r"(a), "r"(rank) : "memory");
-    return v;
-}
 
 // Inclusive prefix sum over the CTA in thread order (tmp: ET / 32 words); the
 // sum of all goes to *total.  Ends with a barrier before tmp is free again.
@@ -167,7 +144,7 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
     // the positions this CTA's selection reads
     const int s_lo = SOLO ? 0 : lo, n_old = SOLO ? old : max(0, min(hi, old) - lo);
     int cached = KEYS;
-    auto key_at = [&](int i) { return i < cached ? keys[i] : key_of(acc[s_lo + i]); };  // i counts from s_lo
+    auto key_at = [&](int i) { return i < cached ? keys[i] : sk::key_of(acc[s_lo + i]); };  // i counts from s_lo
 
     unsigned int low = 0, mask = 0, prefix = 0, need = select ? unsigned(p.budget - p.recent) : 0u;
     unsigned int above = 0;                      // this CTA's keys above the digits found so far
@@ -193,7 +170,7 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
             for (int j = 0; j < 16; ++j) {
                 const int i = i0 + j * ET;
                 if (i < n_old) {
-                    const unsigned int k = key_of(v[j]);
+                    const unsigned int k = sk::key_of(v[j]);
                     if (i < KEYS) keys[i] = k;
                     mn = min(mn, k);
                     mx = max(mx, k);
@@ -211,10 +188,10 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
             mn = sh.range[0];
             mx = sh.range[1];
         } else {
-            cluster_sync();
-            const unsigned int peer = unsigned(lane) & (C - 1u);
-            mn = __reduce_min_sync(0xffffffffu, ld_peer(&sh.range[0], peer));
-            mx = __reduce_max_sync(0xffffffffu, ld_peer(&sh.range[1], peer));
+            sk::cluster_sync();
+            const unsigned int of = unsigned(lane) & (C - 1u);
+            mn = __reduce_min_sync(0xffffffffu, sk::ld_peer_u32(sk::peer(&sh.range[0], of)));
+            mx = __reduce_max_sync(0xffffffffu, sk::ld_peer_u32(sk::peer(&sh.range[1], of)));
         }
         // digits of key - low, from its highest bit down (uniform in the cluster)
         low = mn;
@@ -238,11 +215,11 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
             if constexpr (!SOLO) {
                 hh[BINS - 1 - 2 * tid] = t0;
                 hh[BINS - 2 - 2 * tid] = t1;
-                cluster_sync();
+                sk::cluster_sync();
                 unsigned long long w[MAX_CLUSTER];       // all in flight, each CTA beginning with its own
 #pragma unroll
                 for (unsigned int r = 0; r < MAX_CLUSTER; ++r)
-                    w[r] = r < C ? ld_peer64(reinterpret_cast<const unsigned long long *>(hh + BINS - 2 - 2 * tid), (rank + r) & (C - 1u)) : 0ull;
+                    w[r] = r < C ? sk::ld_peer_u64(sk::peer(hh + BINS - 2 - 2 * tid, (rank + r) & (C - 1u))) : 0ull;
                 t0 = t1 = 0;
 #pragma unroll
                 for (unsigned int r = 0; r < MAX_CLUSTER; ++r) {
@@ -297,12 +274,12 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
     // ---- what the CTAs before this one keep
     unsigned int gt_before = 0, eq_before = 0;
     if (select && !SOLO) {
-        cluster_sync();
+        sk::cluster_sync();
         if (tid < 32) {
             const bool in = unsigned(lane) < C;
-            const unsigned int c0 = in ? ld_peer(&sh.counts[0], unsigned(lane)) : 0u;
-            const unsigned int c1 = in ? ld_peer(&sh.counts[1], unsigned(lane)) : 0u;
-            unsigned int x = in ? ld_peer(&sh.counts[2], unsigned(lane)) : 0u;
+            const unsigned int c0 = in ? sk::ld_peer_u32(sk::peer(&sh.counts[0], unsigned(lane))) : 0u;
+            const unsigned int c1 = in ? sk::ld_peer_u32(sk::peer(&sh.counts[1], unsigned(lane))) : 0u;
+            unsigned int x = in ? sk::ld_peer_u32(sk::peer(&sh.counts[2], unsigned(lane))) : 0u;
             if (in) {
                 sh.gt[lane] = c0;
                 sh.eq[lane] = c1;
@@ -333,7 +310,7 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
             if (unsigned(tid) < total) {
                 unsigned int r = 0;
                 while (sh.first[r + 1] <= unsigned(tid)) ++r;
-                sh.few[tid] = ld_peer64(&sh.mine[unsigned(tid) - sh.first[r]], r);
+                sh.few[tid] = sk::ld_peer_u64(sk::peer(&sh.mine[unsigned(tid) - sh.first[r]], r));
             }
             __syncthreads();
         }
@@ -351,7 +328,7 @@ __global__ void __launch_bounds__(ET) kv4_evict_kernel(const __grid_constant__ E
         if constexpr (!SOLO)    // the candidates of the CTAs before this one that pass
             gt_before += __syncthreads_count(unsigned(tid) < sh.first[rank] && list[tid & (FEW - 1)] >= limit);
     }
-    if (select && !SOLO) cluster_sync();         // no CTA leaves while its counts and candidates are read
+    if (select && !SOLO) sk::cluster_sync();     // no CTA leaves while its counts and candidates are read
     // 2: kept, 1: kept if among the first `need` equal to the threshold, 0: not
     auto kind = [&](int i) -> unsigned int {
         if (all || i >= old) return 2u;

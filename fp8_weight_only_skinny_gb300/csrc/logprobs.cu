@@ -14,6 +14,7 @@
 #include <cstdint>
 
 #include "../../include/skinny.h"
+#include "cluster.cuh"
 #include "internal.h"
 #include "launch_util.cuh"
 #include "ptx.cuh"
@@ -43,12 +44,6 @@ struct LogprobParams {
     int N, top_n;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // max that hands on a NaN instead of dropping it
 __device__ __forceinline__ float max_nan(float a, float b) {
     float y;
@@ -56,10 +51,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 
-__device__ __forceinline__ unsigned int key_of(float v) {
-    const unsigned int u = __float_as_uint(v + 0.f);      // -0 = +0
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
 __device__ __forceinline__ float value_of(unsigned int k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
@@ -69,36 +60,7 @@ __device__ __forceinline__ float floor_of(unsigned int k) {
     return v == v ? v : -__builtin_huge_valf();
 }
 __device__ __forceinline__ unsigned long long cand_of(float v, int i) {
-    return (static_cast<unsigned long long>(key_of(v)) << 32) | static_cast<unsigned int>(~i);
-}
-
-__device__ __forceinline__ unsigned int cluster_rank() {
-    unsigned int r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ unsigned int cluster_size() {
-    unsigned int r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t peer(const void *p, unsigned int rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(sk::smem_u32(p)), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ float ld_peer_f32(uint32_t a) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ unsigned long long ld_peer_u64(uint32_t a) {
-    unsigned long long v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
-    return v;
+    return (static_cast<unsigned long long>(sk::key_of(v)) << 32) | static_cast<unsigned int>(~i);
 }
 
 // Running softmax statistics in units of log2: the maximum m of the raw logits
@@ -110,7 +72,7 @@ __device__ __forceinline__ Stats join(const Stats &a, const Stats &b, float c) {
     Stats r;
     r.m = fmaxf(a.m, b.m);
     const float da = max_nan((a.m - r.m) * c, -200.f), db = max_nan((b.m - r.m) * c, -200.f);
-    const float fa = ex2(da), fb = ex2(db);
+    const float fa = sk::ex2(da), fb = sk::ex2(db);
     r.s = a.s * fa + b.s * fb;
     r.w = fa * (a.w + da * a.s) + fb * (b.w + db * b.s);
     return r;
@@ -261,7 +223,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
     Shared<LT> &sh = *reinterpret_cast<Shared<LT> *>(raw_smem);
     constexpr int VEC = Raw<T, LT>::VEC, ROUND = LT * PER;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const unsigned int rank = LT == NARROW ? 0u : cluster_rank(), C = LT == NARROW ? 1u : cluster_size();
+    const unsigned int rank = LT == NARROW ? 0u : sk::cluster_rank(), C = LT == NARROW ? 1u : sk::cluster_size();
     const int row = first_row + blockIdx.x / C;
     // The first of two launches lets the second start once all of its own CTAs
     // are past their wait, so what the logits depend on is complete; the second
@@ -278,7 +240,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
     const int tok = p.tokens ? p.tokens[row] : -1;
     const bool given = tok >= 0 && tok < p.N;
     const float ztok = given ? one(z0 + tok) : 0.f, zrank = given ? ztok : __builtin_huge_valf();
-    const float ztok_up = value_of(key_of(ztok) + 1u);       // the next larger value
+    const float ztok_up = value_of(sk::key_of(ztok) + 1u);       // the next larger value
     const bool masked_token = ztok == -__builtin_huge_valf();
     const float c = p.inv_t2;
     const int n = min(p.top_n, p.N);
@@ -304,7 +266,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
 #pragma unroll
         for (int j = 1; j < PER; ++j) mx = fmaxf(mx, z[j]);
         if (mx > st.m) {
-            const float d = max_nan((st.m - mx) * c, -200.f), f = ex2(d);
+            const float d = max_nan((st.m - mx) * c, -200.f), f = sk::ex2(d);
             st.w = f * (st.w + d * st.s);
             st.s *= f;
             st.m = mx;
@@ -313,7 +275,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
         // lowest value) adds nothing, and nothing times -200 to the second sum
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const float d = max_nan((z[j] - st.m) * c, -200.f), e = ex2(d);
+            const float d = max_nan((z[j] - st.m) * c, -200.f), e = sk::ex2(d);
             st.s += e;
             st.w = fmaf(e, d, st.w);
         }
@@ -325,7 +287,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
 #pragma unroll
             for (int o = 1; o < LT / GROUPS; o <<= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
             if (tid % (LT / GROUPS) == 0)
-                sh.top[tid / (LT / GROUPS)] = (key_of(gm) & ~255u) | unsigned(GROUPS - 1 - tid / (LT / GROUPS));
+                sh.top[tid / (LT / GROUPS)] = (sk::key_of(gm) & ~255u) | unsigned(GROUPS - 1 - tid / (LT / GROUPS));
             __syncthreads();
             if (wid == 0) {
                 const unsigned int k0 = sh.top[lane], k1 = sh.top[lane + 32];
@@ -422,14 +384,14 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
     // ---- the cluster's: every CTA joins all the statistics, and places its
     // own candidates among everyone's
     if (C > 1) {
-        cluster_sync();
+        sk::cluster_sync();
         if (wid == 0) {
             Stats a = {LOWEST, 0.f, 0.f};
             unsigned int r = 0u;
             if (unsigned(lane) < C) {
-                const uint32_t q = peer(&sh.mine, unsigned(lane));
-                a = Stats{ld_peer_f32(q), ld_peer_f32(q + 4), ld_peer_f32(q + 8)};
-                r = __float_as_uint(ld_peer_f32(peer(&sh.above_mine, unsigned(lane))));
+                const uint32_t q = sk::peer(&sh.mine, unsigned(lane));
+                a = Stats{sk::ld_peer_f32(q), sk::ld_peer_f32(q + 4), sk::ld_peer_f32(q + 8)};
+                r = __float_as_uint(sk::ld_peer_f32(sk::peer(&sh.above_mine, unsigned(lane))));
             }
 #pragma unroll
             for (int o = 1; o < MAX_CLUSTER; o <<= 1) {
@@ -444,7 +406,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
         // everyone's entries, then entry e of this CTA against the sorted entries of CTA k, both by thread
         for (int x = tid; x < int(C) * n; x += LT) {
             const int k = x / n;
-            sh.all_best[x] = ld_peer_u64(peer(&sh.best[x - k * n], unsigned(k)));
+            sh.all_best[x] = sk::ld_peer_u64(sk::peer(&sh.best[x - k * n], unsigned(k)));
         }
         __syncthreads();
         for (int x = tid; x < int(C) * n; x += LT) {
@@ -460,7 +422,7 @@ __global__ void __launch_bounds__(LT) logprobs_kernel(const __grid_constant__ Lo
             }
             if (a) atomicAdd(&sh.place[e], unsigned(a));
         }
-        cluster_sync();                          // and no CTA leaves while its entries are read
+        sk::cluster_sync();                          // and no CTA leaves while its entries are read
     }
     __syncthreads();
     const Stats a = sh.all;

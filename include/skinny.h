@@ -66,7 +66,9 @@
  *         be the kernel immediately preceding a linear call on the same
  *         stream while PDL is on (sk_set_pdl(0) turns it off); anything
  *         launched in between without PDL -- any other kernel, a copy, an
- *         event wait -- ends the hazard.
+ *         event wait -- ends the hazard.  The cache calls and token_logprobs
+ *         are launched with PDL and do not end it; they read nothing before the
+ *         preceding kernel has completed.
  *   - Kernels bound every wait they spin on (about one second).  When a wait
  *     runs out the kernel records SK_ERR_TIMEOUT in a device word, finishes
  *     without further waiting and leaves garbage in y; sk_last_device_error()
@@ -103,7 +105,8 @@ typedef enum {
  * Allocate (cudaMalloc) and initialise the workspace of the CURRENT device
  * (a zeroed 4 KiB control block followed by split-K partial-sum slots, all
  * marked empty; every call leaves them empty again), and behind it 48 MiB of
- * scratch memory for kv4_attention.
+ * scratch memory for kv4_attention (partial sums, up to 30 MiB, and with
+ * acc_out the rows' statistics, up to 16), whether or not it is ever called.
  * workspace_bytes = 0 picks the default, 64 MiB, which covers the largest call
  * below (N = 151936, K = 5120, M = 8 needs about 25 MB).  Calling it again on
  * the same device frees and re-creates the workspace (wait for all work of the
@@ -115,19 +118,22 @@ SK_API sk_status sk_init(size_t workspace_bytes);
 /*
  * A workspace of its own for `stream` (a cudaStream_t; NULL = the legacy
  * default stream) on the CURRENT device, allocated (cudaMalloc) and initialised
- * like sk_init's; workspace_bytes = 0 removes the stream's workspace (its calls
- * fall back to the device's).  Calling it again replaces the workspace (after
- * synchronising the stream).  Every later call on that stream -- linear
- * layers, lm_head, quantizers, sk_last_device_error -- uses it instead of the
+ * like sk_init's, with 48 MiB of scratch memory of its own behind it;
+ * workspace_bytes = 0 removes the stream's workspace (its calls fall back to
+ * the device's).  Calling it again replaces the workspace (after synchronising
+ * the stream).  Every later call on that stream -- linear layers, lm_head,
+ * quantizers, kv4_attention, sk_last_device_error -- uses it instead of the
  * device's, and its linear-layer kernels are launched cooperatively, so that
  * the whole persistent grid is resident before any of its CTAs starts: calls
  * on streams that each have a workspace of their own can then overlap on the
  * GPU without racing on a workspace and without a split-K wait that could run
  * out.  A cooperative kernel starts only when the whole grid fits, so
- * overlapping calls share the SMs in turns rather than at once; such calls
- * are also launched without programmatic dependent launch.  Up to 64 stream
- * workspaces per process; more return SK_ERR_INVALID_ARG.  Call it before
- * capturing a CUDA graph.  Needs no sk_init() (the device's workspace is
+ * overlapping calls share the SMs in turns rather than at once; such
+ * linear-layer calls are also launched without programmatic dependent launch.
+ * (The cache calls and token_logprobs are launched as on any other stream, with
+ * it where sk_set_pdl allows: their CTAs wait for none outside a cluster.)  Up
+ * to 64 stream workspaces per process; more return SK_ERR_INVALID_ARG.  Call it
+ * before capturing a CUDA graph.  Needs no sk_init() (the device's workspace is
  * only the fallback).
  */
 SK_API sk_status sk_stream_workspace(void *stream, size_t workspace_bytes);

@@ -236,10 +236,11 @@ __device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int
 // joined through distributed shared memory.  Otherwise the CTAs share all tiles
 // evenly, and kv4_join_kernel joins what they leave in the scratch memory.
 //
-// Bound by the issue of decoding (conversion, scaling) and products, which add
-// up: 64 sequences of up to 16411 positions, 24 query over 2 kv heads of 256,
-// the call 78 us (281 MB, 3.6 TB/s).  One sequence of
-// 1031 positions, 48 over 4 heads of 128: 5.3 us, all of it latency.
+// Bound by fixed latencies where registers leave two warps a scheduler: 64
+// sequences of up to 16411 positions, 24 query over 2 kv heads of 256, the call
+// 80 us (281 MB, 3.5 TB/s) with issue slots 44 % used, tensor pipe 40 %, DRAM 47
+// %, and most of a warp's time between dependent instructions.  One sequence of
+// 1031 positions, 48 over 4 heads of 128: 5.2 us, all of it latency.
 template <int D, int NR, bool SHORT>
 __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(const __grid_constant__ AttnParams p) {
     using C = Cfg<D, NR>;
@@ -695,9 +696,11 @@ __global__ void __launch_bounds__(JT) kv4_join_rows_kernel(const __grid_constant
 // and sums.  A warp owns the 32 positions of a step, whose sum over the rows is
 // taken in one order; the next step's keys are on their way meanwhile.  (Taken
 // during the attention the weights would need each row's final sum, which is
-// not known until its last position.)  Bound like the attention by decoding and
-// products: 23 sequences of up to 9001 positions, 2 rows, 32 over 8 heads of 64,
-// the whole call 46 us.
+// not known until its last position.)  23 sequences of up to 9001 positions, 2
+// rows, 32 over 8 heads of 64: the whole call 41 us, this pass about 20 of it,
+// issue slots half used.  (Scores kept by the first pass would be 4 bytes per
+// position and row each way: 25 MB twice in this case, 7.5 us at the copy rate.
+// Not built.)
 constexpr int WT_TILES = 16;           // tiles of eight rows held in shared memory at a time
 constexpr int WT_STAGES = 4;
 constexpr int ACC_STEPS = 4;           // steps whose accumulated weights are on their way

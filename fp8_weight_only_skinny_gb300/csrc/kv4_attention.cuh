@@ -30,8 +30,8 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // difference of neighbouring numbers is exact, so that weights near the maximum
 // are right whatever the scores' size (c s - c base, each rounded by itself, is
 // off by up to 2^5 where the scores are 2^28, and the FP16 weights overflow or
-// vanish); two scores at a time, an add and a multiply of f32x2, that costs what
-// an fma each did (0.98 to 1.02 of it, over eighteen shapes).  A base is rounded
+// vanish); two scores at a time, an add and a multiply of f32x2, that costs about
+// what an fma each did (0.96 to 1.02 of the call, over seventeen shapes).  A base is rounded
 // such that (s - base) c is between 0 and P_SHIFT for the maximum, and moves when
 // that exceeds P_SHIFT + SLACK.  The p go to the second product in FP16, at most
 // 2^15 and normal down to 2^-21 of the maximum's (2^-32 is the rounding of the

@@ -5,6 +5,11 @@
 //     logprob = t_tok - m - ln S,   entropy = ln S - sum exp(t_j - m) (t_j - m) / S,
 //     rank    = 1 + #{j : z_j > z_tok, or z_j = z_tok and j < tok},
 //     top     = the top_n largest z_j, ties to the lower j.
+// 2^x and log2 are the hardware's approximations, and the sums FP32: a log
+// probability is within 2^-16 where a thread adds up to 128 logits
+// (tests/test_logprobs_error_gpu.py); measured against 64 bits 1e-7 relative for
+// one to eight rows and 1.9e-7 for 2048 rows of 151936 (exp and log of FP32
+// throughout: 0.7e-7 to 2.1e-7).
 // One pass over the logits: every thread keeps a running maximum, sum and
 // weighted sum (FP32), the count for the rank, and appends what may still be
 // among the top_n to a list in shared memory.

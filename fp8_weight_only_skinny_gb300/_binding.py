@@ -38,7 +38,7 @@ def _load() -> ctypes.CDLL:
         raise ImportError(
             f"{LIB_PATH} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
     L = ctypes.CDLL(LIB_PATH)
-    p, i, f, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
+    p, i, f, ll, d = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong, ctypes.c_double
     sig = {
         "sk_init": ([ctypes.c_size_t], i),
         "sk_shutdown": ([], i),
@@ -62,6 +62,10 @@ def _load() -> ctypes.CDLL:
         "kv4_append": ([p, ll, p, ll, p, p, f, f, p, p, i, i, i, i, i, p], i),
         "kv4_attention": ([p, ll, p, p, p, f, f, f, p, p, p, p, i, i, i, i, i, i, i, i, p], i),
         "kv4_evict": ([p, p, p, p, p, p, p, p, i, i, i, i, i, i, i, i, i, p], i),
+        "rope_frequencies": ([p, i, i, d, d, d, d, d], i),
+        "qk_norm_rope": ([p, ll, p, ll, p, p, p, p, d, d, p, ll, p, ll, i, i, i, i, i, i, p], i),
+        "kv4_append_rope": ([p, ll, p, ll, p, ll, p, p, p, p, p, d, d, p, ll, p, f, f, i, i, i, i, i, i, i, i, p], i),
+        "kv4_window_attention": ([p, ll, p, p, p, f, f, f, i, i, p, p, i, i, i, i, i, i, i, i, p], i),
         "token_logprobs": ([p, i, ll, p, f, i, p, p, p, p, p, i, i, p], i),
     }
     for name, (args, res) in sig.items():
@@ -76,7 +80,8 @@ lib = _load()
 # Names declared in include/skinny.h (the tests check that each is exported).
 EXPORTS = ("sk_init", "sk_shutdown", "sk_stream_workspace", "nvfp4_gemm", "nvfp4_gemm_f16out", "fp8_gemm",
            "fp8_gemm_f16out", "lm_head_argmax", "lm_head_verify", "lm_head_sample", "fp8_quantize",
-           "nvfp4_quantize", "kv4_append", "kv4_attention", "kv4_evict", "token_logprobs",
+           "nvfp4_quantize", "kv4_append", "kv4_attention", "kv4_evict", "rope_frequencies", "qk_norm_rope",
+           "kv4_append_rope", "kv4_window_attention", "token_logprobs",
            "sk_status_string", "sk_last_device_error",
            "sk_set_pdl", "sk_set_variant", "sk_inject_wait_timeout", "nvfp4_gemm_noalloc", "sk_version")
 
@@ -405,6 +410,120 @@ def kv4_attention(q, cache, table, lens, k_scale: float, v_scale: float, scale: 
                              ap, op, seqs, rows, hq, heads, dim, pages, page, width,
                              _raw_stream(stream, cache.get_device())),
            "kv4_attention")
+    return out, lse
+
+
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "turns": 3, "index": 4}
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                     original: float = 0.0, low: float = 1.0, high: float = 32.0, device="cuda"):
+    """The frequencies of rot_dim / 2 pairs as fractions of a turn per position in units of 2^-64 (int64 holding the
+    u64 of include/skinny.h), lengthened for longer contexts by one of ROPE_SCALINGS."""
+    torch = _torch()
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALINGS)}")
+    freqs = torch.empty((max(0, rot_dim) // 2,), dtype=torch.int64)
+    room = freqs if freqs.numel() else torch.empty((1,), dtype=torch.int64)      # an empty tensor has no address
+    _check(lib.rope_frequencies(room.data_ptr(), rot_dim, ROPE_SCALINGS[scaling], base, factor, original, low, high),
+           "rope_frequencies")
+    return freqs.to(device)
+
+
+def _rope_args(q, positions, freqs, q_weight, k_weight, dim):
+    """Pointers of what both rotating calls take, and the rotated components of a head."""
+    torch = _torch()
+    rot = 0 if freqs is None else 2 * freqs.numel()
+    fp = None if rot == 0 else _need(freqs, torch.int64, (rot // 2,), "freqs")
+    pp = None if positions is None else _need(positions, torch.int32, (q.shape[0],), "positions")
+    qw = None if q_weight is None else _need(q_weight, torch.float32, (dim,), "q_weight")
+    kw = None if k_weight is None else _need(k_weight, torch.float32, (dim,), "k_weight")
+    return pp, fp, qw, kw, rot
+
+
+def qk_norm_rope(q, k, positions, freqs, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                 amplitude: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Norm of every query and key head (FP16 [T][heads][head_dim], row stride free; weights float32 [head_dim], or
+    neither) and its rotation by positions (int32 [T]) under freqs (rope_frequencies; None: no rotation).
+
+    q_out and k_out may be q and k themselves.  Returns (q_out, k_out)."""
+    torch = _torch()
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be CUDA float16 tensors [T][heads][head_dim]")
+    hq, dim = q.shape[1:]
+    heads = k.shape[1]
+    n, qs = _rows_f16(q, hq, dim, "q")
+    nk, ks = _rows_f16(k, heads, dim, "k")
+    if n != nk:
+        raise ValueError("q and k have different numbers of tokens")
+    pp, fp, qw, kw, rot = _rope_args(q, positions, freqs, q_weight, k_weight, dim)
+    if q_out is None:
+        q_out = _new((n, hq, dim), torch.float16, q.device, stream)
+    if k_out is None:
+        k_out = _new((n, heads, dim), torch.float16, q.device, stream)
+    nq, qos = _rows_f16(q_out, hq, dim, "q_out")
+    no, kos = _rows_f16(k_out, heads, dim, "k_out")
+    if nq != n or no != n:
+        raise ValueError("q_out and k_out must have as many tokens as q and k")
+    _check(lib.qk_norm_rope(q.data_ptr(), qs, k.data_ptr(), ks, pp, fp, qw, kw, eps, amplitude, q_out.data_ptr(), qos,
+                            k_out.data_ptr(), kos, n, hq, heads, dim, rot, int(interleaved),
+                            _raw_stream(stream, q.get_device())), "qk_norm_rope")
+    return q_out, k_out
+
+
+def kv4_append_rope(q, k, v, slots, positions, freqs, cache, k_scale: float, v_scale: float, q_weight=None, k_weight=None,
+                    eps: float = 1e-6, interleaved: bool = False, amplitude: float = 1.0, q_out=None, stream=None):
+    """qk_norm_rope with the keys and the values (FP16 [T][kv_heads][head_dim]) written to the cache's slots (kv4_append).
+
+    Returns q_out (FP16 [T][q_heads][head_dim], may be q itself)."""
+    torch = _torch()
+    pages, heads, dim, page = _cache_dims(cache)
+    if q.dim() != 3:
+        raise ValueError("q must be a CUDA float16 tensor [T][q_heads][head_dim]")
+    hq = q.shape[1]
+    n, qs = _rows_f16(q, hq, dim, "q")
+    nk, ks = _rows_f16(k, heads, dim, "k")
+    nv, vs = _rows_f16(v, heads, dim, "v")
+    if n != nk or n != nv:
+        raise ValueError("q, k and v have different numbers of tokens")
+    pp, fp, qw, kw, rot = _rope_args(q, positions, freqs, q_weight, k_weight, dim)
+    sp = _need(slots, torch.int32, (n,), "slots")
+    if q_out is None:
+        q_out = _new((n, hq, dim), torch.float16, q.device, stream)
+    no, qos = _rows_f16(q_out, hq, dim, "q_out")
+    if no != n:
+        raise ValueError("q_out must have as many tokens as q")
+    _check(lib.kv4_append_rope(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, sp, pp, fp, qw, kw, eps, amplitude,
+                               q_out.data_ptr(), qos, cache.data_ptr(), k_scale, v_scale, n, pages, hq, heads, dim, page,
+                               rot, int(interleaved), _raw_stream(stream, cache.get_device())), "kv4_append_rope")
+    return q_out
+
+
+def kv4_window_attention(q, cache, table, lens, k_scale: float, v_scale: float, scale: float, window: int, sinks: int = 0,
+                         rows: int = 1, out=None, lse=None, stream=None):
+    """kv4_attention where a row sees only the last `window` positions up to its own and the first `sinks` ones.
+
+    Returns (out FP16, lse float32 [seqs * rows][q_heads])."""
+    torch = _torch()
+    pages, heads, dim, page = _cache_dims(cache)
+    if q.dim() != 3:
+        raise ValueError("q must be a CUDA float16 tensor [seqs * rows][q_heads][head_dim]")
+    hq = q.shape[1]
+    n, qs = _rows_f16(q, hq, dim, "q")
+    if table.dim() != 2:
+        raise ValueError("table must be a contiguous CUDA int32 tensor [seqs][width]")
+    seqs, width = table.shape
+    if seqs * rows != n:
+        raise ValueError(f"q has {n} rows, expected {seqs} sequences x {rows}")
+    if out is None:
+        out = _new((n, hq, dim), torch.float16, q.device, stream)
+    if lse is None:
+        lse = _new((n, hq), torch.float32, q.device, stream)
+    _check(lib.kv4_window_attention(q.data_ptr(), qs, cache.data_ptr(), _need(table, torch.int32, (seqs, width), "table"),
+                                    _need(lens, torch.int32, (seqs,), "lens"), k_scale, v_scale, scale, window, sinks,
+                                    _need(out, torch.float16, (n, hq, dim), "out"),
+                                    _need(lse, torch.float32, (n, hq), "lse"), seqs, rows, hq, heads, dim, pages, page,
+                                    width, _raw_stream(stream, cache.get_device())), "kv4_window_attention")
     return out, lse
 
 

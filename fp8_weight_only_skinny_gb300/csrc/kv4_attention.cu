@@ -241,7 +241,9 @@ __device__ __forceinline__ void write_row(const AttnParams &p, int b, int h, int
 // 80 us (281 MB, 3.5 TB/s) with issue slots 44 % used, tensor pipe 40 %, DRAM 47
 // %, and most of a warp's time between dependent instructions.  One sequence of
 // 1031 positions, 48 over 4 heads of 128: 5.2 us, all of it latency.
-template <int D, int NR, bool SHORT>
+//
+// WIN: of a sequence's positions only those that Seen<true> has are looked at.
+template <int D, int NR, bool SHORT, bool WIN>
 __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(const __grid_constant__ AttnParams p) {
     using C = Cfg<D, NR>;
     constexpr int ROWS = C::ROWS, NX = C::ACC >= 64 || NR > 2 ? 1 : 2;       // records scored together
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
     sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
     Share sh;
-    if constexpr (!SHORT) sh = share_of(p, p.heads * p.RT, sm_share);
+    if constexpr (!SHORT) sh = share_of<WIN>(p, p.heads * p.RT, sm_share);
     const uint32_t CL = SHORT ? sk::cluster_size() : 1u;
     uint32_t at = 0, parity = 0;   // this warp's ring position
     const bool issuer = lane == 0 && !p.stall;
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
             const int which = int(blockIdx.x / CL), rank = int(blockIdx.x % CL);
             b = which / (p.heads * p.RT);
             hr = which - b * (p.heads * p.RT);
-            len = length_of(p, b);
+            len = Seen<WIN>(p, b).len;
             nt = tiles_of(len);
             const int each = (nt + int(CL) - 1) / int(CL);
             t_lo = min(nt, rank * each);
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
         } else {
             if (sh.t >= sh.end || sh.b >= p.B) break;
             b = sh.b;
-            len = length_of(p, b);
+            len = Seen<WIN>(p, b).len;
             nt = tiles_of(len);
             if (nt == 0) {
                 ++sh.b;
@@ -293,6 +295,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
         const int h = hr / p.RT, rt = hr - h * p.RT;
         const int32_t *table = p.table + (long long)b * p.width;
         const int nrec = (len + 15) / 16;
+        const Seen<WIN> seen(p, b);
 
         // this warp's steps: st0, st0 + WARPS, ... (n of them)
         const int st0 = t_lo * WARPS + warp, st_hi = min(t_hi * WARPS, (len + STEP - 1) / STEP);
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
         // 16 k + l / 2; the next batch is fetched a whole batch early.
         auto lookup = [&](int k) {
             const int rec = 2 * (st0 + (16 * k + (lane >> 1)) * WARPS) + (lane & 1);
-            return sk::kv4_record(table, min(rec, nrec - 1), p.recs, p.by_recs, p.pages, p.heads, h);
+            return sk::kv4_record(table, seen.record(min(rec, nrec - 1)), p.recs, p.by_recs, p.pages, p.heads, h);
         };
         uint32_t now = 0, soon = 0;
         // copy step i of this warp into stage `slot`
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
                     qk<D, NX, NR>(k, qs, lane, s);
                 }
                 const int pos = (st0 + i * WARPS) * STEP + 16 * x0;
-                if (pos + 16 * NX > all_see) {
+                if (pos + 16 * NX > all_see || (WIN && pos + 16 * NX > p.sinks && pos < len - p.window)) {
 #pragma unroll
                     for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -376,8 +379,10 @@ __global__ void __launch_bounds__(CT, (Cfg<D, NR>::CTAS)) kv4_attention_kernel(c
 #pragma unroll
                             for (int x = 0; x < NX; ++x)
 #pragma unroll
-                                for (int y = 0; y < 2; ++y)
-                                    if (pos + 16 * x + 8 * y + g >= lim) s[x][r][2 * y + e] = NEG_INF;
+                                for (int y = 0; y < 2; ++y) {
+                                    const int j = pos + 16 * x + 8 * y + g;
+                                    if (j >= lim || (WIN && j >= p.sinks && j < lim - p.window)) s[x][r][2 * y + e] = NEG_INF;
+                                }
                         }
                 }
                 float top[NR][2];
@@ -910,10 +915,10 @@ sk_status join(const AttnParams &p, int tile_rows, int sms, cudaStream_t s) {
 // tiles each one of 16000 takes 12.5 against 11.3.  In place of the tensor cores
 // (rows above TC_ABOVE) half as many: 32 rows, one of 4000 10.1 against 12.5.
 constexpr int SHORT_TILES = 4;
-template <int D, int NR>
+template <int D, int NR, bool WIN>
 int short_cluster(const AttnParams &p, int few) {
     using C = Cfg<D, NR>;
-    constexpr auto kernel = kv4_attention_kernel<D, NR, true>;
+    constexpr auto kernel = kv4_attention_kernel<D, NR, true, WIN>;
     if (sk::prepare_kernel<kernel>(C::SMEM, true) != cudaSuccess) return 0;
     const long long segments = (long long)p.B * p.heads * p.RT, tiles = ((long long)p.cap + TILE - 1) / TILE;
     int c = 1;
@@ -922,27 +927,27 @@ int short_cluster(const AttnParams &p, int few) {
 }
 
 // The launch of that form, where there is one.
-template <int D, int NR>
+template <int D, int NR, bool WIN>
 bool attend_short(const AttnParams &p, int few, cudaStream_t s, sk_status *st) {
-    const int cluster = short_cluster<D, NR>(p, few);
+    const int cluster = short_cluster<D, NR, WIN>(p, few);
     if (!cluster) return false;
     const dim3 grid(unsigned(cluster) * unsigned(p.B * p.heads * p.RT));
-    *st = sk::launch_pdl_cluster(kv4_attention_kernel<D, NR, true>, cluster, grid, dim3(CT), Cfg<D, NR>::SMEM, s, p) ==
+    *st = sk::launch_pdl_cluster(kv4_attention_kernel<D, NR, true, WIN>, cluster, grid, dim3(CT), Cfg<D, NR>::SMEM, s, p) ==
                   cudaSuccess
               ? SK_OK
               : SK_ERR_CUDA;
     return true;
 }
 
-template <int D, int NR>
+template <int D, int NR, bool WIN>
 sk_status attend(AttnParams &p, unsigned char *rest, int sms, cudaStream_t s) {
     using C = Cfg<D, NR>;
     sk_status st;
-    if (attend_short<D, NR>(p, SHORT_TILES, s, &st)) return st;
+    if (attend_short<D, NR, WIN>(p, SHORT_TILES, s, &st)) return st;
     p.ctas = sms * C::CTAS;
     if (!place_partials(p, rest, C::ROWS, D)) return SK_ERR_WORKSPACE;
-    if (sk::prepare_kernel<kv4_attention_kernel<D, NR, false>>(C::SMEM) != cudaSuccess) return SK_ERR_CUDA;
-    if (sk::launch_pdl(kv4_attention_kernel<D, NR, false>, dim3(p.ctas), dim3(CT), C::SMEM, s, p) != cudaSuccess)
+    if (sk::prepare_kernel<kv4_attention_kernel<D, NR, false, WIN>>(C::SMEM) != cudaSuccess) return SK_ERR_CUDA;
+    if (sk::launch_pdl(kv4_attention_kernel<D, NR, false, WIN>, dim3(p.ctas), dim3(CT), C::SMEM, s, p) != cudaSuccess)
         return SK_ERR_CUDA;
     return join<D>(p, C::ROWS, sms, s);
 }
@@ -955,7 +960,7 @@ sk_status attend_tc(AttnParams &p, unsigned char *rest, int sms, cudaStream_t s)
     return join<128>(p, rows, sms, s);
 }
 
-template <int D>
+template <int D, bool WIN>
 sk_status run(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     // Query rows of a kv head in tiles of 8 NR rows, as even as they can be: NR
     // up to 4 (the outputs are D / 4 NR registers a thread; D = 256: up to 2;
@@ -966,14 +971,14 @@ sk_status run(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     const int nr = (tiles + p.RT - 1) / p.RT;
     unsigned char *const rest = place_rows(p, scratch);
     sk_status st;
-    if (D == 128 && p.M * p.G > TC_ABOVE) {
-        const bool done = nr == 3 ? attend_short<128, 3>(p, SHORT_TILES / 2, s, &st)
-                                  : attend_short<128, 2>(p, SHORT_TILES / 2, s, &st);
+    if (D == 128 && !WIN && p.M * p.G > TC_ABOVE) {
+        const bool done = nr == 3 ? attend_short<128, 3, false>(p, SHORT_TILES / 2, s, &st)
+                                  : attend_short<128, 2, false>(p, SHORT_TILES / 2, s, &st);
         if (!done) st = attend_tc(p, rest, sms, s);
-    } else if (nr == 1) st = attend<D, 1>(p, rest, sms, s);
-    else if (nr == 2) st = attend<D, 2>(p, rest, sms, s);
-    else if constexpr (MOST == 4) st = nr == 3 ? attend<D, 3>(p, rest, sms, s) : attend<D, 4>(p, rest, sms, s);
-    else if constexpr (MOST == 3) st = attend<D, 3>(p, rest, sms, s);
+    } else if (nr == 1) st = attend<D, 1, WIN>(p, rest, sms, s);
+    else if (nr == 2) st = attend<D, 2, WIN>(p, rest, sms, s);
+    else if constexpr (MOST == 4) st = nr == 3 ? attend<D, 3, WIN>(p, rest, sms, s) : attend<D, 4, WIN>(p, rest, sms, s);
+    else if constexpr (MOST == 3) st = attend<D, 3, WIN>(p, rest, sms, s);
     else return SK_ERR_UNSUPPORTED_SHAPE;
     if (st != SK_OK || !p.acc_out) return st;
     const int held = tiles < WT_TILES ? tiles : WT_TILES;
@@ -986,13 +991,13 @@ sk_status run(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
                : SK_ERR_CUDA;
 }
 
-}  // namespace
-
-extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint8_t *cache, const int32_t *table,
-                                   const int32_t *lens, float k_scale, float v_scale, float scale, void *out,
-                                   float *lse, const float *acc_in, float *acc_out, int seqs, int rows, int q_heads,
-                                   int kv_heads, int head_dim, int pages, int page_size, int table_width,
-                                   void *stream) {
+// What kv4_attention and kv4_window_attention ask of their arguments (SK_OK with
+// `go` false: nothing to do), and the parameters they share.
+sk_status attention_params(AttnParams &p, bool &go, const void *q, long long q_stride, const uint8_t *cache,
+                           const int32_t *table, const int32_t *lens, float k_scale, float v_scale, float scale, void *out,
+                           float *lse, const float *acc_in, float *acc_out, int seqs, int rows, int q_heads, int kv_heads,
+                           int head_dim, int pages, int page_size, int table_width) {
+    go = false;
     if (seqs < 0 || rows < 1 || rows > 8 || q_heads < 1 || kv_heads < 1 || pages < 1 || page_size < 1 ||
         table_width < 1)
         return SK_ERR_INVALID_ARG;
@@ -1013,7 +1018,7 @@ extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint
     if (q_stride % 8 || !aligned(q, 16) || !aligned(cache, 16) || !aligned(table, 4) || !aligned(lens, 4) ||
         !aligned(out, 16) || !aligned(lse, 4) || !aligned(acc_in, 4) || !aligned(acc_out, 4))
         return SK_ERR_MISALIGNED;
-    AttnParams p = {};
+    p = AttnParams{};
     p.B = seqs;
     p.M = rows;
     p.heads = kv_heads;
@@ -1025,9 +1030,6 @@ extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint
     // tiles of positions, over all segments, fit 31 bits
     if ((long long)seqs * kv_heads * ((rows * p.G + 7) / 8) * (((long long)table_width * page_size + TILE - 1) / TILE) > 0x7FFFFFFFLL)
         return SK_ERR_UNSUPPORTED_SHAPE;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    sk::Scratch sc;
-    if (!sk::scratch_for(s, &sc)) return SK_ERR_NOT_INITIALIZED;
     p.q = static_cast<const __half *>(q);
     p.q_stride = q_stride;
     p.cache = cache;
@@ -1037,7 +1039,6 @@ extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint
     p.lse = lse;
     p.acc_in = acc_in;
     p.acc_out = acc_out;
-    p.err = sc.err;
     p.pages = pages;
     p.recs = page_size / sk::KV4_REC;
     p.by_recs = sk::Div(p.recs);
@@ -1047,10 +1048,52 @@ extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint
     p.shift = P_SHIFT / p.c;
     p.reach = (P_SHIFT + SLACK) / p.c;
     p.vg = v_scale;
+    go = true;
+    return SK_OK;
+}
+
+template <bool WIN>
+sk_status run_on(AttnParams &p, int head_dim, cudaStream_t s) {
+    sk::Scratch sc;
+    if (!sk::scratch_for(s, &sc)) return SK_ERR_NOT_INITIALIZED;
+    p.err = sc.err;
     p.stall = sk::take_inject_stall();
     switch (head_dim) {
-        case 64: return run<64>(p, sc.base, sc.num_sms, s);
-        case 128: return run<128>(p, sc.base, sc.num_sms, s);
-        default: return run<256>(p, sc.base, sc.num_sms, s);
+        case 64: return run<64, WIN>(p, sc.base, sc.num_sms, s);
+        case 128: return run<128, WIN>(p, sc.base, sc.num_sms, s);
+        default: return run<256, WIN>(p, sc.base, sc.num_sms, s);
     }
+}
+
+}  // namespace
+
+extern "C" sk_status kv4_attention(const void *q, long long q_stride, const uint8_t *cache, const int32_t *table,
+                                   const int32_t *lens, float k_scale, float v_scale, float scale, void *out,
+                                   float *lse, const float *acc_in, float *acc_out, int seqs, int rows, int q_heads,
+                                   int kv_heads, int head_dim, int pages, int page_size, int table_width,
+                                   void *stream) {
+    AttnParams p;
+    bool go;
+    const sk_status st = attention_params(p, go, q, q_stride, cache, table, lens, k_scale, v_scale, scale, out, lse, acc_in,
+                                          acc_out, seqs, rows, q_heads, kv_heads, head_dim, pages, page_size, table_width);
+    return go ? run_on<false>(p, head_dim, reinterpret_cast<cudaStream_t>(stream)) : st;
+}
+
+extern "C" sk_status kv4_window_attention(const void *q, long long q_stride, const uint8_t *cache, const int32_t *table,
+                                          const int32_t *lens, float k_scale, float v_scale, float scale, int window,
+                                          int sinks, void *out, float *lse, int seqs, int rows, int q_heads, int kv_heads,
+                                          int head_dim, int pages, int page_size, int table_width, void *stream) {
+    if (window < 1 || sinks < 0) return SK_ERR_INVALID_ARG;
+    AttnParams p;
+    bool go;
+    const sk_status st = attention_params(p, go, q, q_stride, cache, table, lens, k_scale, v_scale, scale, out, lse, nullptr,
+                                          nullptr, seqs, rows, q_heads, kv_heads, head_dim, pages, page_size, table_width);
+    if (!go) return st;
+    // no sequence has more positions than the table holds, nor looks at more than its sinks' and its rows' windows' records
+    p.limit = p.cap;
+    p.window = window < p.limit ? window : p.limit;
+    p.sinks = sinks < p.limit ? sinks : p.limit;
+    const long long most = (long long)p.sinks + p.window + rows + 2 * sk::KV4_REC;
+    if (most < p.cap) p.cap = int(most);
+    return run_on<true>(p, head_dim, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -55,6 +55,7 @@ struct AttnParams {
     unsigned int *err;
     int stall;                 // issue no copies (sk_inject_wait_timeout)
     int pages, heads, recs, width, cap;   // recs: records per page; cap: positions the table can hold
+    int limit, window, sinks;  // of a window: positions the table can hold (cap: that are looked at), see Seen
     int B, M, G, RT, ctas;     // G: query heads per kv head; RT: row tiles
     float c, shift, reach, vg; // scale * key scale * log2 e; P_SHIFT / c; (P_SHIFT + SLACK) / c; value scale
     sk::Div by_recs;
@@ -113,6 +114,27 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t codes) {
 }
 
 __device__ __forceinline__ int length_of(const AttnParams &p, int b) { return min(max(p.lens[b], 0), p.cap); }
+
+// The positions of a sequence that its rows look at.  With a window: those before
+// `sinks` and those from the first row's window on, numbered without the whole
+// records in between: records from `gap` on lie `skip` records further.  Row m
+// sees the number j if j < lim and (j < sinks or j >= lim - window), where lim =
+// len - (M - 1 - m); a gap's ends lie at or below every row's lim - window.
+template <bool WIN>
+struct Seen {
+    int len, gap, skip;
+    __device__ __forceinline__ Seen(const AttnParams &p, int b) : gap(0), skip(0) {
+        if constexpr (WIN) {
+            len = min(max(p.lens[b], 0), p.limit);
+            gap = (min(p.sinks, len) + sk::KV4_REC - 1) / sk::KV4_REC;
+            skip = max(0, max(0, len - (p.M - 1) - p.window) / sk::KV4_REC - gap);
+            len -= skip * sk::KV4_REC;
+        } else {
+            len = length_of(p, b);
+        }
+    }
+    __device__ __forceinline__ int record(int r) const { return WIN && r >= gap ? r + skip : r; }
+};
 __device__ __forceinline__ int tiles_of(int len) { return (len + TILE - 1) / TILE; }
 
 // The CTA's share of all (sequence, head, row tile, position tile) in that
@@ -140,7 +162,9 @@ __device__ __forceinline__ int inclusive_scan(int x, int lane) {
 }
 
 // per_len: segments of a sequence; sm: a word per warp and two more.
+template <bool WIN = false>
 __device__ __forceinline__ Share share_of(const AttnParams &p, int per_len, int *sm) {
+    auto length = [&](int b) { return Seen<WIN>(p, b).len; };
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, nw = blockDim.x >> 5, c = blockIdx.x;
     Share s;
     auto split = [&](int total) {
@@ -153,7 +177,7 @@ __device__ __forceinline__ Share share_of(const AttnParams &p, int per_len, int 
     };
     if (p.B <= 32) {
         // every warp by itself, a lane a sequence
-        const int mine = lane < p.B ? tiles_of(length_of(p, lane)) * per_len : 0;
+        const int mine = lane < p.B ? tiles_of(length(lane)) * per_len : 0;
         const int x = inclusive_scan(mine, lane);
         split(__shfl_sync(0xffffffffu, x, 31));
         const unsigned int past = __ballot_sync(0xffffffffu, x > s.t);
@@ -164,7 +188,7 @@ __device__ __forceinline__ Share share_of(const AttnParams &p, int per_len, int 
     const int each = (p.B + int(blockDim.x) - 1) / int(blockDim.x);
     const int lo = min(p.B, tid * each), hi = min(p.B, lo + each);
     int mine = 0;
-    for (int b = lo; b < hi; ++b) mine += tiles_of(length_of(p, b)) * per_len;
+    for (int b = lo; b < hi; ++b) mine += tiles_of(length(b)) * per_len;
     const int x = inclusive_scan(mine, lane);
     if (lane == 31) sm[wid] = x;
     __syncthreads();
@@ -178,7 +202,7 @@ __device__ __forceinline__ Share share_of(const AttnParams &p, int per_len, int 
     if (s.t < s.end && s.t >= before && s.t < before + mine) {
         int b = lo, left = s.t - before;
         for (; b + 1 < hi; ++b) {
-            const int n = tiles_of(length_of(p, b)) * per_len;
+            const int n = tiles_of(length(b)) * per_len;
             if (left < n) break;
             left -= n;
         }

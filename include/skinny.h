@@ -352,6 +352,87 @@ SK_API sk_status kv4_attention(const void *q, long long q_stride, const uint8_t 
                                int head_dim, int pages, int page_size, int table_width, void *stream);
 
 /*
+ * Rotary positions.  A frequency is a fraction of a turn per position, held as a
+ * u64 in units of 2^-64: the angle of a position, position * F modulo 2^64, is
+ * exact at any distance.  rope_frequencies fills a table in HOST memory (the
+ * caller copies it to the device; a table of other frequencies is as good) of
+ * rot_dim / 2 entries from f_i = base^(-2 i / rot_dim) radians per position,
+ * lengthened for contexts `factor` times the `original` one:
+ *   SK_ROPE_PLAIN   f_i
+ *   SK_ROPE_LINEAR  f_i / factor
+ *   SK_ROPE_BASE    base becomes base * factor^(rot_dim / (rot_dim - 2))
+ *   SK_ROPE_TURNS   f_i (s + (1 - s) / factor), s = (t_i - low) / (high - low) held
+ *                   to [0, 1], t_i = original * f_i / (2 pi) turns in the original context
+ *   SK_ROPE_INDEX   the same with s falling from 1 to 0 linearly in the index, between
+ *                   those of the frequencies that turn `high` times (rounded down,
+ *                   at least 0) and `low` times (rounded up, at most rot_dim / 2 - 1)
+ *   1 < base <= 1e12; 1 <= factor <= 1e6 (not read by PLAIN); TURNS and INDEX:
+ *   1 <= original <= 1e12, 0 < low < high <= 1e6; rot_dim even (BASE: not 2).
+ */
+enum { SK_ROPE_PLAIN = 0, SK_ROPE_LINEAR = 1, SK_ROPE_BASE = 2, SK_ROPE_TURNS = 3, SK_ROPE_INDEX = 4 };
+SK_API sk_status rope_frequencies(uint64_t *freqs, int rot_dim, int scaling, double base, double factor, double original,
+                                  double low, double high);
+
+/*
+ * qk_norm_rope: norm of each query and key head and its rotation by position, in
+ * one pass (between the fused qkv projection and a cache or attention in FP16):
+ *     y = x / sqrt(mean x^2 + eps) * weight          (without weights: y = x)
+ *     (a, b) -> amplitude * (a cos t - b sin t, b cos t + a sin t), t = 2 pi position F_i / 2^64
+ * for pair i of the first rot_dim components: components i and i + rot_dim / 2
+ * (interleaved = 0) or 2 i and 2 i + 1 (interleaved = 1); the others are y.
+ *   q, k       const f16 [tokens][q_heads or kv_heads][D], q_stride and k_stride
+ *              elements from token to token (a multiple of 8, >= heads * D), 16-byte aligned
+ *   positions  const i32 [tokens] (any value, also negative)
+ *   freqs      const u64 [rot_dim / 2], device memory, 8-byte aligned; positions and
+ *              freqs may be NULL if rot_dim = 0 (norm alone)
+ *   q_weight, k_weight  const f32 [D], or both NULL (no norm)
+ *   q_out, k_out  f16, as q and k with strides of their own; q_out may be q and
+ *              k_out may be k with the same stride (in place), no other overlap
+ *   D = head_dim in {64, 128, 256}; rot_dim a multiple of 16, 0 .. D; 0 <= eps <= 1;
+ *   1e-3 <= |amplitude| <= 1e3 (1, or the factor that a lengthened context asks for);
+ *   heads <= 4096.  Computed in FP32 (the norm's sum too), rounded to FP16 once.
+ *   tokens = 0: nothing is launched.  Needs no workspace.
+ */
+SK_API sk_status qk_norm_rope(const void *q, long long q_stride, const void *k, long long k_stride,
+                              const int32_t *positions, const uint64_t *freqs, const float *q_weight,
+                              const float *k_weight, double eps, double amplitude, void *q_out, long long q_out_stride,
+                              void *k_out, long long k_out_stride, int tokens, int q_heads, int kv_heads, int head_dim,
+                              int rot_dim, int interleaved, void *stream);
+
+/*
+ * kv4_append_rope: qk_norm_rope with the keys, and the values beside them, written
+ * to the cache instead of to memory: one launch between the qkv projection and
+ * kv4_attention.  Values are encoded as by kv4_append.  A key's codes are those of
+ * exact arithmetic: block by block  sc = E4M3(max |y| / (6 G)),  S = the value of
+ * sc,  code = E2M1(y / (S G)), y the unrounded normed and rotated key, evaluated
+ * in 64 bits wherever 32 leave a code open; so they do not depend on the order of
+ * a sum, and calls are bit-for-bit reproducible.
+ *   v        const f16 [tokens][kv_heads][D], as k
+ *   slots, cache, k_scale, v_scale, pages, page_size as kv4_append (a token with a
+ *   negative or too large slot has its query rotated all the same); the others as
+ *   qk_norm_rope.  Non-finite keys or values give unspecified codes.
+ */
+SK_API sk_status kv4_append_rope(const void *q, long long q_stride, const void *k, long long k_stride, const void *v,
+                                 long long v_stride, const int32_t *slots, const int32_t *positions,
+                                 const uint64_t *freqs, const float *q_weight, const float *k_weight, double eps,
+                                 double amplitude, void *q_out, long long q_out_stride, uint8_t *cache, float k_scale,
+                                 float v_scale, int tokens, int pages, int q_heads, int kv_heads, int head_dim,
+                                 int page_size, int rot_dim, int interleaved, void *stream);
+
+/*
+ * kv4_window_attention: kv4_attention where a query row at position i sees only
+ * the positions i - window < j <= i and j < sinks (at most i): the last `window`
+ * ones, itself among them, and the first `sinks` tokens.  Only the records that
+ * hold such positions are read.  Query row m of sequence b is at i = lens[b] - M + m.
+ *   window >= 1, sinks >= 0; the other arguments, the results and the workspace
+ *   as kv4_attention without accumulated weights.
+ */
+SK_API sk_status kv4_window_attention(const void *q, long long q_stride, const uint8_t *cache, const int32_t *table,
+                                      const int32_t *lens, float k_scale, float v_scale, float scale, int window,
+                                      int sinks, void *out, float *lse, int seqs, int rows, int q_heads, int kv_heads,
+                                      int head_dim, int pages, int page_size, int table_width, void *stream);
+
+/*
  * kv4_evict: keep at most `budget` positions per sequence and kv head, in their
  * order, copied into other pages.  With n = lens[b]: all n if n <= budget, else
  * the last `recent` and, of the others, the budget - recent with the largest

@@ -66,6 +66,7 @@ def _load() -> ctypes.CDLL:
         "qk_norm_rope": ([p, ll, p, ll, p, p, p, p, d, d, p, ll, p, ll, i, i, i, i, i, i, p], i),
         "kv4_append_rope": ([p, ll, p, ll, p, ll, p, p, p, p, p, d, d, p, ll, p, f, f, i, i, i, i, i, i, i, i, p], i),
         "kv4_window_attention": ([p, ll, p, p, p, f, f, f, i, i, p, p, i, i, i, i, i, i, i, i, p], i),
+        "kv4_chunk_attention": ([p, ll, p, p, p, p, f, f, f, i, i, p, p, i, i, i, i, i, i, i, i, p], i),
         "token_logprobs": ([p, i, ll, p, f, i, p, p, p, p, p, i, i, p], i),
     }
     for name, (args, res) in sig.items():
@@ -81,7 +82,7 @@ lib = _load()
 EXPORTS = ("sk_init", "sk_shutdown", "sk_stream_workspace", "nvfp4_gemm", "nvfp4_gemm_f16out", "fp8_gemm",
            "fp8_gemm_f16out", "lm_head_argmax", "lm_head_verify", "lm_head_sample", "fp8_quantize",
            "nvfp4_quantize", "kv4_append", "kv4_attention", "kv4_evict", "rope_frequencies", "qk_norm_rope",
-           "kv4_append_rope", "kv4_window_attention", "token_logprobs",
+           "kv4_append_rope", "kv4_window_attention", "kv4_chunk_attention", "token_logprobs",
            "sk_status_string", "sk_last_device_error",
            "sk_set_pdl", "sk_set_variant", "sk_inject_wait_timeout", "nvfp4_gemm_noalloc", "sk_version")
 
@@ -524,6 +525,35 @@ def kv4_window_attention(q, cache, table, lens, k_scale: float, v_scale: float, 
                                     _need(out, torch.float16, (n, hq, dim), "out"),
                                     _need(lse, torch.float32, (n, hq), "lse"), seqs, rows, hq, heads, dim, pages, page,
                                     width, _raw_stream(stream, cache.get_device())), "kv4_window_attention")
+    return out, lse
+
+
+def kv4_chunk_attention(q, cache, table, lens, starts, k_scale: float, v_scale: float, scale: float, window: int = 0,
+                        sinks: int = 0, out=None, lse=None, stream=None):
+    """Attention of chunks of new tokens (q FP16 [rows][q_heads][head_dim], row stride free; sequence b's rows are
+    starts[b] .. starts[b + 1] - 1, int32 [seqs + 1], its last positions) over the cache's pages up to lens.
+
+    With window > 0 a row sees only the last `window` positions up to its own and the first `sinks` ones.
+    Returns (out FP16, lse float32 [rows][q_heads]); rows of no sequence are not written."""
+    torch = _torch()
+    pages, heads, dim, page = _cache_dims(cache)
+    if q.dim() != 3:
+        raise ValueError("q must be a CUDA float16 tensor [rows][q_heads][head_dim]")
+    hq = q.shape[1]
+    n, qs = _rows_f16(q, hq, dim, "q")
+    if table.dim() != 2:
+        raise ValueError("table must be a contiguous CUDA int32 tensor [seqs][width]")
+    seqs, width = table.shape
+    i32 = torch.int32
+    if out is None:
+        out = _new((n, hq, dim), torch.float16, q.device, stream)
+    if lse is None:
+        lse = _new((n, hq), torch.float32, q.device, stream)
+    _check(lib.kv4_chunk_attention(q.data_ptr(), qs, cache.data_ptr(), _need(table, i32, (seqs, width), "table"),
+                                   _need(lens, i32, (seqs,), "lens"), _need(starts, i32, (seqs + 1,), "starts"), k_scale,
+                                   v_scale, scale, window, sinks, _need(out, torch.float16, (n, hq, dim), "out"),
+                                   _need(lse, torch.float32, (n, hq), "lse"), n, seqs, hq, heads, dim, pages, page, width,
+                                   _raw_stream(stream, cache.get_device())), "kv4_chunk_attention")
     return out, lse
 
 

@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libskinny.so")
 SOURCES = ["api.cu", "k_nvfp4.cu", "k_fp8.cu", "noalloc.cu", "quant.cu", "sample.cu",
-           "kv4_append.cu", "kv4_attention.cu", "kv4_attention_tc.cu", "kv4_evict.cu", "logprobs.cu", "rope.cu"]
+           "kv4_append.cu", "kv4_attention.cu", "kv4_attention_tc.cu", "kv4_evict.cu", "logprobs.cu", "rope.cu",
+           "kv4_chunk.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 

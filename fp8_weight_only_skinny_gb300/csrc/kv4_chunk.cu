@@ -1,0 +1,848 @@
+// kv4_chunk.cu -- attention of chunks of new tokens, any number per sequence, over
+// the paged 4-bit cache (kv4.cuh), on the fifth-generation tensor cores.
+//
+// Query row i of sequence b (n rows, the last of len positions) and query head x,
+// over the positions j <= at = len - n + i with j > at - window or j < sinks:
+//     z_j = scale * q . k_j,   p_j = exp(z_j - max z),   out = sum p_j v_j / sum p_j
+//
+// The rows of a kv head's G query heads are one list (row i, head g: i G + g), cut
+// into tiles of 128, a row a TMEM lane. For 64 positions at a time
+//     S (128 x 64, TMEM)  = Q (128 x D, TMEM) . K^T      K: decoded into shared memory
+//     O (128 x D, TMEM)  += P (128 x 64, TMEM) . V       V: the same; P over S's own columns
+// so that a softmax thread owns a row: its maximum, base (kv4_attention.cuh) and
+// sum need no other thread, and shared memory carries only the decoded keys and
+// values. Roles: four warps of softmax per tile, warps that decode, one thread
+// that issues the products.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/skinny.h"
+#include "internal.h"
+#include "kv4_attention.cuh"
+#include "launch_util.cuh"
+#include "tcgen05.cuh"
+
+namespace {
+
+using namespace sk::attn;
+namespace t5 = sk::t5;
+
+constexpr int KB = 64;                 // positions per block
+constexpr int SETUP = 4;               // what a tile costs beside its blocks, in blocks
+constexpr int MIN_SHARE = 12;          // least cost a CTA takes, above that of one block: no part of a tile is empty
+
+// T tiles of 128 rows share what is decoded; NB buffers of S per tile; DW warps
+// decode; ST stages of keys and of values.
+template <int D>
+struct Cc {
+    static constexpr int T = D == 256 ? 1 : 2;
+    static constexpr int NB = D == 128 ? 1 : 2;
+    static constexpr int DW = D == 256 ? 8 : 4;
+    static constexpr int ST = D == 256 ? 3 : 4;
+    static constexpr int SW = 4 * T, WARPS_ALL = SW + DW + 1, CT_ALL = WARPS_ALL * 32;
+    static constexpr int ROWS = 128 * T;
+    static constexpr int TILE_B = KB * D * 2, SLAB = KB * 128;         // a stage; 64 components of it
+    static constexpr int ROUNDS = 2 * D / (32 * DW);                   // 16-byte pieces per thread
+    static constexpr int K = 0, V = ST * TILE_B, BARS = 2 * ST * TILE_B;
+    // barriers: keys full, empty, values full, empty (ST each); S full and P ready (T NB each); query rows ready, second
+    // product done (T each); end
+    static constexpr int NBARS = 4 * ST + 2 * T * NB + 2 * T + 1;
+    static constexpr int SCAN = BARS + 8 * NBARS, TMEM = SCAN + 16 * (WARPS_ALL + 1), START = TMEM + 16;
+    static constexpr int BYTES = 1024 + START + 64;
+    static constexpr size_t SMEM = BYTES > 120 * 1024 ? BYTES : 120 * 1024;      // one CTA per SM: all of the TMEM
+    static constexpr int O_COL = 0, Q_COL = T * D, S_COL = Q_COL + T * D / 2;
+    static_assert(S_COL + T * NB * KB <= 512, "TMEM");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static constexpr int MOST_SEQS = 2 * ST * TILE_B / 4 - 1;           // their list lies where the stages will
+};
+
+struct ChunkParams : AttnParams {
+    const int32_t *starts;
+    int rows;                          // in all
+    sk::Div by_g;
+    int4 *join;                        // per CTA: parts of the tile whose first part is its last, head, sequence, tile
+};
+
+// Rows of sequence b: [first, first + n), and its positions.
+struct Seq {
+    int first, n, len;
+    __device__ __forceinline__ Seq(const ChunkParams &p, int b) {
+        first = min(max(p.starts[b], 0), p.rows);
+        n = min(max(p.starts[b + 1], first), p.rows) - first;
+        len = min(max(p.lens[b], 0), p.cap);
+    }
+};
+template <int D>
+__device__ __forceinline__ int tiles_in(const ChunkParams &p, const Seq &s) {
+    return int(((long long)s.n * p.G + Cc<D>::ROWS - 1) / Cc<D>::ROWS);
+}
+
+// A tile of a sequence's rows: what it looks at (positions without the records
+// between sinks and windows, as in Seen) and what it costs.
+template <int D>
+struct Tile {
+    int idx0, count;                   // first of the list, rows
+    int lim0, lim1;                    // first unseen position (numbered without the gap) of its first and last row
+    int gap, skip, blocks, cost, per;
+    __device__ __forceinline__ Tile(const ChunkParams &p, const Seq &s, int t) {
+        using C = Cc<D>;
+        idx0 = t * C::ROWS;
+        count = min(C::ROWS, s.n * p.G - idx0);
+        const int at0 = s.len - s.n + 1;
+        lim0 = at0 + sk::quotient(idx0, p.by_g);
+        lim1 = at0 + sk::quotient(idx0 + count - 1, p.by_g);
+        gap = skip = 0;
+        if (p.window) {
+            gap = (min(p.sinks, max(lim1, 0)) + sk::KV4_REC - 1) / sk::KV4_REC;
+            skip = max(0, max(0, lim0 - p.window) / sk::KV4_REC - gap);
+        }
+        lim0 -= skip * sk::KV4_REC;
+        lim1 -= skip * sk::KV4_REC;
+        blocks = (max(lim1, 0) + KB - 1) / KB;
+        per = C::T == 2 && count > 128 ? 3 : 2;
+        cost = (blocks + SETUP) * per;
+    }
+    __device__ __forceinline__ int block_at(int x) const { return min(max(x / per - SETUP, 0), blocks); }
+};
+
+// The pieces of work of a CTA, in order: blocks [k0, k1) of tile t of sequence b
+// and kv head h. All (head, sequence, tile) cost a total that P CTAs take in equal
+// parts, whatever the lengths; a tile that two of them share is joined later.
+template <int D>
+struct Pieces {
+    long long left;                    // of this CTA's share
+    int h, b, t, x;                    // where it stands: x into the cost of the tile
+    __device__ __forceinline__ bool next(const ChunkParams &p, int &k0, int &k1, Seq &s) {
+        while (left > 0 && h < p.heads) {
+            if (b >= p.B) {
+                b = 0;
+                t = 0;
+                ++h;
+                continue;
+            }
+            s = Seq(p, b);
+            if (t >= tiles_in<D>(p, s)) {
+                ++b;
+                t = 0;
+                continue;
+            }
+            const Tile<D> tile(p, s, t);
+            const int x1 = int(min((long long)tile.cost, x + left));
+            k0 = tile.block_at(x);
+            k1 = tile.block_at(x1);
+            const bool last = x1 == tile.cost;
+            left -= x1 - x;
+            x = x1;
+            if (k1 > k0 || (last && tile.blocks == 0)) return true;
+            done(last);
+        }
+        return false;
+    }
+    // after a piece: to the next tile if this one is finished
+    __device__ __forceinline__ void done(bool last) {
+        if (last) {
+            x = 0;
+            ++t;
+        }
+    }
+    __device__ __forceinline__ void after(const ChunkParams &p, const Seq &s) {
+        const Tile<D> tile(p, s, t);
+        done(x == tile.cost);
+    }
+};
+
+struct Share2 {
+    long long total;                   // over all heads
+    int parts;
+};
+__device__ __forceinline__ long long bound_of(const Share2 &s, int c) { return s.total * c / s.parts; }
+__device__ __forceinline__ int owner_of(const Share2 &s, long long u) { return int(((u + 1) * s.parts - 1) / s.total); }
+
+// Where this CTA's share begins. Every thread of the CTA comes here; `list` holds
+// p.B + 1 numbers, `scan` one per warp and one more.
+template <int D>
+__device__ Share2 find_share(const ChunkParams &p, Pieces<D> &w, int *list, long long *scan, int *start) {
+    using C = Cc<D>;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    auto scanned = [&](long long mine, long long &total) {         // exclusive, over the CTA
+        long long v = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        __syncthreads();
+        if (lane == 31) scan[wid] = v;
+        __syncthreads();
+        long long before = 0;
+        total = 0;
+        for (int i = 0; i < C::WARPS_ALL; ++i) {
+            if (i < wid) before += scan[i];
+            total += scan[i];
+        }
+        return before + v - mine;
+    };
+    // tiles before each sequence
+    const int each_b = (p.B + C::CT_ALL - 1) / C::CT_ALL, b_lo = min(p.B, tid * each_b), b_hi = min(p.B, b_lo + each_b);
+    long long mine = 0, tiles;
+    for (int b = b_lo; b < b_hi; ++b) mine += tiles_in<D>(p, Seq(p, b));
+    int at = int(scanned(mine, tiles));
+    for (int b = b_lo; b < b_hi; ++b) {
+        list[b] = at;
+        at += tiles_in<D>(p, Seq(p, b));
+    }
+    if (tid == 0) {
+        list[p.B] = int(tiles);
+        start[0] = p.B;
+        start[1] = start[2] = 0;
+    }
+    __syncthreads();
+    // this thread's tiles: [lo, hi)
+    const int each = int((tiles + C::CT_ALL - 1) / C::CT_ALL), lo = int(min(tiles, (long long)tid * each)),
+              hi = int(min(tiles, (long long)lo + each));
+    int b0 = 0;
+    if (lo < hi) {                                                 // the last sequence that begins at or before lo
+        int l = 0, r = p.B - 1;
+        while (l < r) {
+            const int m = (l + r + 1) / 2;
+            if (list[m] <= lo) l = m;
+            else r = m - 1;
+        }
+        b0 = l;
+    }
+    auto walk = [&](auto &&visit) {
+        int b = b0;
+        for (int i = lo; i < hi && b < p.B; ++b) {
+            const Seq s(p, b);
+            const int n = tiles_in<D>(p, s);
+            for (int t = i - list[b]; t < n && i < hi; ++t, ++i)
+                if (!visit(b, t, Tile<D>(p, s, t).cost)) return;
+        }
+    };
+    mine = 0;
+    walk([&](int, int, int cost) {
+        mine += cost;
+        return true;
+    });
+    long long per_head;
+    const long long before = scanned(mine, per_head);
+    Share2 sh;
+    sh.total = per_head * p.heads;
+    sh.parts = int(max(1LL, min(sh.total / MIN_SHARE, (long long)p.ctas)));
+    w.left = 0;
+    w.h = w.b = w.t = w.x = 0;
+    if (int(blockIdx.x) < sh.parts && sh.total > 0) {
+        const long long u0 = bound_of(sh, blockIdx.x);
+        w.left = bound_of(sh, blockIdx.x + 1) - u0;
+        w.h = int(u0 / per_head);
+        long long off = u0 - w.h * per_head;
+        if (off >= before && off < before + mine) {
+            off -= before;
+            walk([&](int b, int t, int cost) {
+                if (off < cost) {
+                    start[0] = b;
+                    start[1] = t;
+                    start[2] = int(off);
+                    return false;
+                }
+                off -= cost;
+                return true;
+            });
+        }
+    }
+    __syncthreads();
+    w.b = start[0];
+    w.t = start[1];
+    w.x = start[2];
+    __syncthreads();                                               // the list's place is free
+    return sh;
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&d)[4]) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3]) : "memory");
+}
+__device__ __forceinline__ uint16_t ld_u16(const uint8_t *p) { return *reinterpret_cast<const uint16_t *>(p); }
+
+// Eight codes, scaled, to the 16 bytes at `addr` (exact in FP16).
+__device__ __forceinline__ void put8(uint32_t addr, uint32_t codes, uint32_t scale) {
+    uint32_t d[4];
+    sk::e2m1x8_to_f16x2x4(codes, d);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = sk::hmul2(d[e], scale);
+    st_shared_v4(addr, d);
+}
+
+// What a decoding thread has fetched of a block: 16 bytes of codes of the keys and
+// of the values, and the scales of their two blocks or positions, ROUNDS times.
+template <int D>
+struct Raw {
+    uint4 c[Cc<D>::ROUNDS];
+    uint16_t s[Cc<D>::ROUNDS];
+};
+// Keys: a warp takes eight positions x four 16-byte pieces (D = 64: sixteen x two)
+// at a time, lanes of eight the positions: their stores meet all banks. Decode warp
+// w, round r: position and piece.
+template <int D>
+__device__ __forceinline__ void key_place(int w, int r, int lane, int &row, int &piece) {
+    const int u = r * Cc<D>::DW + w;
+    if constexpr (D == 256) {
+        row = (u >> 1) * 8 + (lane & 7);
+        piece = (u & 1) * 4 + (lane >> 3);
+    } else if constexpr (D == 128) {
+        row = u * 8 + (lane & 7);
+        piece = lane >> 3;
+    } else {
+        row = u * 16 + (lane & 7) + 8 * (lane >> 4);
+        piece = (lane >> 3) & 1;
+    }
+}
+// Values: a 16-byte piece is a pair of positions of a block of 16 components:
+// half record (eight positions), block, pair.
+template <int D>
+__device__ __forceinline__ void value_place(int w, int r, int lane, int &half, int &blk, int &pair) {
+    const int u = r * Cc<D>::DW + w;
+    pair = lane & 3;
+    if constexpr (D == 256) {
+        half = u >> 1;
+        blk = (u & 1) * 8 + (lane >> 2);
+    } else if constexpr (D == 128) {
+        half = u;
+        blk = lane >> 2;
+    } else {
+        half = u * 2 + (lane >> 4);
+        blk = (lane >> 2) & 3;
+    }
+}
+// The record of a block that decode warp w reads in round r (both for keys and for values).
+template <int D>
+__device__ __forceinline__ int record_of(int w, int r) {
+    return (r * Cc<D>::DW + w) * (D == 256 ? 1 : D == 128 ? 2 : 4) / 4;
+}
+
+template <int D>
+__device__ __forceinline__ void fetch_keys(const uint8_t *const (&rec)[Cc<D>::ROUNDS], int w, int lane, Raw<D> &raw) {
+#pragma unroll
+    for (int r = 0; r < Cc<D>::ROUNDS; ++r) {
+        int row, piece;
+        key_place<D>(w, r, lane, row, piece);
+        const int i = row & 15;
+        raw.c[r] = *reinterpret_cast<const uint4 *>(rec[r] + i * (D / 2) + piece * 16);
+        raw.s[r] = ld_u16(rec[r] + 8 * D + i * (D / 16) + piece * 2);
+    }
+}
+template <int D>
+__device__ __forceinline__ void fetch_values(const uint8_t *const (&rec)[Cc<D>::ROUNDS], int w, int lane, Raw<D> &raw) {
+#pragma unroll
+    for (int r = 0; r < Cc<D>::ROUNDS; ++r) {
+        int half, blk, pair;
+        value_place<D>(w, r, lane, half, blk, pair);
+        raw.c[r] = *reinterpret_cast<const uint4 *>(rec[r] + 9 * D + (half & 1) * 4 * D + blk * 64 + pair * 16);
+        raw.s[r] = ld_u16(rec[r] + 17 * D + blk * 16 + (half & 1) * 8 + pair * 2);
+    }
+}
+// Both to the stage at `to`: 64 components (128 bytes) of a position a row, 64
+// rows a slab, 16-byte pieces swizzled within eight rows.
+template <int D>
+__device__ __forceinline__ void decode_keys(uint32_t to, int w, int lane, const Raw<D> &raw) {
+#pragma unroll
+    for (int r = 0; r < Cc<D>::ROUNDS; ++r) {
+        int row, piece;
+        key_place<D>(w, r, lane, row, piece);
+        const uint32_t s = scale_pair(raw.s[r]), lo = sk::bcast_lo(s), hi = sk::bcast_hi(s);
+        const uint32_t at = to + (piece >> 1) * Cc<D>::SLAB + row * 128;
+        const uint32_t x = uint32_t(row & 7), c = (piece & 1) * 4;
+        put8(at + ((c ^ x) << 4), raw.c[r].x, lo);
+        put8(at + (((c + 1) ^ x) << 4), raw.c[r].y, lo);
+        put8(at + (((c + 2) ^ x) << 4), raw.c[r].z, hi);
+        put8(at + (((c + 3) ^ x) << 4), raw.c[r].w, hi);
+    }
+}
+template <int D>
+__device__ __forceinline__ void decode_values(uint32_t to, int w, int lane, const Raw<D> &raw) {
+#pragma unroll
+    for (int r = 0; r < Cc<D>::ROUNDS; ++r) {
+        int half, blk, pair;
+        value_place<D>(w, r, lane, half, blk, pair);
+        const uint32_t s = scale_pair(raw.s[r]);
+        // lanes of an odd block store their second position first: eight lanes meet all banks
+        const bool odd = blk & 1;
+        const uint32_t f0 = odd ? raw.c[r].z : raw.c[r].x, f1 = odd ? raw.c[r].w : raw.c[r].y,
+                       l0 = odd ? raw.c[r].x : raw.c[r].z, l1 = odd ? raw.c[r].y : raw.c[r].w;
+        const uint32_t lo = sk::bcast_lo(s), hi = sk::bcast_hi(s), fs = odd ? hi : lo, ls = odd ? lo : hi;
+        const uint32_t at = to + (blk >> 2) * Cc<D>::SLAB + half * 1024, c = (blk & 3) * 2;
+        const uint32_t rf = uint32_t(2 * pair + odd), rl = rf ^ 1u;
+        put8(at + rf * 128 + ((c ^ rf) << 4), f0, fs);
+        put8(at + rf * 128 + (((c + 1) ^ rf) << 4), f1, fs);
+        put8(at + rl * 128 + ((c ^ rl) << 4), l0, ls);
+        put8(at + rl * 128 + (((c + 1) ^ rl) << 4), l1, ls);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __grid_constant__ ChunkParams p) {
+    using C = Cc<D>;
+    constexpr int T = C::T, NB = C::NB, ST = C::ST;
+    extern __shared__ unsigned char dyn[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t base = (sk::smem_u32(dyn) + 1023u) & ~1023u;
+    unsigned char *const smem = dyn + (base - sk::smem_u32(dyn));
+    const uint32_t bars = base + C::BARS;
+    const uint32_t k_full = bars, k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST,
+                   s_full = v_empty + 8 * ST, p_ready = s_full + 8 * T * NB, q_ready = p_ready + 8 * T * NB,
+                   o_done = q_ready + 8 * T, end = o_done + 8 * T;
+
+    if (warp == 0) t5::alloc(base + C::TMEM, 512);
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            sk::mbar_init(k_full + 8 * i, C::DW);
+            sk::mbar_init(v_full + 8 * i, C::DW);
+            sk::mbar_init(k_empty + 8 * i, 1);
+            sk::mbar_init(v_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < T * NB; ++i) {
+            sk::mbar_init(s_full + 8 * i, 1);
+            sk::mbar_init(p_ready + 8 * i, 4);
+        }
+        for (int i = 0; i < T; ++i) {
+            sk::mbar_init(q_ready + 8 * i, 4);
+            sk::mbar_init(o_done + 8 * i, 1);
+        }
+        sk::mbar_init(end, 1);
+        sk::fence_barrier_init();
+    }
+    t5::fence_before();
+    __syncthreads();
+    t5::fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::TMEM);
+    sk::pdl_launch_dependents();
+    sk::pdl_wait_primary();
+    Pieces<D> work;
+    const Share2 share = find_share<D>(p, work, reinterpret_cast<int *>(smem), reinterpret_cast<long long *>(smem + C::SCAN),
+                                       reinterpret_cast<int *>(smem + C::START));
+    bool dead = false;
+    // Waits for a barrier's phase number `n` (from 0), a second at most; after one
+    // that ran out the thread waits no more.
+    auto wait = [&](uint32_t bar, uint32_t n) {
+        if (dead || sk::wait_limited(bar, n & 1)) return;
+        dead = true;
+        atomicOr(p.err, 1u);
+    };
+    int k0, k1;
+    Seq seq(p, 0);
+
+    if (warp < C::SW) {
+        // ------------------------------------------------------- softmax
+        const int t = warp >> 2, row = tid & 127;
+        const uint32_t mine = tmem + (uint32_t((warp & 3) * 32) << 16);
+        const uint32_t o_at = mine + C::O_COL + t * D, q_at = mine + C::Q_COL + t * (D / 2),
+                       s_at = mine + C::S_COL + t * NB * KB;
+        uint32_t blocks_done = 0, products = 0;              // S buffers read; second products of this tile so far
+        int last_join = 0;                                   // whether a tile's first part, not its last, was this CTA's
+        while (work.next(p, k0, k1, seq)) {
+            const Tile<D> tile(p, seq, work.t);
+            const bool active = t * 128 < tile.count;
+            const int idx = tile.idx0 + t * 128 + row, i = sk::quotient(idx, p.by_g), g = idx - i * p.G;
+            const bool there = t * 128 + row < tile.count;
+            const long long at = (long long)(seq.first + i) * (p.heads * p.G) + work.h * p.G + g;
+            const bool whole = k0 == 0 && k1 == tile.blocks;
+            const int n = k1 - k0;
+            float neg = NO_BASE;
+            float2 sum = make_float2(0.f, 0.f);
+            if (active && n > 0) {
+                const __half *src = p.q + (seq.first + i) * p.q_stride + (long long)(work.h * p.G + g) * D;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                        if (there) x = *reinterpret_cast<const uint4 *>(src + c * 64 + e * 8);
+                        v[4 * e] = x.x;
+                        v[4 * e + 1] = x.y;
+                        v[4 * e + 2] = x.z;
+                        v[4 * e + 3] = x.w;
+                    }
+                    t5::st32(q_at + c * 32, v);
+                }
+                t5::wait_st();
+                t5::fence_before();
+                __syncwarp();
+                if (lane == 0) sk::mbar_arrive(q_ready + 8 * t);
+                const int lim = there ? tile.lim0 + i - sk::quotient(tile.idx0, p.by_g) : 0;
+                const int low = p.window ? lim - p.window : 0;
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t sb = blocks_done % NB, use = blocks_done / NB;
+                    const uint32_t s_col = s_at + sb * KB;
+                    wait(s_full + 8 * (t * NB + sb), use);
+                    __syncwarp();
+                    ++blocks_done;
+                    t5::fence_after();
+                    float s[KB];
+                    t5::ld32(s_col, s);
+                    t5::ld32(s_col + 32, s + 32);
+                    t5::wait_ld();
+                    t5::held<KB>(s);
+                    const int pos = (k0 + j) * KB;
+                    if (pos + KB > tile.lim0 || (p.window && pos + KB > p.sinks && pos < tile.lim1 - p.window)) {
+#pragma unroll
+                        for (int e = 0; e < KB; ++e)
+                            if (pos + e >= lim || (pos + e >= p.sinks && pos + e < low)) s[e] = NEG_INF;
+                    }
+                    float m0 = s[0], m1 = s[1];
+#pragma unroll
+                    for (int e = 2; e < KB; e += 4) {
+                        m0 = fmaxf(m0, fmaxf(s[e], s[e + 1]));
+                        if (e + 2 < KB) m1 = fmaxf(m1, fmaxf(s[e + 2], s[e + 3]));
+                    }
+                    m0 = fmaxf(m0, m1);
+                    if (__any_sync(0xffffffffu, passes(p, m0, neg))) {
+                        const float had = neg;
+                        neg = fminf(had, neg_base(p, m0));
+                        const float f = rebase(p, neg, had);
+                        sum.x *= f;
+                        sum.y *= f;
+                        if (j > 0) {
+                            // the output so far, once the product before this one is done
+                            wait(o_done + 8 * t, products - 1);
+                            __syncwarp();
+                            t5::fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                float o[32];
+                                t5::ld32(o_at + c, o);
+                                t5::wait_ld();
+                                t5::held<32>(o);
+                                uint32_t v[32];
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(o[e] * f);
+                                t5::st32(o_at + c, v);
+                            }
+                        }
+                    }
+                    uint32_t w[KB / 2];
+#pragma unroll
+                    for (int e = 0; e < KB; e += 2) {
+                        const float2 y = weights2(p, s[e], s[e + 1], neg, neg);
+                        sum.x += y.x;
+                        sum.y += y.y;
+                        w[e / 2] = pack_f16(y.x, y.y);
+                    }
+                    t5::st32(s_col, w);
+                    t5::wait_st();
+                    t5::fence_before();
+                    __syncwarp();
+                    if (lane == 0) sk::mbar_arrive(p_ready + 8 * (t * NB + sb));
+                    ++products;
+                }
+                // (with two buffers the last two products may be under way: a barrier tells one phase from the next only)
+                if (NB == 2 && n > 1) wait(o_done + 8 * t, products - 2);
+                wait(o_done + 8 * t, products - 1);
+                __syncwarp();
+                t5::fence_after();
+            }
+            // ---- the rows' outputs, or their part of them
+            const float l = sum.x + sum.y;
+            const size_t slot = size_t(blockIdx.x) * 2 + (k0 == 0 ? 1 : 0);
+            if (active) {
+                const float f = l == 0.f ? 0.f : p.vg / l;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    if (n > 0) {
+                        t5::ld32(o_at + c, o);
+                        t5::wait_ld();
+                        t5::held<32>(o);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                    }
+                    if (!there) {
+                    } else if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4 *>(p.out + at * D + c + e) =
+                                make_uint4(pack_f16(o[e] * f, o[e + 1] * f), pack_f16(o[e + 2] * f, o[e + 3] * f),
+                                           pack_f16(o[e + 4] * f, o[e + 5] * f), pack_f16(o[e + 6] * f, o[e + 7] * f));
+                    } else {
+                        float *to = p.part_o + (slot * C::ROWS + t * 128 + row) * D + c;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(to + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (there) {
+                    if (whole) write_stats(p, at, -neg, l);
+                    else
+                        *reinterpret_cast<float2 *>(p.part_ml + (slot * C::ROWS + t * 128 + row) * 2) = make_float2(-neg, l);
+                }
+            }
+            if (tid == 0 && k0 == 0 && !whole) {
+                // this CTA's last piece: the units of the tile's end tell the last part's owner
+                const long long here = bound_of(share, blockIdx.x + 1);
+                const int c1 = owner_of(share, here + (tile.cost - work.x) - 1);
+                p.join[blockIdx.x] = make_int4(c1 - int(blockIdx.x) + 1, work.h, work.b, work.t);
+                last_join = 1;
+            }
+            t5::fence_before();
+            work.after(p, seq);
+        }
+        if (tid == 0 && !last_join) p.join[blockIdx.x] = make_int4(0, 0, 0, 0);
+    } else if (warp < C::SW + C::DW) {
+        // ------------------------------------------------------- decoding
+        const int w = warp - C::SW;
+        uint32_t made = 0;                                   // blocks
+        while (work.next(p, k0, k1, seq)) {
+            const Tile<D> tile(p, seq, work.t);
+            const int32_t *table = p.table + (long long)work.b * p.width;
+            const int n = k1 - k0, last = max(0, (tile.lim1 + sk::KV4_REC - 1) / sk::KV4_REC - 1);
+            const uint8_t *rec[C::ROUNDS], *soon[C::ROUNDS];
+            auto lookup = [&](int j, const uint8_t *(&r)[C::ROUNDS]) {
+#pragma unroll
+                for (int x = 0; x < C::ROUNDS; ++x) {
+                    const int v = min((k0 + j) * (KB / sk::KV4_REC) + record_of<D>(w, x), last);
+                    r[x] = p.cache + size_t(sk::kv4_record(table, v >= tile.gap ? v + tile.skip : v, p.recs, p.by_recs, p.pages,
+                                                           p.heads, work.h)) * sk::kv4_rec_bytes(D);
+                }
+            };
+            Raw<D> keys, vals;
+            if (n > 0) {
+                lookup(0, rec);
+                fetch_keys<D>(rec, w, lane, keys);
+                fetch_values<D>(rec, w, lane, vals);
+                if (n > 1) lookup(1, soon);
+            }
+            for (int j = 0; j < n; ++j, ++made) {
+                const uint32_t st = made % ST, use = made / ST;
+                if (use > 0) wait(k_empty + 8 * st, use - 1);
+                decode_keys<D>(base + C::K + st * C::TILE_B, w, lane, keys);
+                t5::fence_async_smem();
+                __syncwarp();
+                if (lane == 0 && !p.stall) sk::mbar_arrive(k_full + 8 * st);
+                if (j + 1 < n) fetch_keys<D>(soon, w, lane, keys);
+                if (use > 0) wait(v_empty + 8 * st, use - 1);
+                decode_values<D>(base + C::V + st * C::TILE_B, w, lane, vals);
+                t5::fence_async_smem();
+                __syncwarp();
+                if (lane == 0 && !p.stall) sk::mbar_arrive(v_full + 8 * st);
+                if (j + 1 < n) fetch_values<D>(soon, w, lane, vals);
+                if (j + 2 < n) lookup(j + 2, soon);
+            }
+            work.after(p, seq);
+        }
+    } else if (lane == 0) {
+        // ------------------------------------------------------- products
+        uint32_t kc = 0, vc = 0, pieces = 0, pieces1 = 0;    // blocks of keys and values used; pieces of each tile
+        uint32_t scored = 0, weighted = 0;                   // uses of the first tile's buffers of S (the second's: below)
+        uint32_t scored1 = 0, weighted1 = 0;
+        while (work.next(p, k0, k1, seq)) {
+            const Tile<D> tile(p, seq, work.t);
+            const int n = k1 - k0, act = T == 2 && tile.count > 128 ? 2 : 1;
+            if (n > 0) {
+                for (int t = 0; t < act; ++t) wait(q_ready + 8 * t, t ? pieces1 : pieces);
+                ++pieces;
+                if (act == 2) ++pieces1;
+                // S of tile t from the stage's keys
+                auto scores = [&](int t) {
+                    uint32_t &count = t ? scored1 : scored;
+                    const uint32_t sb = count % NB, st = kc % ST;
+                    ++count;
+                    const uint64_t op = t5::operand(base + C::K + st * C::TILE_B, 16, 1024);
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s)
+                        t5::mma(tmem + C::S_COL + (t * NB + sb) * KB, tmem + C::Q_COL + t * (D / 2) + 8 * s,
+                                op + ((s >> 2) * C::SLAB + (s & 3) * 32) / 16, t5::shape(KB, false), s > 0);
+                    t5::commit(s_full + 8 * (t * NB + sb));
+                };
+                auto keys_ready = [&] {
+                    wait(k_full + 8 * (kc % ST), kc / ST);
+                    t5::fence_after();
+                };
+                auto keys_used = [&] {
+                    t5::commit(k_empty + 8 * (kc % ST));
+                    ++kc;
+                };
+                auto values = [&](int t, bool first) {
+                    uint32_t &count = t ? weighted1 : weighted;
+                    const uint32_t sb = count % NB, st = vc % ST;
+                    wait(p_ready + 8 * (t * NB + sb), count / NB);
+                    ++count;
+                    t5::fence_after();
+                    const uint64_t op = t5::operand(base + C::V + st * C::TILE_B, C::SLAB, 1024);
+#pragma unroll
+                    for (int s = 0; s < KB / 16; ++s)
+                        t5::mma(tmem + C::O_COL + t * D, tmem + C::S_COL + (t * NB + sb) * KB + 8 * s, op + s * 2048 / 16,
+                                t5::shape(D, true), !first || s > 0);
+                    t5::commit(o_done + 8 * t);
+                };
+                keys_ready();
+                for (int t = 0; t < act; ++t) scores(t);
+                keys_used();
+                for (int j = 0; j < n; ++j) {
+                    const bool more = j + 1 < n;
+                    if (NB == 2 && more) {
+                        keys_ready();
+                        for (int t = 0; t < act; ++t) scores(t);
+                        keys_used();
+                    }
+                    wait(v_full + 8 * (vc % ST), vc / ST);
+                    if (NB == 1 && more) keys_ready();
+                    for (int t = 0; t < act; ++t) {
+                        values(t, j == 0);
+                        if (NB == 1 && more) scores(t);
+                    }
+                    if (NB == 1 && more) keys_used();
+                    t5::commit(v_empty + 8 * (vc % ST));
+                    ++vc;
+                }
+            }
+            work.after(p, seq);
+        }
+        // every product is done before the TMEM is given back
+        t5::commit(end);
+        sk::wait_limited(end, 0);
+    }
+    t5::fence_before();
+    __syncthreads();
+    t5::fence_after();
+    if (warp == 0) t5::free(tmem, 512);
+}
+
+// The tiles that several CTAs had parts of: CTA (c, y) joins eight rows of the
+// tile whose first part is CTA c's, a warp a row, in the order of the parts.
+constexpr int JT = 256;
+template <int D>
+__global__ void __launch_bounds__(JT) kv4_chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+    using C = Cc<D>;
+    constexpr int PER = D / 32;
+    sk::pdl_wait_primary();
+    const int4 seg = p.join[blockIdx.x];
+    if (seg.x == 0) return;
+    const Seq s(p, seg.z);
+    const Tile<D> tile(p, s, seg.w);
+    const int lane = threadIdx.x & 31, r = blockIdx.y * (JT / 32) + (threadIdx.x >> 5);
+    if (r >= tile.count) return;
+    const int idx = tile.idx0 + r, i = sk::quotient(idx, p.by_g);
+    const long long at = (long long)(s.first + i) * (p.heads * p.G) + seg.y * p.G + idx - i * p.G;
+    const int n = seg.x;
+    auto slot = [&](int k) { return (size_t(blockIdx.x) + k) * 2 + (k == 0 ? 1 : 0); };
+    float top = NEG_INF, l = 0.f, v[PER];
+#pragma unroll
+    for (int x = 0; x < PER; ++x) v[x] = 0.f;
+    for (int k0 = 0; k0 < n; k0 += 32) {           // 32 parts at a time, under the largest base so far
+        float2 ml = make_float2(NEG_INF, 0.f);
+        if (k0 + lane < n) ml = *reinterpret_cast<const float2 *>(p.part_ml + (slot(k0 + lane) * C::ROWS + r) * 2);
+        float now = ml.x;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
+        now = fmaxf(now, top);
+        const float old = rebase(p, top, now), f = rebase(p, ml.x, now);
+        top = now;
+        float add = ml.y * f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
+        l = l * old + add;
+#pragma unroll
+        for (int x = 0; x < PER; ++x) v[x] *= old;
+        const int kn = min(32, n - k0);
+#pragma unroll 4
+        for (int k = 0; k < kn; ++k) {
+            const float w = __shfl_sync(0xffffffffu, f, k);
+            const float2 *src = reinterpret_cast<const float2 *>(p.part_o + (slot(k0 + k) * C::ROWS + r) * D) + lane;
+#pragma unroll
+            for (int x = 0; x < PER / 2; ++x) {
+                const float2 y = src[32 * x];
+                v[2 * x] += y.x * w;
+                v[2 * x + 1] += y.y * w;
+            }
+        }
+    }
+    const float f = l == 0.f ? 0.f : p.vg / l;
+    __half2 *const out = reinterpret_cast<__half2 *>(p.out + at * D) + lane;
+#pragma unroll
+    for (int x = 0; x < PER / 2; ++x) out[32 * x] = __floats2half2_rn(v[2 * x] * f, v[2 * x + 1] * f);
+    if (lane == 0) write_stats(p, at, top, l);
+}
+
+template <int D>
+sk_status run(ChunkParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
+    using C = Cc<D>;
+    if (p.B > C::MOST_SEQS) return SK_ERR_UNSUPPORTED_SHAPE;
+    p.ctas = sms;
+    p.join = reinterpret_cast<int4 *>(scratch);
+    p.part_ml = reinterpret_cast<float *>(scratch + (size_t(sms) * sizeof(int4) + 255) / 256 * 256);
+    p.part_o = p.part_ml + size_t(sms) * 2 * C::ROWS * 2;
+    if (size_t(reinterpret_cast<unsigned char *>(p.part_o + size_t(sms) * 2 * C::ROWS * D) - scratch) > sk::SCRATCH_BYTES)
+        return SK_ERR_WORKSPACE;
+    if (sk::prepare_kernel<kv4_chunk_kernel<D>>(C::SMEM) != cudaSuccess) return SK_ERR_CUDA;
+    if (sk::launch_pdl(kv4_chunk_kernel<D>, dim3(sms), dim3(C::CT_ALL), C::SMEM, s, p) != cudaSuccess) return SK_ERR_CUDA;
+    return sk::launch_pdl(kv4_chunk_join_kernel<D>, dim3(sms, C::ROWS / (JT / 32)), dim3(JT), 0, s, p) == cudaSuccess
+               ? SK_OK
+               : SK_ERR_CUDA;
+}
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+}  // namespace
+
+extern "C" sk_status kv4_chunk_attention(const void *q, long long q_stride, const uint8_t *cache, const int32_t *table,
+                                         const int32_t *lens, const int32_t *starts, float k_scale, float v_scale,
+                                         float scale, int window, int sinks, void *out, float *lse, int rows, int seqs,
+                                         int q_heads, int kv_heads, int head_dim, int pages, int page_size,
+                                         int table_width, void *stream) {
+    if (seqs < 0 || rows < 0 || q_heads < 1 || kv_heads < 1 || pages < 1 || page_size < 1 || table_width < 1 || window < 0 ||
+        sinks < 0)
+        return SK_ERR_INVALID_ARG;
+    if (q_heads % kv_heads) return SK_ERR_INVALID_ARG;
+    if (!sk::kv4_scale_ok(k_scale) || !sk::kv4_scale_ok(v_scale) || !(scale > 0.f && scale < 1e20f)) return SK_ERR_INVALID_ARG;
+    const double product = double(scale) * double(k_scale);        // bounds as in kv4_attention
+    if (!(product >= 5e-37 && product <= 1e27)) return SK_ERR_INVALID_ARG;
+    if (!sk::kv4_shape_ok(pages, kv_heads, head_dim, page_size)) return SK_ERR_UNSUPPORTED_SHAPE;
+    // positions and rows of a kv head's list with room for a tile and a block, query rows by 31 bits
+    if ((long long)table_width * page_size > 0x7FFFF000LL || (long long)rows * (q_heads / kv_heads) > 0x3FFFF000LL ||
+        (long long)rows * q_heads > 0x7FFFFFFFLL)
+        return SK_ERR_UNSUPPORTED_SHAPE;
+    if (seqs == 0 || rows == 0) return SK_OK;
+    if (!q || !cache || !table || !lens || !starts || !out) return SK_ERR_INVALID_ARG;
+    if (q_stride < (long long)q_heads * head_dim) return SK_ERR_INVALID_ARG;
+    if (q_stride % 8 || !aligned(q, 16) || !aligned(cache, 16) || !aligned(table, 4) || !aligned(lens, 4) ||
+        !aligned(starts, 4) || !aligned(out, 16) || !aligned(lse, 4))
+        return SK_ERR_MISALIGNED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    sk::Scratch sc;
+    if (!sk::scratch_for(s, &sc)) return SK_ERR_NOT_INITIALIZED;
+    ChunkParams p = {};
+    p.q = static_cast<const __half *>(q);
+    p.q_stride = q_stride;
+    p.cache = cache;
+    p.table = table;
+    p.lens = lens;
+    p.starts = starts;
+    p.out = static_cast<__half *>(out);
+    p.lse = lse;
+    p.err = sc.err;
+    p.rows = rows;
+    p.B = seqs;
+    p.heads = kv_heads;
+    p.G = q_heads / kv_heads;
+    p.by_g = sk::Div(uint32_t(p.G));
+    p.pages = pages;
+    p.recs = page_size / sk::KV4_REC;
+    p.by_recs = sk::Div(p.recs);
+    p.width = table_width;
+    p.cap = table_width * page_size;
+    p.window = window < p.cap ? window : p.cap;
+    p.sinks = sinks < p.cap ? sinks : p.cap;
+    p.c = float(product * double(LOG2E));
+    p.shift = P_SHIFT / p.c;
+    p.reach = (P_SHIFT + SLACK) / p.c;
+    p.vg = v_scale;
+    p.stall = sk::take_inject_stall();
+    switch (head_dim) {
+        case 64: return run<64>(p, sc.base, sc.num_sms, s);
+        case 128: return run<128>(p, sc.base, sc.num_sms, s);
+        default: return run<256>(p, sc.base, sc.num_sms, s);
+    }
+}

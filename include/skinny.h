@@ -433,6 +433,31 @@ SK_API sk_status kv4_window_attention(const void *q, long long q_stride, const u
                                       int head_dim, int pages, int page_size, int table_width, void *stream);
 
 /*
+ * kv4_chunk_attention: attention of a chunk of new tokens of each sequence, any
+ * number of them, over the cache (the new tokens' own keys and values already
+ * appended): prompts, whole or in pieces, and steps that mix them with single tokens.
+ *   q        const f16 [rows][q_heads][D], as kv4_attention; the rows of sequence b
+ *            are starts[b] .. starts[b + 1] - 1, its last n = starts[b + 1] - starts[b]
+ *            positions: row i is at position lens[b] - n + i and sees the positions up
+ *            to its own; with window > 0 only the last `window` of them and the first
+ *            `sinks` (sinks is not read with window = 0)
+ *   starts   const i32 [seqs + 1], device memory, ascending, at most `rows`; q, out and
+ *            lse rows outside [starts[0], starts[seqs]) are not read or written
+ *   out, lse as kv4_attention ([rows] rows), lse may be NULL
+ *   Other arguments, weights, sums, empty rows and the workspace as kv4_attention
+ *   (the order of the sums depends on all sequences of the call; repeated calls are
+ *   bitwise identical).  rows * q_heads / kv_heads < 2^30, rows * q_heads < 2^31 and
+ *   seqs < 16384 (larger: SK_ERR_UNSUPPORTED_SHAPE).  A starts that descends or
+ *   passes `rows` is memory-safe, results unspecified.  rows = 0 or seqs = 0: nothing
+ *   is launched.
+ */
+SK_API sk_status kv4_chunk_attention(const void *q, long long q_stride, const uint8_t *cache, const int32_t *table,
+                                     const int32_t *lens, const int32_t *starts, float k_scale, float v_scale,
+                                     float scale, int window, int sinks, void *out, float *lse, int rows, int seqs,
+                                     int q_heads, int kv_heads, int head_dim, int pages, int page_size,
+                                     int table_width, void *stream);
+
+/*
  * kv4_evict: keep at most `budget` positions per sequence and kv head, in their
  * order, copied into other pages.  With n = lens[b]: all n if n <= budget, else
  * the last `recent` and, of the others, the budget - recent with the largest

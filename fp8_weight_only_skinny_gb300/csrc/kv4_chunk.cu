@@ -632,77 +632,89 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             }
             work.after(p, seq);
         }
-    } else if (lane == 0) {
+    } else {
         // ------------------------------------------------------- products
-        uint32_t kc = 0, vc = 0, pieces = 0, pieces1 = 0;    // blocks of keys and values used; pieces of each tile
-        uint32_t scored = 0, weighted = 0;                   // uses of the first tile's buffers of S (the second's: below)
-        uint32_t scored1 = 0, weighted1 = 0;
+        // The warp waits together and one elected lane, always the same, issues: what it issues takes its operands
+        // from uniform registers (from a lane chosen by number a product takes 45 clocks to issue, of the 32 it runs).
+        uint32_t kc = 0, vc = 0, pieces[2] = {0, 0};         // blocks of keys and values used; pieces of each tile
+        uint32_t scored[2] = {0, 0}, weighted[2] = {0, 0};   // uses of the tiles' buffers of S
         while (work.next(p, k0, k1, seq)) {
             const Tile<D> tile(p, seq, work.t);
-            const int n = k1 - k0, act = T == 2 && tile.count > 128 ? 2 : 1;
+            const int n = k1 - k0;
+            const bool two = T == 2 && tile.count > 128;
             if (n > 0) {
-                for (int t = 0; t < act; ++t) wait(q_ready + 8 * t, t ? pieces1 : pieces);
-                ++pieces;
-                if (act == 2) ++pieces1;
                 // S of tile t from the stage's keys
                 auto scores = [&](int t) {
-                    uint32_t &count = t ? scored1 : scored;
-                    const uint32_t sb = count % NB, st = kc % ST;
-                    ++count;
-                    const uint64_t op = t5::operand(base + C::K + st * C::TILE_B, 16, 1024);
+                    const uint32_t sb = scored[t] % NB;
+                    ++scored[t];
+                    const uint64_t op = t5::operand(base + C::K + (kc % ST) * C::TILE_B, 16, 1024);
+                    if (t5::elect()) {
 #pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        t5::mma(tmem + C::S_COL + (t * NB + sb) * KB, tmem + C::Q_COL + t * (D / 2) + 8 * s,
-                                op + ((s >> 2) * C::SLAB + (s & 3) * 32) / 16, t5::shape(KB, false), s > 0);
-                    t5::commit(s_full + 8 * (t * NB + sb));
+                        for (int s = 0; s < D / 16; ++s)
+                            t5::mma(tmem + C::S_COL + (t * NB + sb) * KB, tmem + C::Q_COL + t * (D / 2) + 8 * s,
+                                    op + ((s >> 2) * C::SLAB + (s & 3) * 32) / 16, t5::shape(KB, false), s > 0);
+                        t5::commit(s_full + 8 * (t * NB + sb));
+                    }
                 };
                 auto keys_ready = [&] {
                     wait(k_full + 8 * (kc % ST), kc / ST);
                     t5::fence_after();
                 };
                 auto keys_used = [&] {
-                    t5::commit(k_empty + 8 * (kc % ST));
+                    if (t5::elect()) t5::commit(k_empty + 8 * (kc % ST));
                     ++kc;
                 };
                 auto values = [&](int t, bool first) {
-                    uint32_t &count = t ? weighted1 : weighted;
-                    const uint32_t sb = count % NB, st = vc % ST;
-                    wait(p_ready + 8 * (t * NB + sb), count / NB);
-                    ++count;
+                    const uint32_t sb = weighted[t] % NB;
+                    wait(p_ready + 8 * (t * NB + sb), weighted[t] / NB);
+                    ++weighted[t];
+                    __syncwarp();
                     t5::fence_after();
-                    const uint64_t op = t5::operand(base + C::V + st * C::TILE_B, C::SLAB, 1024);
+                    const uint64_t op = t5::operand(base + C::V + (vc % ST) * C::TILE_B, C::SLAB, 1024);
+                    if (t5::elect()) {
 #pragma unroll
-                    for (int s = 0; s < KB / 16; ++s)
-                        t5::mma(tmem + C::O_COL + t * D, tmem + C::S_COL + (t * NB + sb) * KB + 8 * s, op + s * 2048 / 16,
-                                t5::shape(D, true), !first || s > 0);
-                    t5::commit(o_done + 8 * t);
+                        for (int s = 0; s < KB / 16; ++s)
+                            t5::mma(tmem + C::O_COL + t * D, tmem + C::S_COL + (t * NB + sb) * KB + 8 * s, op + s * 2048 / 16,
+                                    t5::shape(D, true), !first || s > 0);
+                        t5::commit(o_done + 8 * t);
+                    }
                 };
+                wait(q_ready, pieces[0]++);
+                if (two) wait(q_ready + 8, pieces[1]++);
                 keys_ready();
-                for (int t = 0; t < act; ++t) scores(t);
+                __syncwarp();
+                scores(0);
+                if (two) scores(1);
                 keys_used();
                 for (int j = 0; j < n; ++j) {
                     const bool more = j + 1 < n;
                     if (NB == 2 && more) {
                         keys_ready();
-                        for (int t = 0; t < act; ++t) scores(t);
+                        __syncwarp();
+                        scores(0);
+                        if (two) scores(1);
                         keys_used();
                     }
                     wait(v_full + 8 * (vc % ST), vc / ST);
                     if (NB == 1 && more) keys_ready();
-                    for (int t = 0; t < act; ++t) {
-                        values(t, j == 0);
-                        if (NB == 1 && more) scores(t);
+                    values(0, j == 0);
+                    if (NB == 1 && more) scores(0);
+                    if (two) {
+                        values(1, j == 0);
+                        if (NB == 1 && more) scores(1);
                     }
                     if (NB == 1 && more) keys_used();
-                    t5::commit(v_empty + 8 * (vc % ST));
+                    if (t5::elect()) t5::commit(v_empty + 8 * (vc % ST));
                     ++vc;
                 }
             }
             work.after(p, seq);
         }
         // every product is done before the TMEM is given back
-        t5::commit(end);
+        __syncwarp();
+        if (t5::elect()) t5::commit(end);
         sk::wait_limited(end, 0);
+        __syncwarp();
     }
     t5::fence_before();
     __syncthreads();

@@ -46,9 +46,9 @@ struct Cc {
     static constexpr int TILE_B = KB * D * 2, SLAB = KB * 128;         // a stage; 64 components of it
     static constexpr int ROUNDS = 2 * D / (32 * DW);                   // 16-byte pieces per thread
     static constexpr int K = 0, V = ST * TILE_B, BARS = 2 * ST * TILE_B;
-    // barriers: keys full, empty, values full, empty (ST each); S full and P ready (T NB each); query rows ready, second
-    // product done (T each); end
-    static constexpr int NBARS = 4 * ST + 2 * T * NB + 2 * T + 1;
+    // barriers: keys full, empty, values full, empty (ST each); S full and P ready (T NB each); query rows ready, a second
+    // product done, a piece's last one done (T each); end
+    static constexpr int NBARS = 4 * ST + 2 * T * NB + 3 * T + 1;
     static constexpr int SCAN = BARS + 8 * NBARS, TMEM = SCAN + 16 * (WARPS_ALL + 1), START = TMEM + 16;
     static constexpr int BYTES = 1024 + START + 64;
     static constexpr size_t SMEM = BYTES > 120 * 1024 ? BYTES : 120 * 1024;      // one CTA per SM: all of the TMEM
@@ -68,6 +68,7 @@ struct ChunkParams : AttnParams {
 // Rows of sequence b: [first, first + n), and its positions.
 struct Seq {
     int first, n, len;
+    __device__ __forceinline__ Seq() {}
     __device__ __forceinline__ Seq(const ChunkParams &p, int b) {
         first = min(max(p.starts[b], 0), p.rows);
         n = min(max(p.starts[b + 1], first), p.rows) - first;
@@ -86,6 +87,7 @@ struct Tile {
     int idx0, count;                   // first of the list, rows
     int lim0, lim1;                    // first unseen position (numbered without the gap) of its first and last row
     int gap, skip, blocks, cost, per;
+    __device__ __forceinline__ Tile() {}
     __device__ __forceinline__ Tile(const ChunkParams &p, const Seq &s, int t) {
         using C = Cc<D>;
         idx0 = t * C::ROWS;
@@ -107,14 +109,22 @@ struct Tile {
     __device__ __forceinline__ int block_at(int x) const { return min(max(x / per - SETUP, 0), blocks); }
 };
 
-// The pieces of work of a CTA, in order: blocks [k0, k1) of tile t of sequence b
-// and kv head h. All (head, sequence, tile) cost a total that P CTAs take in equal
-// parts, whatever the lengths; a tile that two of them share is joined later.
+// A piece of work: blocks [k0, k1) of a tile of sequence b and kv head h.
+template <int D>
+struct Piece {
+    int h, b, t, k0, k1;
+    Seq seq;
+    Tile<D> tile;
+};
+
+// The pieces of a CTA, in order. All (head, sequence, tile) cost a total that
+// P CTAs take in equal parts, whatever the lengths; a tile that two of them share
+// is joined later.
 template <int D>
 struct Pieces {
     long long left;                    // of this CTA's share
     int h, b, t, x;                    // where it stands: x into the cost of the tile
-    __device__ __forceinline__ bool next(const ChunkParams &p, int &k0, int &k1, Seq &s) {
+    __device__ __forceinline__ bool next(const ChunkParams &p, Piece<D> &w) {
         while (left > 0 && h < p.heads) {
             if (b >= p.B) {
                 b = 0;
@@ -122,34 +132,26 @@ struct Pieces {
                 ++h;
                 continue;
             }
-            s = Seq(p, b);
-            if (t >= tiles_in<D>(p, s)) {
+            w.seq = Seq(p, b);
+            if (t >= tiles_in<D>(p, w.seq)) {
                 ++b;
                 t = 0;
                 continue;
             }
-            const Tile<D> tile(p, s, t);
-            const int x1 = int(min((long long)tile.cost, x + left));
-            k0 = tile.block_at(x);
-            k1 = tile.block_at(x1);
-            const bool last = x1 == tile.cost;
+            w.tile = Tile<D>(p, w.seq, t);
+            const int x1 = int(min((long long)w.tile.cost, x + left));
+            w.h = h;
+            w.b = b;
+            w.t = t;
+            w.k0 = w.tile.block_at(x);
+            w.k1 = w.tile.block_at(x1);
+            const bool last = x1 == w.tile.cost;
             left -= x1 - x;
-            x = x1;
-            if (k1 > k0 || (last && tile.blocks == 0)) return true;
-            done(last);
+            x = last ? 0 : x1;
+            t += last;
+            if (w.k1 > w.k0 || (last && w.tile.blocks == 0)) return true;
         }
         return false;
-    }
-    // after a piece: to the next tile if this one is finished
-    __device__ __forceinline__ void done(bool last) {
-        if (last) {
-            x = 0;
-            ++t;
-        }
-    }
-    __device__ __forceinline__ void after(const ChunkParams &p, const Seq &s) {
-        const Tile<D> tile(p, s, t);
-        done(x == tile.cost);
     }
 };
 
@@ -262,6 +264,12 @@ __device__ Share2 find_share(const ChunkParams &p, Pieces<D> &w, int *list, long
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&d)[4]) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3]) : "memory");
+}
+__device__ __forceinline__ float2 add2(const float2 &a, const float2 &b) {
+    float2 d;
+    asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 __device__ __forceinline__ uint16_t ld_u16(const uint8_t *p) { return *reinterpret_cast<const uint16_t *>(p); }
 
@@ -391,7 +399,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
     const uint32_t bars = base + C::BARS;
     const uint32_t k_full = bars, k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST,
                    s_full = v_empty + 8 * ST, p_ready = s_full + 8 * T * NB, q_ready = p_ready + 8 * T * NB,
-                   o_done = q_ready + 8 * T, end = o_done + 8 * T;
+                   o_done = q_ready + 8 * T, o_end = o_done + 8 * T, end = o_end + 8 * T;
 
     if (warp == 0) t5::alloc(base + C::TMEM, 512);
     if (tid == 0) {
@@ -408,6 +416,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         for (int i = 0; i < T; ++i) {
             sk::mbar_init(q_ready + 8 * i, 4);
             sk::mbar_init(o_done + 8 * i, 1);
+            sk::mbar_init(o_end + 8 * i, 1);
         }
         sk::mbar_init(end, 1);
         sk::fence_barrier_init();
@@ -429,8 +438,6 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         dead = true;
         atomicOr(p.err, 1u);
     };
-    int k0, k1;
-    Seq seq(p, 0);
 
     if (warp < C::SW) {
         // ------------------------------------------------------- softmax
@@ -438,40 +445,47 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         const uint32_t mine = tmem + (uint32_t((warp & 3) * 32) << 16);
         const uint32_t o_at = mine + C::O_COL + t * D, q_at = mine + C::Q_COL + t * (D / 2),
                        s_at = mine + C::S_COL + t * NB * KB;
-        uint32_t blocks_done = 0, products = 0;              // S buffers read; second products of this tile so far
+        uint32_t blocks_done = 0, products = 0, ends = 0;    // S buffers read; second products of this tile so far; pieces
         int last_join = 0;                                   // whether a tile's first part, not its last, was this CTA's
-        while (work.next(p, k0, k1, seq)) {
-            const Tile<D> tile(p, seq, work.t);
-            const bool active = t * 128 < tile.count;
-            const int idx = tile.idx0 + t * 128 + row, i = sk::quotient(idx, p.by_g), g = idx - i * p.G;
-            const bool there = t * 128 + row < tile.count;
-            const long long at = (long long)(seq.first + i) * (p.heads * p.G) + work.h * p.G + g;
-            const bool whole = k0 == 0 && k1 == tile.blocks;
-            const int n = k1 - k0;
+        Piece<D> w;
+        // the piece's query rows of this tile, to TMEM; the products of the piece before it with its own are done
+        auto load_q = [&] {
+            if (t * 128 >= w.tile.count || w.k1 == w.k0) return;
+            const int idx = w.tile.idx0 + t * 128 + row, i = sk::quotient(idx, p.by_g);
+            const bool there = t * 128 + row < w.tile.count;
+            const __half *src = p.q + (w.seq.first + i) * p.q_stride + (long long)(w.h * p.G + idx - i * p.G) * D;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t v[32];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    if (there) x = *reinterpret_cast<const uint4 *>(src + c * 64 + e * 8);
+                    v[4 * e] = x.x;
+                    v[4 * e + 1] = x.y;
+                    v[4 * e + 2] = x.z;
+                    v[4 * e + 3] = x.w;
+                }
+                __syncwarp();
+                t5::st32(q_at + c * 32, v);
+            }
+            t5::wait_st();
+            t5::fence_before();
+            __syncwarp();
+            if (lane == 0) sk::mbar_arrive(q_ready + 8 * t);
+        };
+        bool have = work.next(p, w);
+        if (have) load_q();
+        while (have) {
+            const bool active = t * 128 < w.tile.count, there = t * 128 + row < w.tile.count;
+            const int n = w.k1 - w.k0;
             float neg = NO_BASE;
             float2 sum = make_float2(0.f, 0.f);
             if (active && n > 0) {
-                const __half *src = p.q + (seq.first + i) * p.q_stride + (long long)(work.h * p.G + g) * D;
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    uint32_t v[32];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                        if (there) x = *reinterpret_cast<const uint4 *>(src + c * 64 + e * 8);
-                        v[4 * e] = x.x;
-                        v[4 * e + 1] = x.y;
-                        v[4 * e + 2] = x.z;
-                        v[4 * e + 3] = x.w;
-                    }
-                    t5::st32(q_at + c * 32, v);
-                }
-                t5::wait_st();
-                t5::fence_before();
-                __syncwarp();
-                if (lane == 0) sk::mbar_arrive(q_ready + 8 * t);
-                const int lim = there ? tile.lim0 + i - sk::quotient(tile.idx0, p.by_g) : 0;
+                const int i = sk::quotient(w.tile.idx0 + t * 128 + row, p.by_g);
+                const int lim = there ? w.tile.lim0 + i - sk::quotient(w.tile.idx0, p.by_g) : 0;
                 const int low = p.window ? lim - p.window : 0;
+                const int lim0 = w.tile.lim0, low1 = p.window ? w.tile.lim1 - p.window : 0;
                 for (int j = 0; j < n; ++j) {
                     const uint32_t sb = blocks_done % NB, use = blocks_done / NB;
                     const uint32_t s_col = s_at + sb * KB;
@@ -484,19 +498,21 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     t5::ld32(s_col + 32, s + 32);
                     t5::wait_ld();
                     t5::held<KB>(s);
-                    const int pos = (k0 + j) * KB;
-                    if (pos + KB > tile.lim0 || (p.window && pos + KB > p.sinks && pos < tile.lim1 - p.window)) {
+                    const int pos = (w.k0 + j) * KB;
+                    if (pos + KB > lim0 || (pos + KB > p.sinks && pos < low1)) {
 #pragma unroll
                         for (int e = 0; e < KB; ++e)
                             if (pos + e >= lim || (pos + e >= p.sinks && pos + e < low)) s[e] = NEG_INF;
                     }
-                    float m0 = s[0], m1 = s[1];
+                    float m0 = NEG_INF, m1 = NEG_INF, m2 = NEG_INF, m3 = NEG_INF;
 #pragma unroll
-                    for (int e = 2; e < KB; e += 4) {
-                        m0 = fmaxf(m0, fmaxf(s[e], s[e + 1]));
-                        if (e + 2 < KB) m1 = fmaxf(m1, fmaxf(s[e + 2], s[e + 3]));
+                    for (int e = 0; e < KB; e += 8) {        // maxima of three
+                        m0 = fmaxf(fmaxf(s[e], s[e + 1]), m0);
+                        m1 = fmaxf(fmaxf(s[e + 2], s[e + 3]), m1);
+                        m2 = fmaxf(fmaxf(s[e + 4], s[e + 5]), m2);
+                        m3 = fmaxf(fmaxf(s[e + 6], s[e + 7]), m3);
                     }
-                    m0 = fmaxf(m0, m1);
+                    m0 = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
                     if (__any_sync(0xffffffffu, passes(p, m0, neg))) {
                         const float had = neg;
                         neg = fminf(had, neg_base(p, m0));
@@ -504,7 +520,8 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                         sum.x *= f;
                         sum.y *= f;
                         if (j > 0) {
-                            // the output so far, once the product before this one is done
+                            // The output so far, once the product before this one is done. (A barrier tells a phase from the
+                            // next only; the product before that is done, its scores' successors being here.)
                             wait(o_done + 8 * t, products - 1);
                             __syncwarp();
                             t5::fence_after();
@@ -521,32 +538,37 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                             }
                         }
                     }
-                    uint32_t w[KB / 2];
+                    uint32_t y16[KB / 2];
 #pragma unroll
                     for (int e = 0; e < KB; e += 2) {
                         const float2 y = weights2(p, s[e], s[e + 1], neg, neg);
-                        sum.x += y.x;
-                        sum.y += y.y;
-                        w[e / 2] = pack_f16(y.x, y.y);
+                        sum = add2(sum, y);
+                        y16[e / 2] = pack_f16(y.x, y.y);
                     }
-                    t5::st32(s_col, w);
+                    t5::st32(s_col, y16);
                     t5::wait_st();
                     t5::fence_before();
                     __syncwarp();
                     if (lane == 0) sk::mbar_arrive(p_ready + 8 * (t * NB + sb));
                     ++products;
                 }
-                // (with two buffers the last two products may be under way: a barrier tells one phase from the next only)
-                if (NB == 2 && n > 1) wait(o_done + 8 * t, products - 2);
-                wait(o_done + 8 * t, products - 1);
-                __syncwarp();
-                t5::fence_after();
             }
+            // The next piece's query rows first: its scores are formed beside this one's end.
+            const Piece<D> was = w;
+            have = work.next(p, w);
+            if (have) load_q();
             // ---- the rows' outputs, or their part of them
-            const float l = sum.x + sum.y;
-            const size_t slot = size_t(blockIdx.x) * 2 + (k0 == 0 ? 1 : 0);
+            const bool whole = was.k0 == 0 && was.k1 == was.tile.blocks;
+            const size_t slot = size_t(blockIdx.x) * 2 + (was.k0 == 0 ? 1 : 0);
             if (active) {
-                const float f = l == 0.f ? 0.f : p.vg / l;
+                if (n > 0) {
+                    wait(o_end + 8 * t, ends++);
+                    __syncwarp();
+                    t5::fence_after();
+                }
+                const float l = sum.x + sum.y, f = l == 0.f ? 0.f : p.vg / l;
+                const int idx = was.tile.idx0 + t * 128 + row, i = sk::quotient(idx, p.by_g);
+                const long long at = (long long)(was.seq.first + i) * (p.heads * p.G) + was.h * p.G + idx - i * p.G;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
@@ -579,58 +601,78 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                         *reinterpret_cast<float2 *>(p.part_ml + (slot * C::ROWS + t * 128 + row) * 2) = make_float2(-neg, l);
                 }
             }
-            if (tid == 0 && k0 == 0 && !whole) {
-                // this CTA's last piece: the units of the tile's end tell the last part's owner
-                const long long here = bound_of(share, blockIdx.x + 1);
-                const int c1 = owner_of(share, here + (tile.cost - work.x) - 1);
-                p.join[blockIdx.x] = make_int4(c1 - int(blockIdx.x) + 1, work.h, work.b, work.t);
+            if (tid == 0 && was.k0 == 0 && !whole) {
+                // This CTA's last piece: its share ends within the tile, whose last unit tells the last part's owner.
+                const int c1 = owner_of(share, bound_of(share, blockIdx.x + 1) + (was.tile.cost - work.x) - 1);
+                p.join[blockIdx.x] = make_int4(c1 - int(blockIdx.x) + 1, was.h, was.b, was.t);
                 last_join = 1;
             }
             t5::fence_before();
-            work.after(p, seq);
         }
         if (tid == 0 && !last_join) p.join[blockIdx.x] = make_int4(0, 0, 0, 0);
     } else if (warp < C::SW + C::DW) {
         // ------------------------------------------------------- decoding
+        // One stream of blocks over all pieces: the records of a block are looked up three blocks ahead of its
+        // decoding, their bytes fetched two ahead.
         const int w = warp - C::SW;
-        uint32_t made = 0;                                   // blocks
-        while (work.next(p, k0, k1, seq)) {
-            const Tile<D> tile(p, seq, work.t);
-            const int32_t *table = p.table + (long long)work.b * p.width;
-            const int n = k1 - k0, last = max(0, (tile.lim1 + sk::KV4_REC - 1) / sk::KV4_REC - 1);
-            const uint8_t *rec[C::ROUNDS], *soon[C::ROUNDS];
-            auto lookup = [&](int j, const uint8_t *(&r)[C::ROUNDS]) {
-#pragma unroll
-                for (int x = 0; x < C::ROUNDS; ++x) {
-                    const int v = min((k0 + j) * (KB / sk::KV4_REC) + record_of<D>(w, x), last);
-                    r[x] = p.cache + size_t(sk::kv4_record(table, v >= tile.gap ? v + tile.skip : v, p.recs, p.by_recs, p.pages,
-                                                           p.heads, work.h)) * sk::kv4_rec_bytes(D);
-                }
-            };
-            Raw<D> keys, vals;
-            if (n > 0) {
-                lookup(0, rec);
-                fetch_keys<D>(rec, w, lane, keys);
-                fetch_values<D>(rec, w, lane, vals);
-                if (n > 1) lookup(1, soon);
+        Piece<D> piece;
+        int j = 0, n = 0, last = 0;
+        const int32_t *table = p.table;
+        const uint8_t *rec[C::ROUNDS];
+        auto look_up = [&] {                                 // the next block's records; false after the last block
+            while (j == n) {
+                if (!work.next(p, piece)) return false;
+                j = 0;
+                n = piece.k1 - piece.k0;
+                table = p.table + (long long)piece.b * p.width;
+                last = max(0, (piece.tile.lim1 + sk::KV4_REC - 1) / sk::KV4_REC - 1);
             }
-            for (int j = 0; j < n; ++j, ++made) {
+#pragma unroll
+            for (int x = 0; x < C::ROUNDS; ++x) {
+                const int v = min((piece.k0 + j) * (KB / sk::KV4_REC) + record_of<D>(w, x), last);
+                rec[x] = p.cache + size_t(sk::kv4_record(table, v >= piece.tile.gap ? v + piece.tile.skip : v, p.recs, p.by_recs,
+                                                         p.pages, p.heads, piece.h)) * sk::kv4_rec_bytes(D);
+            }
+            ++j;
+            return true;
+        };
+        Raw<D> keys[2], vals[2];
+        bool there[2], more = look_up();                     // blocks fetched; whether rec is another's
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            there[x] = more;
+            if (more) {
+                fetch_keys<D>(rec, w, lane, keys[x]);
+                fetch_values<D>(rec, w, lane, vals[x]);
+                more = look_up();
+            }
+        }
+        for (uint32_t made = 0; there[0];) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (!there[x]) {
+                    there[0] = false;
+                    break;
+                }
                 const uint32_t st = made % ST, use = made / ST;
                 if (use > 0) wait(k_empty + 8 * st, use - 1);
-                decode_keys<D>(base + C::K + st * C::TILE_B, w, lane, keys);
+                decode_keys<D>(base + C::K + st * C::TILE_B, w, lane, keys[x]);
                 t5::fence_async_smem();
                 __syncwarp();
                 if (lane == 0 && !p.stall) sk::mbar_arrive(k_full + 8 * st);
-                if (j + 1 < n) fetch_keys<D>(soon, w, lane, keys);
+                there[x] = more;
+                if (more) fetch_keys<D>(rec, w, lane, keys[x]);
                 if (use > 0) wait(v_empty + 8 * st, use - 1);
-                decode_values<D>(base + C::V + st * C::TILE_B, w, lane, vals);
+                decode_values<D>(base + C::V + st * C::TILE_B, w, lane, vals[x]);
                 t5::fence_async_smem();
                 __syncwarp();
                 if (lane == 0 && !p.stall) sk::mbar_arrive(v_full + 8 * st);
-                if (j + 1 < n) fetch_values<D>(soon, w, lane, vals);
-                if (j + 2 < n) lookup(j + 2, soon);
+                if (more) {
+                    fetch_values<D>(rec, w, lane, vals[x]);
+                    more = look_up();
+                }
+                ++made;
             }
-            work.after(p, seq);
         }
     } else {
         // ------------------------------------------------------- products
@@ -638,10 +680,10 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         // from uniform registers (from a lane chosen by number a product takes 45 clocks to issue, of the 32 it runs).
         uint32_t kc = 0, vc = 0, pieces[2] = {0, 0};         // blocks of keys and values used; pieces of each tile
         uint32_t scored[2] = {0, 0}, weighted[2] = {0, 0};   // uses of the tiles' buffers of S
-        while (work.next(p, k0, k1, seq)) {
-            const Tile<D> tile(p, seq, work.t);
-            const int n = k1 - k0;
-            const bool two = T == 2 && tile.count > 128;
+        Piece<D> piece;
+        while (work.next(p, piece)) {
+            const int n = piece.k1 - piece.k0;
+            const bool two = T == 2 && piece.tile.count > 128;
             if (n > 0) {
                 // S of tile t from the stage's keys
                 auto scores = [&](int t) {
@@ -664,7 +706,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     if (t5::elect()) t5::commit(k_empty + 8 * (kc % ST));
                     ++kc;
                 };
-                auto values = [&](int t, bool first) {
+                auto values = [&](int t, bool first, bool last) {
                     const uint32_t sb = weighted[t] % NB;
                     wait(p_ready + 8 * (t * NB + sb), weighted[t] / NB);
                     ++weighted[t];
@@ -677,6 +719,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                             t5::mma(tmem + C::O_COL + t * D, tmem + C::S_COL + (t * NB + sb) * KB + 8 * s, op + s * 2048 / 16,
                                     t5::shape(D, true), !first || s > 0);
                         t5::commit(o_done + 8 * t);
+                        if (last) t5::commit(o_end + 8 * t);
                     }
                 };
                 wait(q_ready, pieces[0]++);
@@ -697,10 +740,10 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     }
                     wait(v_full + 8 * (vc % ST), vc / ST);
                     if (NB == 1 && more) keys_ready();
-                    values(0, j == 0);
+                    values(0, j == 0, !more);
                     if (NB == 1 && more) scores(0);
                     if (two) {
-                        values(1, j == 0);
+                        values(1, j == 0, !more);
                         if (NB == 1 && more) scores(1);
                     }
                     if (NB == 1 && more) keys_used();
@@ -708,7 +751,6 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     ++vc;
                 }
             }
-            work.after(p, seq);
         }
         // every product is done before the TMEM is given back
         __syncwarp();

@@ -33,18 +33,18 @@ constexpr int KB = 64;                 // positions per block
 constexpr int SETUP = 4;               // what a tile costs beside its blocks, in blocks
 constexpr int MIN_SHARE = 12;          // least cost a CTA takes, above that of one block: no part of a tile is empty
 
-// T tiles of 128 rows share what is decoded; NB buffers of S per tile; DW warps
-// decode; ST stages of keys and of values.
+// T tiles of 128 rows share what is decoded; NB buffers of S per tile; HW warps
+// decode keys and as many values; ST stages of each.
 template <int D>
 struct Cc {
     static constexpr int T = D == 256 ? 1 : 2;
     static constexpr int NB = D == 128 ? 1 : 2;
-    static constexpr int DW = D == 256 ? 8 : 4;
+    static constexpr int HW = D == 256 ? 4 : 2, DW = 2 * HW;
     static constexpr int ST = D == 256 ? 3 : 4;
     static constexpr int SW = 4 * T, WARPS_ALL = SW + DW + 1, CT_ALL = WARPS_ALL * 32;
     static constexpr int ROWS = 128 * T;
     static constexpr int TILE_B = KB * D * 2, SLAB = KB * 128;         // a stage; 64 components of it
-    static constexpr int ROUNDS = 2 * D / (32 * DW);                   // 16-byte pieces per thread
+    static constexpr int ROUNDS = 2 * D / (32 * HW);                   // 16-byte pieces per thread
     static constexpr int K = 0, V = ST * TILE_B, BARS = 2 * ST * TILE_B;
     // barriers: keys full, empty, values full, empty (ST each); S full and P ready (T NB each); query rows ready, a second
     // product done, a piece's last one done (T each); end
@@ -282,8 +282,8 @@ __device__ __forceinline__ void put8(uint32_t addr, uint32_t codes, uint32_t sca
     st_shared_v4(addr, d);
 }
 
-// What a decoding thread has fetched of a block: 16 bytes of codes of the keys and
-// of the values, and the scales of their two blocks or positions, ROUNDS times.
+// What a decoding thread has fetched of a block's keys or values: 16 bytes of codes
+// and the scales of their two blocks or positions, ROUNDS times.
 template <int D>
 struct Raw {
     uint4 c[Cc<D>::ROUNDS];
@@ -294,7 +294,7 @@ struct Raw {
 // w, round r: position and piece.
 template <int D>
 __device__ __forceinline__ void key_place(int w, int r, int lane, int &row, int &piece) {
-    const int u = r * Cc<D>::DW + w;
+    const int u = r * Cc<D>::HW + w;
     if constexpr (D == 256) {
         row = (u >> 1) * 8 + (lane & 7);
         piece = (u & 1) * 4 + (lane >> 3);
@@ -310,7 +310,7 @@ __device__ __forceinline__ void key_place(int w, int r, int lane, int &row, int 
 // half record (eight positions), block, pair.
 template <int D>
 __device__ __forceinline__ void value_place(int w, int r, int lane, int &half, int &blk, int &pair) {
-    const int u = r * Cc<D>::DW + w;
+    const int u = r * Cc<D>::HW + w;
     pair = lane & 3;
     if constexpr (D == 256) {
         half = u >> 1;
@@ -326,7 +326,7 @@ __device__ __forceinline__ void value_place(int w, int r, int lane, int &half, i
 // The record of a block that decode warp w reads in round r (both for keys and for values).
 template <int D>
 __device__ __forceinline__ int record_of(int w, int r) {
-    return (r * Cc<D>::DW + w) * (D == 256 ? 1 : D == 128 ? 2 : 4) / 4;
+    return (r * Cc<D>::HW + w) * (D == 256 ? 1 : D == 128 ? 2 : 4) / 4;
 }
 
 template <int D>
@@ -350,41 +350,57 @@ __device__ __forceinline__ void fetch_values(const uint8_t *const (&rec)[Cc<D>::
         raw.s[r] = ld_u16(rec[r] + 17 * D + blk * 16 + (half & 1) * 8 + pair * 2);
     }
 }
-// Both to the stage at `to`: 64 components (128 bytes) of a position a row, 64
-// rows a slab, 16-byte pieces swizzled within eight rows.
+// Where a thread's four 16-byte pieces go in a stage of keys or of values: 64
+// components (128 bytes) of a position a row, 64 rows a slab, pieces swizzled within
+// eight rows. A later round lies ROUND bytes further.
 template <int D>
-__device__ __forceinline__ void decode_keys(uint32_t to, int w, int lane, const Raw<D> &raw) {
+constexpr int ROUND = (D == 64 ? 32 : 16) * 128;
+template <int D>
+__device__ __forceinline__ void key_offsets(int w, int lane, uint32_t (&to)[4]) {
+    int row, piece;
+    key_place<D>(w, 0, lane, row, piece);
+    const uint32_t at = (piece >> 1) * Cc<D>::SLAB + row * 128, x = uint32_t(row & 7), c = (piece & 1) * 4;
 #pragma unroll
-    for (int r = 0; r < Cc<D>::ROUNDS; ++r) {
-        int row, piece;
-        key_place<D>(w, r, lane, row, piece);
-        const uint32_t s = scale_pair(raw.s[r]), lo = sk::bcast_lo(s), hi = sk::bcast_hi(s);
-        const uint32_t at = to + (piece >> 1) * Cc<D>::SLAB + row * 128;
-        const uint32_t x = uint32_t(row & 7), c = (piece & 1) * 4;
-        put8(at + ((c ^ x) << 4), raw.c[r].x, lo);
-        put8(at + (((c + 1) ^ x) << 4), raw.c[r].y, lo);
-        put8(at + (((c + 2) ^ x) << 4), raw.c[r].z, hi);
-        put8(at + (((c + 3) ^ x) << 4), raw.c[r].w, hi);
+    for (uint32_t e = 0; e < 4; ++e) to[e] = at + (((c + e) ^ x) << 4);
+}
+// (of values: first and second half of the block at the pair's first position, then
+// at its second. Lanes of an odd block have the halves exchanged, so that eight
+// lanes' stores meet all banks: `odd`.)
+template <int D>
+__device__ __forceinline__ void value_offsets(int w, int lane, uint32_t (&to)[4], bool &odd) {
+    int half, blk, pair;
+    value_place<D>(w, 0, lane, half, blk, pair);
+    odd = blk & 1;
+    const uint32_t at = (blk >> 2) * Cc<D>::SLAB + half * 1024, c = (blk & 3) * 2;
+#pragma unroll
+    for (uint32_t e = 0; e < 4; ++e) {
+        const uint32_t x = uint32_t(2 * pair) + (e >> 1), z = (e & 1) ^ uint32_t(odd);
+        to[e] = at + x * 128 + (((c + z) ^ x) << 4);
     }
 }
 template <int D>
-__device__ __forceinline__ void decode_values(uint32_t to, int w, int lane, const Raw<D> &raw) {
+__device__ __forceinline__ void decode_keys(uint32_t stage, const uint32_t (&to)[4], const Raw<D> &raw) {
+    const uint32_t at[4] = {stage + to[0], stage + to[1], stage + to[2], stage + to[3]};
 #pragma unroll
     for (int r = 0; r < Cc<D>::ROUNDS; ++r) {
-        int half, blk, pair;
-        value_place<D>(w, r, lane, half, blk, pair);
-        const uint32_t s = scale_pair(raw.s[r]);
-        // lanes of an odd block store their second position first: eight lanes meet all banks
-        const bool odd = blk & 1;
-        const uint32_t f0 = odd ? raw.c[r].z : raw.c[r].x, f1 = odd ? raw.c[r].w : raw.c[r].y,
-                       l0 = odd ? raw.c[r].x : raw.c[r].z, l1 = odd ? raw.c[r].y : raw.c[r].w;
-        const uint32_t lo = sk::bcast_lo(s), hi = sk::bcast_hi(s), fs = odd ? hi : lo, ls = odd ? lo : hi;
-        const uint32_t at = to + (blk >> 2) * Cc<D>::SLAB + half * 1024, c = (blk & 3) * 2;
-        const uint32_t rf = uint32_t(2 * pair + odd), rl = rf ^ 1u;
-        put8(at + rf * 128 + ((c ^ rf) << 4), f0, fs);
-        put8(at + rf * 128 + (((c + 1) ^ rf) << 4), f1, fs);
-        put8(at + rl * 128 + ((c ^ rl) << 4), l0, ls);
-        put8(at + rl * 128 + (((c + 1) ^ rl) << 4), l1, ls);
+        const uint32_t s = scale_pair(raw.s[r]), lo = sk::bcast_lo(s), hi = sk::bcast_hi(s);
+        put8(at[0] + r * ROUND<D>, raw.c[r].x, lo);
+        put8(at[1] + r * ROUND<D>, raw.c[r].y, lo);
+        put8(at[2] + r * ROUND<D>, raw.c[r].z, hi);
+        put8(at[3] + r * ROUND<D>, raw.c[r].w, hi);
+    }
+}
+template <int D>
+__device__ __forceinline__ void decode_values(uint32_t stage, const uint32_t (&to)[4], bool odd, const Raw<D> &raw) {
+    const uint32_t at[4] = {stage + to[0], stage + to[1], stage + to[2], stage + to[3]};
+#pragma unroll
+    for (int r = 0; r < Cc<D>::ROUNDS; ++r) {
+        const uint32_t s = scale_pair(raw.s[r]), lo = sk::bcast_lo(s), hi = sk::bcast_hi(s);
+        const uint4 c = raw.c[r];
+        put8(at[0] + r * ROUND<D>, odd ? c.y : c.x, lo);
+        put8(at[1] + r * ROUND<D>, odd ? c.x : c.y, lo);
+        put8(at[2] + r * ROUND<D>, odd ? c.w : c.z, hi);
+        put8(at[3] + r * ROUND<D>, odd ? c.z : c.w, hi);
     }
 }
 
@@ -404,8 +420,8 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
     if (warp == 0) t5::alloc(base + C::TMEM, 512);
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
-            sk::mbar_init(k_full + 8 * i, C::DW);
-            sk::mbar_init(v_full + 8 * i, C::DW);
+            sk::mbar_init(k_full + 8 * i, C::HW);
+            sk::mbar_init(v_full + 8 * i, C::HW);
             sk::mbar_init(k_empty + 8 * i, 1);
             sk::mbar_init(v_empty + 8 * i, 1);
         }
@@ -612,9 +628,16 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         if (tid == 0 && !last_join) p.join[blockIdx.x] = make_int4(0, 0, 0, 0);
     } else if (warp < C::SW + C::DW) {
         // ------------------------------------------------------- decoding
-        // One stream of blocks over all pieces: the records of a block are looked up three blocks ahead of its
-        // decoding, their bytes fetched two ahead.
-        const int w = warp - C::SW;
+        // One stream of blocks over all pieces, of keys for the one half of the warps and of values for the other (a
+        // warp that does both meets two waits and two fences a block). The records of a block are looked up three blocks
+        // ahead of its decoding, their bytes fetched two ahead.
+        const bool value = warp >= C::SW + C::HW;
+        const int w = warp - C::SW - (value ? C::HW : 0);
+        const uint32_t full = value ? v_full : k_full, empty = value ? v_empty : k_empty, ring = base + (value ? C::V : C::K);
+        uint32_t to[4];
+        bool odd = false;
+        if (value) value_offsets<D>(w, lane, to, odd);
+        else key_offsets<D>(w, lane, to);
         Piece<D> piece;
         int j = 0, n = 0, last = 0;
         const int32_t *table = p.table;
@@ -636,14 +659,17 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             ++j;
             return true;
         };
-        Raw<D> keys[2], vals[2];
+        auto fetch = [&](Raw<D> &raw) {
+            if (value) fetch_values<D>(rec, w, lane, raw);
+            else fetch_keys<D>(rec, w, lane, raw);
+        };
+        Raw<D> raw[2];
         bool there[2], more = look_up();                     // blocks fetched; whether rec is another's
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             there[x] = more;
             if (more) {
-                fetch_keys<D>(rec, w, lane, keys[x]);
-                fetch_values<D>(rec, w, lane, vals[x]);
+                fetch(raw[x]);
                 more = look_up();
             }
         }
@@ -655,20 +681,15 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     break;
                 }
                 const uint32_t st = made % ST, use = made / ST;
-                if (use > 0) wait(k_empty + 8 * st, use - 1);
-                decode_keys<D>(base + C::K + st * C::TILE_B, w, lane, keys[x]);
+                if (use > 0) wait(empty + 8 * st, use - 1);
+                if (value) decode_values<D>(ring + st * C::TILE_B, to, odd, raw[x]);
+                else decode_keys<D>(ring + st * C::TILE_B, to, raw[x]);
                 t5::fence_async_smem();
                 __syncwarp();
-                if (lane == 0 && !p.stall) sk::mbar_arrive(k_full + 8 * st);
+                if (lane == 0 && !p.stall) sk::mbar_arrive(full + 8 * st);
                 there[x] = more;
-                if (more) fetch_keys<D>(rec, w, lane, keys[x]);
-                if (use > 0) wait(v_empty + 8 * st, use - 1);
-                decode_values<D>(base + C::V + st * C::TILE_B, w, lane, vals[x]);
-                t5::fence_async_smem();
-                __syncwarp();
-                if (lane == 0 && !p.stall) sk::mbar_arrive(v_full + 8 * st);
                 if (more) {
-                    fetch_values<D>(rec, w, lane, vals[x]);
+                    fetch(raw[x]);
                     more = look_up();
                 }
                 ++made;

@@ -16,6 +16,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 
 #include "../../include/skinny.h"
@@ -27,6 +28,7 @@
 namespace {
 
 using namespace sk::attn;
+using sk::ex2;
 namespace t5 = sk::t5;
 
 constexpr int KB = 64;                 // positions per block
@@ -38,25 +40,39 @@ constexpr int MIN_SHARE = 12;          // least cost a CTA takes, above that of 
 template <int D>
 struct Cc {
     static constexpr int T = D == 256 ? 1 : 2;
-    static constexpr int NB = D == 128 ? 1 : 2;
+    static constexpr int NB = 2;
+    // The query rows lie in TMEM where there is room, else in shared memory (whose rate the scores then also need: a
+    // product of 64 columns takes 48 clocks, not 32).
+    static constexpr bool QS = D == 128;
+    static constexpr int Q_TILE = 128 * D * 2, Q_SLAB = 128 * 128;
     static constexpr int HW = D == 256 ? 4 : 2, DW = 2 * HW;
     static constexpr int ST = D == 256 ? 3 : 4;
     static constexpr int SW = 4 * T, WARPS_ALL = SW + DW + 1, CT_ALL = WARPS_ALL * 32;
     static constexpr int ROWS = 128 * T;
     static constexpr int TILE_B = KB * D * 2, SLAB = KB * 128;         // a stage; 64 components of it
     static constexpr int ROUNDS = 2 * D / (32 * HW);                   // 16-byte pieces per thread
-    static constexpr int K = 0, V = ST * TILE_B, BARS = 2 * ST * TILE_B;
+    static constexpr int K = 0, V = ST * TILE_B, Q = 2 * ST * TILE_B, BARS = Q + (QS ? T * Q_TILE : 0);
     // barriers: keys full, empty, values full, empty (ST each); S full and P ready (T NB each); query rows ready, a second
     // product done, a piece's last one done (T each); end
     static constexpr int NBARS = 4 * ST + 2 * T * NB + 3 * T + 1;
     static constexpr int SCAN = BARS + 8 * NBARS, TMEM = SCAN + 16 * (WARPS_ALL + 1), START = TMEM + 16;
     static constexpr int BYTES = 1024 + START + 64;
     static constexpr size_t SMEM = BYTES > 120 * 1024 ? BYTES : 120 * 1024;      // one CTA per SM: all of the TMEM
-    static constexpr int O_COL = 0, Q_COL = T * D, S_COL = Q_COL + T * D / 2;
+    static constexpr int O_COL = 0, Q_COL = T * D, S_COL = QS ? Q_COL : Q_COL + T * D / 2;
     static_assert(S_COL + T * NB * KB <= 512, "TMEM");
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static constexpr int MOST_SEQS = 2 * ST * TILE_B / 4 - 1;           // their list lies where the stages will
 };
+
+// Each row's weights are 2^(c s - t) with c = scale * key scale * log2 e and t, the
+// row's base, a whole number, so that one fma gives the exponent, rounded once. t is
+// P_SHIFT below a maximum that the row had earlier and is moved only when an exponent
+// passes P_SHIFT + SLACK; the weights go to the second product in FP16, between
+// 2^-32 and 2^15, their sum is taken unrounded. An exponent is off by what c s is
+// rounded by before the difference: 2^-24 of it, as the score itself (FP32).
+__device__ __forceinline__ void write_lse(const AttnParams &p, long long row, float base, float l) {
+    if (p.lse) p.lse[row] = l == 0.f ? NEG_INF : (base + __log2f(l)) * LN2;
+}
 
 struct ChunkParams : AttnParams {
     const int32_t *starts;
@@ -265,10 +281,25 @@ __device__ Share2 find_share(const ChunkParams &p, Pieces<D> &w, int *list, long
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&d)[4]) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(d[0]), "r"(d[1]), "r"(d[2]), "r"(d[3]) : "memory");
 }
-__device__ __forceinline__ float2 add2(const float2 &a, const float2 &b) {
+// Two floats in one register pair, and the operations on both.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 apart(uint64_t v) {
     float2 d;
-    asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
-        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
 __device__ __forceinline__ uint16_t ld_u16(const uint8_t *p) { return *reinterpret_cast<const uint16_t *>(p); }
@@ -329,30 +360,24 @@ __device__ __forceinline__ int record_of(int w, int r) {
     return (r * Cc<D>::HW + w) * (D == 256 ? 1 : D == 128 ? 2 : 4) / 4;
 }
 
+// Where in a record a thread's codes and scales lie, the same in every round.
 template <int D>
-__device__ __forceinline__ void fetch_keys(const uint8_t *const (&rec)[Cc<D>::ROUNDS], int w, int lane, Raw<D> &raw) {
-#pragma unroll
-    for (int r = 0; r < Cc<D>::ROUNDS; ++r) {
-        int row, piece;
-        key_place<D>(w, r, lane, row, piece);
-        const int i = row & 15;
-        raw.c[r] = *reinterpret_cast<const uint4 *>(rec[r] + i * (D / 2) + piece * 16);
-        raw.s[r] = ld_u16(rec[r] + 8 * D + i * (D / 16) + piece * 2);
-    }
-}
-template <int D>
-__device__ __forceinline__ void fetch_values(const uint8_t *const (&rec)[Cc<D>::ROUNDS], int w, int lane, Raw<D> &raw) {
-#pragma unroll
-    for (int r = 0; r < Cc<D>::ROUNDS; ++r) {
+__device__ __forceinline__ void source_offsets(bool value, int w, int lane, uint32_t &codes, uint32_t &scales) {
+    if (value) {
         int half, blk, pair;
-        value_place<D>(w, r, lane, half, blk, pair);
-        raw.c[r] = *reinterpret_cast<const uint4 *>(rec[r] + 9 * D + (half & 1) * 4 * D + blk * 64 + pair * 16);
-        raw.s[r] = ld_u16(rec[r] + 17 * D + blk * 16 + (half & 1) * 8 + pair * 2);
+        value_place<D>(w, 0, lane, half, blk, pair);
+        codes = 9 * D + (half & 1) * 4 * D + blk * 64 + pair * 16;
+        scales = 17 * D + blk * 16 + (half & 1) * 8 + pair * 2;
+    } else {
+        int row, piece;
+        key_place<D>(w, 0, lane, row, piece);
+        codes = (row & 15) * (D / 2) + piece * 16;
+        scales = 8 * D + (row & 15) * (D / 16) + piece * 2;
     }
 }
 // Where a thread's four 16-byte pieces go in a stage of keys or of values: 64
 // components (128 bytes) of a position a row, 64 rows a slab, pieces swizzled within
-// eight rows. A later round lies ROUND bytes further.
+// eight rows. A later round lies ROUND bytes (32 rows) further.
 template <int D>
 constexpr int ROUND = (D == 64 ? 32 : 16) * 128;
 template <int D>
@@ -447,10 +472,10 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
     const Share2 share = find_share<D>(p, work, reinterpret_cast<int *>(smem), reinterpret_cast<long long *>(smem + C::SCAN),
                                        reinterpret_cast<int *>(smem + C::START));
     bool dead = false;
-    // Waits for a barrier's phase number `n` (from 0), a second at most; after one
-    // that ran out the thread waits no more.
-    auto wait = [&](uint32_t bar, uint32_t n) {
-        if (dead || sk::wait_limited(bar, n & 1)) return;
+    // Waits for a barrier's phase of this parity, a second at most; after one that
+    // ran out the thread waits no more.
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (dead || t5::wait_spin(bar, parity)) return;
         dead = true;
         atomicOr(p.err, 1u);
     };
@@ -461,7 +486,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         const uint32_t mine = tmem + (uint32_t((warp & 3) * 32) << 16);
         const uint32_t o_at = mine + C::O_COL + t * D, q_at = mine + C::Q_COL + t * (D / 2),
                        s_at = mine + C::S_COL + t * NB * KB;
-        uint32_t blocks_done = 0, products = 0, ends = 0;    // S buffers read; second products of this tile so far; pieces
+        uint32_t blocks_done = 0, ends = 0;                  // blocks of this tile so far, and pieces
         int last_join = 0;                                   // whether a tile's first part, not its last, was this CTA's
         Piece<D> w;
         // the piece's query rows of this tile, to TMEM; the products of the piece before it with its own are done
@@ -470,6 +495,25 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             const int idx = w.tile.idx0 + t * 128 + row, i = sk::quotient(idx, p.by_g);
             const bool there = t * 128 + row < w.tile.count;
             const __half *src = p.q + (w.seq.first + i) * p.q_stride + (long long)(w.h * p.G + idx - i * p.G) * D;
+            if constexpr (C::QS) {
+                const uint32_t to = base + C::Q + t * C::Q_TILE + row * 128;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    uint4 x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x[e] = there ? *reinterpret_cast<const uint4 *>(src + c * 64 + e * 8) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t d[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+                        st_shared_v4(to + c * C::Q_SLAB + ((e ^ (row & 7)) << 4), d);
+                    }
+                }
+                t5::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) sk::mbar_arrive(q_ready + 8 * t);
+                return;
+            }
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 uint32_t v[32];
@@ -495,17 +539,17 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         while (have) {
             const bool active = t * 128 < w.tile.count, there = t * 128 + row < w.tile.count;
             const int n = w.k1 - w.k0;
-            float neg = NO_BASE;
-            float2 sum = make_float2(0.f, 0.f);
+            float t0 = 0.f, most = -FLT_MAX;                 // the row's base, and what moves it (at first: any score)
+            uint64_t sum = two(0.f, 0.f);
             if (active && n > 0) {
                 const int i = sk::quotient(w.tile.idx0 + t * 128 + row, p.by_g);
                 const int lim = there ? w.tile.lim0 + i - sk::quotient(w.tile.idx0, p.by_g) : 0;
                 const int low = p.window ? lim - p.window : 0;
                 const int lim0 = w.tile.lim0, low1 = p.window ? w.tile.lim1 - p.window : 0;
                 for (int j = 0; j < n; ++j) {
-                    const uint32_t sb = blocks_done % NB, use = blocks_done / NB;
+                    const uint32_t sb = blocks_done & 1u;
                     const uint32_t s_col = s_at + sb * KB;
-                    wait(s_full + 8 * (t * NB + sb), use);
+                    wait(s_full + 8 * (t * NB + sb), (blocks_done >> 1) & 1u);
                     __syncwarp();
                     ++blocks_done;
                     t5::fence_after();
@@ -521,24 +565,28 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                             if (pos + e >= lim || (pos + e >= p.sinks && pos + e < low)) s[e] = NEG_INF;
                     }
                     float m0 = NEG_INF, m1 = NEG_INF, m2 = NEG_INF, m3 = NEG_INF;
+                    const uint64_t c2 = two(p.c, p.c), n2 = two(-t0, -t0);
 #pragma unroll
-                    for (int e = 0; e < KB; e += 8) {        // maxima of three
-                        m0 = fmaxf(fmaxf(s[e], s[e + 1]), m0);
-                        m1 = fmaxf(fmaxf(s[e + 2], s[e + 3]), m1);
-                        m2 = fmaxf(fmaxf(s[e + 4], s[e + 5]), m2);
-                        m3 = fmaxf(fmaxf(s[e + 6], s[e + 7]), m3);
+                    for (int e = 0; e < KB; e += 2) {
+                        const float2 x = apart(fma2(two(s[e], s[e + 1]), c2, n2));
+                        s[e] = x.x;
+                        s[e + 1] = x.y;
+                        float &m = e % 8 == 0 ? m0 : e % 8 == 2 ? m1 : e % 8 == 4 ? m2 : m3;
+                        m = fmaxf(fmaxf(x.x, x.y), m);       // (one instruction)
                     }
                     m0 = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
-                    if (__any_sync(0xffffffffu, passes(p, m0, neg))) {
-                        const float had = neg;
-                        neg = fminf(had, neg_base(p, m0));
-                        const float f = rebase(p, neg, had);
-                        sum.x *= f;
-                        sum.y *= f;
+                    if (__any_sync(0xffffffffu, m0 > most)) {
+                        const float by = m0 > most ? ceilf(m0) - P_SHIFT : 0.f, f = most < 0.f ? 0.f : ex2(-by);
+                        if (m0 > most) most = P_SHIFT + SLACK;
+                        t0 += by;
+                        const float2 l = apart(sum);
+                        sum = two(l.x * f, l.y * f);
+#pragma unroll
+                        for (int e = 0; e < KB; ++e) s[e] -= by;
                         if (j > 0) {
                             // The output so far, once the product before this one is done. (A barrier tells a phase from the
                             // next only; the product before that is done, its scores' successors being here.)
-                            wait(o_done + 8 * t, products - 1);
+                            wait(o_done + 8 * t, (blocks_done - 2) & 1u);
                             __syncwarp();
                             t5::fence_after();
 #pragma unroll 1
@@ -557,16 +605,15 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     uint32_t y16[KB / 2];
 #pragma unroll
                     for (int e = 0; e < KB; e += 2) {
-                        const float2 y = weights2(p, s[e], s[e + 1], neg, neg);
-                        sum = add2(sum, y);
-                        y16[e / 2] = pack_f16(y.x, y.y);
+                        const float y0 = ex2(s[e]), y1 = ex2(s[e + 1]);
+                        sum = add2(sum, two(y0, y1));
+                        y16[e / 2] = pack_f16(y0, y1);
                     }
                     t5::st32(s_col, y16);
                     t5::wait_st();
                     t5::fence_before();
                     __syncwarp();
                     if (lane == 0) sk::mbar_arrive(p_ready + 8 * (t * NB + sb));
-                    ++products;
                 }
             }
             // The next piece's query rows first: its scores are formed beside this one's end.
@@ -578,11 +625,12 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             const size_t slot = size_t(blockIdx.x) * 2 + (was.k0 == 0 ? 1 : 0);
             if (active) {
                 if (n > 0) {
-                    wait(o_end + 8 * t, ends++);
+                    wait(o_end + 8 * t, ends++ & 1u);
                     __syncwarp();
                     t5::fence_after();
                 }
-                const float l = sum.x + sum.y, f = l == 0.f ? 0.f : p.vg / l;
+                const float2 ll = apart(sum);
+                const float l = ll.x + ll.y, f = l == 0.f ? 0.f : p.vg / l;
                 const int idx = was.tile.idx0 + t * 128 + row, i = sk::quotient(idx, p.by_g);
                 const long long at = (long long)(was.seq.first + i) * (p.heads * p.G) + was.h * p.G + idx - i * p.G;
 #pragma unroll 1
@@ -612,9 +660,9 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     __syncwarp();
                 }
                 if (there) {
-                    if (whole) write_stats(p, at, -neg, l);
+                    if (whole) write_lse(p, at, t0, l);
                     else
-                        *reinterpret_cast<float2 *>(p.part_ml + (slot * C::ROWS + t * 128 + row) * 2) = make_float2(-neg, l);
+                        *reinterpret_cast<float2 *>(p.part_ml + (slot * C::ROWS + t * 128 + row) * 2) = make_float2(t0, l);
                 }
             }
             if (tid == 0 && was.k0 == 0 && !whole) {
@@ -638,10 +686,13 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         bool odd = false;
         if (value) value_offsets<D>(w, lane, to, odd);
         else key_offsets<D>(w, lane, to);
+        uint32_t codes_at, scales_at;
+        source_offsets<D>(value, w, lane, codes_at, scales_at);
         Piece<D> piece;
         int j = 0, n = 0, last = 0;
         const int32_t *table = p.table;
-        const uint8_t *rec[C::ROUNDS];
+        int entry = 0, in_page = 0, head = 0;                // of the block looked up: the page and the record in it that this
+                                                             // lane asked for (used only when fetched: the load has time)
         auto look_up = [&] {                                 // the next block's records; false after the last block
             while (j == n) {
                 if (!work.next(p, piece)) return false;
@@ -650,18 +701,25 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 table = p.table + (long long)piece.b * p.width;
                 last = max(0, (piece.tile.lim1 + sk::KV4_REC - 1) / sk::KV4_REC - 1);
             }
-#pragma unroll
-            for (int x = 0; x < C::ROUNDS; ++x) {
-                const int v = min((piece.k0 + j) * (KB / sk::KV4_REC) + record_of<D>(w, x), last);
-                rec[x] = p.cache + size_t(sk::kv4_record(table, v >= piece.tile.gap ? v + piece.tile.skip : v, p.recs, p.by_recs,
-                                                         p.pages, p.heads, piece.h)) * sk::kv4_rec_bytes(D);
-            }
+            const int v = min((piece.k0 + j) * (KB / sk::KV4_REC) + (lane & 3), last);
+            const int r = v >= piece.tile.gap ? v + piece.tile.skip : v, pg = sk::quotient(r, p.by_recs);
+            entry = table[pg];
+            in_page = r - pg * p.recs;
+            head = piece.h;
             ++j;
             return true;
         };
         auto fetch = [&](Raw<D> &raw) {
-            if (value) fetch_values<D>(rec, w, lane, raw);
-            else fetch_keys<D>(rec, w, lane, raw);
+            const uint8_t *rec[C::ROUNDS];
+            const uint32_t found = (uint32_t(min(max(entry, 0), p.pages - 1)) * p.heads + head) * p.recs + in_page;
+#pragma unroll
+            for (int x = 0; x < C::ROUNDS; ++x)
+                rec[x] = p.cache + size_t(__shfl_sync(0xffffffffu, found, record_of<D>(w, x))) * sk::kv4_rec_bytes(D);
+#pragma unroll
+            for (int x = 0; x < C::ROUNDS; ++x) {
+                raw.c[x] = *reinterpret_cast<const uint4 *>(rec[x] + codes_at);
+                raw.s[x] = ld_u16(rec[x] + scales_at);
+            }
         };
         Raw<D> raw[2];
         bool there[2], more = look_up();                     // blocks fetched; whether rec is another's
@@ -673,110 +731,108 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 more = look_up();
             }
         }
-        for (uint32_t made = 0; there[0];) {
+        uint32_t st = 0, parity = 1;                         // (the first use of each stage finds it free)
+        while (there[0]) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 if (!there[x]) {
                     there[0] = false;
                     break;
                 }
-                const uint32_t st = made % ST, use = made / ST;
-                if (use > 0) wait(empty + 8 * st, use - 1);
+                wait(empty + 8 * st, parity);
                 if (value) decode_values<D>(ring + st * C::TILE_B, to, odd, raw[x]);
                 else decode_keys<D>(ring + st * C::TILE_B, to, raw[x]);
                 t5::fence_async_smem();
                 __syncwarp();
                 if (lane == 0 && !p.stall) sk::mbar_arrive(full + 8 * st);
+                if (++st == ST) {
+                    st = 0;
+                    parity ^= 1u;
+                }
                 there[x] = more;
                 if (more) {
                     fetch(raw[x]);
                     more = look_up();
                 }
-                ++made;
             }
         }
     } else {
         // ------------------------------------------------------- products
-        // The warp waits together and one elected lane, always the same, issues: what it issues takes its operands
-        // from uniform registers (from a lane chosen by number a product takes 45 clocks to issue, of the 32 it runs).
-        uint32_t kc = 0, vc = 0, pieces[2] = {0, 0};         // blocks of keys and values used; pieces of each tile
-        uint32_t scored[2] = {0, 0}, weighted[2] = {0, 0};   // uses of the tiles' buffers of S
-        Piece<D> piece;
-        while (work.next(p, piece)) {
-            const int n = piece.k1 - piece.k0;
-            const bool two = T == 2 && piece.tile.count > 128;
-            if (n > 0) {
-                // S of tile t from the stage's keys
-                auto scores = [&](int t) {
-                    const uint32_t sb = scored[t] % NB;
-                    ++scored[t];
-                    const uint64_t op = t5::operand(base + C::K + (kc % ST) * C::TILE_B, 16, 1024);
-                    if (t5::elect()) {
+        // One elected lane: what it issues takes its operands from uniform registers (from a lane chosen by number a
+        // product of 64 columns takes 45 clocks to issue, of the 32 it runs). Stages, parities and operands are carried
+        // along: a lone warp's instructions are ten clocks apart, and a block's turn here is on everyone's path.
+        if (t5::elect()) {
+            constexpr uint64_t STEP = C::TILE_B / 16;
+            const uint64_t k_op0 = t5::operand(base + C::K, 16, 1024), v_op0 = t5::operand(base + C::V, C::SLAB, 1024),
+                           q_op = t5::operand(base + C::Q, 16, 1024);     // (of query rows in shared memory)
+            uint64_t k_op = k_op0, v_op = v_op0;
+            uint32_t ks = 0, kp = 0, vs = 0, vp = 0;             // stages of keys and values and their parities
+            uint32_t sb[2] = {0, 0};                             // blocks scored, of each tile
+            uint32_t wb[2] = {0, 0};                             // blocks weighted
+            uint32_t pieces[2] = {0, 0};
+            // S of tile t from the stage's keys
+            auto scores = [&](int t) {
+                const uint32_t b = sb[t]++ & 1u, d = tmem + C::S_COL + (t * NB + b) * KB;
 #pragma unroll
-                        for (int s = 0; s < D / 16; ++s)
-                            t5::mma(tmem + C::S_COL + (t * NB + sb) * KB, tmem + C::Q_COL + t * (D / 2) + 8 * s,
-                                    op + ((s >> 2) * C::SLAB + (s & 3) * 32) / 16, t5::shape(KB, false), s > 0);
-                        t5::commit(s_full + 8 * (t * NB + sb));
-                    }
-                };
-                auto keys_ready = [&] {
-                    wait(k_full + 8 * (kc % ST), kc / ST);
-                    t5::fence_after();
-                };
-                auto keys_used = [&] {
-                    if (t5::elect()) t5::commit(k_empty + 8 * (kc % ST));
-                    ++kc;
-                };
-                auto values = [&](int t, bool first, bool last) {
-                    const uint32_t sb = weighted[t] % NB;
-                    wait(p_ready + 8 * (t * NB + sb), weighted[t] / NB);
-                    ++weighted[t];
-                    __syncwarp();
-                    t5::fence_after();
-                    const uint64_t op = t5::operand(base + C::V + (vc % ST) * C::TILE_B, C::SLAB, 1024);
-                    if (t5::elect()) {
-#pragma unroll
-                        for (int s = 0; s < KB / 16; ++s)
-                            t5::mma(tmem + C::O_COL + t * D, tmem + C::S_COL + (t * NB + sb) * KB + 8 * s, op + s * 2048 / 16,
-                                    t5::shape(D, true), !first || s > 0);
-                        t5::commit(o_done + 8 * t);
-                        if (last) t5::commit(o_end + 8 * t);
-                    }
-                };
-                wait(q_ready, pieces[0]++);
-                if (two) wait(q_ready + 8, pieces[1]++);
-                keys_ready();
-                __syncwarp();
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint64_t k = k_op + ((s >> 2) * C::SLAB + (s & 3) * 32) / 16;
+                    if constexpr (C::QS)
+                        t5::mma_smem(d, q_op + (t * C::Q_TILE + (s >> 2) * C::Q_SLAB + (s & 3) * 32) / 16, k, t5::shape(KB, false),
+                                     s > 0);
+                    else t5::mma(d, tmem + C::Q_COL + t * (D / 2) + 8 * s, k, t5::shape(KB, false), s > 0);
+                }
+                t5::commit(s_full + 8 * (t * NB + b));
+            };
+            auto score = [&](bool two) {
+                wait(k_full + 8 * ks, kp);
+                t5::fence_after();
                 scores(0);
-                if (two) scores(1);
-                keys_used();
+                if (T == 2 && two) scores(1);
+                t5::commit(k_empty + 8 * ks);
+                k_op += STEP;
+                if (++ks == ST) {
+                    ks = 0;
+                    kp ^= 1u;
+                    k_op = k_op0;
+                }
+            };
+            auto values = [&](int t, bool first, bool last) {
+                const uint32_t n = wb[t]++, b = n & 1u, a = tmem + C::S_COL + (t * NB + b) * KB;
+                wait(p_ready + 8 * (t * NB + b), (n >> 1) & 1u);
+                t5::fence_after();
+#pragma unroll
+                for (int s = 0; s < KB / 16; ++s)
+                    t5::mma(tmem + C::O_COL + t * D, a + 8 * s, v_op + s * 2048 / 16, t5::shape(D, true), !first || s > 0);
+                t5::commit(o_done + 8 * t);
+                if (last) t5::commit(o_end + 8 * t);
+            };
+            Piece<D> piece;
+            while (work.next(p, piece)) {
+                const int n = piece.k1 - piece.k0;
+                const bool two = T == 2 && piece.tile.count > 128;
+                if (n == 0) continue;
+                wait(q_ready, pieces[0]++ & 1u);
+                if (two) wait(q_ready + 8, pieces[1]++ & 1u);
+                score(two);
                 for (int j = 0; j < n; ++j) {
-                    const bool more = j + 1 < n;
-                    if (NB == 2 && more) {
-                        keys_ready();
-                        __syncwarp();
-                        scores(0);
-                        if (two) scores(1);
-                        keys_used();
+                    const bool last = j + 1 == n;
+                    if (!last) score(two);
+                    wait(v_full + 8 * vs, vp);
+                    values(0, j == 0, last);
+                    if (T == 2 && two) values(1, j == 0, last);
+                    t5::commit(v_empty + 8 * vs);
+                    v_op += STEP;
+                    if (++vs == ST) {
+                        vs = 0;
+                        vp ^= 1u;
+                        v_op = v_op0;
                     }
-                    wait(v_full + 8 * (vc % ST), vc / ST);
-                    if (NB == 1 && more) keys_ready();
-                    values(0, j == 0, !more);
-                    if (NB == 1 && more) scores(0);
-                    if (two) {
-                        values(1, j == 0, !more);
-                        if (NB == 1 && more) scores(1);
-                    }
-                    if (NB == 1 && more) keys_used();
-                    if (t5::elect()) t5::commit(v_empty + 8 * (vc % ST));
-                    ++vc;
                 }
             }
+            // every product is done before the TMEM is given back
+            t5::commit(end);
+            t5::wait_spin(end, 0);
         }
-        // every product is done before the TMEM is given back
-        __syncwarp();
-        if (t5::elect()) t5::commit(end);
-        sk::wait_limited(end, 0);
         __syncwarp();
     }
     t5::fence_before();
@@ -809,11 +865,12 @@ __global__ void __launch_bounds__(JT) kv4_chunk_join_kernel(const __grid_constan
     for (int k0 = 0; k0 < n; k0 += 32) {           // 32 parts at a time, under the largest base so far
         float2 ml = make_float2(NEG_INF, 0.f);
         if (k0 + lane < n) ml = *reinterpret_cast<const float2 *>(p.part_ml + (slot(k0 + lane) * C::ROWS + r) * 2);
-        float now = ml.x;
+        // (a part in which the row saw nothing has no base)
+        float now = ml.y == 0.f ? -FLT_MAX : ml.x;
 #pragma unroll
         for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
         now = fmaxf(now, top);
-        const float old = rebase(p, top, now), f = rebase(p, ml.x, now);
+        const float old = ex2(top - now), f = ml.y == 0.f ? 0.f : ex2(ml.x - now);
         top = now;
         float add = ml.y * f;
 #pragma unroll
@@ -838,7 +895,7 @@ __global__ void __launch_bounds__(JT) kv4_chunk_join_kernel(const __grid_constan
     __half2 *const out = reinterpret_cast<__half2 *>(p.out + at * D) + lane;
 #pragma unroll
     for (int x = 0; x < PER / 2; ++x) out[32 * x] = __floats2half2_rn(v[2 * x] * f, v[2 * x + 1] * f);
-    if (lane == 0) write_stats(p, at, top, l);
+    if (lane == 0) write_lse(p, at, top, l);
 }
 
 template <int D>

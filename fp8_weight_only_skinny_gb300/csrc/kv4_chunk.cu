@@ -35,10 +35,13 @@ constexpr int KB = 64;                 // positions per block
 constexpr int SETUP = 4;               // what a tile costs beside its blocks, in blocks
 constexpr int MIN_SHARE = 12;          // least cost a CTA takes, above that of one block: no part of a tile is empty
 
-// T tiles of 128 rows share what is decoded; NB buffers of S per tile; HW warps
-// decode keys and as many values; ST stages of each.
+// T tiles of 128 rows share what a CTA decodes; NB buffers of S per tile; HW warps
+// decode keys and as many values; ST stages of each. PAIR: two CTAs, each with a tile
+// of its own, share what is decoded, each decoding half the keys of a block and half
+// the components of its values; the first one issues the products of both.
 template <int D>
 struct Cc {
+    static constexpr bool PAIR = D == 256;
     static constexpr int T = D == 256 ? 1 : 2;
     static constexpr int NB = 2;
     // The query rows lie in TMEM where there is room, else in shared memory (whose rate the scores then also need: a
@@ -46,12 +49,16 @@ struct Cc {
     static constexpr bool QS = D == 128;
     static constexpr int Q_TILE = 128 * D * 2, Q_SLAB = 128 * 128;
     static constexpr int HW = D == 256 ? 4 : 2, DW = 2 * HW;
-    static constexpr int ST = D == 256 ? 3 : 4;
+    static constexpr int ST = PAIR ? 6 : 4;
     static constexpr int SW = 4 * T, WARPS_ALL = SW + DW + 1, CT_ALL = WARPS_ALL * 32;
-    static constexpr int ROWS = 128 * T;
-    static constexpr int TILE_B = KB * D * 2, SLAB = KB * 128;         // a stage; 64 components of it
-    static constexpr int ROUNDS = 2 * D / (32 * HW);                   // 16-byte pieces per thread
-    static constexpr int K = 0, V = ST * TILE_B, Q = 2 * ST * TILE_B, BARS = Q + (QS ? T * Q_TILE : 0);
+    static constexpr int ROWS = PAIR ? 256 : 128 * T;                  // of a tile of the work
+    static constexpr int KEYS = PAIR ? KB / 2 : KB, COMPS = PAIR ? D / 2 : D;   // a CTA's, of a block
+    static constexpr int STAGE = KEYS * D * 2;                         // bytes, of keys or of values
+    static constexpr int K_SLAB = KEYS * 128, V_SLAB = KB * 128;       // 64 components of it
+    static constexpr int ROUNDS = STAGE / 64 / (32 * HW);              // 16-byte pieces of codes per thread
+    // bytes from a thread's piece to its next round's
+    static constexpr int K_ROUND = (D == 64 ? 32 : 16) * 128, V_ROUND = (D == 64 || PAIR ? 32 : 16) * 128;
+    static constexpr int K = 0, V = ST * STAGE, Q = 2 * ST * STAGE, BARS = Q + (QS ? T * Q_TILE : 0);
     // barriers: keys full, empty, values full, empty (ST each); S full and P ready (T NB each); query rows ready, a second
     // product done, a piece's last one done (T each); end
     static constexpr int NBARS = 4 * ST + 2 * T * NB + 3 * T + 1;
@@ -61,8 +68,13 @@ struct Cc {
     static constexpr int O_COL = 0, Q_COL = T * D, S_COL = QS ? Q_COL : Q_COL + T * D / 2;
     static_assert(S_COL + T * NB * KB <= 512, "TMEM");
     static_assert(SMEM <= 227 * 1024, "shared memory");
-    static constexpr int MOST_SEQS = 2 * ST * TILE_B / 4 - 1;           // their list lies where the stages will
+    static constexpr int MOST_SEQS = 2 * ST * STAGE / 4 - 1;            // their list lies where the stages will
 };
+// The CTAs that share a piece of work count as one.
+template <int D>
+__device__ __forceinline__ int worker() {
+    return int(blockIdx.x) / (Cc<D>::PAIR ? 2 : 1);
+}
 
 // Each row's weights are 2^(c s - t) with c = scale * key scale * log2 e and t, the
 // row's base, a whole number, so that one fma gives the exponent, rounded once. t is
@@ -183,7 +195,7 @@ __device__ __forceinline__ int owner_of(const Share2 &s, long long u) { return i
 template <int D>
 __device__ Share2 find_share(const ChunkParams &p, Pieces<D> &w, int *list, long long *scan, int *start) {
     using C = Cc<D>;
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, me = worker<D>();
     auto scanned = [&](long long mine, long long &total) {         // exclusive, over the CTA
         long long v = mine;
 #pragma unroll
@@ -251,9 +263,9 @@ __device__ Share2 find_share(const ChunkParams &p, Pieces<D> &w, int *list, long
     sh.parts = int(max(1LL, min(sh.total / MIN_SHARE, (long long)p.ctas)));
     w.left = 0;
     w.h = w.b = w.t = w.x = 0;
-    if (int(blockIdx.x) < sh.parts && sh.total > 0) {
-        const long long u0 = bound_of(sh, blockIdx.x);
-        w.left = bound_of(sh, blockIdx.x + 1) - u0;
+    if (me < sh.parts && sh.total > 0) {
+        const long long u0 = bound_of(sh, me);
+        w.left = bound_of(sh, me + 1) - u0;
         w.h = int(u0 / per_head);
         long long off = u0 - w.h * per_head;
         if (off >= before && off < before + mine) {
@@ -338,34 +350,35 @@ __device__ __forceinline__ void key_place(int w, int r, int lane, int &row, int 
     }
 }
 // Values: a 16-byte piece is a pair of positions of a block of 16 components:
-// half record (eight positions), block, pair.
+// half record (eight positions), block (of this CTA's), pair.
 template <int D>
 __device__ __forceinline__ void value_place(int w, int r, int lane, int &half, int &blk, int &pair) {
     const int u = r * Cc<D>::HW + w;
     pair = lane & 3;
-    if constexpr (D == 256) {
-        half = u >> 1;
-        blk = (u & 1) * 8 + (lane >> 2);
-    } else if constexpr (D == 128) {
+    if constexpr (Cc<D>::COMPS == 128) {
         half = u;
         blk = lane >> 2;
     } else {
+        static_assert(Cc<D>::COMPS == 64 || Cc<D>::COMPS == 128, "components of a CTA");
         half = u * 2 + (lane >> 4);
         blk = (lane >> 2) & 3;
     }
 }
-// The record of a block that decode warp w reads in round r (both for keys and for values).
+// The record of a block that decode warp w reads in round r, in the CTA `rank` of a pair.
 template <int D>
-__device__ __forceinline__ int record_of(int w, int r) {
-    return (r * Cc<D>::HW + w) * (D == 256 ? 1 : D == 128 ? 2 : 4) / 4;
+__device__ __forceinline__ int record_of(bool value, int w, int r, int rank) {
+    const int u = r * Cc<D>::HW + w;
+    if (value) return Cc<D>::COMPS == 128 ? u >> 1 : u;
+    return D == 256 ? (Cc<D>::KEYS / sk::KV4_REC) * rank + (u >> 2) : D == 128 ? u >> 1 : u;
 }
 
 // Where in a record a thread's codes and scales lie, the same in every round.
 template <int D>
-__device__ __forceinline__ void source_offsets(bool value, int w, int lane, uint32_t &codes, uint32_t &scales) {
+__device__ __forceinline__ void source_offsets(bool value, int w, int lane, int rank, uint32_t &codes, uint32_t &scales) {
     if (value) {
         int half, blk, pair;
         value_place<D>(w, 0, lane, half, blk, pair);
+        blk += rank * (Cc<D>::COMPS / 16);
         codes = 9 * D + (half & 1) * 4 * D + blk * 64 + pair * 16;
         scales = 17 * D + blk * 16 + (half & 1) * 8 + pair * 2;
     } else {
@@ -376,15 +389,13 @@ __device__ __forceinline__ void source_offsets(bool value, int w, int lane, uint
     }
 }
 // Where a thread's four 16-byte pieces go in a stage of keys or of values: 64
-// components (128 bytes) of a position a row, 64 rows a slab, pieces swizzled within
-// eight rows. A later round lies ROUND bytes (32 rows) further.
-template <int D>
-constexpr int ROUND = (D == 64 ? 32 : 16) * 128;
+// components (128 bytes) of a position a row, the rows of 64 components a slab, pieces
+// swizzled within eight rows.
 template <int D>
 __device__ __forceinline__ void key_offsets(int w, int lane, uint32_t (&to)[4]) {
     int row, piece;
     key_place<D>(w, 0, lane, row, piece);
-    const uint32_t at = (piece >> 1) * Cc<D>::SLAB + row * 128, x = uint32_t(row & 7), c = (piece & 1) * 4;
+    const uint32_t at = (piece >> 1) * Cc<D>::K_SLAB + row * 128, x = uint32_t(row & 7), c = (piece & 1) * 4;
 #pragma unroll
     for (uint32_t e = 0; e < 4; ++e) to[e] = at + (((c + e) ^ x) << 4);
 }
@@ -396,7 +407,7 @@ __device__ __forceinline__ void value_offsets(int w, int lane, uint32_t (&to)[4]
     int half, blk, pair;
     value_place<D>(w, 0, lane, half, blk, pair);
     odd = blk & 1;
-    const uint32_t at = (blk >> 2) * Cc<D>::SLAB + half * 1024, c = (blk & 3) * 2;
+    const uint32_t at = (blk >> 2) * Cc<D>::V_SLAB + half * 1024, c = (blk & 3) * 2;
 #pragma unroll
     for (uint32_t e = 0; e < 4; ++e) {
         const uint32_t x = uint32_t(2 * pair) + (e >> 1), z = (e & 1) ^ uint32_t(odd);
@@ -409,10 +420,10 @@ __device__ __forceinline__ void decode_keys(uint32_t stage, const uint32_t (&to)
 #pragma unroll
     for (int r = 0; r < Cc<D>::ROUNDS; ++r) {
         const uint32_t s = scale_pair(raw.s[r]), lo = sk::bcast_lo(s), hi = sk::bcast_hi(s);
-        put8(at[0] + r * ROUND<D>, raw.c[r].x, lo);
-        put8(at[1] + r * ROUND<D>, raw.c[r].y, lo);
-        put8(at[2] + r * ROUND<D>, raw.c[r].z, hi);
-        put8(at[3] + r * ROUND<D>, raw.c[r].w, hi);
+        put8(at[0] + r * Cc<D>::K_ROUND, raw.c[r].x, lo);
+        put8(at[1] + r * Cc<D>::K_ROUND, raw.c[r].y, lo);
+        put8(at[2] + r * Cc<D>::K_ROUND, raw.c[r].z, hi);
+        put8(at[3] + r * Cc<D>::K_ROUND, raw.c[r].w, hi);
     }
 }
 template <int D>
@@ -422,17 +433,17 @@ __device__ __forceinline__ void decode_values(uint32_t stage, const uint32_t (&t
     for (int r = 0; r < Cc<D>::ROUNDS; ++r) {
         const uint32_t s = scale_pair(raw.s[r]), lo = sk::bcast_lo(s), hi = sk::bcast_hi(s);
         const uint4 c = raw.c[r];
-        put8(at[0] + r * ROUND<D>, odd ? c.y : c.x, lo);
-        put8(at[1] + r * ROUND<D>, odd ? c.x : c.y, lo);
-        put8(at[2] + r * ROUND<D>, odd ? c.w : c.z, hi);
-        put8(at[3] + r * ROUND<D>, odd ? c.z : c.w, hi);
+        put8(at[0] + r * Cc<D>::V_ROUND, odd ? c.y : c.x, lo);
+        put8(at[1] + r * Cc<D>::V_ROUND, odd ? c.x : c.y, lo);
+        put8(at[2] + r * Cc<D>::V_ROUND, odd ? c.w : c.z, hi);
+        put8(at[3] + r * Cc<D>::V_ROUND, odd ? c.z : c.w, hi);
     }
 }
 
 template <int D>
 __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __grid_constant__ ChunkParams p) {
     using C = Cc<D>;
-    constexpr int T = C::T, NB = C::NB, ST = C::ST;
+    constexpr int T = C::T, NB = C::NB, ST = C::ST, CTAS = C::PAIR ? 2 : 1;
     extern __shared__ unsigned char dyn[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = (sk::smem_u32(dyn) + 1023u) & ~1023u;
@@ -442,28 +453,31 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                    s_full = v_empty + 8 * ST, p_ready = s_full + 8 * T * NB, q_ready = p_ready + 8 * T * NB,
                    o_done = q_ready + 8 * T, o_end = o_done + 8 * T, end = o_end + 8 * T;
 
-    if (warp == 0) t5::alloc(base + C::TMEM, 512);
+    const int rank = C::PAIR ? int(sk::cluster_rank()) : 0;
+    if (warp == 0) t5::alloc<C::PAIR>(base + C::TMEM, 512);
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
-            sk::mbar_init(k_full + 8 * i, C::HW);
-            sk::mbar_init(v_full + 8 * i, C::HW);
+            sk::mbar_init(k_full + 8 * i, C::HW * CTAS);
+            sk::mbar_init(v_full + 8 * i, C::HW * CTAS);
             sk::mbar_init(k_empty + 8 * i, 1);
             sk::mbar_init(v_empty + 8 * i, 1);
         }
         for (int i = 0; i < T * NB; ++i) {
             sk::mbar_init(s_full + 8 * i, 1);
-            sk::mbar_init(p_ready + 8 * i, 4);
+            sk::mbar_init(p_ready + 8 * i, 4 * CTAS);
         }
         for (int i = 0; i < T; ++i) {
-            sk::mbar_init(q_ready + 8 * i, 4);
+            sk::mbar_init(q_ready + 8 * i, 4 * CTAS);
             sk::mbar_init(o_done + 8 * i, 1);
             sk::mbar_init(o_end + 8 * i, 1);
         }
         sk::mbar_init(end, 1);
         sk::fence_barrier_init();
     }
+    __syncwarp();
     t5::fence_before();
-    __syncthreads();
+    if constexpr (C::PAIR) sk::cluster_sync();
+    else __syncthreads();
     t5::fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::TMEM);
     sk::pdl_launch_dependents();
@@ -479,10 +493,16 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         dead = true;
         atomicOr(p.err, 1u);
     };
+    // Arrive at a barrier that the products wait at: the first CTA's.
+    auto arrive = [&](uint32_t bar) {
+        if constexpr (C::PAIR) t5::arrive_cluster(sk::peer(bar, 0));
+        else sk::mbar_arrive(bar);
+    };
 
     if (warp < C::SW) {
         // ------------------------------------------------------- softmax
         const int t = warp >> 2, row = tid & 127;
+        const int first = (C::PAIR ? rank : t) * 128;        // of this CTA's or warpgroup's rows in the tile
         const uint32_t mine = tmem + (uint32_t((warp & 3) * 32) << 16);
         const uint32_t o_at = mine + C::O_COL + t * D, q_at = mine + C::Q_COL + t * (D / 2),
                        s_at = mine + C::S_COL + t * NB * KB;
@@ -491,9 +511,10 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         Piece<D> w;
         // the piece's query rows of this tile, to TMEM; the products of the piece before it with its own are done
         auto load_q = [&] {
-            if (t * 128 >= w.tile.count || w.k1 == w.k0) return;
-            const int idx = w.tile.idx0 + t * 128 + row, i = sk::quotient(idx, p.by_g);
-            const bool there = t * 128 + row < w.tile.count;
+            // (a pair's products take both CTAs' rows, also where the second has none)
+            if ((!C::PAIR && first >= w.tile.count) || w.k1 == w.k0) return;
+            const int idx = w.tile.idx0 + first + row, i = sk::quotient(idx, p.by_g);
+            const bool there = first + row < w.tile.count;
             const __half *src = p.q + (w.seq.first + i) * p.q_stride + (long long)(w.h * p.G + idx - i * p.G) * D;
             if constexpr (C::QS) {
                 const uint32_t to = base + C::Q + t * C::Q_TILE + row * 128;
@@ -511,7 +532,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 }
                 t5::fence_async_smem();
                 __syncwarp();
-                if (lane == 0) sk::mbar_arrive(q_ready + 8 * t);
+                if (lane == 0) arrive(q_ready + 8 * t);
                 return;
             }
 #pragma unroll
@@ -532,17 +553,17 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             t5::wait_st();
             t5::fence_before();
             __syncwarp();
-            if (lane == 0) sk::mbar_arrive(q_ready + 8 * t);
+            if (lane == 0) arrive(q_ready + 8 * t);
         };
         bool have = work.next(p, w);
         if (have) load_q();
         while (have) {
-            const bool active = t * 128 < w.tile.count, there = t * 128 + row < w.tile.count;
+            const bool active = C::PAIR || first < w.tile.count, there = first + row < w.tile.count;
             const int n = w.k1 - w.k0;
             float t0 = 0.f, most = -FLT_MAX;                 // the row's base, and what moves it (at first: any score)
             uint64_t sum = two(0.f, 0.f);
             if (active && n > 0) {
-                const int i = sk::quotient(w.tile.idx0 + t * 128 + row, p.by_g);
+                const int i = sk::quotient(w.tile.idx0 + first + row, p.by_g);
                 const int lim = there ? w.tile.lim0 + i - sk::quotient(w.tile.idx0, p.by_g) : 0;
                 const int low = p.window ? lim - p.window : 0;
                 const int lim0 = w.tile.lim0, low1 = p.window ? w.tile.lim1 - p.window : 0;
@@ -613,7 +634,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     t5::wait_st();
                     t5::fence_before();
                     __syncwarp();
-                    if (lane == 0) sk::mbar_arrive(p_ready + 8 * (t * NB + sb));
+                    if (lane == 0) arrive(p_ready + 8 * (t * NB + sb));
                 }
             }
             // The next piece's query rows first: its scores are formed beside this one's end.
@@ -622,7 +643,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             if (have) load_q();
             // ---- the rows' outputs, or their part of them
             const bool whole = was.k0 == 0 && was.k1 == was.tile.blocks;
-            const size_t slot = size_t(blockIdx.x) * 2 + (was.k0 == 0 ? 1 : 0);
+            const size_t slot = size_t(worker<D>()) * 2 + (was.k0 == 0 ? 1 : 0);
             if (active) {
                 if (n > 0) {
                     wait(o_end + 8 * t, ends++ & 1u);
@@ -631,7 +652,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 }
                 const float2 ll = apart(sum);
                 const float l = ll.x + ll.y, f = l == 0.f ? 0.f : p.vg / l;
-                const int idx = was.tile.idx0 + t * 128 + row, i = sk::quotient(idx, p.by_g);
+                const int idx = was.tile.idx0 + first + row, i = sk::quotient(idx, p.by_g);
                 const long long at = (long long)(was.seq.first + i) * (p.heads * p.G) + was.h * p.G + idx - i * p.G;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
@@ -652,7 +673,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                                 make_uint4(pack_f16(o[e] * f, o[e + 1] * f), pack_f16(o[e + 2] * f, o[e + 3] * f),
                                            pack_f16(o[e + 4] * f, o[e + 5] * f), pack_f16(o[e + 6] * f, o[e + 7] * f));
                     } else {
-                        float *to = p.part_o + (slot * C::ROWS + t * 128 + row) * D + c;
+                        float *to = p.part_o + (slot * C::ROWS + first + row) * D + c;
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             *reinterpret_cast<float4 *>(to + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
@@ -662,18 +683,18 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 if (there) {
                     if (whole) write_lse(p, at, t0, l);
                     else
-                        *reinterpret_cast<float2 *>(p.part_ml + (slot * C::ROWS + t * 128 + row) * 2) = make_float2(t0, l);
+                        *reinterpret_cast<float2 *>(p.part_ml + (slot * C::ROWS + first + row) * 2) = make_float2(t0, l);
                 }
             }
-            if (tid == 0 && was.k0 == 0 && !whole) {
+            if (tid == 0 && rank == 0 && was.k0 == 0 && !whole) {
                 // This CTA's last piece: its share ends within the tile, whose last unit tells the last part's owner.
-                const int c1 = owner_of(share, bound_of(share, blockIdx.x + 1) + (was.tile.cost - work.x) - 1);
-                p.join[blockIdx.x] = make_int4(c1 - int(blockIdx.x) + 1, was.h, was.b, was.t);
+                const int me = worker<D>(), c1 = owner_of(share, bound_of(share, me + 1) + (was.tile.cost - work.x) - 1);
+                p.join[me] = make_int4(c1 - me + 1, was.h, was.b, was.t);
                 last_join = 1;
             }
             t5::fence_before();
         }
-        if (tid == 0 && !last_join) p.join[blockIdx.x] = make_int4(0, 0, 0, 0);
+        if (tid == 0 && rank == 0 && !last_join) p.join[worker<D>()] = make_int4(0, 0, 0, 0);
     } else if (warp < C::SW + C::DW) {
         // ------------------------------------------------------- decoding
         // One stream of blocks over all pieces, of keys for the one half of the warps and of values for the other (a
@@ -687,7 +708,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         if (value) value_offsets<D>(w, lane, to, odd);
         else key_offsets<D>(w, lane, to);
         uint32_t codes_at, scales_at;
-        source_offsets<D>(value, w, lane, codes_at, scales_at);
+        source_offsets<D>(value, w, lane, rank, codes_at, scales_at);
         Piece<D> piece;
         int j = 0, n = 0, last = 0;
         const int32_t *table = p.table;
@@ -714,7 +735,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             const uint32_t found = (uint32_t(min(max(entry, 0), p.pages - 1)) * p.heads + head) * p.recs + in_page;
 #pragma unroll
             for (int x = 0; x < C::ROUNDS; ++x)
-                rec[x] = p.cache + size_t(__shfl_sync(0xffffffffu, found, record_of<D>(w, x))) * sk::kv4_rec_bytes(D);
+                rec[x] = p.cache + size_t(__shfl_sync(0xffffffffu, found, record_of<D>(value, w, x, rank))) * sk::kv4_rec_bytes(D);
 #pragma unroll
             for (int x = 0; x < C::ROUNDS; ++x) {
                 raw.c[x] = *reinterpret_cast<const uint4 *>(rec[x] + codes_at);
@@ -740,11 +761,11 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     break;
                 }
                 wait(empty + 8 * st, parity);
-                if (value) decode_values<D>(ring + st * C::TILE_B, to, odd, raw[x]);
-                else decode_keys<D>(ring + st * C::TILE_B, to, raw[x]);
+                if (value) decode_values<D>(ring + st * C::STAGE, to, odd, raw[x]);
+                else decode_keys<D>(ring + st * C::STAGE, to, raw[x]);
                 t5::fence_async_smem();
                 __syncwarp();
-                if (lane == 0 && !p.stall) sk::mbar_arrive(full + 8 * st);
+                if (lane == 0 && !p.stall) arrive(full + 8 * st);
                 if (++st == ST) {
                     st = 0;
                     parity ^= 1u;
@@ -761,9 +782,14 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         // One elected lane: what it issues takes its operands from uniform registers (from a lane chosen by number a
         // product of 64 columns takes 45 clocks to issue, of the 32 it runs). Stages, parities and operands are carried
         // along: a lone warp's instructions are ten clocks apart, and a block's turn here is on everyone's path.
-        if (t5::elect()) {
-            constexpr uint64_t STEP = C::TILE_B / 16;
-            const uint64_t k_op0 = t5::operand(base + C::K, 16, 1024), v_op0 = t5::operand(base + C::V, C::SLAB, 1024),
+        if (rank == 0 && t5::elect()) {
+            constexpr uint64_t STEP = C::STAGE / 16;
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                if (dead || t5::wait_spin<C::PAIR>(bar, parity)) return;
+                dead = true;
+                atomicOr(p.err, 1u);
+            };
+            const uint64_t k_op0 = t5::operand(base + C::K, 16, 1024), v_op0 = t5::operand(base + C::V, C::V_SLAB, 1024),
                            q_op = t5::operand(base + C::Q, 16, 1024);     // (of query rows in shared memory)
             uint64_t k_op = k_op0, v_op = v_op0;
             uint32_t ks = 0, kp = 0, vs = 0, vp = 0;             // stages of keys and values and their parities
@@ -775,20 +801,20 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 const uint32_t b = sb[t]++ & 1u, d = tmem + C::S_COL + (t * NB + b) * KB;
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    const uint64_t k = k_op + ((s >> 2) * C::SLAB + (s & 3) * 32) / 16;
+                    const uint64_t k = k_op + ((s >> 2) * C::K_SLAB + (s & 3) * 32) / 16;
                     if constexpr (C::QS)
-                        t5::mma_smem(d, q_op + (t * C::Q_TILE + (s >> 2) * C::Q_SLAB + (s & 3) * 32) / 16, k, t5::shape(KB, false),
+                        t5::mma_smem(d, q_op + (t * C::Q_TILE + (s >> 2) * C::Q_SLAB + (s & 3) * 32) / 16, k, t5::shape<C::PAIR>(KB, false),
                                      s > 0);
-                    else t5::mma(d, tmem + C::Q_COL + t * (D / 2) + 8 * s, k, t5::shape(KB, false), s > 0);
+                    else t5::mma<C::PAIR>(d, tmem + C::Q_COL + t * (D / 2) + 8 * s, k, t5::shape<C::PAIR>(KB, false), s > 0);
                 }
-                t5::commit(s_full + 8 * (t * NB + b));
+                t5::commit<C::PAIR>(s_full + 8 * (t * NB + b));
             };
             auto score = [&](bool two) {
                 wait(k_full + 8 * ks, kp);
                 t5::fence_after();
                 scores(0);
                 if (T == 2 && two) scores(1);
-                t5::commit(k_empty + 8 * ks);
+                t5::commit<C::PAIR>(k_empty + 8 * ks);
                 k_op += STEP;
                 if (++ks == ST) {
                     ks = 0;
@@ -802,9 +828,9 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 t5::fence_after();
 #pragma unroll
                 for (int s = 0; s < KB / 16; ++s)
-                    t5::mma(tmem + C::O_COL + t * D, a + 8 * s, v_op + s * 2048 / 16, t5::shape(D, true), !first || s > 0);
-                t5::commit(o_done + 8 * t);
-                if (last) t5::commit(o_end + 8 * t);
+                    t5::mma<C::PAIR>(tmem + C::O_COL + t * D, a + 8 * s, v_op + s * 2048 / 16, t5::shape<C::PAIR>(D, true), !first || s > 0);
+                t5::commit<C::PAIR>(o_done + 8 * t);
+                if (last) t5::commit<C::PAIR>(o_end + 8 * t);
             };
             Piece<D> piece;
             while (work.next(p, piece)) {
@@ -820,7 +846,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     wait(v_full + 8 * vs, vp);
                     values(0, j == 0, last);
                     if (T == 2 && two) values(1, j == 0, last);
-                    t5::commit(v_empty + 8 * vs);
+                    t5::commit<C::PAIR>(v_empty + 8 * vs);
                     v_op += STEP;
                     if (++vs == ST) {
                         vs = 0;
@@ -830,15 +856,23 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 }
             }
             // every product is done before the TMEM is given back
-            t5::commit(end);
+            t5::commit<C::PAIR>(end);
             t5::wait_spin(end, 0);
         }
         __syncwarp();
     }
-    t5::fence_before();
-    __syncthreads();
+    if constexpr (C::PAIR) {
+        // neither CTA leaves while the other, or a product's end, may arrive at its barriers
+        if (warp == 0) t5::wait_spin(end, 0);
+        __syncwarp();
+        t5::fence_before();
+        sk::cluster_sync();
+    } else {
+        t5::fence_before();
+        __syncthreads();
+    }
     t5::fence_after();
-    if (warp == 0) t5::free(tmem, 512);
+    if (warp == 0) t5::free<C::PAIR>(tmem, 512);
 }
 
 // The tiles that several CTAs had parts of: CTA (c, y) joins eight rows of the
@@ -902,15 +936,19 @@ template <int D>
 sk_status run(ChunkParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     using C = Cc<D>;
     if (p.B > C::MOST_SEQS) return SK_ERR_UNSUPPORTED_SHAPE;
-    p.ctas = sms;
+    p.ctas = C::PAIR ? sms / 2 : sms;
+    if (p.ctas < 1) return SK_ERR_CUDA;
     p.join = reinterpret_cast<int4 *>(scratch);
-    p.part_ml = reinterpret_cast<float *>(scratch + (size_t(sms) * sizeof(int4) + 255) / 256 * 256);
-    p.part_o = p.part_ml + size_t(sms) * 2 * C::ROWS * 2;
-    if (size_t(reinterpret_cast<unsigned char *>(p.part_o + size_t(sms) * 2 * C::ROWS * D) - scratch) > sk::SCRATCH_BYTES)
+    p.part_ml = reinterpret_cast<float *>(scratch + (size_t(p.ctas) * sizeof(int4) + 255) / 256 * 256);
+    p.part_o = p.part_ml + size_t(p.ctas) * 2 * C::ROWS * 2;
+    if (size_t(reinterpret_cast<unsigned char *>(p.part_o + size_t(p.ctas) * 2 * C::ROWS * D) - scratch) > sk::SCRATCH_BYTES)
         return SK_ERR_WORKSPACE;
     if (sk::prepare_kernel<kv4_chunk_kernel<D>>(C::SMEM) != cudaSuccess) return SK_ERR_CUDA;
-    if (sk::launch_pdl(kv4_chunk_kernel<D>, dim3(sms), dim3(C::CT_ALL), C::SMEM, s, p) != cudaSuccess) return SK_ERR_CUDA;
-    return sk::launch_pdl(kv4_chunk_join_kernel<D>, dim3(sms, C::ROWS / (JT / 32)), dim3(JT), 0, s, p) == cudaSuccess
+    const int cluster = C::PAIR ? 2 : 1;
+    if (sk::launch_pdl_cluster(kv4_chunk_kernel<D>, cluster, dim3(unsigned(p.ctas * cluster)), dim3(C::CT_ALL), C::SMEM, s, p) !=
+        cudaSuccess)
+        return SK_ERR_CUDA;
+    return sk::launch_pdl(kv4_chunk_join_kernel<D>, dim3(unsigned(p.ctas), C::ROWS / (JT / 32)), dim3(JT), 0, s, p) == cudaSuccess
                ? SK_OK
                : SK_ERR_CUDA;
 }

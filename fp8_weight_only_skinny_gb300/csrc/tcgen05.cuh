@@ -8,12 +8,22 @@
 namespace sk {
 namespace t5 {
 
+// (PAIR: what two CTAs of a cluster do together)
+template <bool PAIR>
 __device__ __forceinline__ void alloc(uint32_t slot, uint32_t cols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
 }
+template <bool PAIR>
 __device__ __forceinline__ void free(uint32_t addr, uint32_t cols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -33,25 +43,42 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32
     return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((lead >> 4) & 0x3FFFu) << 16) |
            (uint64_t((stride >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
-// D (FP32) of M = 128, N columns, FP16 operands; bit 16: B stored along N.
+// D (FP32) of M = 128 rows (of each CTA of a pair), N columns, FP16 operands; bit 16: B stored along N.
+template <bool PAIR>
 __host__ __device__ constexpr uint32_t shape(int n, bool b_along_n) {
-    return (1u << 4) | (uint32_t(b_along_n) << 16) | (uint32_t(n >> 3) << 17) | (8u << 24);
+    return (1u << 4) | (uint32_t(b_along_n) << 16) | (uint32_t(n >> 3) << 17) | ((PAIR ? 16u : 8u) << 24);
 }
-// D (+)= A B^T, A in TMEM.
+// D (+)= A B^T, A in TMEM. A pair's CTAs have their own rows of A and D, and half of B's N each, at the same addresses.
+template <bool PAIR>
 __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)) : "memory");
+    if constexpr (PAIR)
+        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p; }"
+                     ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)) : "memory");
+    else
+        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+                     ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)) : "memory");
 }
-// The same, A in shared memory.
+// The same of one CTA, A in shared memory.
 __device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
                  ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)) : "memory");
 }
-// Arrive on `bar` when the products issued so far by this thread are done.
+// Arrive on `bar` (of both CTAs of a pair) when the products issued so far by this thread are done.
+template <bool PAIR>
 __device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if constexpr (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     ::"r"(bar), "h"(uint16_t(3)) : "memory");
+    else asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Arrive on a barrier of any CTA of the cluster (an address of peer()). What this
+// thread did is ordered for its own CTA, whose memory the products read it from: a
+// release for the cluster takes 1200 clocks.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // 32 columns of this warp's 32 lanes, without waiting: wait_ld, then held<> before their use.
@@ -90,10 +117,19 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t *v) {
 // Wait until `bar`'s phase of this parity is complete, for a second at most. The
 // clock is read every 1024 tries: read after every one (as where a wait is rare),
 // its latency is added to each wait that is not over at once.
+// CLUSTER: for what the cluster's other CTA did before it arrived.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_spin(uint32_t bar, uint32_t parity) {
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if constexpr (CLUSTER) {
+            uint32_t ok;
+            asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; "
+                         "selp.u32 %0, 1, 0, p; }" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+            if (ok) return true;
+        } else if (mbar_try_wait(bar, parity)) {
+            return true;
+        }
         if (i % 1024 == 0) {
             const uint64_t t = globaltimer_ns();
             if (t0 == 0) t0 = t;

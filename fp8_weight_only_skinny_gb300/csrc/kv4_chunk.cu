@@ -33,6 +33,7 @@ namespace t5 = sk::t5;
 
 constexpr int KB = 64;                 // positions per block
 constexpr int SETUP = 4;               // what a tile costs beside its blocks, in blocks
+constexpr int WHOLE_BLOCKS = 12;       // tables of no more blocks are not worth a second kernel where each tile has a CTA
 constexpr int MIN_SHARE = 12;          // least cost a CTA takes, above that of one block: no part of a tile is empty
 
 // T tiles of 128 rows share what a CTA decodes; NB buffers of S per tile; HW warps
@@ -50,7 +51,7 @@ struct Cc {
     static constexpr int Q_TILE = 128 * D * 2, Q_SLAB = 128 * 128;
     static constexpr int HW = D == 256 ? 4 : 2, DW = 2 * HW;
     static constexpr int ST = PAIR ? 6 : 4;
-    static constexpr int SW = 4 * T, WARPS_ALL = SW + DW + 1, CT_ALL = WARPS_ALL * 32;
+    static constexpr int SW = 4 * T, WARPS_ALL = SW + DW + 2, CT_ALL = WARPS_ALL * 32;
     static constexpr int ROWS = PAIR ? 256 : 128 * T;                  // of a tile of the work
     static constexpr int KEYS = PAIR ? KB / 2 : KB, COMPS = PAIR ? D / 2 : D;   // a CTA's, of a block
     static constexpr int STAGE = KEYS * D * 2;                         // bytes, of keys or of values
@@ -61,9 +62,12 @@ struct Cc {
     static constexpr int K = 0, V = ST * STAGE, Q = 2 * ST * STAGE, BARS = Q + (QS ? T * Q_TILE : 0);
     // barriers: keys full, empty, values full, empty (ST each); S full and P ready (T NB each); query rows ready, a second
     // product done, a piece's last one done (T each); end
-    static constexpr int NBARS = 4 * ST + 2 * T * NB + 3 * T + 1;
-    static constexpr int SCAN = BARS + 8 * NBARS, TMEM = SCAN + 16 * (WARPS_ALL + 1), START = TMEM + 16;
-    static constexpr int BYTES = 1024 + START + 64;
+    // and of the list of pieces, full and empty (LIST each)
+    static constexpr int LIST = 4;
+    static constexpr int NBARS = 4 * ST + 2 * T * NB + 3 * T + 1 + 2 * LIST;
+    static constexpr int SCAN = BARS + 8 * NBARS, TMEM = SCAN + 16 * (WARPS_ALL + 1), START = TMEM + 16, PIECES = START + 16;
+    static constexpr int OUT = (PIECES + LIST * 64 + 127) / 128 * 128;         // 128 bytes of a row, per thread of the softmax
+    static constexpr int BYTES = 1024 + OUT + SW * 32 * 128;
     static constexpr size_t SMEM = BYTES > 120 * 1024 ? BYTES : 120 * 1024;      // one CTA per SM: all of the TMEM
     static constexpr int O_COL = 0, Q_COL = T * D, S_COL = QS ? Q_COL : Q_COL + T * D / 2;
     static_assert(S_COL + T * NB * KB <= 512, "TMEM");
@@ -90,7 +94,15 @@ struct ChunkParams : AttnParams {
     const int32_t *starts;
     int rows;                          // in all
     sk::Div by_g;
-    int4 *join;                        // per CTA: parts of the tile whose first part is its last, head, sequence, tile
+    int whole;                         // every tile is one CTA's (and costs the same)
+    int4 *join;                        // of a tile in parts: first CTA, parts (0: whole), and which: head, sequence and tile ...
+    int by_tile;                       // ... at its number, or else at its first CTA's
+    int *tiles;                        // tiles of a head
+};
+struct Join {
+    static __device__ __forceinline__ int4 of(int first, int parts, int h, int b, int t) {
+        return make_int4(first, parts | h << 16, b, t);
+    }
 };
 
 // Rows of sequence b: [first, first + n), and its positions.
@@ -132,18 +144,22 @@ struct Tile {
         lim1 -= skip * sk::KV4_REC;
         blocks = (max(lim1, 0) + KB - 1) / KB;
         per = C::T == 2 && count > 128 ? 3 : 2;
-        cost = (blocks + SETUP) * per;
+        cost = p.whole ? 1 : (blocks + SETUP) * per;
     }
-    __device__ __forceinline__ int block_at(int x) const { return min(max(x / per - SETUP, 0), blocks); }
+    __device__ __forceinline__ int block_at(int x) const {
+        return x == cost ? blocks : min(max(x / per - SETUP, 0), blocks);
+    }
 };
 
-// A piece of work: blocks [k0, k1) of a tile of sequence b and kv head h.
-template <int D>
+// A piece of work: blocks [k0, k1) of a tile of sequence b and kv head h; k1 < 0: the
+// end. One warp lists a CTA's pieces, the others read them from shared memory.
 struct Piece {
-    int h, b, t, k0, k1;
-    Seq seq;
-    Tile<D> tile;
+    int k0, k1, blocks, h, b;
+    int row0, idx0, count;             // the sequence's first row; of its list of rows, the tile's first and how many
+    int lim0, lim1, gap, skip;         // as in Tile
+    int pad[4];
 };
+static_assert(sizeof(Piece) == 64, "read in 16-byte words");
 
 // The pieces of a CTA, in order. All (head, sequence, tile) cost a total that
 // P CTAs take in equal parts, whatever the lengths; a tile that two of them share
@@ -152,50 +168,144 @@ template <int D>
 struct Pieces {
     long long left;                    // of this CTA's share
     int h, b, t, x;                    // where it stands: x into the cost of the tile
-    __device__ __forceinline__ bool next(const ChunkParams &p, Piece<D> &w) {
+    int number;                        // the tile's among those of a head
+    Seq seq;                           // of sequence `held`
+    int held;
+    __device__ __forceinline__ bool next(const ChunkParams &p, Piece &w, int &tile_t, int &tile_number, int &cost) {
         while (left > 0 && h < p.heads) {
             if (b >= p.B) {
                 b = 0;
                 t = 0;
+                number = 0;
                 ++h;
                 continue;
             }
-            w.seq = Seq(p, b);
-            if (t >= tiles_in<D>(p, w.seq)) {
+            if (held != b) {
+                seq = Seq(p, b);
+                held = b;
+            }
+            if (t >= tiles_in<D>(p, seq)) {
                 ++b;
                 t = 0;
                 continue;
             }
-            w.tile = Tile<D>(p, w.seq, t);
-            const int x1 = int(min((long long)w.tile.cost, x + left));
+            const Tile<D> tile(p, seq, t);
+            const int x1 = int(min((long long)tile.cost, x + left));
+            w.k0 = tile.block_at(x);
+            w.k1 = tile.block_at(x1);
+            w.blocks = tile.blocks;
             w.h = h;
             w.b = b;
-            w.t = t;
-            w.k0 = w.tile.block_at(x);
-            w.k1 = w.tile.block_at(x1);
-            const bool last = x1 == w.tile.cost;
+            w.row0 = seq.first;
+            w.idx0 = tile.idx0;
+            w.count = tile.count;
+            w.lim0 = tile.lim0;
+            w.lim1 = tile.lim1;
+            w.gap = tile.gap;
+            w.skip = tile.skip;
+            tile_t = t;
+            tile_number = number;
+            cost = tile.cost;
+            const bool last = x1 == tile.cost;
             left -= x1 - x;
             x = last ? 0 : x1;
             t += last;
-            if (w.k1 > w.k0 || (last && w.tile.blocks == 0)) return true;
+            number += last;
+            if (w.k1 > w.k0 || (last && tile.blocks == 0)) return true;
         }
         return false;
     }
 };
 
-struct Share2 {
+// a / b, where both are small by the shorter division.
+__device__ __forceinline__ long long divided(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (unsigned int)a / (unsigned int)b;
+    return a / b;
+}
+struct Split {
     long long total;                   // over all heads
     int parts;
 };
-__device__ __forceinline__ long long bound_of(const Share2 &s, int c) { return s.total * c / s.parts; }
-__device__ __forceinline__ int owner_of(const Share2 &s, long long u) { return int(((u + 1) * s.parts - 1) / s.total); }
+__device__ __forceinline__ long long bound_of(const Split &s, int c) { return divided(s.total * c, s.parts); }
+__device__ __forceinline__ int owner_of(const Split &s, long long u) { return int(divided((u + 1) * s.parts - 1, s.total)); }
 
-// Where this CTA's share begins. Every thread of the CTA comes here; `list` holds
-// p.B + 1 numbers, `scan` one per warp and one more.
+// Where this CTA's share begins. With up to FEW sequences one warp comes here, else
+// every thread of the CTA; `list` holds p.B + 1 numbers, `scan` one per warp.
+constexpr int FEW = 32;
 template <int D>
-__device__ Share2 find_share(const ChunkParams &p, Pieces<D> &w, int *list, long long *scan, int *start) {
+__device__ Split find_share(const ChunkParams &p, Pieces<D> &w, int *list, long long *scan, int *start, int &tiles_of_head) {
     using C = Cc<D>;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, me = worker<D>();
+    w.left = 0;
+    w.h = w.b = w.t = w.x = w.number = 0;
+    w.held = -1;
+    // (no part of a tile in parts is empty: MIN_SHARE)
+    auto split = [&](long long per_head) {
+        Split sh;
+        sh.total = per_head * p.heads;
+        sh.parts = int(max(1LL, min(p.whole ? sh.total : divided(sh.total, MIN_SHARE), (long long)p.ctas)));
+        return sh;
+    };
+    if (p.B <= FEW) {
+        // a lane a sequence, then a lane a tile
+        Seq s;
+        s.first = s.n = s.len = 0;
+        if (lane < p.B) s = Seq(p, lane);
+        const int n = tiles_in<D>(p, s), upto = inclusive_scan(n, lane), tiles = __shfl_sync(0xffffffffu, upto, 31);
+        tiles_of_head = tiles;
+        {
+            auto at = [&](int i, int &b, int &t, Seq &of) {        // tile i: all lanes come here
+                b = 0;
+                int before = 0;
+                for (int k = 0; k < p.B; ++k) {
+                    const int u = __shfl_sync(0xffffffffu, upto, k);
+                    if (u <= i) {
+                        b = k + 1;
+                        before = u;
+                    }
+                }
+                t = i - before;
+                const int from = min(b, 31);
+                of.first = __shfl_sync(0xffffffffu, s.first, from);
+                of.n = __shfl_sync(0xffffffffu, s.n, from);
+                of.len = __shfl_sync(0xffffffffu, s.len, from);
+            };
+            long long per_head = 0;
+            int b, t;
+            Seq of;
+            for (int i0 = 0; i0 < tiles; i0 += 32) {
+                at(min(i0 + lane, tiles - 1), b, t, of);
+                int cost = i0 + lane < tiles ? Tile<D>(p, of, t).cost : 0;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
+                per_head += cost;
+            }
+            const Split sh = split(per_head);
+            if (me >= sh.parts || sh.total == 0) return sh;
+            const long long u0 = bound_of(sh, me);
+            w.left = bound_of(sh, me + 1) - u0;
+            w.h = int(divided(u0, per_head));
+            long long off = u0 - w.h * per_head;
+            for (int i0 = 0; i0 < tiles; i0 += 32) {
+                at(min(i0 + lane, tiles - 1), b, t, of);
+                const int cost = i0 + lane < tiles ? Tile<D>(p, of, t).cost : 0, x = inclusive_scan(cost, lane);
+                const unsigned int past = __ballot_sync(0xffffffffu, x > off);
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    w.b = w.held = __shfl_sync(0xffffffffu, b, l);
+                    w.t = __shfl_sync(0xffffffffu, t, l);
+                    w.x = int(off) - __shfl_sync(0xffffffffu, x - cost, l);
+                    w.number = i0 + l;
+                    w.seq.first = __shfl_sync(0xffffffffu, of.first, l);
+                    w.seq.n = __shfl_sync(0xffffffffu, of.n, l);
+                    w.seq.len = __shfl_sync(0xffffffffu, of.len, l);
+                    break;
+                }
+                off -= __shfl_sync(0xffffffffu, x, 31);
+            }
+            return sh;
+        }
+    }
     auto scanned = [&](long long mine, long long &total) {         // exclusive, over the CTA
         long long v = mine;
 #pragma unroll
@@ -206,13 +316,15 @@ __device__ Share2 find_share(const ChunkParams &p, Pieces<D> &w, int *list, long
         __syncthreads();
         if (lane == 31) scan[wid] = v;
         __syncthreads();
-        long long before = 0;
-        total = 0;
-        for (int i = 0; i < C::WARPS_ALL; ++i) {
-            if (i < wid) before += scan[i];
-            total += scan[i];
+        long long w = lane < C::WARPS_ALL ? scan[lane] : 0;
+        const long long own = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
         }
-        return before + v - mine;
+        total = __shfl_sync(0xffffffffu, w, 31);
+        return __shfl_sync(0xffffffffu, w - own, wid) + v - mine;
     };
     // tiles before each sequence
     const int each_b = (p.B + C::CT_ALL - 1) / C::CT_ALL, b_lo = min(p.B, tid * each_b), b_hi = min(p.B, b_lo + each_b);
@@ -226,8 +338,9 @@ __device__ Share2 find_share(const ChunkParams &p, Pieces<D> &w, int *list, long
     if (tid == 0) {
         list[p.B] = int(tiles);
         start[0] = p.B;
-        start[1] = start[2] = 0;
+        start[1] = start[2] = start[3] = 0;
     }
+    tiles_of_head = int(tiles);
     __syncthreads();
     // this thread's tiles: [lo, hi)
     const int each = int((tiles + C::CT_ALL - 1) / C::CT_ALL), lo = int(min(tiles, (long long)tid * each)),
@@ -258,15 +371,11 @@ __device__ Share2 find_share(const ChunkParams &p, Pieces<D> &w, int *list, long
     });
     long long per_head;
     const long long before = scanned(mine, per_head);
-    Share2 sh;
-    sh.total = per_head * p.heads;
-    sh.parts = int(max(1LL, min(sh.total / MIN_SHARE, (long long)p.ctas)));
-    w.left = 0;
-    w.h = w.b = w.t = w.x = 0;
+    const Split sh = split(per_head);
     if (me < sh.parts && sh.total > 0) {
         const long long u0 = bound_of(sh, me);
         w.left = bound_of(sh, me + 1) - u0;
-        w.h = int(u0 / per_head);
+        w.h = int(divided(u0, per_head));
         long long off = u0 - w.h * per_head;
         if (off >= before && off < before + mine) {
             off -= before;
@@ -275,6 +384,7 @@ __device__ Share2 find_share(const ChunkParams &p, Pieces<D> &w, int *list, long
                     start[0] = b;
                     start[1] = t;
                     start[2] = int(off);
+                    start[3] = list[b] + t;
                     return false;
                 }
                 off -= cost;
@@ -286,6 +396,7 @@ __device__ Share2 find_share(const ChunkParams &p, Pieces<D> &w, int *list, long
     w.b = start[0];
     w.t = start[1];
     w.x = start[2];
+    w.number = start[3];
     __syncthreads();                                               // the list's place is free
     return sh;
 }
@@ -451,7 +562,8 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
     const uint32_t bars = base + C::BARS;
     const uint32_t k_full = bars, k_empty = k_full + 8 * ST, v_full = k_empty + 8 * ST, v_empty = v_full + 8 * ST,
                    s_full = v_empty + 8 * ST, p_ready = s_full + 8 * T * NB, q_ready = p_ready + 8 * T * NB,
-                   o_done = q_ready + 8 * T, o_end = o_done + 8 * T, end = o_end + 8 * T;
+                   o_done = q_ready + 8 * T, o_end = o_done + 8 * T, end = o_end + 8 * T,
+                   l_full = end + 8, l_empty = l_full + 8 * C::LIST;
 
     const int rank = C::PAIR ? int(sk::cluster_rank()) : 0;
     if (warp == 0) t5::alloc<C::PAIR>(base + C::TMEM, 512);
@@ -472,6 +584,10 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             sk::mbar_init(o_end + 8 * i, 1);
         }
         sk::mbar_init(end, 1);
+        for (int i = 0; i < C::LIST; ++i) {
+            sk::mbar_init(l_full + 8 * i, 1);
+            sk::mbar_init(l_empty + 8 * i, C::SW + C::DW + 1);
+        }
         sk::fence_barrier_init();
     }
     __syncwarp();
@@ -483,8 +599,12 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
     sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
     Pieces<D> work;
-    const Share2 share = find_share<D>(p, work, reinterpret_cast<int *>(smem), reinterpret_cast<long long *>(smem + C::SCAN),
-                                       reinterpret_cast<int *>(smem + C::START));
+    Split share;
+    int tiles;
+    const bool lister = warp == C::WARPS_ALL - 1;
+    if (p.B > FEW || lister)
+        share = find_share<D>(p, work, reinterpret_cast<int *>(smem), reinterpret_cast<long long *>(smem + C::SCAN),
+                              reinterpret_cast<int *>(smem + C::START), tiles);
     bool dead = false;
     // Waits for a barrier's phase of this parity, a second at most; after one that
     // ran out the thread waits no more.
@@ -492,6 +612,17 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         if (dead || t5::wait_spin(bar, parity)) return;
         dead = true;
         atomicOr(p.err, 1u);
+    };
+    // This warp's or thread's way through the list: the place of its next piece.
+    const Piece *const list = reinterpret_cast<const Piece *>(smem + C::PIECES);
+    uint32_t at = 0, lap = 0;
+    auto here = [&] { wait(l_full + 8 * at, lap); };
+    auto leave = [&](bool one) {       // by one thread, when no other of those it stands for reads the piece any more
+        if (one) sk::mbar_arrive(l_empty + 8 * at);
+        if (++at == C::LIST) {
+            at = 0;
+            lap ^= 1u;
+        }
     };
     // Arrive at a barrier that the products wait at: the first CTA's.
     auto arrive = [&](uint32_t bar) {
@@ -507,66 +638,66 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         const uint32_t o_at = mine + C::O_COL + t * D, q_at = mine + C::Q_COL + t * (D / 2),
                        s_at = mine + C::S_COL + t * NB * KB;
         uint32_t blocks_done = 0, ends = 0;                  // blocks of this tile so far, and pieces
-        int last_join = 0;                                   // whether a tile's first part, not its last, was this CTA's
-        Piece<D> w;
-        // the piece's query rows of this tile, to TMEM; the products of the piece before it with its own are done
-        auto load_q = [&] {
+        // A piece's query rows of this tile, to TMEM (or shared memory); the products of the piece before it with its own
+        // are done.
+        auto load_q = [&](const Piece &w) {
             // (a pair's products take both CTAs' rows, also where the second has none)
-            if ((!C::PAIR && first >= w.tile.count) || w.k1 == w.k0) return;
-            const int idx = w.tile.idx0 + first + row, i = sk::quotient(idx, p.by_g);
-            const bool there = first + row < w.tile.count;
-            const __half *src = p.q + (w.seq.first + i) * p.q_stride + (long long)(w.h * p.G + idx - i * p.G) * D;
-            if constexpr (C::QS) {
-                const uint32_t to = base + C::Q + t * C::Q_TILE + row * 128;
+            if ((!C::PAIR && first >= w.count) || w.k1 <= w.k0) return;
+            const int idx = w.idx0 + first + row, i = sk::quotient(idx, p.by_g);
+            const bool there = first + row < w.count;
+            const __half *src = p.q + (w.row0 + i) * p.q_stride + (long long)(w.h * p.G + idx - i * p.G) * D;
+            constexpr int AT = D < 128 ? D / 8 : 16;         // 16-byte loads in flight
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    uint4 x[8];
+            for (int c = 0; c < D / 8; c += AT) {
+                uint4 x[AT];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[e] = there ? *reinterpret_cast<const uint4 *>(src + c * 64 + e * 8) : make_uint4(0u, 0u, 0u, 0u);
+                for (int e = 0; e < AT; ++e)
+                    x[e] = there ? *reinterpret_cast<const uint4 *>(src + (c + e) * 8) : make_uint4(0u, 0u, 0u, 0u);
+                __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t d[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
-                        st_shared_v4(to + c * C::Q_SLAB + ((e ^ (row & 7)) << 4), d);
+                for (int e = 0; e < AT; e += 8) {            // 64 components
+                    if constexpr (C::QS) {
+                        const uint32_t to = base + C::Q + t * C::Q_TILE + (c + e) / 8 * C::Q_SLAB + row * 128;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t d[4] = {x[e + i].x, x[e + i].y, x[e + i].z, x[e + i].w};
+                            st_shared_v4(to + ((i ^ (row & 7)) << 4), d);
+                        }
+                    } else {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            v[4 * i] = x[e + i].x;
+                            v[4 * i + 1] = x[e + i].y;
+                            v[4 * i + 2] = x[e + i].z;
+                            v[4 * i + 3] = x[e + i].w;
+                        }
+                        t5::st32(q_at + (c + e) * 4, v);
                     }
                 }
-                t5::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive(q_ready + 8 * t);
-                return;
             }
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                uint32_t v[32];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (there) x = *reinterpret_cast<const uint4 *>(src + c * 64 + e * 8);
-                    v[4 * e] = x.x;
-                    v[4 * e + 1] = x.y;
-                    v[4 * e + 2] = x.z;
-                    v[4 * e + 3] = x.w;
-                }
-                __syncwarp();
-                t5::st32(q_at + c * 32, v);
-            }
-            t5::wait_st();
+            if constexpr (C::QS) t5::fence_async_smem();
+            else t5::wait_st();
             t5::fence_before();
             __syncwarp();
             if (lane == 0) arrive(q_ready + 8 * t);
         };
-        bool have = work.next(p, w);
-        if (have) load_q();
-        while (have) {
-            const bool active = C::PAIR || first < w.tile.count, there = first + row < w.tile.count;
+        here();
+        __syncwarp();
+        load_q(list[at]);
+        // (a wait that ran out ends every role's way: what is listed after it may be an earlier lap's)
+        while (!__any_sync(0xffffffffu, dead) && list[at].k1 >= 0) {
+            const Piece &w = list[at];
             const int n = w.k1 - w.k0;
+            const bool active = C::PAIR || first < w.count;
             float t0 = 0.f, most = -FLT_MAX;                 // the row's base, and what moves it (at first: any score)
             uint64_t sum = two(0.f, 0.f);
             if (active && n > 0) {
-                const int i = sk::quotient(w.tile.idx0 + first + row, p.by_g);
-                const int lim = there ? w.tile.lim0 + i - sk::quotient(w.tile.idx0, p.by_g) : 0;
+                const int i = sk::quotient(w.idx0 + first + row, p.by_g);
+                const int lim = first + row < w.count ? w.lim0 + i - sk::quotient(w.idx0, p.by_g) : 0;
                 const int low = p.window ? lim - p.window : 0;
-                const int lim0 = w.tile.lim0, low1 = p.window ? w.tile.lim1 - p.window : 0;
+                const int lim0 = w.lim0, low1 = p.window ? w.lim1 - p.window : 0;
+                int pos = w.k0 * KB;
                 for (int j = 0; j < n; ++j) {
                     const uint32_t sb = blocks_done & 1u;
                     const uint32_t s_col = s_at + sb * KB;
@@ -579,7 +710,6 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     t5::ld32(s_col + 32, s + 32);
                     t5::wait_ld();
                     t5::held<KB>(s);
-                    const int pos = (w.k0 + j) * KB;
                     if (pos + KB > lim0 || (pos + KB > p.sinks && pos < low1)) {
 #pragma unroll
                         for (int e = 0; e < KB; ++e)
@@ -635,15 +765,17 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     t5::fence_before();
                     __syncwarp();
                     if (lane == 0) arrive(p_ready + 8 * (t * NB + sb));
+                    pos += KB;
                 }
             }
             // The next piece's query rows first: its scores are formed beside this one's end.
-            const Piece<D> was = w;
-            have = work.next(p, w);
-            if (have) load_q();
+            const uint32_t after = at + 1 == C::LIST ? 0 : at + 1;
+            wait(l_full + 8 * after, after ? lap : lap ^ 1u);
+            __syncwarp();
+            load_q(list[after]);
             // ---- the rows' outputs, or their part of them
-            const bool whole = was.k0 == 0 && was.k1 == was.tile.blocks;
-            const size_t slot = size_t(worker<D>()) * 2 + (was.k0 == 0 ? 1 : 0);
+            const bool whole = w.k0 == 0 && w.k1 == w.blocks, there = first + row < w.count;
+            const size_t slot = size_t(worker<D>()) * 2 + (w.k0 == 0 ? 1 : 0);
             if (active) {
                 if (n > 0) {
                     wait(o_end + 8 * t, ends++ & 1u);
@@ -652,11 +784,18 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 }
                 const float2 ll = apart(sum);
                 const float l = ll.x + ll.y, f = l == 0.f ? 0.f : p.vg / l;
-                const int idx = was.tile.idx0 + first + row, i = sk::quotient(idx, p.by_g);
-                const long long at = (long long)(was.seq.first + i) * (p.heads * p.G) + was.h * p.G + idx - i * p.G;
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
+                const int idx = w.idx0 + first + row, i = sk::quotient(idx, p.by_g);
+                const int to = (w.row0 + i) * (p.heads * p.G) + w.h * p.G + idx - i * p.G;      // (rows by 31 bits)
+                // 128 bytes of every row at a time, turned in shared memory so that eight lanes store them: 64 components
+                // of the output, or 32 of a part of it (a lane a row, a store meets 32 lines: 6000 clocks a tile of 256
+                // components, this way a third)
+                const uint32_t room = base + C::OUT + warp * 4096;
+                const int rows = min(32, w.count - first - (warp & 3) * 32);
+                auto put = [&](int piece, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+                    const uint32_t v[4] = {a, b, c, d};
+                    st_shared_v4(room + lane * 128 + ((piece ^ (lane & 7)) << 4), v);
+                };
+                auto columns = [&](int c, float *o) {
                     if (n > 0) {
                         t5::ld32(o_at + c, o);
                         t5::wait_ld();
@@ -665,36 +804,60 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = 0.f;
                     }
-                    if (!there) {
-                    } else if (whole) {
+                };
+                const int r0 = lane >> 3, piece = lane & 7;
+                if (whole) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 64) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4 *>(p.out + at * D + c + e) =
-                                make_uint4(pack_f16(o[e] * f, o[e + 1] * f), pack_f16(o[e + 2] * f, o[e + 3] * f),
-                                           pack_f16(o[e + 4] * f, o[e + 5] * f), pack_f16(o[e + 6] * f, o[e + 7] * f));
-                    } else {
-                        float *to = p.part_o + (slot * C::ROWS + first + row) * D + c;
+                        for (int hf = 0; hf < 2; ++hf) {
+                            float o[32];
+                            columns(c + 32 * hf, o);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+                                put(4 * hf + e / 8, pack_f16(o[e] * f, o[e + 1] * f), pack_f16(o[e + 2] * f, o[e + 3] * f),
+                                    pack_f16(o[e + 4] * f, o[e + 5] * f), pack_f16(o[e + 6] * f, o[e + 7] * f));
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const int r = 4 * x + r0;
+                            const uint4 v = sk::ld_shared_v4(room + r * 128 + ((piece ^ (r & 7)) << 4));
+                            const int its = __shfl_sync(0xffffffffu, to, r);
+                            if (r < rows) *reinterpret_cast<uint4 *>(p.out + (long long)its * D + c + piece * 8) = v;
+                        }
+                        __syncwarp();
+                    }
+                } else {
+                    float *part = p.part_o + (slot * C::ROWS + first + (warp & 3) * 32) * D;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        columns(c, o);
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(to + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            put(e / 4, __float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
+                                __float_as_uint(o[e + 3]));
+                        __syncwarp();
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const int r = 4 * x + r0;
+                            const uint4 v = sk::ld_shared_v4(room + r * 128 + ((piece ^ (r & 7)) << 4));
+                            if (r < rows) *reinterpret_cast<uint4 *>(part + r * D + c + piece * 4) = v;
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
                 if (there) {
-                    if (whole) write_lse(p, at, t0, l);
+                    if (whole) write_lse(p, to, t0, l);
                     else
                         *reinterpret_cast<float2 *>(p.part_ml + (slot * C::ROWS + first + row) * 2) = make_float2(t0, l);
                 }
             }
-            if (tid == 0 && rank == 0 && was.k0 == 0 && !whole) {
-                // This CTA's last piece: its share ends within the tile, whose last unit tells the last part's owner.
-                const int me = worker<D>(), c1 = owner_of(share, bound_of(share, me + 1) + (was.tile.cost - work.x) - 1);
-                p.join[me] = make_int4(c1 - me + 1, was.h, was.b, was.t);
-                last_join = 1;
-            }
             t5::fence_before();
+            __syncwarp();
+            leave(lane == 0);
         }
-        if (tid == 0 && rank == 0 && !last_join) p.join[worker<D>()] = make_int4(0, 0, 0, 0);
     } else if (warp < C::SW + C::DW) {
         // ------------------------------------------------------- decoding
         // One stream of blocks over all pieces, of keys for the one half of the warps and of values for the other (a
@@ -709,25 +872,32 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         else key_offsets<D>(w, lane, to);
         uint32_t codes_at, scales_at;
         source_offsets<D>(value, w, lane, rank, codes_at, scales_at);
-        Piece<D> piece;
-        int j = 0, n = 0, last = 0;
+        int block = 0, end_block = 0, last = 0, gap = 0, skip = 0, next_head = 0;
         const int32_t *table = p.table;
         int entry = 0, in_page = 0, head = 0;                // of the block looked up: the page and the record in it that this
                                                              // lane asked for (used only when fetched: the load has time)
         auto look_up = [&] {                                 // the next block's records; false after the last block
-            while (j == n) {
-                if (!work.next(p, piece)) return false;
-                j = 0;
-                n = piece.k1 - piece.k0;
-                table = p.table + (long long)piece.b * p.width;
-                last = max(0, (piece.tile.lim1 + sk::KV4_REC - 1) / sk::KV4_REC - 1);
+            while (block == end_block) {
+                here();
+                __syncwarp();
+                const Piece &w = list[at];
+                if (__any_sync(0xffffffffu, dead) || w.k1 < 0) return false;
+                block = w.k0;
+                end_block = w.k1;
+                table = p.table + (long long)w.b * p.width;
+                last = max(0, (w.lim1 + sk::KV4_REC - 1) / sk::KV4_REC - 1);
+                gap = w.gap;
+                skip = w.skip;
+                next_head = w.h;
+                __syncwarp();
+                leave(lane == 0);
             }
-            const int v = min((piece.k0 + j) * (KB / sk::KV4_REC) + (lane & 3), last);
-            const int r = v >= piece.tile.gap ? v + piece.tile.skip : v, pg = sk::quotient(r, p.by_recs);
+            const int v = min(block * (KB / sk::KV4_REC) + (lane & 3), last);
+            const int r = v >= gap ? v + skip : v, pg = sk::quotient(r, p.by_recs);
             entry = table[pg];
             in_page = r - pg * p.recs;
-            head = piece.h;
-            ++j;
+            head = next_head;
+            ++block;
             return true;
         };
         auto fetch = [&](Raw<D> &raw) {
@@ -777,12 +947,20 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 }
             }
         }
-    } else {
+    } else if (warp == C::SW + C::DW) {
         // ------------------------------------------------------- products
         // One elected lane: what it issues takes its operands from uniform registers (from a lane chosen by number a
         // product of 64 columns takes 45 clocks to issue, of the 32 it runs). Stages, parities and operands are carried
         // along: a lone warp's instructions are ten clocks apart, and a block's turn here is on everyone's path.
-        if (rank == 0 && t5::elect()) {
+        if (rank != 0) {
+            while (true) {             // (the first CTA's thread reads the pieces that this one lists)
+                here();
+                __syncwarp();
+                if (__any_sync(0xffffffffu, dead) || list[at].k1 < 0) break;
+                __syncwarp();
+                leave(lane == 0);
+            }
+        } else if (t5::elect()) {
             constexpr uint64_t STEP = C::STAGE / 16;
             auto wait = [&](uint32_t bar, uint32_t parity) {
                 if (dead || t5::wait_spin<C::PAIR>(bar, parity)) return;
@@ -832,10 +1010,13 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 t5::commit<C::PAIR>(o_done + 8 * t);
                 if (last) t5::commit<C::PAIR>(o_end + 8 * t);
             };
-            Piece<D> piece;
-            while (work.next(p, piece)) {
-                const int n = piece.k1 - piece.k0;
-                const bool two = T == 2 && piece.tile.count > 128;
+            while (true) {
+                wait(l_full + 8 * at, lap);
+                if (dead) break;
+                const int k1 = list[at].k1, n = k1 - list[at].k0;
+                const bool two = T == 2 && list[at].count > 128;
+                if (k1 < 0) break;
+                leave(true);
                 if (n == 0) continue;
                 wait(q_ready, pieces[0]++ & 1u);
                 if (two) wait(q_ready + 8, pieces[1]++ & 1u);
@@ -860,6 +1041,43 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             t5::wait_spin(end, 0);
         }
         __syncwarp();
+    } else {
+        // ------------------------------------------------------- the list
+        if (lane == 0 && blockIdx.x == 0) *p.tiles = tiles;
+        Piece w;
+        int t = 0, number = 0, cost = 0, last_join = 0;
+        const int me = worker<D>();
+        for (bool more = true; more && !__any_sync(0xffffffffu, dead);) {
+            more = work.next(p, w, t, number, cost);
+            if (!more) w.k1 = -1;
+            if (more && rank == 0 && !p.whole && w.k0 == 0) {
+                // A tile in parts is this CTA's last piece: its share ends within it, and the tile's last unit tells the last
+                // part's owner.
+                int parts = 0;
+                if (w.k1 != w.blocks) parts = owner_of(share, bound_of(share, me + 1) + (cost - work.x) - 1) - me + 1;
+                if (lane == 0) {
+                    if (p.by_tile) p.join[w.h * tiles + number] = Join::of(me, parts, w.h, w.b, t);
+                    else if (parts) p.join[me] = Join::of(me, parts, w.h, w.b, t);
+                }
+                last_join |= parts;
+            }
+            // (a piece may take longer than any other wait)
+            if (!dead && !t5::wait_spin(l_empty + 8 * at, lap ^ 1u, 60)) {
+                dead = true;
+                atomicOr(p.err, 1u);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                *reinterpret_cast<Piece *>(smem + C::PIECES + at * 64) = w;
+                sk::mbar_arrive(l_full + 8 * at);
+            }
+            if (++at == C::LIST) {
+                at = 0;
+                lap ^= 1u;
+            }
+        }
+        if (lane == 0 && rank == 0 && !p.by_tile && !last_join) p.join[me] = Join::of(0, 0, 0, 0, 0);
+        __syncwarp();
     }
     if constexpr (C::PAIR) {
         // neither CTA leaves while the other, or a product's end, may arrive at its barriers
@@ -875,24 +1093,25 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
     if (warp == 0) t5::free<C::PAIR>(tmem, 512);
 }
 
-// The tiles that several CTAs had parts of: CTA (c, y) joins eight rows of the
-// tile whose first part is CTA c's, a warp a row, in the order of the parts.
+// The tiles that several CTAs had parts of: CTA (c, y) joins eight rows of a tile, a
+// warp a row, in the order of the parts.
 constexpr int JT = 256;
 template <int D>
 __global__ void __launch_bounds__(JT) kv4_chunk_join_kernel(const __grid_constant__ ChunkParams p) {
     using C = Cc<D>;
     constexpr int PER = D / 32;
     sk::pdl_wait_primary();
+    if (p.by_tile && int(blockIdx.x) >= *p.tiles * p.heads) return;
     const int4 seg = p.join[blockIdx.x];
-    if (seg.x == 0) return;
+    const int n = seg.y & 0xFFFF, h = seg.y >> 16;
+    if (n == 0) return;
     const Seq s(p, seg.z);
     const Tile<D> tile(p, s, seg.w);
     const int lane = threadIdx.x & 31, r = blockIdx.y * (JT / 32) + (threadIdx.x >> 5);
     if (r >= tile.count) return;
     const int idx = tile.idx0 + r, i = sk::quotient(idx, p.by_g);
-    const long long at = (long long)(s.first + i) * (p.heads * p.G) + seg.y * p.G + idx - i * p.G;
-    const int n = seg.x;
-    auto slot = [&](int k) { return (size_t(blockIdx.x) + k) * 2 + (k == 0 ? 1 : 0); };
+    const long long at = (long long)(s.first + i) * (p.heads * p.G) + h * p.G + idx - i * p.G;
+    auto slot = [&](int k) { return (size_t(seg.x) + k) * 2 + (k == 0 ? 1 : 0); };
     float top = NEG_INF, l = 0.f, v[PER];
 #pragma unroll
     for (int x = 0; x < PER; ++x) v[x] = 0.f;
@@ -938,8 +1157,15 @@ sk_status run(ChunkParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     if (p.B > C::MOST_SEQS) return SK_ERR_UNSUPPORTED_SHAPE;
     p.ctas = C::PAIR ? sms / 2 : sms;
     if (p.ctas < 1) return SK_ERR_CUDA;
-    p.join = reinterpret_cast<int4 *>(scratch);
-    p.part_ml = reinterpret_cast<float *>(scratch + (size_t(p.ctas) * sizeof(int4) + 255) / 256 * 256);
+    // No more tiles than these, and no more blocks in one.
+    const long long list = (long long)p.rows * p.G, tiles = ((list + C::ROWS - 1) / C::ROWS + (p.B < p.rows ? p.B : p.rows)) * p.heads;
+    const long long seen = p.window ? (long long)p.window + p.sinks + list / p.G + 2 * sk::KV4_REC : p.cap;
+    const long long blocks = ((seen < p.cap ? seen : p.cap) + KB - 1) / KB;
+    p.whole = tiles <= p.ctas && blocks <= WHOLE_BLOCKS;
+    p.by_tile = tiles <= p.ctas;
+    p.tiles = reinterpret_cast<int *>(scratch);
+    p.join = reinterpret_cast<int4 *>(scratch + 256);
+    p.part_ml = reinterpret_cast<float *>(scratch + 256 + (size_t(p.ctas) * sizeof(int4) + 255) / 256 * 256);
     p.part_o = p.part_ml + size_t(p.ctas) * 2 * C::ROWS * 2;
     if (size_t(reinterpret_cast<unsigned char *>(p.part_o + size_t(p.ctas) * 2 * C::ROWS * D) - scratch) > sk::SCRATCH_BYTES)
         return SK_ERR_WORKSPACE;
@@ -948,7 +1174,10 @@ sk_status run(ChunkParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     if (sk::launch_pdl_cluster(kv4_chunk_kernel<D>, cluster, dim3(unsigned(p.ctas * cluster)), dim3(C::CT_ALL), C::SMEM, s, p) !=
         cudaSuccess)
         return SK_ERR_CUDA;
-    return sk::launch_pdl(kv4_chunk_join_kernel<D>, dim3(unsigned(p.ctas), C::ROWS / (JT / 32)), dim3(JT), 0, s, p) == cudaSuccess
+    if (p.whole) return SK_OK;
+    const unsigned int rows = unsigned(list < C::ROWS ? list : C::ROWS);
+    return sk::launch_pdl(kv4_chunk_join_kernel<D>, dim3(unsigned(p.by_tile ? tiles : p.ctas), (rows + JT / 32 - 1) / (JT / 32)),
+                          dim3(JT), 0, s, p) == cudaSuccess
                ? SK_OK
                : SK_ERR_CUDA;
 }

@@ -114,12 +114,12 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t *v) {
                  "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(addr) : "memory");
 }
 
-// Wait until `bar`'s phase of this parity is complete, for a second at most. The
+// Wait until `bar`'s phase of this parity is complete, for so many seconds at most. The
 // clock is read every 1024 tries: read after every one (as where a wait is rare),
 // its latency is added to each wait that is not over at once.
 // CLUSTER: for what the cluster's other CTA did before it arrived.
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool wait_spin(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_spin(uint32_t bar, uint32_t parity, uint64_t seconds = 1) {
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
         if constexpr (CLUSTER) {
@@ -133,7 +133,7 @@ __device__ __forceinline__ bool wait_spin(uint32_t bar, uint32_t parity) {
         if (i % 1024 == 0) {
             const uint64_t t = globaltimer_ns();
             if (t0 == 0) t0 = t;
-            else if (t - t0 > 1000000000ull) return false;
+            else if (t - t0 > seconds * 1000000000ull) return false;
         }
     }
 }

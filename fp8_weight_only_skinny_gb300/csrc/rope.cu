@@ -354,7 +354,8 @@ __device__ __forceinline__ void append(const RopeParams &p, const Lane<D, INTER>
         const float u = (p.kw ? 24.f : 12.f) * 0x1p-24f * r * fmaxf(1.f, fabsf(float(p.amplitude)));
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            y[e] = fmaf(x[e], cw[e], xp[e] * sw[e]) * r;
+            // (a component that is not turned keeps the sign of its zero)
+            y[e] = (ln.rotated ? fmaf(x[e], cw[e], xp[e] * sw[e]) : x[e] * cw[e]) * r;
             const float mw = p.kw ? fabsf(p.kw[ln.c0 + e]) : 1.f, ow = p.kw ? fabsf(p.kw[ln.other(e)]) : 1.f;
             err[e] = (fabsf(x[e]) * mw + (ln.rotated ? fabsf(xp[e]) * ow : 0.f)) * u;
         }

@@ -24,11 +24,13 @@
 namespace {
 
 constexpr int RT = 128;        // threads per CTA
-constexpr int MIN_CTAS = 6;    // per SM (80 registers a thread)
+constexpr int MIN_CTAS = 8;    // per SM (64 registers a thread)
 // Units whose loads are in flight, and the most a warp takes: as many as keep
-// every SM full once (8191 tokens, 32 + 8 heads of 128: up to 32 units 32.8 us,
-// 8 36.9, 4 45.1: a warp forms its angles once).
-constexpr int AHEAD = 4, MOST_UNITS = 32;
+// every SM full once, since a warp forms its angles once (8191 tokens, 32 + 8 heads
+// of 128: up to 32 units 33 us, 8 37, 4 45). Three units ahead and eight CTAs: 16387
+// tokens of 24 + 2 + 2 heads of 256 to the cache 99 us; four and eight 106, four and
+// seven 104, three and ten (48 registers) 119, two units of keys a warp 110.
+constexpr int AHEAD = 3, MOST_UNITS = 32;
 
 struct RopeParams {
     const __half *q, *k, *v;
@@ -42,6 +44,7 @@ struct RopeParams {
     int tokens, hq, hk, R;
     int uq, uk;                                  // units (a warp's heads) of the queries and of the keys
     int per, chunks, kper, kchunks;              // units per warp and warps per token, for each
+    unsigned int ratio;                          // CTAs of keys among all, in units of 2^-32 (without a cache: of queries)
     // kv4_append_rope
     const int32_t *slots;
     uint8_t *cache;
@@ -323,72 +326,97 @@ __device__ __forceinline__ void rotate(const RopeParams &p, const Lane<D, INTER>
     }
 }
 
-// One token's keys or values of a unit of heads, to the cache.
+// One token's keys and values of a unit of heads, to the cache.
 template <int D, bool INTER>
-__device__ __forceinline__ void append(const RopeParams &p, const Lane<D, INTER> &ln, int token, bool value, int unit) {
-    const int h = unit * Lane<D, INTER>::HW + ln.head;
-    const bool there = h < p.hk;
-    uint4 mine = make_uint4(0u, 0u, 0u, 0u);
-    if (there)
-        mine = *reinterpret_cast<const uint4 *>((value ? p.v + token * p.v_stride : p.k + token * p.k_stride) + h * D + ln.c0);
-    const int slot = p.slots[token], page = slot / p.page;
-    float x[8];
-    sk::unpack8(mine, x);
-    uint32_t codes, sc;
-    if (value) {
-        value_codes(x, p.gv, codes, sc);
-    } else {
-        const int position = p.positions ? p.positions[token] : 0;
-        float cw[8], sw[8], xp[8], y[8], err[8];
-        {
-            float c[Lane<D, INTER>::NP], s[Lane<D, INTER>::NP];
-            angles<D, INTER>(p, ln, position, c, s);
-            weigh<D, INTER>(ln, p.kw, c, s, cw, sw);
-        }
-        const float r = p.kw ? norm_of<Lane<D, INTER>::L>(p, x) : 1.f;
-        partners<D, INTER>(ln, mine, x, xp);
-        // In units of u = 2^-24 of the two terms a cosine or sine of one would leave: the norm's sum of 13 roundings and
-        // eps's 2, halved by the root, and 4 of rsqrtf's two last places, 11.5; an angle's 3.2 (pi times its rounding), one
-        // of sincospif's last places, amplitude's 2, the weight's 1; products, sum and factor 3: 21.7, of 24 (without a
-        // norm 10.2, of 12).
-        const float u = (p.kw ? 24.f : 12.f) * 0x1p-24f * r * fmaxf(1.f, fabsf(float(p.amplitude)));
+__device__ __forceinline__ void append(const RopeParams &p, const Lane<D, INTER> &ln, int token, int unit) {
+    using LN = Lane<D, INTER>;
+    const int h = unit * LN::HW + ln.head;
+    uint4 key = make_uint4(0u, 0u, 0u, 0u), value = key;
+    if (h < p.hk) {
+        key = *reinterpret_cast<const uint4 *>(p.k + token * p.k_stride + h * D + ln.c0);
+        value = *reinterpret_cast<const uint4 *>(p.v + token * p.v_stride + h * D + ln.c0);
+    }
+    const int slot = p.slots[token], position = p.positions ? p.positions[token] : 0;
+    const int page = slot / p.page, at = slot - page * p.page, b = ln.l >> 1, pos = at & 15;
+    const bool kept = h < p.hk && slot >= 0 && page < p.pages;
+    uint8_t *const rec = p.cache + (kept ? ((size_t(page) * p.hk + h) * p.recs + (at >> 4)) * sk::kv4_rec_bytes(D) : 0);
+    float cw[8], sw[8], wm[8], wo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        wm[e] = p.kw ? p.kw[ln.c0 + e] : 1.f;
+        wo[e] = p.kw ? p.kw[ln.other(e)] : 1.f;
+    }
+    {
+        float c[LN::NP], s[LN::NP];
+        angles<D, INTER>(p, ln, position, c, s);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            // (a component that is not turned keeps the sign of its zero)
-            y[e] = (ln.rotated ? fmaf(x[e], cw[e], xp[e] * sw[e]) : x[e] * cw[e]) * r;
-            const float mw = p.kw ? fabsf(p.kw[ln.c0 + e]) : 1.f, ow = p.kw ? fabsf(p.kw[ln.other(e)]) : 1.f;
-            err[e] = (fabsf(x[e]) * mw + (ln.rotated ? fabsf(xp[e]) * ow : 0.f)) * u;
+            const int j = INTER ? e / 2 : e;
+            cw[e] = c[j] * wm[e];
+            sw[e] = (ln.second(e) ? s[j] : -s[j]) * wo[e];
+            wm[e] = fabsf(wm[e]);
+            wo[e] = ln.rotated ? fabsf(wo[e]) : 0.f;
         }
-        key_codes<D, INTER>(p, ln, mine, position, x, xp, y, err, codes, sc);
     }
-    if (!there || slot < 0 || page >= p.pages) return;
-    const int at = slot - page * p.page, b = ln.l >> 1, pos = at & 15;
-    uint8_t *rec = p.cache + ((size_t(page) * p.hk + h) * p.recs + (at >> 4)) * sk::kv4_rec_bytes(D);
-    *reinterpret_cast<uint32_t *>(rec + (value ? sk::kv4_code_at<true>(D, pos, b) : sk::kv4_code_at<false>(D, pos, b)) +
-                                  4 * (ln.l & 1)) = codes;
-    if (!(ln.l & 1)) rec[value ? sk::kv4_scale_at<true>(D, pos, b) : sk::kv4_scale_at<false>(D, pos, b)] = uint8_t(sc);
+    uint32_t codes, sc;
+    float x[8];
+    sk::unpack8(value, x);
+    value_codes(x, p.gv, codes, sc);
+    if (kept) {
+        *reinterpret_cast<uint32_t *>(rec + sk::kv4_code_at<true>(D, pos, b) + 4 * (ln.l & 1)) = codes;
+        if (!(ln.l & 1)) rec[sk::kv4_scale_at<true>(D, pos, b)] = uint8_t(sc);
+    }
+    sk::unpack8(key, x);
+    float xp[8], y[8], err[8];
+    const float r = p.kw ? norm_of<LN::L>(p, x) : 1.f;
+    partners<D, INTER>(ln, key, x, xp);
+    // In units of u = 2^-24 of the two terms a cosine or sine of one would leave: the norm's sum of 13 roundings and
+    // eps's 2, halved by the root, and 4 of rsqrtf's two last places, 11.5; an angle's 3.2 (pi times its rounding), one
+    // of sincospif's last places, amplitude's 2, the weight's 1; products, sum and factor 3: 21.7, of 24 (without a
+    // norm 10.2, of 12).
+    const float u = (p.kw ? 24.f : 12.f) * 0x1p-24f * r * fmaxf(1.f, fabsf(float(p.amplitude)));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        // (a component that is not turned keeps the sign of its zero)
+        y[e] = (ln.rotated ? fmaf(x[e], cw[e], xp[e] * sw[e]) : x[e] * cw[e]) * r;
+        err[e] = fmaf(fabsf(x[e]), wm[e], fabsf(xp[e]) * wo[e]) * u;
+    }
+    key_codes<D, INTER>(p, ln, key, position, x, xp, y, err, codes, sc);
+    if (kept) {
+        *reinterpret_cast<uint32_t *>(rec + sk::kv4_code_at<false>(D, pos, b) + 4 * (ln.l & 1)) = codes;
+        if (!(ln.l & 1)) rec[sk::kv4_scale_at<false>(D, pos, b)] = uint8_t(sc);
+    }
 }
 
 // A warp takes up to `per` units of one token's queries, so that the angles are
-// formed once for all of them, or of its keys; with APPEND one unit of its keys
-// or values. blockIdx.y: queries, keys, values.
+// formed once for all of them, or up to `kper` of its keys (with APPEND one, and its
+// values). The CTAs
+// of keys are spread evenly among those of queries: the ones wait for memory, the
+// others compute (16387 tokens of 24 + 2 + 2 heads of 256: one kind after the other
+// 132 us, mixed 111).
 template <int D, bool INTER, bool APPEND>
 __global__ void __launch_bounds__(RT, MIN_CTAS) rope_kernel(const __grid_constant__ RopeParams p) {
     sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
-    const int lane = threadIdx.x & 31, part = blockIdx.y;
-    const unsigned int w = blockIdx.x * (RT / 32) + (threadIdx.x >> 5), chunks = part ? p.kchunks : p.chunks;
+    const int lane = threadIdx.x & 31;
+    // of the first i CTAs, floor(i ratio / 2^32) are of keys
+    const unsigned int before = APPEND ? (unsigned long long)blockIdx.x * p.ratio >> 32
+                                       : blockIdx.x < p.ratio ? 0 : blockIdx.x - p.ratio,
+                       upto = ((unsigned long long)blockIdx.x + 1) * p.ratio >> 32;
+    const bool keys = APPEND ? upto != before : blockIdx.x >= p.ratio;
+    const unsigned int w = (keys ? before : APPEND ? blockIdx.x - before : blockIdx.x) * (RT / 32) + (threadIdx.x >> 5),
+                       chunks = keys ? p.kchunks : p.chunks;
     const unsigned int token = w / chunks, chunk = w - token * chunks;
     if (token >= unsigned(p.tokens)) return;
     const Lane<D, INTER> ln(lane, p.R);
-    if (APPEND && part) {
-        append<D, INTER>(p, ln, token, part == 2, chunk);
+    const int per = keys ? p.kper : p.per, u0 = chunk * per, u1 = min(keys ? p.uk : p.uq, u0 + per);
+    if (APPEND && keys) {
+        append<D, INTER>(p, ln, token, u0);
         return;
     }
-    const int per = part ? p.kper : p.per, units = part ? p.uk : p.uq, u0 = chunk * per;
-    rotate<D, INTER>(p, ln, p.positions ? p.positions[token] : 0, part ? p.k + token * p.k_stride : p.q + token * p.q_stride,
-                     part ? p.k_out + token * p.ko_stride : p.q_out + token * p.qo_stride, part ? p.kw : p.qw,
-                     part ? p.hk : p.hq, u0, min(units, u0 + per));
+    rotate<D, INTER>(p, ln, p.positions ? p.positions[token] : 0, keys ? p.k + token * p.k_stride : p.q + token * p.q_stride,
+                     keys ? p.k_out + token * p.ko_stride : p.q_out + token * p.qo_stride, keys ? p.kw : p.qw,
+                     keys ? p.hk : p.hq, u0, u1);
 }
 
 template <int D, bool INTER, bool APPEND>
@@ -397,21 +425,20 @@ sk_status launch(RopeParams &p, int sms, cudaStream_t s) {
     p.uq = (p.hq + HW - 1) / HW;
     p.uk = (p.hk + HW - 1) / HW;
     const long long held = (long long)sms * MIN_CTAS * (RT / 32);
-    auto share = [&](int units) {
+    auto share = [&](int units, int most) {
         const long long per = (long long)p.tokens * units / held;
-        return int(per < 1 ? 1 : per > MOST_UNITS ? MOST_UNITS : per);
+        return int(per < 1 ? 1 : per > most ? most : per);
     };
-    p.per = share(p.uq);
-    p.kper = APPEND ? 1 : share(p.uk);
+    p.per = share(p.uq, MOST_UNITS);
+    p.kper = share(p.uk, APPEND ? 1 : MOST_UNITS);
     p.chunks = (p.uq + p.per - 1) / p.per;
     p.kchunks = (p.uk + p.kper - 1) / p.kper;
-    const long long most = p.chunks > p.kchunks ? p.chunks : p.kchunks;
-    const long long warps = (long long)p.tokens * most, grid = (warps + RT / 32 - 1) / (RT / 32);
-    if (grid * (RT / 32) > 0x7FFFFFFFLL) return SK_ERR_UNSUPPORTED_SHAPE;
-    return sk::launch_pdl(rope_kernel<D, INTER, APPEND>, dim3(unsigned(grid), APPEND ? 3 : 2), dim3(RT), 0, s, p) ==
-                   cudaSuccess
-               ? SK_OK
-               : SK_ERR_CUDA;
+    auto ctas = [&](int chunks) { return ((long long)p.tokens * chunks + RT / 32 - 1) / (RT / 32); };
+    const long long kctas = ctas(p.kchunks), all = ctas(p.chunks) + kctas;
+    if (all * (RT / 32) > 0x7FFFFFFFLL) return SK_ERR_UNSUPPORTED_SHAPE;
+    p.ratio = (unsigned int)(APPEND ? (((unsigned long long)kctas << 32) + all - 1) / all : all - kctas);      // (kctas < all)
+    return sk::launch_pdl(rope_kernel<D, INTER, APPEND>, dim3(unsigned(all)), dim3(RT), 0, s, p) == cudaSuccess ? SK_OK
+                                                                                                               : SK_ERR_CUDA;
 }
 
 template <bool APPEND>

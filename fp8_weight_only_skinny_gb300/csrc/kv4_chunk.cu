@@ -80,11 +80,12 @@ __device__ __forceinline__ int worker() {
     return int(blockIdx.x) / (Cc<D>::PAIR ? 2 : 1);
 }
 
-// Each row's weights are 2^(c s - t) with c = scale * key scale * log2 e and t, the
-// row's base, a whole number, so that one fma gives the exponent, rounded once. t is
-// P_SHIFT below a maximum that the row had earlier and is moved only when an exponent
-// passes P_SHIFT + SLACK; the weights go to the second product in FP16, between
-// 2^-32 and 2^15, their sum is taken unrounded. An exponent is off by what c s is
+// Each row's weights are 2^(c s - t) with c = scale * key scale * log2 e and t the
+// row's base: one fma gives the exponent, rounded once. t is P_SHIFT below a maximum
+// that the row had earlier and is moved only when an exponent passes P_SHIFT + SLACK;
+// the weights go to the second product in FP16, between 2^-32 and 2^15 (that of the
+// maximum the base was set by is a power of two: the largest weight of most rows is
+// not rounded), their sum is taken unrounded. An exponent is off by what c s is
 // rounded by before the difference: 2^-24 of it, as the score itself (FP32).
 __device__ __forceinline__ void write_lse(const AttnParams &p, long long row, float base, float l) {
     if (p.lse) p.lse[row] = l == 0.f ? NEG_INF : (base + __log2f(l)) * LN2;
@@ -727,7 +728,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     }
                     m0 = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
                     if (__any_sync(0xffffffffu, m0 > most)) {
-                        const float by = m0 > most ? ceilf(m0) - P_SHIFT : 0.f, f = most < 0.f ? 0.f : ex2(-by);
+                        const float by = m0 > most ? m0 - P_SHIFT : 0.f, f = most < 0.f ? 0.f : ex2(-by);
                         if (m0 > most) most = P_SHIFT + SLACK;
                         t0 += by;
                         const float2 l = apart(sum);

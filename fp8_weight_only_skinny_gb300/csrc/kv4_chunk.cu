@@ -707,10 +707,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     ++blocks_done;
                     t5::fence_after();
                     float s[KB];
-                    t5::ld32(s_col, s);
-                    t5::ld32(s_col + 32, s + 32);
-                    t5::wait_ld();
-                    t5::held<KB>(s);
+                    t5::ld64(s_col, s);
                     if (pos + KB > lim0 || (pos + KB > p.sinks && pos < low1)) {
 #pragma unroll
                         for (int e = 0; e < KB; ++e)
@@ -745,8 +742,6 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                             for (int c = 0; c < D; c += 32) {
                                 float o[32];
                                 t5::ld32(o_at + c, o);
-                                t5::wait_ld();
-                                t5::held<32>(o);
                                 uint32_t v[32];
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(o[e] * f);
@@ -796,11 +791,9 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     const uint32_t v[4] = {a, b, c, d};
                     st_shared_v4(room + lane * 128 + ((piece ^ (lane & 7)) << 4), v);
                 };
-                auto columns = [&](int c, float *o) {
+                auto columns = [&](int c, float (&o)[32]) {
                     if (n > 0) {
                         t5::ld32(o_at + c, o);
-                        t5::wait_ld();
-                        t5::held<32>(o);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = 0.f;

@@ -981,11 +981,11 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 }
                 t5::commit<C::PAIR>(s_full + 8 * (t * NB + b));
             };
-            auto score = [&](bool two) {
+            auto keys_ready = [&] {
                 wait(k_full + 8 * ks, kp);
                 t5::fence_after();
-                scores(0);
-                if (T == 2 && two) scores(1);
+            };
+            auto keys_used = [&] {
                 t5::commit<C::PAIR>(k_empty + 8 * ks);
                 k_op += STEP;
                 if (++ks == ST) {
@@ -1014,13 +1014,26 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 if (n == 0) continue;
                 wait(q_ready, pieces[0]++ & 1u);
                 if (two) wait(q_ready + 8, pieces[1]++ & 1u);
-                score(two);
+                for (int j = 0; j < min(n, 2); ++j) {
+                    keys_ready();
+                    scores(0);
+                    if (T == 2 && two) scores(1);
+                    keys_used();
+                }
+                // A tile's scores two blocks on follow its product directly: a tile need not wait for the other's weights.
                 for (int j = 0; j < n; ++j) {
-                    const bool last = j + 1 == n;
-                    if (!last) score(two);
+                    const bool last = j + 1 == n, more = j + 2 < n;
                     wait(v_full + 8 * vs, vp);
                     values(0, j == 0, last);
-                    if (T == 2 && two) values(1, j == 0, last);
+                    if (more) {
+                        keys_ready();
+                        scores(0);
+                    }
+                    if (T == 2 && two) {
+                        values(1, j == 0, last);
+                        if (more) scores(1);
+                    }
+                    if (more) keys_used();
                     t5::commit<C::PAIR>(v_empty + 8 * vs);
                     v_op += STEP;
                     if (++vs == ST) {

@@ -1068,6 +1068,16 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 }
                 last_join |= parts;
             }
+            // its query rows, on their way to L2
+            if (more && w.k1 > w.k0) {
+                const int lo = C::PAIR ? rank * 128 : 0, hi = min(w.count, lo + 128 * T);
+                for (int r = lo + lane; r < hi; r += 32) {
+                    const int i = sk::quotient(w.idx0 + r, p.by_g), g = w.idx0 + r - i * p.G;
+                    const __half *src = p.q + (w.row0 + i) * p.q_stride + (long long)(w.h * p.G + g) * D;
+#pragma unroll
+                    for (int c = 0; c < D; c += 64) sk::prefetch_l2(src + c);
+                }
+            }
             // (a piece may take longer than any other wait)
             if (!dead && !t5::wait_spin(l_empty + 8 * at, lap ^ 1u, 60)) {
                 dead = true;

@@ -32,9 +32,11 @@ using sk::ex2;
 namespace t5 = sk::t5;
 
 constexpr int KB = 64;                 // positions per block
-constexpr int SETUP = 4;               // what a tile costs beside its blocks, in blocks
+// What a tile costs beside its blocks, in blocks (4099 rows over themselves, heads of
+// 256: 4 213 us, 8 176, 12 180; 8195 rows in windows of 1024, heads of 128: 282, 269, 275).
+constexpr int SETUP = 8;
 constexpr int WHOLE_BLOCKS = 12;       // tables of no more blocks are not worth a second kernel where each tile has a CTA
-constexpr int MIN_SHARE = 12;          // least cost a CTA takes, above that of one block: no part of a tile is empty
+constexpr int MIN_SHARE = 40;          // least cost a CTA takes, above that of one block: no part of a tile is empty
 
 // T tiles of 128 rows share what a CTA decodes; NB buffers of S per tile; HW warps
 // decode keys and as many values; ST stages of each. PAIR: two CTAs, each with a tile
@@ -144,7 +146,8 @@ struct Tile {
         lim0 -= skip * sk::KV4_REC;
         lim1 -= skip * sk::KV4_REC;
         blocks = (max(lim1, 0) + KB - 1) / KB;
-        per = C::T == 2 && count > 128 ? 3 : 2;
+        // (a block of one tile of 128 rows takes nearly as long as of two: 1750 clocks of 2000, at head size 64 1200 of 1490)
+        per = C::T == 1 || count > 128 ? 10 : D == 64 ? 8 : 9;
         cost = p.whole ? 1 : (blocks + SETUP) * per;
     }
     __device__ __forceinline__ int block_at(int x) const {

@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <cfloat>
+#include <cstddef>
 #include <cstdint>
 
 #include "../../include/skinny.h"
@@ -32,6 +33,7 @@ using sk::ex2;
 namespace t5 = sk::t5;
 
 constexpr int KB = 64;                 // positions per block
+constexpr int MOST_SEQS = 16383;
 // What a tile costs beside its blocks, in blocks (4099 rows over themselves, heads of
 // 256: 4 213 us, 8 176, 12 180; 8195 rows in windows of 1024, heads of 128: 282, 269, 275).
 constexpr int SETUP = 8;
@@ -334,9 +336,11 @@ __device__ Split find_share(const ChunkParams &p, Pieces<D> &w, int *list, long 
     const int each_b = (p.B + C::CT_ALL - 1) / C::CT_ALL, b_lo = min(p.B, tid * each_b), b_hi = min(p.B, b_lo + each_b);
     long long mine = 0, tiles;
     for (int b = b_lo; b < b_hi; ++b) mine += tiles_in<D>(p, Seq(p, b));
-    int at = int(scanned(mine, tiles));
+    constexpr long long MOST_TILES = 1 << 30;              // (more only where starts descends)
+    long long at = scanned(mine, tiles);
+    tiles = min(tiles, MOST_TILES);
     for (int b = b_lo; b < b_hi; ++b) {
-        list[b] = at;
+        list[b] = int(min(at, MOST_TILES));
         at += tiles_in<D>(p, Seq(p, b));
     }
     if (tid == 0) {
@@ -594,6 +598,9 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         }
         sk::fence_barrier_init();
     }
+    // (every place of the list an end: a thread that gave up waiting finds nothing else)
+    if (tid < C::LIST * 16) reinterpret_cast<int *>(smem + C::PIECES)[tid] = tid % 16 == 1 ? -1 : 0;
+    static_assert(offsetof(Piece, k1) == 4, "the second word of a piece");
     __syncwarp();
     t5::fence_before();
     if constexpr (C::PAIR) sk::cluster_sync();
@@ -646,7 +653,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         // are done.
         auto load_q = [&](const Piece &w) {
             // (a pair's products take both CTAs' rows, also where the second has none)
-            if ((!C::PAIR && first >= w.count) || w.k1 <= w.k0) return;
+            if (w.k1 <= w.k0 || (!C::PAIR && first >= w.count)) return;
             const int idx = w.idx0 + first + row, i = sk::quotient(idx, p.by_g);
             const bool there = first + row < w.count;
             const __half *src = p.q + (w.row0 + i) * p.q_stride + (long long)(w.h * p.G + idx - i * p.G) * D;
@@ -1054,20 +1061,24 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
     } else {
         // ------------------------------------------------------- the list
         if (lane == 0 && blockIdx.x == 0) *p.tiles = tiles;
-        Piece w;
+        Piece w = {};
         int t = 0, number = 0, cost = 0, last_join = 0;
         const int me = worker<D>();
         for (bool more = true; more && !__any_sync(0xffffffffu, dead);) {
             more = work.next(p, w, t, number, cost);
-            if (!more) w.k1 = -1;
+            if (!more) {
+                w = Piece{};               // the end: nothing of it may be taken for a piece's
+                w.k1 = -1;
+            }
             if (more && rank == 0 && !p.whole && w.k0 == 0) {
                 // A tile in parts is this CTA's last piece: its share ends within it, and the tile's last unit tells the last
                 // part's owner.
                 int parts = 0;
                 if (w.k1 != w.blocks) parts = owner_of(share, bound_of(share, me + 1) + (cost - work.x) - 1) - me + 1;
                 if (lane == 0) {
-                    if (p.by_tile) p.join[w.h * tiles + number] = Join::of(me, parts, w.h, w.b, t);
-                    else if (parts) p.join[me] = Join::of(me, parts, w.h, w.b, t);
+                    const long long place = (long long)w.h * tiles + number;       // (more only where starts descends)
+                    if (p.by_tile && place < p.ctas) p.join[place] = Join::of(me, parts, w.h, w.b, t);
+                    if (!p.by_tile && parts) p.join[me] = Join::of(me, parts, w.h, w.b, t);
                 }
                 last_join |= parts;
             }
@@ -1174,7 +1185,7 @@ __global__ void __launch_bounds__(JT) kv4_chunk_join_kernel(const __grid_constan
 template <int D>
 sk_status run(ChunkParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     using C = Cc<D>;
-    if (p.B > C::MOST_SEQS) return SK_ERR_UNSUPPORTED_SHAPE;
+    static_assert(C::MOST_SEQS >= MOST_SEQS, "the list of sequences");
     p.ctas = C::PAIR ? sms / 2 : sms;
     if (p.ctas < 1) return SK_ERR_CUDA;
     // No more tiles than these, and no more blocks in one.
@@ -1220,7 +1231,7 @@ extern "C" sk_status kv4_chunk_attention(const void *q, long long q_stride, cons
     if (!(product >= 5e-37 && product <= 1e27)) return SK_ERR_INVALID_ARG;
     if (!sk::kv4_shape_ok(pages, kv_heads, head_dim, page_size)) return SK_ERR_UNSUPPORTED_SHAPE;
     // positions and rows of a kv head's list with room for a tile and a block, query rows by 31 bits
-    if ((long long)table_width * page_size > 0x7FFFF000LL || (long long)rows * (q_heads / kv_heads) > 0x3FFFF000LL ||
+    if (seqs > MOST_SEQS || (long long)table_width * page_size > 0x7FFFF000LL || (long long)rows * (q_heads / kv_heads) > 0x3FFFF000LL ||
         (long long)rows * q_heads > 0x7FFFFFFFLL)
         return SK_ERR_UNSUPPORTED_SHAPE;
     if (seqs == 0 || rows == 0) return SK_OK;

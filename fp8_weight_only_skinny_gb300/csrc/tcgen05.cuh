@@ -81,8 +81,7 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
 }
 
 // 32 and 64 columns of this warp's 32 lanes. Loads and their wait are one statement:
-// between two, the compiler may give a register that a load has yet to write to
-// something else.
+// no copy of a value can come between.
 __device__ __forceinline__ void ld32(uint32_t addr, float (&v)[32]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
                  "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"

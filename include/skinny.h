@@ -443,7 +443,7 @@ SK_API sk_status kv4_window_attention(const void *q, long long q_stride, const u
  *            `sinks` (sinks is not read with window = 0)
  *   starts   const i32 [seqs + 1], device memory, ascending, at most `rows`; q, out and
  *            lse rows outside [starts[0], starts[seqs]) are not read or written
- *   out, lse as kv4_attention ([rows] rows), lse may be NULL
+ *   out, lse as kv4_attention ([rows] rows), lse may be NULL; out does not overlap q
  *   Other arguments, weights, sums, empty rows and the workspace as kv4_attention
  *   (the order of the sums depends on all sequences of the call; repeated calls are
  *   bitwise identical).  rows * q_heads / kv_heads < 2^30, rows * q_heads < 2^31 and

@@ -110,6 +110,7 @@ def test_attention_sizes_and_pointers(call):
 def test_chunks_alone():
     assert _chunk(rows=-1) == INVALID and _chunk(starts=None) == INVALID and _chunk(starts=A + 2) == MISALIGNED
     assert _chunk(rows=0) == OK
+    assert _chunk(B=16384) == UNSUPPORTED
     assert _chunk(rows=1 << 29) == UNSUPPORTED                # rows of a kv head's list
     assert _chunk(width=1 << 26) == UNSUPPORTED               # positions
     assert _window(window=0) == INVALID and _window(M=0) == INVALID and _window(M=9) == INVALID

@@ -869,6 +869,14 @@ constexpr int MAX_SEGMENTS = 131072;
 // 28 against 30 and 16 of 20000 139 against 153, 24 rows 27 against 25 and 139
 // against 118.
 constexpr int TC_ABOVE = 24;
+// Rows of a window that take the registers' kernel four passes or more go to that
+// for chunks, which decodes a position once for all rows, where there is enough to
+// do for its longer way in and out. 96 rows a kv head: 64 sequences, windows of 2000,
+// heads of 256 125 -> 71 us, of 128 116 -> 73 (windows of 200: 38 -> 27, 34 -> 27);
+// one sequence, window of 8000, heads of 256 17 against 26, of 128 18 against 22.
+// Three passes: 68 against 67 at most.
+constexpr int CHUNK_PASSES = 4;
+constexpr long long CHUNK_WORK = 160000;      // positions, over all kv heads and passes
 
 // The scratch memory: the segment list, the rows' statistics where weights are
 // accumulated (16 MiB at most: MAX_SEGMENTS tiles of 16 rows), and in the rest
@@ -969,6 +977,8 @@ sk_status run(AttnParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     const int tiles = (p.M * p.G + NROW - 1) / NROW;       // of eight rows
     p.RT = (tiles + MOST - 1) / MOST;
     const int nr = (tiles + p.RT - 1) / p.RT;
+    if (WIN && p.RT >= CHUNK_PASSES && p.B <= CHUNK_SEQS && (long long)p.B * p.heads * p.cap * p.RT >= CHUNK_WORK)
+        return chunk_rows(p, D, scratch, sms, s);
     unsigned char *const rest = place_rows(p, scratch);
     sk_status st;
     if (D == 128 && !WIN && p.M * p.G > TC_ABOVE) {

@@ -5,6 +5,7 @@
 
 #include <cstdint>
 
+#include "../../include/skinny.h"
 #include "cluster.cuh"
 #include "kv4.cuh"
 
@@ -221,6 +222,11 @@ constexpr int TC_MOST = 96, TC_CTAS = 2;
 // Rows per tile it takes `rows` in, and how many tiles.
 int tc_rows(int rows, int *tiles);
 cudaError_t launch_tc(AttnParams &p, int rows_per_tile, cudaStream_t s);
+
+// The kernel for chunks of any length (kv4_chunk.cu), for M rows of every sequence
+// with `limit`, `window` and `sinks` set; up to CHUNK_SEQS sequences.
+constexpr int CHUNK_SEQS = 16383;
+sk_status chunk_rows(const AttnParams &a, int head_dim, unsigned char *scratch, int sms, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace sk

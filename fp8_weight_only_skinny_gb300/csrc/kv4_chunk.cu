@@ -33,7 +33,7 @@ using sk::ex2;
 namespace t5 = sk::t5;
 
 constexpr int KB = 64;                 // positions per block
-constexpr int MOST_SEQS = 16383;
+constexpr int MOST_SEQS = CHUNK_SEQS;
 // What a tile costs beside its blocks, in blocks (4099 rows over themselves, heads of
 // 256: 4 213 us, 8 176, 12 180; 8195 rows in windows of 1024, heads of 128: 282, 269, 275).
 constexpr int SETUP = 8;
@@ -96,7 +96,7 @@ __device__ __forceinline__ void write_lse(const AttnParams &p, long long row, fl
 }
 
 struct ChunkParams : AttnParams {
-    const int32_t *starts;
+    const int32_t *starts;             // null: M rows of every sequence
     int rows;                          // in all
     sk::Div by_g;
     int whole;                         // every tile is one CTA's (and costs the same)
@@ -115,8 +115,8 @@ struct Seq {
     int first, n, len;
     __device__ __forceinline__ Seq() {}
     __device__ __forceinline__ Seq(const ChunkParams &p, int b) {
-        first = min(max(p.starts[b], 0), p.rows);
-        n = min(max(p.starts[b + 1], first), p.rows) - first;
+        first = p.starts ? min(max(p.starts[b], 0), p.rows) : b * p.M;
+        n = p.starts ? min(max(p.starts[b + 1], first), p.rows) - first : p.M;
         len = min(max(p.lens[b], 0), p.cap);
     }
 };
@@ -1216,6 +1216,25 @@ sk_status run(ChunkParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace
+
+namespace sk {
+namespace attn {
+
+sk_status chunk_rows(const AttnParams &a, int head_dim, unsigned char *scratch, int sms, cudaStream_t s) {
+    ChunkParams p = {};
+    static_cast<AttnParams &>(p) = a;
+    p.cap = a.limit;
+    p.rows = a.B * a.M;
+    p.by_g = sk::Div(uint32_t(a.G));
+    switch (head_dim) {
+        case 64: return run<64>(p, scratch, sms, s);
+        case 128: return run<128>(p, scratch, sms, s);
+        default: return run<256>(p, scratch, sms, s);
+    }
+}
+
+}  // namespace attn
+}  // namespace sk
 
 extern "C" sk_status kv4_chunk_attention(const void *q, long long q_stride, const uint8_t *cache, const int32_t *table,
                                          const int32_t *lens, const int32_t *starts, float k_scale, float v_scale,

@@ -231,6 +231,15 @@ def test_windows(sk, Hq, H, D, page, rows, width, window, sinks):
     _check_window(sk, cache, table, lens, q, rows, Hq, D, window, sinks)
 
 
+@pytest.mark.parametrize("D,Hq,H,rows,page", [(256, 12, 1, 8, 16), (256, 24, 2, 6, 48), (128, 12, 1, 8, 32), (64, 16, 1, 8, 16)])
+@pytest.mark.parametrize("window,sinks", [(40, 4), (7000, 0), (130, 6000)])
+def test_windows_of_many_rows(sk, D, Hq, H, rows, page, window, sinks):
+    """Rows that take several passes, and tables wide enough for the kernel of chunks; with a narrow window they keep to
+    the passes."""
+    cache, table, lens, q = _case(D + rows, [0, 1, 5, 16, 130, 260, 47], rows, Hq, H, D, page, width=7500 // page)
+    _check_window(sk, cache, table, lens, q, rows, Hq, D, window, sinks)
+
+
 @pytest.mark.parametrize("D,Hq,H,rows", [(64, 8, 1, 1), (128, 12, 2, 2), (256, 24, 2, 1)])
 @pytest.mark.parametrize("window,sinks", [(900, 4), (1300, 700)])
 def test_long_windows_in_parts(sk, D, Hq, H, rows, window, sinks):

@@ -119,12 +119,6 @@ __device__ __forceinline__ void st32(uint32_t addr, const uint32_t *v) {
                  "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(addr) : "memory");
 }
 
-__device__ __forceinline__ void st16(uint32_t addr, const uint32_t *v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
-                 ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-                 "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(addr) : "memory");
-}
-
 // Wait until `bar`'s phase of this parity is complete, for so many seconds at most. The
 // clock is read every 1024 tries: read after every one (as where a wait is rare),
 // its latency is added to each wait that is not over at once.
@@ -147,14 +141,6 @@ __device__ __forceinline__ bool wait_spin(uint32_t bar, uint32_t parity, uint64_
             else if (t - t0 > seconds * 1000000000ull) return false;
         }
     }
-}
-
-// Whether `x` holds in any of the `threads` that meet at barrier `id`.
-__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t threads, bool x) {
-    uint32_t any;
-    asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %3, 0; barrier.cta.red.or.pred q, %1, %2, p; selp.u32 %0, 1, 0, q; }"
-                 : "=r"(any) : "r"(id), "r"(threads), "r"(uint32_t(x)) : "memory");
-    return any != 0;
 }
 
 }  // namespace t5

@@ -105,8 +105,9 @@ typedef enum {
  * Allocate (cudaMalloc) and initialise the workspace of the CURRENT device
  * (a zeroed 4 KiB control block followed by split-K partial-sum slots, all
  * marked empty; every call leaves them empty again), and behind it 48 MiB of
- * scratch memory for kv4_attention (partial sums, up to 30 MiB, and with
- * acc_out the rows' statistics, up to 16), whether or not it is ever called.
+ * scratch memory for kv4_attention, kv4_window_attention and kv4_chunk_attention
+ * (partial sums, and with acc_out the rows' statistics, up to 16 MiB), whether or
+ * not one is ever called.
  * workspace_bytes = 0 picks the default, 64 MiB, which covers the largest call
  * below (N = 151936, K = 5120, M = 8 needs about 25 MB).  Calling it again on
  * the same device frees and re-creates the workspace (wait for all work of the
@@ -122,7 +123,7 @@ SK_API sk_status sk_init(size_t workspace_bytes);
  * workspace_bytes = 0 removes the stream's workspace (its calls fall back to
  * the device's).  Calling it again replaces the workspace (after synchronising
  * the stream).  Every later call on that stream -- linear layers, lm_head,
- * quantizers, kv4_attention, sk_last_device_error -- uses it instead of the
+ * quantizers, the attentions over the cache, sk_last_device_error -- uses it instead of the
  * device's, and its linear-layer kernels are launched cooperatively, so that
  * the whole persistent grid is resident before any of its CTAs starts: calls
  * on streams that each have a workspace of their own can then overlap on the
@@ -542,8 +543,9 @@ SK_API int sk_set_variant(int variant);
 
 /*
  * Failure-injection hook for tests: with enable = 1 the next linear-layer,
- * kv4_attention or kv4_evict call of this process on any device issues no bulk
- * copies, so that its kernels' bounded waits run out (about one second, twice
+ * kv4_attention, kv4_window_attention, kv4_chunk_attention or kv4_evict call of
+ * this process on any device issues no bulk copies (kv4_chunk_attention: decodes
+ * blocks but never says so), so that its kernels' bounded waits run out (about one second, twice
  * that in the cache kernels); they then finish without further waiting and
  * record SK_ERR_TIMEOUT, which sk_last_device_error() returns.  The hook clears
  * itself after that one call.  No fault, trap or unbounded wait is involved.

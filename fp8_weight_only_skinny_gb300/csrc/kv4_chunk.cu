@@ -7,12 +7,23 @@
 //
 // The rows of a kv head's G query heads are one list (row i, head g: i G + g), cut
 // into tiles of 128, a row a TMEM lane. For 64 positions at a time
-//     S (128 x 64, TMEM)  = Q (128 x D, TMEM) . K^T      K: decoded into shared memory
+//     S (128 x 64, TMEM)  = Q (128 x D, TMEM; D = 128: shared memory) . K^T      K: decoded into shared memory
 //     O (128 x D, TMEM)  += P (128 x 64, TMEM) . V       V: the same; P over S's own columns
-// so that a softmax thread owns a row: its maximum, base (kv4_attention.cuh) and
-// sum need no other thread, and shared memory carries only the decoded keys and
-// values. Roles: four warps of softmax per tile, warps that decode, one thread
-// that issues the products.
+// so that a softmax thread owns a row: its maximum, base and sum need no other
+// thread, and shared memory carries only the decoded keys and values. Roles: four
+// warps of softmax per tile, warps that decode keys and warps that decode values, one
+// thread that issues the products, one warp that lists the work. At head size 256 a
+// pair of CTAs takes two tiles and decodes each block once for both: decoding alone
+// bounds a single CTA there (2048 rows over 61003 positions, 24 over 2 heads: 2346 us
+// against 1684).
+//
+// At head size 256 bound by the products: that case 1693 us, 1783 TFLOP/s, alone, and
+// 1763 to 1797 in a long run of calls. At 128 and 64 by the softmax's chain from a
+// product to the next (2000 and 1490 clocks a block of two tiles, whose products take
+// 1280 and 512): 2048 rows over 16384 positions, 48 over 4 heads of 128, 609 us, 1270
+// TFLOP/s; issue slots, ALU and XU are below half of their rates. Twenty warps there,
+// with registers moved to the softmax's, spilled and took longer (644 -> 763). Calls
+// of a row over 24 to 4096 positions: 6 to 18 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 

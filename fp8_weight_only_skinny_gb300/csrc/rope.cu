@@ -9,6 +9,11 @@
 //     t = 2 pi frac(position F / 2^64),
 // F the pair's frequency as a fraction of a turn in units of 2^-64: the product
 // modulo 2^64 is exact, so that the angle is right at any position.
+//
+// Bound by DRAM and instructions together: 8191 tokens of 32 + 8 heads of 128, interleaved
+// and normed, 31 us (168 MB, 5.4 TB/s); 16387 tokens of 24 + 2 + 2 heads of 256 to the
+// cache 99 us (446 MB, 4.5 TB/s; issue 64 %, DRAM 52 %). One token 2.9 us.
+// Two components an instruction, f32x2, gained nothing: 99 -> 105 us, 31 -> 31.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 

@@ -18,7 +18,7 @@
 // against 1684).
 //
 // At head size 256 bound by the products: that case 1693 us, 1783 TFLOP/s, alone, and
-// 1763 to 1797 in a long run of calls. At 128 and 64 by the softmax's chain from a
+// 1763 to 1865 in long runs of calls. At 128 and 64 by the softmax's chain from a
 // product to the next (2000 and 1490 clocks a block of two tiles, whose products take
 // 1280 and 512): 2048 rows over 16384 positions, 48 over 4 heads of 128, 609 us, 1270
 // TFLOP/s; issue slots, ALU and XU are below half of their rates. Twenty warps there,

@@ -891,12 +891,21 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         const int32_t *table = p.table;
         int entry = 0, in_page = 0, head = 0;                // of the block looked up: the page and the record in it that this
                                                              // lane asked for (used only when fetched: the load has time)
-        auto look_up = [&] {                                 // the next block's records; false after the last block
+        // The next block's records; false after the last block, or where the piece that it would come from is not listed
+        // yet and it may not be waited for. A warp that holds a block not decoded does not wait: the place of the next
+        // piece may be free only when a piece before it, of this very block, is done (a one-block piece and more without
+        // blocks than the list has places).
+        bool ended = false;
+        auto look_up = [&](bool may_wait) {
             while (block == end_block) {
-                here();
+                if (ended || (!may_wait && !__all_sync(0xffffffffu, t5::test(l_full + 8 * at, lap)))) return false;
+                if (may_wait) here();
                 __syncwarp();
                 const Piece &w = list[at];
-                if (__any_sync(0xffffffffu, dead) || w.k1 < 0) return false;
+                if (__any_sync(0xffffffffu, dead) || w.k1 < 0) {
+                    ended = true;
+                    return false;
+                }
                 block = w.k0;
                 end_block = w.k1;
                 table = p.table + (long long)w.b * p.width;
@@ -928,39 +937,31 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             }
         };
         Raw<D> raw[2];
-        bool there[2], more = look_up();                     // blocks fetched; whether rec is another's
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            there[x] = more;
-            if (more) {
-                fetch(raw[x]);
-                more = look_up();
-            }
-        }
+        bool there[2] = {false, false}, more = false;        // blocks fetched; whether the one looked up is still to be
         uint32_t st = 0, parity = 1;                         // (the first use of each stage finds it free)
-        while (there[0]) {
+        while (true) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                if (!there[x]) {
-                    there[0] = false;
-                    break;
+                if (there[x]) {
+                    wait(empty + 8 * st, parity);
+                    if (value) decode_values<D>(ring + st * C::STAGE, to, odd, raw[x]);
+                    else decode_keys<D>(ring + st * C::STAGE, to, raw[x]);
+                    t5::fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && !p.stall) arrive(full + 8 * st);
+                    if (++st == ST) {
+                        st = 0;
+                        parity ^= 1u;
+                    }
                 }
-                wait(empty + 8 * st, parity);
-                if (value) decode_values<D>(ring + st * C::STAGE, to, odd, raw[x]);
-                else decode_keys<D>(ring + st * C::STAGE, to, raw[x]);
-                t5::fence_async_smem();
-                __syncwarp();
-                if (lane == 0 && !p.stall) arrive(full + 8 * st);
-                if (++st == ST) {
-                    st = 0;
-                    parity ^= 1u;
-                }
+                if (!more) more = look_up(!there[x ^ 1]);
                 there[x] = more;
                 if (more) {
                     fetch(raw[x]);
-                    more = look_up();
+                    more = look_up(false);
                 }
             }
+            if (ended && !there[0] && !there[1]) break;
         }
     } else if (warp == C::SW + C::DW) {
         // ------------------------------------------------------- products

@@ -168,7 +168,7 @@ struct Tile {
     }
 };
 
-// A piece of work: blocks [k0, k1) of a tile of sequence b and kv head h; k1 < 0: the
+// A piece of work: blocks [k0, k1) of a tile of sequence b and kv head h, one at least; k1 < 0: the
 // end. One warp lists a CTA's pieces, the others read them from shared memory.
 struct Piece {
     int k0, k1, blocks, h, b;
@@ -570,6 +570,19 @@ __device__ __forceinline__ void decode_values(uint32_t stage, const uint32_t (&t
     }
 }
 
+// The results of this CTA's rows of a tile that sees nothing, by one warp.
+template <int D>
+__device__ __forceinline__ void nothing_seen(const ChunkParams &p, const Piece &w, int lo, int lane) {
+    constexpr int LANES = D / 8;                             // of a row, 16 bytes each
+    const int hi = min(w.count, lo + 128 * Cc<D>::T);
+    for (int r = lo + lane / LANES; r < hi; r += 32 / LANES) {
+        const int idx = w.idx0 + r, i = sk::quotient(idx, p.by_g);
+        const long long to = (long long)(w.row0 + i) * (p.heads * p.G) + w.h * p.G + idx - i * p.G;
+        reinterpret_cast<uint4 *>(p.out + to * D)[lane % LANES] = make_uint4(0u, 0u, 0u, 0u);
+        if (lane % LANES == 0) write_lse(p, to, 0.f, 0.f);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __grid_constant__ ChunkParams p) {
     using C = Cc<D>;
@@ -664,7 +677,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         // are done.
         auto load_q = [&](const Piece &w) {
             // (a pair's products take both CTAs' rows, also where the second has none)
-            if (w.k1 <= w.k0 || (!C::PAIR && first >= w.count)) return;
+            if (w.k1 < 0 || (!C::PAIR && first >= w.count)) return;
             const int idx = w.idx0 + first + row, i = sk::quotient(idx, p.by_g);
             const bool there = first + row < w.count;
             const __half *src = p.q + (w.row0 + i) * p.q_stride + (long long)(w.h * p.G + idx - i * p.G) * D;
@@ -714,7 +727,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             const bool active = C::PAIR || first < w.count;
             float t0 = 0.f, most = -FLT_MAX;                 // the row's base, and what moves it (at first: any score)
             uint64_t sum = two(0.f, 0.f);
-            if (active && n > 0) {
+            if (active) {
                 const int i = sk::quotient(w.idx0 + first + row, p.by_g);
                 const int lim = first + row < w.count ? w.lim0 + i - sk::quotient(w.idx0, p.by_g) : 0;
                 const int low = p.window ? lim - p.window : 0;
@@ -794,11 +807,9 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             const bool whole = w.k0 == 0 && w.k1 == w.blocks, there = first + row < w.count;
             const size_t slot = size_t(worker<D>()) * 2 + (w.k0 == 0 ? 1 : 0);
             if (active) {
-                if (n > 0) {
-                    wait(o_end + 8 * t, ends++ & 1u);
-                    __syncwarp();
-                    t5::fence_after();
-                }
+                wait(o_end + 8 * t, ends++ & 1u);
+                __syncwarp();
+                t5::fence_after();
                 const float2 ll = apart(sum);
                 const float l = ll.x + ll.y, f = l == 0.f ? 0.f : p.vg / l;
                 const int idx = w.idx0 + first + row, i = sk::quotient(idx, p.by_g);
@@ -812,14 +823,6 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     const uint32_t v[4] = {a, b, c, d};
                     st_shared_v4(room + lane * 128 + ((piece ^ (lane & 7)) << 4), v);
                 };
-                auto columns = [&](int c, float (&o)[32]) {
-                    if (n > 0) {
-                        t5::ld32(o_at + c, o);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                    }
-                };
                 const int r0 = lane >> 3, piece = lane & 7;
                 if (whole) {
 #pragma unroll 1
@@ -827,7 +830,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
                             float o[32];
-                            columns(c + 32 * hf, o);
+                            t5::ld32(o_at + c + 32 * hf, o);
 #pragma unroll
                             for (int e = 0; e < 32; e += 8)
                                 put(4 * hf + e / 8, pack_f16(o[e] * f, o[e + 1] * f), pack_f16(o[e + 2] * f, o[e + 3] * f),
@@ -848,7 +851,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         float o[32];
-                        columns(c, o);
+                        t5::ld32(o_at + c, o);
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             put(e / 4, __float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
@@ -891,21 +894,12 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         const int32_t *table = p.table;
         int entry = 0, in_page = 0, head = 0;                // of the block looked up: the page and the record in it that this
                                                              // lane asked for (used only when fetched: the load has time)
-        // The next block's records; false after the last block, or where the piece that it would come from is not listed
-        // yet and it may not be waited for. A warp that holds a block not decoded does not wait: the place of the next
-        // piece may be free only when a piece before it, of this very block, is done (a one-block piece and more without
-        // blocks than the list has places).
-        bool ended = false;
-        auto look_up = [&](bool may_wait) {
+        auto look_up = [&] {                                 // the next block's records; false after the last block
             while (block == end_block) {
-                if (ended || (!may_wait && !__all_sync(0xffffffffu, t5::test(l_full + 8 * at, lap)))) return false;
-                if (may_wait) here();
+                here();
                 __syncwarp();
                 const Piece &w = list[at];
-                if (__any_sync(0xffffffffu, dead) || w.k1 < 0) {
-                    ended = true;
-                    return false;
-                }
+                if (__any_sync(0xffffffffu, dead) || w.k1 < 0) return false;
                 block = w.k0;
                 end_block = w.k1;
                 table = p.table + (long long)w.b * p.width;
@@ -937,31 +931,39 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             }
         };
         Raw<D> raw[2];
-        bool there[2] = {false, false}, more = false;        // blocks fetched; whether the one looked up is still to be
+        bool there[2], more = look_up();                     // blocks fetched; whether rec is another's
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            there[x] = more;
+            if (more) {
+                fetch(raw[x]);
+                more = look_up();
+            }
+        }
         uint32_t st = 0, parity = 1;                         // (the first use of each stage finds it free)
-        while (true) {
+        while (there[0]) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                if (there[x]) {
-                    wait(empty + 8 * st, parity);
-                    if (value) decode_values<D>(ring + st * C::STAGE, to, odd, raw[x]);
-                    else decode_keys<D>(ring + st * C::STAGE, to, raw[x]);
-                    t5::fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && !p.stall) arrive(full + 8 * st);
-                    if (++st == ST) {
-                        st = 0;
-                        parity ^= 1u;
-                    }
+                if (!there[x]) {
+                    there[0] = false;
+                    break;
                 }
-                if (!more) more = look_up(!there[x ^ 1]);
+                wait(empty + 8 * st, parity);
+                if (value) decode_values<D>(ring + st * C::STAGE, to, odd, raw[x]);
+                else decode_keys<D>(ring + st * C::STAGE, to, raw[x]);
+                t5::fence_async_smem();
+                __syncwarp();
+                if (lane == 0 && !p.stall) arrive(full + 8 * st);
+                if (++st == ST) {
+                    st = 0;
+                    parity ^= 1u;
+                }
                 there[x] = more;
                 if (more) {
                     fetch(raw[x]);
-                    more = look_up(false);
+                    more = look_up();
                 }
             }
-            if (ended && !there[0] && !there[1]) break;
         }
     } else if (warp == C::SW + C::DW) {
         // ------------------------------------------------------- products
@@ -1033,7 +1035,6 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 const bool two = T == 2 && list[at].count > 128;
                 if (k1 < 0) break;
                 leave(true);
-                if (n == 0) continue;
                 wait(q_ready, pieces[0]++ & 1u);
                 if (two) wait(q_ready + 8, pieces[1]++ & 1u);
                 for (int j = 0; j < min(n, 2); ++j) {
@@ -1094,8 +1095,15 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 }
                 last_join |= parts;
             }
+            // Rows that see nothing are done here: a piece without blocks is not listed. (The decoding warps ask for the
+            // next piece while they hold two blocks not decoded, whose pieces keep their places meanwhile: the list has
+            // places enough as long as every piece has a block.)
+            if (more && w.k1 == w.k0) {
+                nothing_seen<D>(p, w, C::PAIR ? rank * 128 : 0, lane);
+                continue;
+            }
             // its query rows, on their way to L2
-            if (more && w.k1 > w.k0) {
+            if (more) {
                 const int lo = C::PAIR ? rank * 128 : 0, hi = min(w.count, lo + 128 * T);
                 for (int r = lo + lane; r < hi; r += 32) {
                     const int i = sk::quotient(w.idx0 + r, p.by_g), g = w.idx0 + r - i * p.G;

@@ -119,14 +119,6 @@ __device__ __forceinline__ void st32(uint32_t addr, const uint32_t *v) {
                  "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(addr) : "memory");
 }
 
-// Whether `bar`'s phase of this parity is complete.
-__device__ __forceinline__ bool test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
-
 // Wait until `bar`'s phase of this parity is complete, for so many seconds at most. The
 // clock is read every 1024 tries: read after every one (as where a wait is rare),
 // its latency is added to each wait that is not over at once.

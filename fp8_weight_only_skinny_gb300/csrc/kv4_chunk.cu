@@ -96,16 +96,23 @@ __device__ __forceinline__ int worker() {
 }
 
 // Each row's weights are 2^(c s - t) with c = scale * key scale * log2 e and t the
-// row's base: one fma gives the exponent, rounded once. t is P_SHIFT below a maximum
-// that the row had earlier and is moved only when an exponent passes P_SHIFT + SLACK;
-// the weights go to the second product in FP16, between 2^-32 and 2^15 (that of the
-// maximum the base was set by is a power of two: the largest weight of most rows is
-// not rounded), their sum is taken unrounded. An exponent is off by what c s is
-// rounded by before the difference: 2^-24 of it, as the score itself (FP32).
-__device__ __forceinline__ void write_lse(const AttnParams &p, long long row, float base, float l) {
-    if (p.lse) p.lse[row] = l == 0.f ? NEG_INF : (base + __log2f(l)) * LN2;
+// row's base, one number for all that is summed under it: one fma gives the exponent,
+// rounded once, at the size of the difference, so that equal scores get equal weights in
+// any block, and weights near the maximum are right whatever the scores' size. The base is
+// t0, a float P_SHIFT below a maximum that the row had earlier, and is moved only when an
+// exponent passes P_SHIFT + SLACK. From FAR on floats lie too far apart for that: there
+// the base is t0 + t1, t0 the float nearest to c times the maximum and t1 what that leaves,
+// taken off in a second step (by a loop of its own: as a branch of the common one, never
+// taken, that step cost 3 to 7 %).
+// The weights go to the second product in FP16, between 2^-32 and 2^15 (that of the
+// maximum by which the base was set is a power of two but for the exponent's rounding: the
+// largest weight of most rows is not rounded), their sum is taken unrounded.
+constexpr float FAR = 0x1p24f;
+__device__ __forceinline__ void write_lse(const AttnParams &p, long long row, float t0, float t1, float l) {
+    if (p.lse) p.lse[row] = l == 0.f ? NEG_INF : (t0 + (t1 + __log2f(l))) * LN2;
 }
 
+// (part_ml: per row of a partial slot t0, t1 and the sum)
 struct ChunkParams : AttnParams {
     const int32_t *starts;             // null: M rows of every sequence
     int rows;                          // in all
@@ -579,7 +586,7 @@ __device__ __forceinline__ void nothing_seen(const ChunkParams &p, const Piece &
         const int idx = w.idx0 + r, i = sk::quotient(idx, p.by_g);
         const long long to = (long long)(w.row0 + i) * (p.heads * p.G) + w.h * p.G + idx - i * p.G;
         reinterpret_cast<uint4 *>(p.out + to * D)[lane % LANES] = make_uint4(0u, 0u, 0u, 0u);
-        if (lane % LANES == 0) write_lse(p, to, 0.f, 0.f);
+        if (lane % LANES == 0) write_lse(p, to, 0.f, 0.f, 0.f);
     }
 }
 
@@ -725,7 +732,8 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             const Piece &w = list[at];
             const int n = w.k1 - w.k0;
             const bool active = C::PAIR || first < w.count;
-            float t0 = 0.f, most = -FLT_MAX;                 // the row's base, and what moves it (at first: any score)
+            float t0 = 0.f, t1 = 0.f, most = -FLT_MAX;       // the row's base, and what moves it (at first: any score)
+            bool far = false;                                // whether a row of the warp has a t1
             uint64_t sum = two(0.f, 0.f);
             if (active) {
                 const int i = sk::quotient(w.idx0 + first + row, p.by_g);
@@ -740,6 +748,13 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     __syncwarp();
                     ++blocks_done;
                     t5::fence_after();
+                    auto weighted = [&] {
+                        t5::wait_st();
+                        t5::fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive(p_ready + 8 * (t * NB + sb));
+                        pos += KB;
+                    };
                     float s[KB];
                     t5::ld64(s_col, s);
                     if (pos + KB > lim0 || (pos + KB > p.sinks && pos < low1)) {
@@ -748,24 +763,24 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                             if (pos + e >= lim || (pos + e >= p.sinks && pos + e < low)) s[e] = NEG_INF;
                     }
                     float m0 = NEG_INF, m1 = NEG_INF, m2 = NEG_INF, m3 = NEG_INF;
-                    const uint64_t c2 = two(p.c, p.c), n2 = two(-t0, -t0);
 #pragma unroll
                     for (int e = 0; e < KB; e += 2) {
-                        const float2 x = apart(fma2(two(s[e], s[e + 1]), c2, n2));
-                        s[e] = x.x;
-                        s[e + 1] = x.y;
                         float &m = e % 8 == 0 ? m0 : e % 8 == 2 ? m1 : e % 8 == 4 ? m2 : m3;
-                        m = fmaxf(fmaxf(x.x, x.y), m);       // (one instruction)
+                        m = fmaxf(fmaxf(s[e], s[e + 1]), m);       // (one instruction)
                     }
                     m0 = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
-                    if (__any_sync(0xffffffffu, m0 > most)) {
-                        const float by = m0 > most ? m0 - P_SHIFT : 0.f, f = most < 0.f ? 0.f : ex2(-by);
-                        if (m0 > most) most = P_SHIFT + SLACK;
-                        t0 += by;
+                    const bool moves = fmaf(m0, p.c, -t0) - t1 > most;
+                    if (__any_sync(0xffffffffu, moves || far)) {
+                        const float h = m0 * p.c, was0 = t0, was1 = t1;
+                        if (moves) {
+                            t0 = fabsf(h) < FAR ? h - P_SHIFT : h;
+                            t1 = fabsf(h) < FAR ? 0.f : __fadd_ru(fmaf(m0, p.c, -h), -P_SHIFT);
+                        }
+                        const float f = most < 0.f ? 0.f : ex2((was0 - t0) + (was1 - t1));
+                        if (moves) most = P_SHIFT + SLACK;
+                        far = __any_sync(0xffffffffu, t1 != 0.f);
                         const float2 l = apart(sum);
                         sum = two(l.x * f, l.y * f);
-#pragma unroll
-                        for (int e = 0; e < KB; ++e) s[e] -= by;
                         if (j > 0) {
                             // The output so far, once the product before this one is done. (A barrier tells a phase from the
                             // next only; the product before that is done, its scores' successors being here.)
@@ -782,6 +797,36 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                                 t5::st32(o_at + c, v);
                             }
                         }
+                        if (far) {
+#pragma unroll 1
+                            for (int c = 0; c < KB; c += 8) {          // (weights over scores already read)
+                                float x[8];
+                                uint32_t y16[4];
+                                t5::ld8(s_col + c, x);
+#pragma unroll
+                                for (int e = 0; e < 8; e += 2) {
+                                    float y[2];
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i) {
+                                        const int at = pos + c + e + i;
+                                        const bool seen = at < lim && (at < p.sinks || at >= low);
+                                        y[i] = seen ? ex2(fmaf(x[e + i], p.c, -t0) - t1) : 0.f;
+                                    }
+                                    sum = add2(sum, two(y[0], y[1]));
+                                    y16[e / 2] = pack_f16(y[0], y[1]);
+                                }
+                                t5::st4(s_col + c / 2, y16);
+                            }
+                            weighted();
+                            continue;
+                        }
+                    }
+                    const uint64_t c2 = two(p.c, p.c), n2 = two(-t0, -t0);
+#pragma unroll
+                    for (int e = 0; e < KB; e += 2) {
+                        const float2 x = apart(fma2(two(s[e], s[e + 1]), c2, n2));
+                        s[e] = x.x;
+                        s[e + 1] = x.y;
                     }
                     uint32_t y16[KB / 2];
 #pragma unroll
@@ -791,11 +836,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                         y16[e / 2] = pack_f16(y0, y1);
                     }
                     t5::st32(s_col, y16);
-                    t5::wait_st();
-                    t5::fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive(p_ready + 8 * (t * NB + sb));
-                    pos += KB;
+                    weighted();
                 }
             }
             // The next piece's query rows first: its scores are formed beside this one's end.
@@ -867,9 +908,9 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     }
                 }
                 if (there) {
-                    if (whole) write_lse(p, to, t0, l);
+                    if (whole) write_lse(p, to, t0, t1, l);
                     else
-                        *reinterpret_cast<float2 *>(p.part_ml + (slot * C::ROWS + first + row) * 2) = make_float2(t0, l);
+                        *reinterpret_cast<float4 *>(p.part_ml + (slot * C::ROWS + first + row) * 4) = make_float4(t0, t1, l, 0.f);
                 }
             }
             t5::fence_before();
@@ -1163,20 +1204,25 @@ __global__ void __launch_bounds__(JT) kv4_chunk_join_kernel(const __grid_constan
     const int idx = tile.idx0 + r, i = sk::quotient(idx, p.by_g);
     const long long at = (long long)(s.first + i) * (p.heads * p.G) + h * p.G + idx - i * p.G;
     auto slot = [&](int k) { return (size_t(seg.x) + k) * 2 + (k == 0 ? 1 : 0); };
-    float top = NEG_INF, l = 0.f, v[PER];
+    float top0 = -FLT_MAX, top1 = 0.f, l = 0.f, v[PER];
 #pragma unroll
     for (int x = 0; x < PER; ++x) v[x] = 0.f;
     for (int k0 = 0; k0 < n; k0 += 32) {           // 32 parts at a time, under the largest base so far
-        float2 ml = make_float2(NEG_INF, 0.f);
-        if (k0 + lane < n) ml = *reinterpret_cast<const float2 *>(p.part_ml + (slot(k0 + lane) * C::ROWS + r) * 2);
+        float4 ml = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + lane < n) ml = *reinterpret_cast<const float4 *>(p.part_ml + (slot(k0 + lane) * C::ROWS + r) * 4);
         // (a part in which the row saw nothing has no base)
-        float now = ml.y == 0.f ? -FLT_MAX : ml.x;
+        const float old0 = top0, old1 = top1, base = ml.z == 0.f ? -FLT_MAX : ml.x;
+        auto larger = [&](float x0, float x1) {    // (bases of FP64 numbers took 30 us for 57000 rows)
+            if ((x0 - top0) + (x1 - top1) > 0.f) {
+                top0 = x0;
+                top1 = x1;
+            }
+        };
+        larger(base, ml.y);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, o));
-        now = fmaxf(now, top);
-        const float old = ex2(top - now), f = ml.y == 0.f ? 0.f : ex2(ml.x - now);
-        top = now;
-        float add = ml.y * f;
+        for (int o = 16; o; o >>= 1) larger(__shfl_xor_sync(0xffffffffu, top0, o), __shfl_xor_sync(0xffffffffu, top1, o));
+        const float old = ex2((old0 - top0) + (old1 - top1)), f = ml.z == 0.f ? 0.f : ex2((base - top0) + (ml.y - top1));
+        float add = ml.z * f;
 #pragma unroll
         for (int o = 16; o; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
         l = l * old + add;
@@ -1199,7 +1245,7 @@ __global__ void __launch_bounds__(JT) kv4_chunk_join_kernel(const __grid_constan
     __half2 *const out = reinterpret_cast<__half2 *>(p.out + at * D) + lane;
 #pragma unroll
     for (int x = 0; x < PER / 2; ++x) out[32 * x] = __floats2half2_rn(v[2 * x] * f, v[2 * x + 1] * f);
-    if (lane == 0) write_lse(p, at, top, l);
+    if (lane == 0) write_lse(p, at, top0, top1, l);
 }
 
 template <int D>
@@ -1217,7 +1263,7 @@ sk_status run(ChunkParams &p, unsigned char *scratch, int sms, cudaStream_t s) {
     p.tiles = reinterpret_cast<int *>(scratch);
     p.join = reinterpret_cast<int4 *>(scratch + 256);
     p.part_ml = reinterpret_cast<float *>(scratch + 256 + (size_t(p.ctas) * sizeof(int4) + 255) / 256 * 256);
-    p.part_o = p.part_ml + size_t(p.ctas) * 2 * C::ROWS * 2;
+    p.part_o = p.part_ml + size_t(p.ctas) * 2 * C::ROWS * 4;
     if (size_t(reinterpret_cast<unsigned char *>(p.part_o + size_t(p.ctas) * 2 * C::ROWS * D) - scratch) > sk::SCRATCH_BYTES)
         return SK_ERR_WORKSPACE;
     if (sk::prepare_kernel<kv4_chunk_kernel<D>>(C::SMEM) != cudaSuccess) return SK_ERR_CUDA;

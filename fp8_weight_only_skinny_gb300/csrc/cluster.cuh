@@ -29,6 +29,9 @@ __device__ __forceinline__ uint32_t peer(uint32_t addr, uint32_t rank) {
     return r;
 }
 __device__ __forceinline__ uint32_t peer(const void *p, uint32_t rank) { return peer(smem_u32(p), rank); }
+__device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.volatile.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t ld_peer_u32(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");

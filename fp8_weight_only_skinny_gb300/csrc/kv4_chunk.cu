@@ -80,7 +80,8 @@ struct Cc {
     // and of the list of pieces, full and empty (LIST each)
     static constexpr int LIST = 4;
     static constexpr int NBARS = 4 * ST + 2 * T * NB + 3 * T + 1 + 2 * LIST;
-    static constexpr int SCAN = BARS + 8 * NBARS, TMEM = SCAN + 16 * (WARPS_ALL + 1), START = TMEM + 16, PIECES = START + 16;
+    // (and behind the TMEM's address whether a wait has run out)
+    static constexpr int SCAN = BARS + 8 * NBARS, TMEM = SCAN + 16 * (WARPS_ALL + 1), GONE = TMEM + 8, START = TMEM + 16, PIECES = START + 16;
     static constexpr int OUT = (PIECES + LIST * 64 + 127) / 128 * 128;         // 128 bytes of a row, per thread of the softmax
     static constexpr int BYTES = 1024 + OUT + SW * 32 * 128;
     static constexpr size_t SMEM = BYTES > 120 * 1024 ? BYTES : 120 * 1024;      // one CTA per SM: all of the TMEM
@@ -632,6 +633,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
     // (every place of the list an end: a thread that gave up waiting finds nothing else)
     if (tid < C::LIST * 16) reinterpret_cast<int *>(smem + C::PIECES)[tid] = tid % 16 == 1 ? -1 : 0;
     static_assert(offsetof(Piece, k1) == 4, "the second word of a piece");
+    if (tid == 0) *reinterpret_cast<volatile uint32_t *>(smem + C::GONE) = 0u;
     __syncwarp();
     t5::fence_before();
     if constexpr (C::PAIR) sk::cluster_sync();
@@ -650,10 +652,18 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
     bool dead = false;
     // Waits for a barrier's phase of this parity, a second at most; after one that
     // ran out the thread waits no more.
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (dead || t5::wait_spin(bar, parity)) return;
+    auto give_up = [&] {
         dead = true;
-        atomicOr(p.err, 1u);
+        sk::st_shared_volatile(base + C::GONE, 1u);
+        if constexpr (C::PAIR) sk::st_peer_u32(sk::peer(base + C::GONE, rank ^ 1), 1u);
+    };
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!dead && !t5::wait_spin(bar, parity)) give_up();
+    };
+    // The warps that do nothing but follow the list wait for whole pieces: a minute at most, and no longer than until
+    // another wait of the CTA (or the pair) has run out. (Read in every wait, that word cost up to 4 %.)
+    auto wait_long = [&](uint32_t bar, uint32_t parity) {
+        if (!dead && !t5::wait_spin(bar, parity, 60, base + C::GONE)) give_up();
     };
     // This warp's or thread's way through the list: the place of its next piece.
     const Piece *const list = reinterpret_cast<const Piece *>(smem + C::PIECES);
@@ -843,7 +853,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
             const uint32_t after = at + 1 == C::LIST ? 0 : at + 1;
             wait(l_full + 8 * after, after ? lap : lap ^ 1u);
             __syncwarp();
-            load_q(list[after]);
+            if (!__any_sync(0xffffffffu, dead)) load_q(list[after]);      // (else it may be half written)
             // ---- the rows' outputs, or their part of them
             const bool whole = w.k0 == 0 && w.k1 == w.blocks, there = first + row < w.count;
             const size_t slot = size_t(worker<D>()) * 2 + (w.k0 == 0 ? 1 : 0);
@@ -1013,7 +1023,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         // along: a lone warp's instructions are ten clocks apart, and a block's turn here is on everyone's path.
         if (rank != 0) {
             while (true) {             // (the first CTA's thread reads the pieces that this one lists)
-                here();
+                wait_long(l_full + 8 * at, lap);
                 __syncwarp();
                 if (__any_sync(0xffffffffu, dead) || list[at].k1 < 0) break;
                 __syncwarp();
@@ -1022,9 +1032,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         } else if (t5::elect()) {
             constexpr uint64_t STEP = C::STAGE / 16;
             auto wait = [&](uint32_t bar, uint32_t parity) {
-                if (dead || t5::wait_spin<C::PAIR>(bar, parity)) return;
-                dead = true;
-                atomicOr(p.err, 1u);
+                if (!dead && !t5::wait_spin<C::PAIR>(bar, parity)) give_up();
             };
             const uint64_t k_op0 = t5::operand(base + C::K, 16, 1024), v_op0 = t5::operand(base + C::V, C::V_SLAB, 1024),
                            q_op = t5::operand(base + C::Q, 16, 1024);     // (of query rows in shared memory)
@@ -1118,7 +1126,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         Piece w = {};
         int t = 0, number = 0, cost = 0, last_join = 0;
         const int me = worker<D>();
-        for (bool more = true; more && !__any_sync(0xffffffffu, dead);) {
+        for (bool more = true; more;) {
             more = work.next(p, w, t, number, cost);
             if (!more) {
                 w = Piece{};               // the end: nothing of it may be taken for a piece's
@@ -1136,6 +1144,8 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                 }
                 last_join |= parts;
             }
+            // (after a wait that ran out the tiles in parts are listed all the same: the join reads of every one where it is)
+            if (__any_sync(0xffffffffu, dead)) continue;
             // Rows that see nothing are done here: a piece without blocks is not listed. (The decoding warps ask for the
             // next piece while they hold two blocks not decoded, whose pieces keep their places meanwhile: the list has
             // places enough as long as every piece has a block.)
@@ -1153,12 +1163,8 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
                     for (int c = 0; c < D; c += 64) sk::prefetch_l2(src + c);
                 }
             }
-            // (a piece may take longer than any other wait)
-            if (!dead && !t5::wait_spin(l_empty + 8 * at, lap ^ 1u, 60)) {
-                dead = true;
-                atomicOr(p.err, 1u);
-            }
-            __syncwarp();
+            wait_long(l_empty + 8 * at, lap ^ 1u);
+            if (__any_sync(0xffffffffu, dead)) continue;
             if (lane == 0) {
                 *reinterpret_cast<Piece *>(smem + C::PIECES + at * 64) = w;
                 sk::mbar_arrive(l_full + 8 * at);
@@ -1171,6 +1177,7 @@ __global__ void __launch_bounds__(Cc<D>::CT_ALL, 1) kv4_chunk_kernel(const __gri
         if (lane == 0 && rank == 0 && !p.by_tile && !last_join) p.join[me] = Join::of(0, 0, 0, 0, 0);
         __syncwarp();
     }
+    if (dead) atomicOr(p.err, 1u);
     if constexpr (C::PAIR) {
         // neither CTA leaves while the other, or a product's end, may arrive at its barriers
         if (warp == 0) t5::wait_spin(end, 0);

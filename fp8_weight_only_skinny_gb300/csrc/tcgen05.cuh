@@ -130,12 +130,13 @@ __device__ __forceinline__ void st32(uint32_t addr, const uint32_t *v) {
                  "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(addr) : "memory");
 }
 
-// Wait until `bar`'s phase of this parity is complete, for so many seconds at most. The
-// clock is read every 1024 tries: read after every one (as where a wait is rare),
-// its latency is added to each wait that is not over at once.
+// Wait until `bar`'s phase of this parity is complete, for so many seconds at most, or
+// until the word of shared memory at `gone` (0: none) says that another wait ran out. The
+// clock and that word are read every 1024 tries: read after every one (as where a wait is
+// rare), the clock's latency is added to each wait that is not over at once.
 // CLUSTER: for what the cluster's other CTA did before it arrived.
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool wait_spin(uint32_t bar, uint32_t parity, uint64_t seconds = 1) {
+__device__ __forceinline__ bool wait_spin(uint32_t bar, uint32_t parity, uint64_t seconds = 1, uint32_t gone = 0) {
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
         if constexpr (CLUSTER) {
@@ -150,6 +151,7 @@ __device__ __forceinline__ bool wait_spin(uint32_t bar, uint32_t parity, uint64_
             const uint64_t t = globaltimer_ns();
             if (t0 == 0) t0 = t;
             else if (t - t0 > seconds * 1000000000ull) return false;
+            if (gone && ld_shared_volatile(gone)) return false;
         }
     }
 }

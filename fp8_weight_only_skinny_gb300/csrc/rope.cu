@@ -485,7 +485,7 @@ extern "C" sk_status rope_frequencies(uint64_t *freqs, int rot_dim, int scaling,
     if (scaling == SK_ROPE_BASE && rot_dim) base *= std::pow(factor, r / (r - 2));
     // the index at which a frequency turns `t` times within the original context
     auto at = [&](double t) { return r * std::log(original / (t * two_pi)) / (2 * std::log(base)); };
-    const double first = std::fmax(0.0, std::floor(at(high))), last = std::fmin(r / 2 - 1, std::ceil(at(low)));
+    const double first = std::fmax(0.0, std::floor(at(high))), last = std::fmin(r - 1, std::ceil(at(low)));
     for (int i = 0; i < rot_dim / 2; ++i) {
         double f = std::pow(base, -2.0 * i / r);
         double keep = 1.0;

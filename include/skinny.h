@@ -366,7 +366,9 @@ SK_API sk_status kv4_attention(const void *q, long long q_stride, const uint8_t 
  *                   to [0, 1], t_i = original * f_i / (2 pi) turns in the original context
  *   SK_ROPE_INDEX   the same with s falling from 1 to 0 linearly in the index, between
  *                   those of the frequencies that turn `high` times (rounded down,
- *                   at least 0) and `low` times (rounded up, at most rot_dim / 2 - 1)
+ *                   at least 0) and `low` times (rounded up, at most rot_dim - 1: beyond
+ *                   the last index rot_dim / 2 - 1 where that turns more than `low` times,
+ *                   so that its s is above 0)
  *   1 < base <= 1e12; 1 <= factor <= 1e6 (not read by PLAIN); TURNS and INDEX:
  *   1 <= original <= 1e12, 0 < low < high <= 1e6; rot_dim even (BASE: not 2).
  */

@@ -32,7 +32,7 @@ def frequencies(rot, base, scaling="plain", factor=1.0, original=0.0, low=1.0, h
         elif scaling == "turns":
             keep = (original * f / (2 * math.pi) - low) / (high - low)
         elif scaling == "index":
-            first, last = max(0, math.floor(at(high))), min(rot // 2 - 1, math.ceil(at(low)))
+            first, last = max(0, math.floor(at(high))), min(rot - 1, math.ceil(at(low)))
             keep = 1 - (i - first) / max(1e-3, last - first)
         keep = min(1.0, max(0.0, keep))
         out.append(f if scaling in ("plain", "base") else f * (keep + (1 - keep) / factor))

@@ -153,10 +153,11 @@ __device__ __forceinline__ int cta_of(const Share &s, int tile) {
     return tile < large ? tile / (s.base + 1) : s.extra + (tile - large) / s.base;
 }
 
-__device__ __forceinline__ int inclusive_scan(int x, int lane) {
+template <typename T>
+__device__ __forceinline__ T inclusive_scan(T x, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     return x;

@@ -300,7 +300,7 @@ __device__ Split find_share(const ChunkParams &p, Pieces<D> &w, int *list, long 
             Seq of;
             for (int i0 = 0; i0 < tiles; i0 += 32) {
                 at(min(i0 + lane, tiles - 1), b, t, of);
-                int cost = i0 + lane < tiles ? Tile<D>(p, of, t).cost : 0;
+                long long cost = i0 + lane < tiles ? Tile<D>(p, of, t).cost : 0;      // (32 of them may pass 31 bits)
 #pragma unroll
                 for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xffffffffu, cost, o);
                 per_head += cost;
@@ -313,13 +313,13 @@ __device__ Split find_share(const ChunkParams &p, Pieces<D> &w, int *list, long 
             long long off = u0 - w.h * per_head;
             for (int i0 = 0; i0 < tiles; i0 += 32) {
                 at(min(i0 + lane, tiles - 1), b, t, of);
-                const int cost = i0 + lane < tiles ? Tile<D>(p, of, t).cost : 0, x = inclusive_scan(cost, lane);
+                const long long cost = i0 + lane < tiles ? Tile<D>(p, of, t).cost : 0, x = inclusive_scan(cost, lane);
                 const unsigned int past = __ballot_sync(0xffffffffu, x > off);
                 if (past) {
                     const int l = __ffs(past) - 1;
                     w.b = w.held = __shfl_sync(0xffffffffu, b, l);
                     w.t = __shfl_sync(0xffffffffu, t, l);
-                    w.x = int(off) - __shfl_sync(0xffffffffu, x - cost, l);
+                    w.x = int(off - __shfl_sync(0xffffffffu, x - cost, l));
                     w.number = i0 + l;
                     w.seq.first = __shfl_sync(0xffffffffu, of.first, l);
                     w.seq.n = __shfl_sync(0xffffffffu, of.n, l);

@@ -66,9 +66,9 @@
  *         be the kernel immediately preceding a linear call on the same
  *         stream while PDL is on (sk_set_pdl(0) turns it off); anything
  *         launched in between without PDL -- any other kernel, a copy, an
- *         event wait -- ends the hazard.  The cache calls and token_logprobs
- *         are launched with PDL and do not end it; they read nothing before the
- *         preceding kernel has completed.
+ *         event wait -- ends the hazard.  The cache calls, qk_norm_rope and
+ *         token_logprobs are launched with PDL and do not end it; they read
+ *         nothing before the preceding kernel has completed.
  *   - Kernels bound every wait they spin on (about one second).  When a wait
  *     runs out the kernel records SK_ERR_TIMEOUT in a device word, finishes
  *     without further waiting and leaves garbage in y; sk_last_device_error()
@@ -131,8 +131,9 @@ SK_API sk_status sk_init(size_t workspace_bytes);
  * out.  A cooperative kernel starts only when the whole grid fits, so
  * overlapping calls share the SMs in turns rather than at once; such
  * linear-layer calls are also launched without programmatic dependent launch.
- * (The cache calls and token_logprobs are launched as on any other stream, with
- * it where sk_set_pdl allows: their CTAs wait for none outside a cluster.)  Up
+ * (The cache calls, qk_norm_rope and token_logprobs are launched as on any other
+ * stream, with it where sk_set_pdl allows: their CTAs wait for none outside a
+ * cluster.)  Up
  * to 64 stream workspaces per process; more return SK_ERR_INVALID_ARG.  Call it
  * before capturing a CUDA graph.  Needs no sk_init() (the device's workspace is
  * only the fallback).

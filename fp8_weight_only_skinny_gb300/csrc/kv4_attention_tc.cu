@@ -28,10 +28,12 @@
 #include "internal.h"
 #include "kv4_attention.cuh"
 #include "launch_util.cuh"
+#include "tcgen05.cuh"
 
 namespace {
 
 using namespace sk::attn;
+namespace t5 = sk::t5;
 
 constexpr int D = 128;
 static_assert(TILE == 128, "positions per tile");
@@ -58,43 +60,6 @@ struct Tc {
 
 // ------------------------------------------------------- tcgen05 ----------
 
-__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
-}
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// Shared-memory operand: start address, the two strides, swizzle (0 none, 2 of
-// 128 bytes).
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride, uint64_t swizzle) {
-    return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((lead >> 4) & 0x3FFFu) << 16) |
-           (uint64_t((stride >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (swizzle << 61);
-}
-// D (FP32) of M = 128, N columns, FP16 operands; bits 15 and 16: A and B stored
-// along M and N.
-__host__ __device__ constexpr uint32_t shape(int n, bool a_along_m, bool b_along_n) {
-    return (1u << 4) | (uint32_t(a_along_m) << 15) | (uint32_t(b_along_n) << 16) | (uint32_t(n >> 3) << 17) | (8u << 24);
-}
-__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)) : "memory");
-}
-__device__ __forceinline__ void mma_smem_a(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)) : "memory");
-}
-// Arrive on `bar` when the products issued so far by this thread are done.
-__device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
 // NH columns of this warp's 32 lanes, all loads in flight together.
 template <int NH>
 __device__ __forceinline__ void ld_row(uint32_t addr, float (&v)[NH]) {
@@ -110,16 +75,6 @@ __device__ __forceinline__ void ld_row(uint32_t addr, float (&v)[NH]) {
     for (int c = 0; c < NH; c += 8)
         asm volatile("" : "+f"(v[c]), "+f"(v[c + 1]), "+f"(v[c + 2]), "+f"(v[c + 3]), "+f"(v[c + 4]), "+f"(v[c + 5]),
                           "+f"(v[c + 6]), "+f"(v[c + 7]));
-}
-// Eight columns of this warp's 32 lanes.
-__device__ __forceinline__ void ld8(uint32_t addr, float (&v)[8]) {
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-                 "tcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(addr) : "memory");
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void st8(uint32_t addr, const float (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};"
@@ -230,22 +185,22 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
     float *const of_warp = reinterpret_cast<float *>(smem + C::WARP);
     const uint32_t bars = base + C::BARS, bar_s = bars + 8 * UNITS, bar_o = bar_s + 8, bar_end = bar_o + 8;
 
-    if (warp == 0) tmem_alloc(base + C::TMEM, 256);
+    if (warp == 0) t5::alloc<false>(base + C::TMEM, 256);
     if (tid == 0) {
         for (int i = 0; i < UNITS + 3; ++i) sk::mbar_init(bars + 8 * i, 1);
         sk::fence_barrier_init();
     }
-    fence_before();
+    t5::fence_before();
     __syncthreads();
-    fence_after();
+    t5::fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + C::TMEM);
     const uint32_t my_lanes = tmem + (uint32_t(quad * 32) << 16);
     sk::pdl_launch_dependents();
     sk::pdl_wait_primary();
     Share sh = share_of(p, p.heads * p.RT, sm_share);
     // the products' shared-memory operands at their first k16 step
-    const uint64_t q_op = operand(base + C::Q, 16, 1024, 2), v_op = operand(base + C::V, 16384, 1024, 2),
-                   p_op = operand(base + C::P, 128, 2048, 0);
+    const uint64_t q_op = t5::operand(base + C::Q, 16, 1024), v_op = t5::operand(base + C::V, 16384, 1024),
+                   p_op = t5::operand(base + C::P, 128, 2048, 0);
     uint32_t unit0 = 0, ph_s = 0, ph_o = 0;                  // units consumed; parities of the two products' barriers
     bool dead = false;
     // Copies of unit u (counted from the kernel's start), and a product beside which the units from u on are in flight.
@@ -319,7 +274,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
         float l[NH];
 #pragma unroll
         for (int i = 0; i < NH; ++i) l[i] = 0.f;
-        fence_async_smem();
+        t5::fence_async_smem();
         __syncthreads();
 
         for (int i = 0; i < tiles; ++i) {
@@ -330,17 +285,17 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             {
                 const int r = 2 * quad + side;               // record, in this warp's lanes
                 decode_keys(keys + r * PART, tmem + (uint32_t(16 * r) << 16), g, t);
-                wait_st();
+                t5::wait_st();
             }
-            fence_before();
+            t5::fence_before();
             __syncthreads();
             if (tid == 0) {
-                fence_after();
+                t5::fence_after();
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                    mma_tmem_a(tmem + C::S_COL, tmem + 8 * s, q_op + ((s >> 2) * (N * 128) + (s & 3) * 32) / 16,
-                               shape(N, false, false), s > 0);
-                commit(bar_s);
+                    t5::mma<false>(tmem + C::S_COL, tmem + 8 * s, q_op + ((s >> 2) * (N * 128) + (s & 3) * 32) / 16,
+                                   t5::shape<false>(N, false), s > 0);
+                t5::commit<false>(bar_s);
             }
             if (warp == 1) {
                 idx3 = lookup(i + 3);
@@ -350,7 +305,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             if (i > 0) {
                 wait_product(bar_o, ph_o, uv);
                 ph_o ^= 1;
-                fence_after();
+                t5::fence_after();
             }
             wait_unit(uv);
             decode_values(vals + warp * PART, base + C::V, warp * 16, lane);
@@ -358,7 +313,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             // of a position in 16 bytes, positions 16 bytes apart
             wait_product(bar_s, ph_s, uv + 1);
             ph_s ^= 1;
-            fence_after();
+            t5::fence_after();
             const int at = quad * 32 + lane, pos = (t_lo + i) * TILE + at;
             const bool edge = (t_lo + i + 1) * TILE > len - (p.M - 1);
             // CH scores of this position, rows side * NH + c and on
@@ -403,8 +358,8 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                     }
                     store_weights(c, s);
                 }
-                fence_async_smem();
-                fence_before();
+                t5::fence_async_smem();
+                t5::fence_before();
             }
             const bool any = __syncthreads_or(rise);         // the ring's records are decoded, too
             if (warp == 1) {
@@ -416,7 +371,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
                 // move the bases: each row's maximum over this warp's
                 // positions first, eight rows at a time, halving what a lane
                 // keeps (lanes 4 i .. 4 i + 3 end with row i)
-                fence_after();
+                t5::fence_after();
 #pragma unroll
                 for (int c = 0; c < NH; c += CH) {
                     float s[CH];
@@ -472,24 +427,24 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
 #pragma unroll 1
                     for (int c = 0; c < NH; c += 8) {
                         float o[8];
-                        ld8(my_lanes + C::O_COL + side * NH + c, o);
+                        t5::ld8(my_lanes + C::O_COL + side * NH + c, o);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) o[e] *= fac[side * NH + c + e];
                         st8(my_lanes + C::O_COL + side * NH + c, o);
                     }
-                    wait_st();
+                    t5::wait_st();
                 }
-                fence_async_smem();
-                fence_before();
+                t5::fence_async_smem();
+                t5::fence_before();
                 __syncthreads();
             }
             if (tid == 0) {
-                fence_after();
+                t5::fence_after();
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                    mma_smem_a(tmem + C::O_COL, v_op + s * 2048 / 16, p_op + s * 256 / 16, shape(N, true, true),
-                               i > 0 || s > 0);
-                commit(bar_o);
+                    t5::mma_smem(tmem + C::O_COL, v_op + s * 2048 / 16, p_op + s * 256 / 16, t5::shape<false>(N, true, true),
+                                 i > 0 || s > 0);
+                t5::commit<false>(bar_o);
             }
         }
         unit0 += 2 * tiles;
@@ -517,7 +472,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
         }
         wait_product(bar_o, ph_o, unit0);
         ph_o ^= 1;
-        fence_after();
+        t5::fence_after();
         __syncthreads();
         const bool whole = t_lo == 0 && t_hi == nt;
         const int rows = min(N, p.M * p.G - rt * N), d = quad * 32 + lane;
@@ -541,7 +496,7 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
 #pragma unroll 1
         for (int c = 0; c < NH; c += 8) {
             float o[8];
-            ld8(my_lanes + C::O_COL + side * NH + c, o);
+            t5::ld8(my_lanes + C::O_COL + side * NH + c, o);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int n = side * NH + c + e;
@@ -554,9 +509,9 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
             const int c1 = cta_of(sh, sh.t + nt - 1);     // of the segment's last tile
             p.seg[(b * p.heads + h) * p.RT + rt] = make_int2(int(blockIdx.x), whole ? 0 : c1 - int(blockIdx.x) + 1);
         }
-        fence_before();
+        t5::fence_before();
         __syncthreads();
-        fence_after();
+        t5::fence_after();
         sh.t += t_hi - t_lo;
         sh.off += t_hi - t_lo;
         if (sh.off == nt * p.heads * p.RT) {
@@ -566,12 +521,12 @@ __global__ void __launch_bounds__(TT, 2) kv4_attention_tc_kernel(const __grid_co
     }
     if (__syncthreads_or(dead)) {
         // a product may still be under way: its end, too, is waited for
-        if (tid == 0) commit(bar_end);
+        if (tid == 0) t5::commit<false>(bar_end);
         sk::wait_limited(bar_end, 0);
-        fence_after();
+        t5::fence_after();
         __syncthreads();
     }
-    if (warp == 0) tmem_free(tmem, 256);
+    if (warp == 0) t5::free<false>(tmem, 256);
 }
 
 template <int N>

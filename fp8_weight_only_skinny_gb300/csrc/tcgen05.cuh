@@ -1,5 +1,6 @@
 // tcgen05.cuh -- inline PTX of the fifth-generation tensor cores that
-// kv4_chunk.cu uses: TMEM, operands, products of one CTA, loads and stores of rows.
+// kv4_attention_tc.cu and kv4_chunk.cu use: TMEM, operands, products of one CTA or a
+// pair, loads and stores of rows.
 #pragma once
 #include <cstdint>
 
@@ -37,15 +38,17 @@ __device__ __forceinline__ bool elect() {
     return ok != 0;
 }
 
-// Shared-memory operand in 128-byte rows, 128-byte swizzle: start address, the two strides.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
+// Shared-memory operand: start address, the two strides, swizzle (0 none, 2 of 128
+// bytes, rows of 128 bytes).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride, uint64_t swizzle = 2) {
     return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((lead >> 4) & 0x3FFFu) << 16) |
-           (uint64_t((stride >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+           (uint64_t((stride >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (swizzle << 61);
 }
-// D (FP32) of M = 128 rows (of each CTA of a pair), N columns, FP16 operands; bit 16: B stored along N.
+// D (FP32) of M = 128 rows (of each CTA of a pair), N columns, FP16 operands; bits 15
+// and 16: A and B stored along M and N.
 template <bool PAIR>
-__host__ __device__ constexpr uint32_t shape(int n, bool b_along_n) {
-    return (1u << 4) | (uint32_t(b_along_n) << 16) | (uint32_t(n >> 3) << 17) | ((PAIR ? 16u : 8u) << 24);
+__host__ __device__ constexpr uint32_t shape(int n, bool b_along_n, bool a_along_m = false) {
+    return (1u << 4) | (uint32_t(a_along_m) << 15) | (uint32_t(b_along_n) << 16) | (uint32_t(n >> 3) << 17) | ((PAIR ? 16u : 8u) << 24);
 }
 // D (+)= A B^T, A in TMEM. A pair's CTAs have their own rows of A and D, and half of B's N each, at the same addresses.
 template <bool PAIR>

@@ -2,7 +2,8 @@
 everything, the second to a window and the first few tokens.
 
 Of every piece the queries and keys are normed and turned by position, the keys and values go to the cache in the same
-pass (kv4_append_rope), and the piece's rows attend to what the cache holds (kv4_chunk_attention). Then tokens are
+pass (kv4_append_rope), and the piece's rows attend to what the cache holds (kv4_chunk_attention). The framework's linear
+layers take 1 to 8 rows, so a piece is multiplied by a second, FP16 copy of the weights through PyTorch. Then tokens are
 decoded one by one: the linear layers in FP8, the same append, and attention of single rows (kv4_attention,
 kv4_window_attention).
 

@@ -872,9 +872,9 @@ constexpr int TC_ABOVE = 24;
 // Rows of a window that take the registers' kernel four passes or more go to that
 // for chunks, which decodes a position once for all rows, where there is enough to
 // do for its longer way in and out. 96 rows a kv head: 64 sequences, windows of 2000,
-// heads of 256 125 -> 71 us, of 128 116 -> 73 (windows of 200: 38 -> 27, 34 -> 27);
-// one sequence, window of 8000, heads of 256 17 against 26, of 128 18 against 22.
-// Three passes: 68 against 67 at most.
+// heads of 256 125 -> 70 us, of 128 116 -> 73 (windows of 200: 38 -> 27, 34 -> 27);
+// one sequence, window of 8000, heads of 256 17 against 27, of 128 18 against 23.
+// 48 rows, three passes at 256: 70 against 67; two at 128: 64 against 70.
 constexpr int CHUNK_PASSES = 4;
 constexpr long long CHUNK_WORK = 160000;      // positions, over all kv heads and passes
 

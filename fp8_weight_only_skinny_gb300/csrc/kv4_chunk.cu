@@ -15,15 +15,16 @@
 // thread that issues the products, one warp that lists the work. At head size 256 a
 // pair of CTAs takes two tiles and decodes each block once for both: decoding alone
 // bounds a single CTA there (2048 rows over 61003 positions, 24 over 2 heads: 2346 us
-// against 1684).
+// against 1684, when the pairs were new).
 //
-// At head size 256 bound by the products: that case 1693 us, 1783 TFLOP/s, alone, and
-// 1763 to 1865 in long runs of calls. At 128 and 64 by the softmax's chain from a
-// product to the next (2000 and 1490 clocks a block of two tiles, whose products take
-// 1280 and 512): 2048 rows over 16384 positions, 48 over 4 heads of 128, 609 us, 1270
-// TFLOP/s; issue slots, ALU and XU are below half of their rates. Twenty warps there,
-// with registers moved to the softmax's, spilled and took longer (644 -> 763). Calls
-// of a row over 24 to 4096 positions: 6 to 18 us.
+// At head size 256 bound by the products: that case 1699 to 1765 us over several runs of
+// calls, 1710 to 1777 TFLOP/s. At 128 and 64 by the softmax's chain from a
+// product to the next (1900 and 1520 clocks a block of two tiles, whose products take
+// 1280 and 512): 2048 rows over 16384 positions, 48 over 4 heads of 128, 590 us, 1310
+// TFLOP/s; issue slots, ALU and XU are below half of their rates. 128 registers a thread,
+// of which 44, 72 and 60 bytes are spilled at head sizes 256, 128 and 64 (92 bytes loaded
+// again at most). Twenty warps at 128, with registers moved to the softmax's, spilled far
+// more and took longer (644 -> 763). Calls of a row over 24 to 4096 positions: 6 to 18 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -46,7 +47,7 @@ namespace t5 = sk::t5;
 constexpr int KB = 64;                 // positions per block
 constexpr int MOST_SEQS = CHUNK_SEQS;
 // What a tile costs beside its blocks, in blocks (4099 rows over themselves, heads of
-// 256: 4 213 us, 8 176, 12 180; 8195 rows in windows of 1024, heads of 128: 282, 269, 275).
+// 256: 4 207 us, 8 169, 12 173; 8195 rows in windows of 1024, heads of 128: 284, 255, 259).
 constexpr int SETUP = 8;
 constexpr int WHOLE_BLOCKS = 12;       // tables of no more blocks are not worth a second kernel where each tile has a CTA
 constexpr int MIN_SHARE = 40;          // least cost a CTA takes, above that of one block: no part of a tile is empty
@@ -167,7 +168,7 @@ struct Tile {
         lim0 -= skip * sk::KV4_REC;
         lim1 -= skip * sk::KV4_REC;
         blocks = (max(lim1, 0) + KB - 1) / KB;
-        // (a block of one tile of 128 rows takes nearly as long as of two: 1750 clocks of 2000, at head size 64 1200 of 1490)
+        // (a block of one tile of 128 rows takes nearly as long as of two: 1730 clocks of 1900, at head size 64 1230 of 1520)
         per = C::T == 1 || count > 128 ? 10 : D == 64 ? 8 : 9;
         cost = p.whole ? 1 : (blocks + SETUP) * per;
     }

@@ -13,7 +13,8 @@
 // Bound by DRAM and instructions together: 8191 tokens of 32 + 8 heads of 128, interleaved
 // and normed, 31 us (168 MB, 5.4 TB/s); 16387 tokens of 24 + 2 + 2 heads of 256 to the
 // cache 99 us (446 MB, 4.5 TB/s; issue 64 %, DRAM 52 %). One token 2.9 us.
-// Two components an instruction, f32x2, gained nothing: 99 -> 105 us, 31 -> 31.
+// Two components an instruction, f32x2, gained nothing: 99 -> 105 us, 31 -> 31. At 64
+// registers a thread the append's kernels spill 28 to 56 bytes, the rotation's none.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 

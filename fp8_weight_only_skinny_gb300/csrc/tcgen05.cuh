@@ -78,7 +78,9 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 }
 // Arrive on a barrier of any CTA of the cluster (an address of peer()). What this
 // thread did is ordered for its own CTA, whose memory the products read it from: a
-// release for the cluster takes 1200 clocks.
+// release for the cluster takes 1200 clocks. (The memory model promises the order to
+// threads of this CTA only; that the products of a thread of the other CTA meet it rests
+// on their reading this CTA's memory through this CTA.)
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

@@ -389,10 +389,12 @@ SK_API sk_status rope_frequencies(uint64_t *freqs, int rot_dim, int scaling, dou
  *   positions  const i32 [tokens] (any value, also negative)
  *   freqs      const u64 [rot_dim / 2], device memory, 8-byte aligned; positions and
  *              freqs may be NULL if rot_dim = 0 (norm alone)
- *   q_weight, k_weight  const f32 [D], or both NULL (no norm)
+ *   q_weight, k_weight  const f32 [D] of magnitude 1e30 at most, or both NULL (no
+ *              norm)
  *   q_out, k_out  f16, as q and k with strides of their own; q_out may be q and
  *              k_out may be k with the same stride (in place), no other overlap
- *   D = head_dim in {64, 128, 256}; rot_dim a multiple of 16, 0 .. D; 0 <= eps <= 1;
+ *   D = head_dim in {64, 128, 256}; rot_dim a multiple of 16, 0 .. D; 0 <= eps <= 1
+ *   (0: a head of zeros has no norm and becomes NaN);
  *   1e-3 <= |amplitude| <= 1e3 (1, or the factor that a lengthened context asks for);
  *   heads <= 4096.  Computed in FP32 (the norm's sum too), rounded to FP16 once.
  *   tokens = 0: nothing is launched.  Needs no workspace.
